@@ -330,6 +330,145 @@ moe_status moe_ffn_forward(moe_ffn_t ffn, const uint16_t *u, int num_tokens, con
 moe_status moe_quantize_nvfp4(const void *src, int32_t src_dtype, int64_t rows, int32_t n, float a,
                               uint8_t *codes, uint8_t *scales, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------
+ * The attention beside the FFN: what a serving step (decode, the verify pass
+ * of drafted rows, prefill) runs over a paged key/value cache before it calls
+ * the FFN.  One step is
+ *   moe_kv_plan    request lengths -> new pages in the block table, a cache
+ *                  slot per row, positions, and tree masks from parents
+ *   moe_kv_append  the step's key / value rows -> their slots
+ *   moe_attn_prompt (whole prompts, nothing cached: reads the rows) or
+ *   moe_attn_tree  (rows over the cache: single tokens, drafted trees, or the
+ *                  next part of a prompt)
+ *
+ * Request b has cached[b] tokens in the cache and fresh[b] rows of this step.
+ * The rows of all requests are packed: those of request b are rows
+ * cu[b] .. cu[b + 1) - 1 of every per-row array.
+ * A cache (one for keys, one for values) is [num_pages][kv_heads][page_size]
+ * [head_dim]: token p of request b is at page block_table[b][p / page_size],
+ * place p % page_size.  A slot is page * page_size + place.
+ * Query head h reads kv head h / (q_heads / kv_heads).
+ * Elements are bf16 or f16 (the same in rows, caches and outputs); products
+ * are accumulated, and the softmax's maximum and sum kept, in fp32.
+ * Nothing here synchronises or allocates: every call can be captured.
+ * Rows, caches and the workspace are 16-byte aligned; int32, uint64 and fp32
+ * arrays need their own alignment only. */
+typedef struct moe_attn *moe_attn_t;
+
+#define MOE_ATTN_BF16 0
+#define MOE_ATTN_F16 1
+#define MOE_ATTN_MAX_REQUESTS 1024
+#define MOE_ATTN_MAX_ROWS 1048576      /* rows of a call */
+#define MOE_ATTN_MAX_TREE 64           /* rows of a drafted tree: bits of a mask word */
+
+typedef struct {
+  int32_t q_heads;        /* a multiple of kv_heads; q_heads / kv_heads <= 128 */
+  int32_t kv_heads;       /* >= 1 */
+  int32_t head_dim;       /* 64 or 128 */
+  int32_t page_size;      /* tokens of a page: 16, 32, 64 or 128 */
+  int32_t num_pages;      /* pages of a cache: num_pages * page_size < 2^31 */
+  int32_t max_pages;      /* entries of a block-table row (its stride) */
+  int32_t dtype;          /* MOE_ATTN_BF16 or MOE_ATTN_F16 */
+  float softmax_scale;    /* multiplies q . k (finite, > 0); 1 / sqrt(head_dim) as a rule */
+  uint32_t flags;         /* must be 0 */
+} moe_attn_config;
+
+/* Per-row vectors [rows][heads][head_dim]: element (t, h, d) is at
+ * data + t * row_stride + h * head_stride + d (strides in elements, positive
+ * multiples of 8 up to 2^36; data device, 16-byte aligned).  So q, k and v may
+ * be parts of one fused projection's output, in either order of rows and heads.
+ * The strides of an axis of length one are not looked at. */
+typedef struct {
+  void *data;
+  int64_t row_stride, head_stride;
+} moe_attn_rows;
+
+/* Flag bits of moe_kv_plan's info[3]. */
+#define MOE_KV_FLAG_LENGTH 0x1    /* a negative length (taken as 0), or more fresh rows than num_rows */
+#define MOE_KV_FLAG_TABLE 0x2     /* a context longer than a block-table row: its rows past the row's end have no slot */
+#define MOE_KV_FLAG_PAGES 0x4     /* free pages ran out, or a page id is out of range: rows without a page have no slot */
+#define MOE_KV_FLAG_TREE 0x8      /* a parent that is not an earlier row of its request, or a tree of more than 64 rows */
+
+/* A host-side handle (allocates no device memory). */
+moe_status moe_attn_create(const moe_attn_config *cfg, int device, moe_attn_t *out);
+moe_status moe_attn_destroy(moe_attn_t attn);
+
+/* Workspace of moe_attn_prompt and moe_attn_tree for up to num_requests
+ * requests and num_rows rows; device memory of the caller, ZERO-FILLED once
+ * before its first use.  Concurrent calls need different workspaces. */
+moe_status moe_attn_workspace_bytes(moe_attn_t attn, int num_requests, int num_rows, size_t *bytes);
+
+/* Block tables and slot maps from the requests' lengths.
+ *   cached, fresh  device int32 [num_requests] (0 <= num_requests <= 1024)
+ *   free_pages     device int32 [num_free]: page ids to hand out, in this order
+ *                  (request by request, then page by page of its context)
+ *   parents        device int32 [num_rows] or NULL: the row (0 = the first of
+ *                  its request) that a drafted row hangs from, an earlier one;
+ *                  -1 hangs it from the context
+ *   block_table    device int32 [num_requests][max_pages], read and written:
+ *                  entries below ceil(cached / page_size) are kept, entries up
+ *                  to ceil((cached + fresh) / page_size) get free pages (-1
+ *                  where none is left), the others stay as they are
+ *   cu             device int32 [num_requests + 1], written: offsets of the rows
+ *   slots          device int32 [num_rows], written: the slot of each row's key
+ *                  and value; -1 for rows past cu[num_requests] and rows
+ *                  without a page
+ *   positions      device int32 [num_rows], written: cached + the row's depth
+ *                  (its place among the fresh rows, or with parents its number
+ *                  of ancestors); -1 past cu[num_requests]
+ *   tree_mask      device uint64 [num_rows] or NULL, with parents only,
+ *                  written: bit j of row i's word is set when row j of the
+ *                  request is row i or an ancestor of it; 0 past the end and
+ *                  for rows from the 65th of a request on
+ *   info           device int32 [4], zero-filled once by the caller: written
+ *                  {rows, pages handed out, longest context}; MOE_KV_FLAG_*
+ *                  bits are OR-ed into info[3] and stay until the caller clears
+ * Calls with the same inputs write the same outputs (nothing is consumed: the
+ * caller drops the first info[1] free pages). */
+moe_status moe_kv_plan(moe_attn_t attn, int num_requests, int num_rows, const int32_t *cached, const int32_t *fresh,
+                       const int32_t *free_pages, int num_free, const int32_t *parents, int32_t *block_table,
+                       int32_t *cu, int32_t *slots, int32_t *positions, uint64_t *tree_mask, int32_t *info,
+                       cudaStream_t stream);
+
+/* Write key and value rows into the caches: for every row t with 0 <=
+ * slots[t] < num_pages * page_size (others are skipped), k[t] and v[t]
+ * ([kv_heads][head_dim]) go to slot slots[t].  Slots must be distinct.
+ * After a verify pass the accepted rows are appended again at their final
+ * slots, the others with slot -1.  k_cache, v_cache: device, 16-byte aligned. */
+moe_status moe_kv_append(moe_attn_t attn, int num_rows, const moe_attn_rows *k, const moe_attn_rows *v,
+                         const int32_t *slots, void *k_cache, void *v_cache, cudaStream_t stream);
+
+/* Causal attention over whole prompts: for row i of request b and query head h
+ *   o[i] = sum_{j <= i} w_j v[j],  w = softmax_j(softmax_scale * q[i] . k[j])
+ * over the rows j of the same request, from the packed rows themselves.
+ * cu: device int32 [num_requests + 1], 0 <= cu[b] <= cu[b + 1] <= num_rows; a
+ * request may be empty.  Rows outside cu[0] .. cu[num_requests] are not written.
+ * out: rows of q_heads heads (may not overlap the inputs); lse: device fp32
+ * [num_rows][q_heads] or NULL, the natural logarithm of the sum of
+ * exp(softmax_scale * q . k).  Keys and values of rows j > i and of other requests
+ * have no effect on row i, whatever they hold. */
+moe_status moe_attn_prompt(moe_attn_t attn, int num_requests, int num_rows, const moe_attn_rows *q,
+                           const moe_attn_rows *k, const moe_attn_rows *v, const int32_t *cu,
+                           const moe_attn_rows *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of the fresh rows over the cache: row i of request b sees all
+ * cached[b] tokens and, of the request's fresh rows (their keys and values are
+ * at places cached[b] + j of its context: moe_kv_append), row j
+ *   tree_mask == NULL: when j <= i (a decode step with one row, or the next
+ *                      part of a prompt);
+ *   tree_mask != NULL: when bit j of tree_mask[cu[b] + i] is set (device uint64
+ *                      [num_rows]; rows from the 65th on are seen by none).
+ * A row that sees nothing gets out = 0 and lse = -infinity.  Tokens that a row
+ * does not see, tokens past the context, and tokens whose block-table entry is
+ * not in [0, num_pages) have no effect on it, whatever the cache holds there.
+ * cached[b] + the fresh rows may not pass max_pages * page_size (tokens past it
+ * are not seen).  Results do not depend on timing: the parts of a long context
+ * are joined in a fixed order. */
+moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const moe_attn_rows *q, const int32_t *cu,
+                         const int32_t *cached, const int32_t *block_table, const uint64_t *tree_mask,
+                         const void *k_cache, const void *v_cache, const moe_attn_rows *out, float *lse, void *ws,
+                         size_t ws_bytes, cudaStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *moe_status_string(moe_status status);
 

@@ -1,0 +1,54 @@
+// attn.h -- the handle, argument blocks and launchers of the attention beside
+// the FFN and of its paged cache (host side).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+struct moe_attn {
+  moe_attn_config cfg;
+  int device;
+  int num_sms;
+  int page_shift;             // log2 of the page size
+};
+
+namespace moe {
+
+// Rows as the kernels see them (strides in elements).
+struct RowView {
+  uint16_t *p;
+  long long row, head;
+};
+
+struct KvPlanArgs {
+  const int32_t *cached, *fresh, *free_pages, *parents;
+  int32_t *block_table, *cu, *slots, *positions, *info;
+  uint64_t *tree_mask;
+  int B, T, num_free, max_pages, num_pages, page_shift;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs &a, int num_sms, cudaStream_t stream);
+
+struct KvAppendArgs {
+  RowView k, v;
+  const int32_t *slots;
+  uint16_t *k_cache, *v_cache;
+  int T, kv_heads, head_dim, page_shift, num_slots;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, cudaStream_t stream);
+
+struct AttnArgs {
+  RowView q, k, v, out;       // k, v: the packed rows of a prompt; unused over a cache
+  const int32_t *cu;          // [B + 1]
+  const int32_t *cached;      // [B]; null for a prompt
+  const int32_t *block_table; // [B][max_pages]; null for a prompt
+  const uint64_t *tree_mask;  // [T] or null
+  const uint16_t *k_cache, *v_cache;
+  float *lse;                 // [T][q_heads] or null
+  int B, T, q_heads, kv_heads, group, head_dim, page_shift, max_pages, num_pages, f16;
+  float scale;
+};
+cudaError_t launch_attn_rows(const AttnArgs &a, int num_sms, cudaStream_t stream);
+
+}  // namespace moe

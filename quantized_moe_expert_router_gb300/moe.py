@@ -31,6 +31,11 @@ CONFIG_MXFP4 = 0x1                      # MXFP4 weights (e8m0 scale per 32 eleme
 CONFIG_GROUPED_ABOVE_8 = 0x2            # the grouped tcgen05 path for every call of more than 8 tokens
 CONFIG_W4A4 = 0x4                       # activations quantized to NVFP4 with each matrix's input scale
 ACT_BF16, ACT_F32 = 0, 1                # source types of moe_quantize_nvfp4
+ATTN_BF16, ATTN_F16 = 0, 1              # element types of an Attention
+KV_FLAG_LENGTH = 0x1                    # moe_kv_plan's info[3]: a negative length, or more rows than given
+KV_FLAG_TABLE = 0x2                     # a context longer than a block-table row
+KV_FLAG_PAGES = 0x4                     # free pages ran out, or a page id is out of range
+KV_FLAG_TREE = 0x8                      # a bad parent, or a tree of more than 64 rows
 
 EXPORTED = (
     "moe_layer_create", "moe_layer_destroy", "moe_packed_bytes", "moe_workspace_bytes",
@@ -38,6 +43,8 @@ EXPORTED = (
     "moe_set_stage_events", "moe_route_noalloc", "moe_route_forward",
     "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_packed_bytes", "moe_ffn_workspace_bytes",
     "moe_ffn_pack_weights", "moe_ffn_partial", "moe_ffn_finish", "moe_ffn_forward", "moe_quantize_nvfp4",
+    "moe_attn_create", "moe_attn_destroy", "moe_attn_workspace_bytes", "moe_kv_plan", "moe_kv_append",
+    "moe_attn_prompt", "moe_attn_tree",
     "moe_status_string",
 )
 
@@ -71,6 +78,16 @@ class moe_ffn_config(ctypes.Structure):
 class moe_ffn_weights(ctypes.Structure):
     _fields_ = [("routed_down", moe_fp4_tensor), ("routed_up", moe_fp4_tensor),
                 ("shared", moe_canonical_weights), ("norm_gamma", ctypes.c_void_p)]
+
+
+class moe_attn_config(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class moe_attn_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -107,6 +124,14 @@ def load_library(path: str = LIB_PATH):
             lib.moe_ffn_finish.argtypes = [P, P, I32, P, P, P, P, SZ, P]
             lib.moe_ffn_forward.argtypes = [P, P, I32, P, P, P, P, P, P, P, P, SZ, P]
             lib.moe_quantize_nvfp4.argtypes = [P, I32, ctypes.c_int64, I32, ctypes.c_float, P, P, P]
+            R = ctypes.POINTER(moe_attn_rows)
+            lib.moe_attn_create.argtypes = [ctypes.POINTER(moe_attn_config), I32, ctypes.POINTER(P)]
+            lib.moe_attn_destroy.argtypes = [P]
+            lib.moe_attn_workspace_bytes.argtypes = [P, I32, I32, ctypes.POINTER(SZ)]
+            lib.moe_kv_plan.argtypes = [P, I32, I32, P, P, P, I32, P, P, P, P, P, P, P, P]
+            lib.moe_kv_append.argtypes = [P, I32, R, R, P, P, P, P]
+            lib.moe_attn_prompt.argtypes = [P, I32, I32, R, R, R, P, R, P, P, SZ, P]
+            lib.moe_attn_tree.argtypes = [P, I32, I32, R, P, P, P, P, P, P, R, P, P, SZ, P]
             lib.moe_status_string.argtypes = [I32]
             lib.moe_status_string.restype = ctypes.c_char_p
             for name in EXPORTED[:-1]:
@@ -336,3 +361,136 @@ def alloc_ffn_workspace(ffn: Ffn, num_tokens: int, device=None) -> torch.Tensor:
 
 def alloc_ffn_packed(ffn: Ffn, device=None) -> torch.Tensor:
     return torch.empty(moe_ffn_packed_bytes(ffn), dtype=torch.uint8, device=device or f"cuda:{ffn.routed.device}")
+
+
+# ------------------------------------------------ the attention beside the FFN
+
+class Attention:
+    """Owns one ``moe_attn_t`` handle (host memory only): the geometry of the
+    heads and of the paged cache, [num_pages][kv_heads][page_size][head_dim]
+    each for keys and values.  ``softmax_scale`` is 1 / sqrt(head_dim) unless
+    given."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, page_size, num_pages, max_pages, dtype=torch.bfloat16,
+                 softmax_scale=None, device=0):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"Attention: unsupported dtype {dtype}")
+        lib = load_library()
+        scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
+        self.cfg = moe_attn_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_pages,
+                                   ATTN_F16 if dtype == torch.float16 else ATTN_BF16, scale, 0)
+        self.dtype, self.device = dtype, device
+        h = ctypes.c_void_p()
+        _check("moe_attn_create", lib.moe_attn_create(ctypes.byref(self.cfg), device, ctypes.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and _lib is not None:
+            _lib.moe_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        self.close()
+
+
+def moe_attn_workspace_bytes(attn: Attention, num_requests: int, num_rows: int) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_attn_workspace_bytes", load_library().moe_attn_workspace_bytes(
+        attn.handle, num_requests, num_rows, ctypes.byref(n)))
+    return n.value
+
+
+def alloc_attn_workspace(attn: Attention, num_requests: int, num_rows: int, device=None) -> torch.Tensor:
+    """Zero-filled workspace (uint8) of moe_attn_workspace_bytes."""
+    n = moe_attn_workspace_bytes(attn, num_requests, num_rows)
+    return torch.zeros(n, dtype=torch.uint8, device=device or f"cuda:{attn.device}")
+
+
+def _attn_tensor(fn, name, t, dtype, shape, device):
+    """A contiguous device tensor of a dtype (and shape, where None fits any length)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous() or not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{fn}: {name} is not a contiguous tensor on cuda:{device}")
+    return t.data_ptr() if t.numel() else None
+
+
+def _attn_rows(fn, name, attn, t, rows, heads):
+    """[rows][heads][head_dim] with a contiguous last axis and any strides of the others."""
+    if t.dtype != attn.dtype:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, not {attn.dtype}")
+    if tuple(t.shape) != (rows, heads, attn.cfg.head_dim):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {(rows, heads, attn.cfg.head_dim)}")
+    if t.stride(2) != 1 or not t.is_cuda or t.device.index != attn.device:
+        raise ValueError(f"{fn}: {name} is not on cuda:{attn.device} with a contiguous last axis")
+    return moe_attn_rows(t.data_ptr() if t.numel() else None, t.stride(0), t.stride(1))
+
+
+def _attn_cache(fn, attn, k_cache, v_cache):
+    c = attn.cfg
+    shape = (c.num_pages, c.kv_heads, c.page_size, c.head_dim)
+    return (_attn_tensor(fn, "k_cache", k_cache, attn.dtype, shape, attn.device),
+            _attn_tensor(fn, "v_cache", v_cache, attn.dtype, shape, attn.device))
+
+
+def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
+                stream=None) -> None:
+    """Block table entries, row offsets, slots, positions and (from parents)
+    tree masks of one step; int32 tensors, tree_mask int64."""
+    fn, dev, i32 = "moe_kv_plan", attn.device, torch.int32
+    B, T = cached.shape[0], slots.shape[0]
+    args = [_attn_tensor(fn, "cached", cached, i32, (B,), dev), _attn_tensor(fn, "fresh", fresh, i32, (B,), dev),
+            _attn_tensor(fn, "free_pages", free_pages, i32, (None,), dev), free_pages.shape[0],
+            None if parents is None else _attn_tensor(fn, "parents", parents, i32, (T,), dev),
+            _attn_tensor(fn, "block_table", block_table, i32, (B, attn.cfg.max_pages), dev),
+            _attn_tensor(fn, "cu", cu, i32, (B + 1,), dev), _attn_tensor(fn, "slots", slots, i32, (T,), dev),
+            _attn_tensor(fn, "positions", positions, i32, (T,), dev),
+            None if tree_mask is None else _attn_tensor(fn, "tree_mask", tree_mask, torch.int64, (T,), dev),
+            _attn_tensor(fn, "info", info, i32, (4,), dev)]
+    _check(fn, load_library().moe_kv_plan(attn.handle, B, T, *args, _stream(stream)))
+
+
+def moe_kv_append(attn, k, v, slots, k_cache, v_cache, stream=None) -> None:
+    """Write k and v rows [rows][kv_heads][head_dim] to their slots (negative: skipped)."""
+    fn, T = "moe_kv_append", slots.shape[0]
+    kr, vr = (_attn_rows(fn, n, attn, t, T, attn.cfg.kv_heads) for n, t in (("k", k), ("v", v)))
+    caches = _attn_cache(fn, attn, k_cache, v_cache)
+    _check(fn, load_library().moe_kv_append(
+        attn.handle, T, ctypes.byref(kr), ctypes.byref(vr), _attn_tensor(fn, "slots", slots, torch.int32, (T,), attn.device),
+        *caches, _stream(stream)))
+
+
+def _attn_common(fn, attn, q, cu, out, lse):
+    T, B, dev = q.shape[0], cu.shape[0] - 1, attn.device
+    return (B, T, _attn_rows(fn, "q", attn, q, T, attn.cfg.q_heads), _attn_rows(fn, "out", attn, out, T, attn.cfg.q_heads),
+            _attn_tensor(fn, "cu", cu, torch.int32, (None,), dev),
+            None if lse is None else _attn_tensor(fn, "lse", lse, torch.float32, (T, attn.cfg.q_heads), dev))
+
+
+def moe_attn_prompt(attn, q, k, v, cu, out, ws, lse=None, stream=None) -> None:
+    """Causal attention over packed prompts: q, out [rows][q_heads][head_dim],
+    k, v [rows][kv_heads][head_dim], cu int32 [requests + 1], lse fp32
+    [rows][q_heads]."""
+    fn = "moe_attn_prompt"
+    B, T, qr, outr, cup, lsep = _attn_common(fn, attn, q, cu, out, lse)
+    kr, vr = (_attn_rows(fn, n, attn, t, T, attn.cfg.kv_heads) for n, t in (("k", k), ("v", v)))
+    _check(fn, load_library().moe_attn_prompt(
+        attn.handle, B, T, ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), cup, ctypes.byref(outr), lsep,
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, tree_mask=None, lse=None,
+                  stream=None) -> None:
+    """Attention of the step's rows over the cache: all cached tokens of the
+    row's request, and its fresh rows as the row's word of tree_mask (int64)
+    says, or up to the row itself without one."""
+    fn, dev = "moe_attn_tree", attn.device
+    B, T, qr, outr, cup, lsep = _attn_common(fn, attn, q, cu, out, lse)
+    caches = _attn_cache(fn, attn, k_cache, v_cache)
+    _check(fn, load_library().moe_attn_tree(
+        attn.handle, B, T, ctypes.byref(qr), cup, _attn_tensor(fn, "cached", cached, torch.int32, (B,), dev),
+        _attn_tensor(fn, "block_table", block_table, torch.int32, (B, attn.cfg.max_pages), dev),
+        None if tree_mask is None else _attn_tensor(fn, "tree_mask", tree_mask, torch.int64, (T,), dev),
+        *caches, ctypes.byref(outr), lsep, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
