@@ -398,6 +398,12 @@ moe_status moe_attn_destroy(moe_attn_t attn);
  * before its first use.  Concurrent calls need different workspaces. */
 moe_status moe_attn_workspace_bytes(moe_attn_t attn, int num_requests, int num_rows, size_t *bytes);
 
+/* Synchronise `stream`, return the flag bits that moe_attn_prompt and
+ * moe_attn_tree calls have left in `ws` since the last call (MOE_FLAG_TIMEOUT:
+ * a bounded device wait ran out, the outputs of that call are invalid), and
+ * leave the workspace as new.  No other call may be in flight on `ws`. */
+moe_status moe_attn_get_device_status(moe_attn_t attn, void *ws, cudaStream_t stream, int32_t *flags);
+
 /* Block tables and slot maps from the requests' lengths.
  *   cached, fresh  device int32 [num_requests] (0 <= num_requests <= 1024)
  *   free_pages     device int32 [num_free]: page ids to hand out, in this order

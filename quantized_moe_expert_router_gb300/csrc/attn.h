@@ -51,4 +51,12 @@ struct AttnArgs {
 };
 cudaError_t launch_attn_rows(const AttnArgs &a, int num_sms, cudaStream_t stream);
 
+// First 256 bytes of the workspace: zero between calls, but for the flags.
+constexpr int kAttnCtrlBytes = 256;
+constexpr int kAttnCtrlNext = 0, kAttnCtrlDone = 1, kAttnCtrlFlags = 2;   // ints
+
+// Opt-in shared memory of the prompt kernel (idempotent).
+cudaError_t attn_prompt_setup(int head_dim, int f16);
+cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaStream_t stream);
+
 }  // namespace moe

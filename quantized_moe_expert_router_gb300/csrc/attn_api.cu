@@ -64,7 +64,7 @@ AttnArgs attn_args(const moe_attn &L, int B, int T) {
   return a;
 }
 
-size_t attn_ws_bytes(const moe_attn &L, int B, int T) { return 256; }
+size_t attn_ws_bytes(const moe_attn &L, int B, int T) { return kAttnCtrlBytes; }
 
 }  // namespace
 
@@ -87,6 +87,7 @@ moe_status moe_attn_create(const moe_attn_config *cfg, int device, moe_attn_t *o
   DeviceGuard g(device);
   int sms = 0;
   if (!g.ok || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return MOE_ERR_CUDA;
+  if (attn_prompt_setup(cfg->head_dim, cfg->dtype == MOE_ATTN_F16) != cudaSuccess) return MOE_ERR_CUDA;
   moe_attn *a = new (std::nothrow) moe_attn;
   if (!a) return MOE_ERR_OUT_OF_MEMORY;
   a->cfg = *cfg;
@@ -106,6 +107,19 @@ moe_status moe_attn_workspace_bytes(moe_attn_t attn, int num_requests, int num_r
   if (!attn || !bytes || !counts_ok(num_requests, num_rows)) return MOE_ERR_INVALID_ARG;
   if (num_requests > MOE_ATTN_MAX_REQUESTS || num_rows > MOE_ATTN_MAX_ROWS) return MOE_ERR_UNSUPPORTED_SHAPE;
   *bytes = attn_ws_bytes(*attn, num_requests, num_rows);
+  return MOE_OK;
+}
+
+moe_status moe_attn_get_device_status(moe_attn_t attn, void *ws, cudaStream_t stream, int32_t *flags) {
+  if (!attn || !given(ws) || !flags) return MOE_ERR_INVALID_ARG;
+  DeviceGuard g(attn->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  int32_t got = 0;
+  cudaError_t err = cudaMemcpyAsync(&got, static_cast<int *>(ws) + kAttnCtrlFlags, sizeof(got), cudaMemcpyDeviceToHost, stream);
+  if (err == cudaSuccess) err = cudaMemsetAsync(ws, 0, kAttnCtrlBytes, stream);
+  if (err == cudaSuccess) err = cudaStreamSynchronize(stream);
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  *flags = got;
   return MOE_OK;
 }
 
@@ -167,7 +181,7 @@ moe_status moe_attn_prompt(moe_attn_t attn, int num_requests, int num_rows, cons
   a.lse = lse;
   DeviceGuard g(attn->device);
   if (!g.ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_attn_rows(a, attn->num_sms, stream));
+  return cuda_status(launch_attn_prompt(a, static_cast<int *>(ws), attn->num_sms, stream));
 }
 
 moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const moe_attn_rows *q, const int32_t *cu,

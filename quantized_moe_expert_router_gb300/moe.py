@@ -44,7 +44,7 @@ EXPORTED = (
     "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_packed_bytes", "moe_ffn_workspace_bytes",
     "moe_ffn_pack_weights", "moe_ffn_partial", "moe_ffn_finish", "moe_ffn_forward", "moe_quantize_nvfp4",
     "moe_attn_create", "moe_attn_destroy", "moe_attn_workspace_bytes", "moe_kv_plan", "moe_kv_append",
-    "moe_attn_prompt", "moe_attn_tree",
+    "moe_attn_prompt", "moe_attn_tree", "moe_attn_get_device_status",
     "moe_status_string",
 )
 
@@ -132,6 +132,7 @@ def load_library(path: str = LIB_PATH):
             lib.moe_kv_append.argtypes = [P, I32, R, R, P, P, P, P]
             lib.moe_attn_prompt.argtypes = [P, I32, I32, R, R, R, P, R, P, P, SZ, P]
             lib.moe_attn_tree.argtypes = [P, I32, I32, R, P, P, P, P, P, P, R, P, P, SZ, P]
+            lib.moe_attn_get_device_status.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_int32)]
             lib.moe_status_string.argtypes = [I32]
             lib.moe_status_string.restype = ctypes.c_char_p
             for name in EXPORTED[:-1]:
@@ -404,6 +405,13 @@ def alloc_attn_workspace(attn: Attention, num_requests: int, num_rows: int, devi
     """Zero-filled workspace (uint8) of moe_attn_workspace_bytes."""
     n = moe_attn_workspace_bytes(attn, num_requests, num_rows)
     return torch.zeros(n, dtype=torch.uint8, device=device or f"cuda:{attn.device}")
+
+
+def moe_attn_get_device_status(attn: Attention, ws: torch.Tensor, stream=None) -> int:
+    f = ctypes.c_int32()
+    _check("moe_attn_get_device_status", load_library().moe_attn_get_device_status(
+        attn.handle, _ptr(ws), _stream(stream), ctypes.byref(f)))
+    return f.value
 
 
 def _attn_tensor(fn, name, t, dtype, shape, device):

@@ -4,7 +4,7 @@ it matters, and the error that their kernels may have.
 Bound of an output element.  Let w be the row's softmax weights and
 A = sum_j w_j |v_j|.  The kernels form scores from exact products of 2-byte
 elements summed in fp32, round each weight to the element type before it
-multiplies v (unit roundoff u: 2^-9 bf16, 2^-12 f16), sum in fp32 and round
+multiplies v (unit roundoff u: half of the type's epsilon), sum in fp32 and round
 the result (u again).  A score is off by at most (D + 4) 2^-24 S, with S the
 largest sum over the head of |scale q k| of the row's visible tokens (the
 scale and the base-2 exponent's argument are among the 4), and a weight, a
@@ -20,7 +20,7 @@ import math
 import numpy as np
 import torch
 
-U = {torch.bfloat16: 2.0 ** -9, torch.float16: 2.0 ** -12}
+U = {t: torch.finfo(t).eps / 2 for t in (torch.bfloat16, torch.float16)}      # 8 and 11 significant bits
 LOST = {torch.bfloat16: 2.0 ** -60, torch.float16: 2.0 ** -25}
 
 

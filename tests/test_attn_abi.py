@@ -68,3 +68,11 @@ def test_reference_visibility_of_words():
     assert vis.tolist() == [[True, False, False], [True, True, False], [True, True, True]]
     wide = ref.words_to_visible(torch.full((70,), -1, dtype=torch.int64), 70)
     assert wide[:, :64].all() and not wide[:, 64:].any()
+
+
+def test_reference_roundoff_is_that_of_the_types():
+    """The largest relative error of rounding 1 + x, x in [0, 1], is u / (1 + u)."""
+    x = 1 + torch.arange(2 ** 16, dtype=torch.float64) / 2 ** 16
+    for dt, u in ref.U.items():
+        err = ((x.to(dt).double() - x) / x).abs().max()
+        assert abs(float(err) - u / (1 + u)) < 1e-4 * u
