@@ -49,8 +49,6 @@ struct AttnArgs {
   int B, T, q_heads, kv_heads, group, head_dim, page_shift, max_pages, num_pages, f16;
   float scale;
 };
-cudaError_t launch_attn_rows(const AttnArgs &a, int num_sms, cudaStream_t stream);
-
 // First 256 bytes of the workspace: zero between calls, but for the flags.
 constexpr int kAttnCtrlBytes = 256;
 constexpr int kAttnCtrlNext = 0, kAttnCtrlDone = 1, kAttnCtrlFlags = 2;   // ints
@@ -58,5 +56,13 @@ constexpr int kAttnCtrlNext = 0, kAttnCtrlDone = 1, kAttnCtrlFlags = 2;   // int
 // Opt-in shared memory of the prompt kernel (idempotent).
 cudaError_t attn_prompt_setup(int head_dim, int f16);
 cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaStream_t stream);
+
+// Byte offsets of moe_attn_tree's workspace (after the control words).
+struct AttnTreeWs {
+  size_t tickets, stat, part, total;
+};
+AttnTreeWs attn_tree_ws(int group, int kv_heads, int head_dim, int B, int T, int num_sms);
+cudaError_t attn_tree_setup(int head_dim, int f16);
+cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -64,7 +64,9 @@ AttnArgs attn_args(const moe_attn &L, int B, int T) {
   return a;
 }
 
-size_t attn_ws_bytes(const moe_attn &L, int B, int T) { return kAttnCtrlBytes; }
+size_t attn_ws_bytes(const moe_attn &L, int B, int T) {
+  return attn_tree_ws(L.cfg.q_heads / L.cfg.kv_heads, L.cfg.kv_heads, L.cfg.head_dim, B, T, L.num_sms).total;
+}
 
 }  // namespace
 
@@ -87,7 +89,9 @@ moe_status moe_attn_create(const moe_attn_config *cfg, int device, moe_attn_t *o
   DeviceGuard g(device);
   int sms = 0;
   if (!g.ok || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return MOE_ERR_CUDA;
-  if (attn_prompt_setup(cfg->head_dim, cfg->dtype == MOE_ATTN_F16) != cudaSuccess) return MOE_ERR_CUDA;
+  const int f16 = cfg->dtype == MOE_ATTN_F16;
+  if (attn_prompt_setup(cfg->head_dim, f16) != cudaSuccess || attn_tree_setup(cfg->head_dim, f16) != cudaSuccess)
+    return MOE_ERR_CUDA;
   moe_attn *a = new (std::nothrow) moe_attn;
   if (!a) return MOE_ERR_OUT_OF_MEMORY;
   a->cfg = *cfg;
@@ -206,7 +210,7 @@ moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const 
   a.lse = lse;
   DeviceGuard g(attn->device);
   if (!g.ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_attn_rows(a, attn->num_sms, stream));
+  return cuda_status(launch_attn_tree(a, static_cast<uint8_t *>(ws), attn->num_sms, stream));
 }
 
 }  // extern "C"
