@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -86,10 +87,6 @@ class moe_attn_config(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
 
-class moe_attn_rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
 _lock = threading.Lock()
 _lib = None
 
@@ -124,7 +121,7 @@ def load_library(path: str = LIB_PATH):
             lib.moe_ffn_finish.argtypes = [P, P, I32, P, P, P, P, SZ, P]
             lib.moe_ffn_forward.argtypes = [P, P, I32, P, P, P, P, P, P, P, P, SZ, P]
             lib.moe_quantize_nvfp4.argtypes = [P, I32, ctypes.c_int64, I32, ctypes.c_float, P, P, P]
-            R = ctypes.POINTER(moe_attn_rows)
+            R = P                                    # a moe_attn_rows, as bytes
             lib.moe_attn_create.argtypes = [ctypes.POINTER(moe_attn_config), I32, ctypes.POINTER(P)]
             lib.moe_attn_destroy.argtypes = [P]
             lib.moe_attn_workspace_bytes.argtypes = [P, I32, I32, ctypes.POINTER(SZ)]
@@ -381,6 +378,8 @@ class Attention:
         self.cfg = moe_attn_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_pages,
                                    ATTN_F16 if dtype == torch.float16 else ATTN_BF16, scale, 0)
         self.dtype, self.device = dtype, device
+        self.q_heads, self.kv_heads, self.head_dim, self.max_pages = q_heads, kv_heads, head_dim, max_pages
+        self.cache_shape = (num_pages, kv_heads, page_size, head_dim)
         h = ctypes.c_void_p()
         _check("moe_attn_create", lib.moe_attn_create(ctypes.byref(self.cfg), device, ctypes.byref(h)))
         self.handle = h
@@ -414,79 +413,82 @@ def moe_attn_get_device_status(attn: Attention, ws: torch.Tensor, stream=None) -
     return f.value
 
 
-def _attn_tensor(fn, name, t, dtype, shape, device):
-    """A contiguous device tensor of a dtype (and shape, where None fits any length)."""
-    if t.dtype != dtype:
+# The calls below run once or more per step and layer, so their checks are kept
+# to a few attribute reads per tensor; what went wrong is found out only then.
+
+_pack_rows = struct.Struct("@Pqq").pack         # a moe_attn_rows
+
+
+def _attn_words(fn, name, t, dtype, shape, device):
+    """Address of a contiguous tensor of this dtype and shape on cuda:device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{fn}: {name} is {t.dtype}, not {dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {shape}")
-    if not t.is_contiguous() or not t.is_cuda or t.device.index != device:
-        raise ValueError(f"{fn}: {name} is not a contiguous tensor on cuda:{device}")
-    return t.data_ptr() if t.numel() else None
+    raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)} on {t.device} is not a contiguous {shape} on cuda:{device}")
 
 
-def _attn_rows(fn, name, attn, t, rows, heads):
-    """[rows][heads][head_dim] with a contiguous last axis and any strides of the others."""
-    if t.dtype != attn.dtype:
+def _attn_rows(fn, name, attn, t, shape):
+    """The moe_attn_rows of [rows][heads][head_dim] with a contiguous last axis and any strides of the others."""
+    s = t.stride()
+    if t.dtype is attn.dtype and t.shape == shape and s[2] == 1 and t.get_device() == attn.device:
+        return _pack_rows(t.data_ptr(), s[0], s[1])
+    if t.dtype is not attn.dtype:
         raise TypeError(f"{fn}: {name} is {t.dtype}, not {attn.dtype}")
-    if tuple(t.shape) != (rows, heads, attn.cfg.head_dim):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {(rows, heads, attn.cfg.head_dim)}")
-    if t.stride(2) != 1 or not t.is_cuda or t.device.index != attn.device:
-        raise ValueError(f"{fn}: {name} is not on cuda:{attn.device} with a contiguous last axis")
-    return moe_attn_rows(t.data_ptr() if t.numel() else None, t.stride(0), t.stride(1))
+    raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)}, strides {s}, on {t.device} is not {shape} with a contiguous "
+                     f"last axis on cuda:{attn.device}")
 
 
-def _attn_cache(fn, attn, k_cache, v_cache):
-    c = attn.cfg
-    shape = (c.num_pages, c.kv_heads, c.page_size, c.head_dim)
-    return (_attn_tensor(fn, "k_cache", k_cache, attn.dtype, shape, attn.device),
-            _attn_tensor(fn, "v_cache", v_cache, attn.dtype, shape, attn.device))
+def _raw_stream(attn, stream):
+    return torch._C._cuda_getCurrentRawStream(attn.device) if stream is None else stream.cuda_stream
 
 
 def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
                 stream=None) -> None:
     """Block table entries, row offsets, slots, positions and (from parents)
     tree masks of one step; int32 tensors, tree_mask int64."""
-    fn, dev, i32 = "moe_kv_plan", attn.device, torch.int32
-    B, T = cached.shape[0], slots.shape[0]
-    args = [_attn_tensor(fn, "cached", cached, i32, (B,), dev), _attn_tensor(fn, "fresh", fresh, i32, (B,), dev),
-            _attn_tensor(fn, "free_pages", free_pages, i32, (None,), dev), free_pages.shape[0],
-            None if parents is None else _attn_tensor(fn, "parents", parents, i32, (T,), dev),
-            _attn_tensor(fn, "block_table", block_table, i32, (B, attn.cfg.max_pages), dev),
-            _attn_tensor(fn, "cu", cu, i32, (B + 1,), dev), _attn_tensor(fn, "slots", slots, i32, (T,), dev),
-            _attn_tensor(fn, "positions", positions, i32, (T,), dev),
-            None if tree_mask is None else _attn_tensor(fn, "tree_mask", tree_mask, torch.int64, (T,), dev),
-            _attn_tensor(fn, "info", info, i32, (4,), dev)]
-    _check(fn, load_library().moe_kv_plan(attn.handle, B, T, *args, _stream(stream)))
+    fn, dev, i32, w = "moe_kv_plan", attn.device, torch.int32, _attn_words
+    B, T, F = cached.shape[0], slots.shape[0], free_pages.shape[0]
+    rows, reqs = (T,), (B,)
+    status = _lib.moe_kv_plan(
+        attn.handle, B, T, w(fn, "cached", cached, i32, reqs, dev), w(fn, "fresh", fresh, i32, reqs, dev),
+        w(fn, "free_pages", free_pages, i32, (F,), dev), F,
+        None if parents is None else w(fn, "parents", parents, i32, rows, dev),
+        w(fn, "block_table", block_table, i32, (B, attn.max_pages), dev), w(fn, "cu", cu, i32, (B + 1,), dev),
+        w(fn, "slots", slots, i32, rows, dev), w(fn, "positions", positions, i32, rows, dev),
+        None if tree_mask is None else w(fn, "tree_mask", tree_mask, torch.int64, rows, dev),
+        w(fn, "info", info, i32, (4,), dev), _raw_stream(attn, stream))
+    if status:
+        _check(fn, status)
 
 
 def moe_kv_append(attn, k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Write k and v rows [rows][kv_heads][head_dim] to their slots (negative: skipped)."""
-    fn, T = "moe_kv_append", slots.shape[0]
-    kr, vr = (_attn_rows(fn, n, attn, t, T, attn.cfg.kv_heads) for n, t in (("k", k), ("v", v)))
-    caches = _attn_cache(fn, attn, k_cache, v_cache)
-    _check(fn, load_library().moe_kv_append(
-        attn.handle, T, ctypes.byref(kr), ctypes.byref(vr), _attn_tensor(fn, "slots", slots, torch.int32, (T,), attn.device),
-        *caches, _stream(stream)))
-
-
-def _attn_common(fn, attn, q, cu, out, lse):
-    T, B, dev = q.shape[0], cu.shape[0] - 1, attn.device
-    return (B, T, _attn_rows(fn, "q", attn, q, T, attn.cfg.q_heads), _attn_rows(fn, "out", attn, out, T, attn.cfg.q_heads),
-            _attn_tensor(fn, "cu", cu, torch.int32, (None,), dev),
-            None if lse is None else _attn_tensor(fn, "lse", lse, torch.float32, (T, attn.cfg.q_heads), dev))
+    fn, dev, T = "moe_kv_append", attn.device, slots.shape[0]
+    shape = (T, attn.kv_heads, attn.head_dim)
+    status = _lib.moe_kv_append(
+        attn.handle, T, _attn_rows(fn, "k", attn, k, shape), _attn_rows(fn, "v", attn, v, shape),
+        _attn_words(fn, "slots", slots, torch.int32, (T,), dev),
+        _attn_words(fn, "k_cache", k_cache, attn.dtype, attn.cache_shape, dev),
+        _attn_words(fn, "v_cache", v_cache, attn.dtype, attn.cache_shape, dev), _raw_stream(attn, stream))
+    if status:
+        _check(fn, status)
 
 
 def moe_attn_prompt(attn, q, k, v, cu, out, ws, lse=None, stream=None) -> None:
     """Causal attention over packed prompts: q, out [rows][q_heads][head_dim],
     k, v [rows][kv_heads][head_dim], cu int32 [requests + 1], lse fp32
     [rows][q_heads]."""
-    fn = "moe_attn_prompt"
-    B, T, qr, outr, cup, lsep = _attn_common(fn, attn, q, cu, out, lse)
-    kr, vr = (_attn_rows(fn, n, attn, t, T, attn.cfg.kv_heads) for n, t in (("k", k), ("v", v)))
-    _check(fn, load_library().moe_attn_prompt(
-        attn.handle, B, T, ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), cup, ctypes.byref(outr), lsep,
-        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    fn, dev, T, n = "moe_attn_prompt", attn.device, q.shape[0], cu.shape[0]
+    qs, ks = (T, attn.q_heads, attn.head_dim), (T, attn.kv_heads, attn.head_dim)
+    status = _lib.moe_attn_prompt(
+        attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), _attn_rows(fn, "k", attn, k, ks),
+        _attn_rows(fn, "v", attn, v, ks), _attn_words(fn, "cu", cu, torch.int32, (n,), dev),
+        _attn_rows(fn, "out", attn, out, qs),
+        None if lse is None else _attn_words(fn, "lse", lse, torch.float32, (T, attn.q_heads), dev),
+        ws.data_ptr(), ws.nbytes, _raw_stream(attn, stream))
+    if status:
+        _check(fn, status)
 
 
 def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, tree_mask=None, lse=None,
@@ -494,11 +496,15 @@ def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, t
     """Attention of the step's rows over the cache: all cached tokens of the
     row's request, and its fresh rows as the row's word of tree_mask (int64)
     says, or up to the row itself without one."""
-    fn, dev = "moe_attn_tree", attn.device
-    B, T, qr, outr, cup, lsep = _attn_common(fn, attn, q, cu, out, lse)
-    caches = _attn_cache(fn, attn, k_cache, v_cache)
-    _check(fn, load_library().moe_attn_tree(
-        attn.handle, B, T, ctypes.byref(qr), cup, _attn_tensor(fn, "cached", cached, torch.int32, (B,), dev),
-        _attn_tensor(fn, "block_table", block_table, torch.int32, (B, attn.cfg.max_pages), dev),
-        None if tree_mask is None else _attn_tensor(fn, "tree_mask", tree_mask, torch.int64, (T,), dev),
-        *caches, ctypes.byref(outr), lsep, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    fn, dev, i32, w, T, n = "moe_attn_tree", attn.device, torch.int32, _attn_words, q.shape[0], cu.shape[0]
+    qs = (T, attn.q_heads, attn.head_dim)
+    status = _lib.moe_attn_tree(
+        attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), w(fn, "cu", cu, i32, (n,), dev),
+        w(fn, "cached", cached, i32, (n - 1,), dev), w(fn, "block_table", block_table, i32, (n - 1, attn.max_pages), dev),
+        None if tree_mask is None else w(fn, "tree_mask", tree_mask, torch.int64, (T,), dev),
+        w(fn, "k_cache", k_cache, attn.dtype, attn.cache_shape, dev),
+        w(fn, "v_cache", v_cache, attn.dtype, attn.cache_shape, dev), _attn_rows(fn, "out", attn, out, qs),
+        None if lse is None else w(fn, "lse", lse, torch.float32, (T, attn.q_heads), dev),
+        ws.data_ptr(), ws.nbytes, _raw_stream(attn, stream))
+    if status:
+        _check(fn, status)
