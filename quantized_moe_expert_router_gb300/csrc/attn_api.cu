@@ -90,7 +90,7 @@ moe_status moe_attn_create(const moe_attn_config *cfg, int device, moe_attn_t *o
   int sms = 0;
   if (!g.ok || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return MOE_ERR_CUDA;
   const int f16 = cfg->dtype == MOE_ATTN_F16;
-  if (attn_prompt_setup(cfg->head_dim, f16) != cudaSuccess || attn_tree_setup(cfg->head_dim, f16) != cudaSuccess)
+  if (attn_wide_setup(cfg->head_dim, f16) != cudaSuccess || attn_tree_setup(cfg->head_dim, f16) != cudaSuccess)
     return MOE_ERR_CUDA;
   moe_attn *a = new (std::nothrow) moe_attn;
   if (!a) return MOE_ERR_OUT_OF_MEMORY;

@@ -90,6 +90,13 @@ __device__ __forceinline__ void at_tma_3d(uint32_t dst, const CUtensorMap *map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void at_tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void at_cp16(uint32_t dst, const void *src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
@@ -141,6 +148,22 @@ inline AttnMapEncodeFn attn_map_encoder() {
     return reinterpret_cast<AttnMapEncodeFn>(p);
   }();
   return fn;
+}
+
+// A cache [pages][kv_heads][page][D] in boxes of 64 elements x `tokens` tokens
+// under the 128-byte swizzle.
+inline cudaError_t attn_encode_cache(CUtensorMap *map, const void *base, const AttnArgs &a, int tokens) {
+  const AttnMapEncodeFn enc = attn_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t page = 1ull << a.page_shift, row = 2ull * a.head_dim;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, page, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_pages};
+  const cuuint64_t strides[3] = {row, row * page, row * page * a.kv_heads};
+  const cuuint32_t box[4] = {64, (cuuint32_t)tokens, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult e = enc(map, a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                         const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace moe

@@ -37,6 +37,7 @@ constexpr int kAtStageBytes = 8192;
 constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least: one per warp costs no more time than one
 constexpr int kAtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kAtSlack = 8.f;
+constexpr int kAtMostRows = 32;                  // mean rows of a request and kv head; more go to attn_wide.cu
 
 struct AtArgs {
   CUtensorMap kmap, vmap;      // (64, 16, 1, 1) boxes over [pages][kv_heads][page_size][D]
@@ -92,14 +93,6 @@ __device__ __forceinline__ void at_ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void at_tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // A place in the line of chunks.
 struct AtPos {
   int b, item, chunk;          // request, item of the request (kv head * row tiles + row tile), chunk
@@ -582,20 +575,6 @@ AtKernel at_kernel(int head_dim, int f16, int mt) {
   return f16 ? at_kernel2<128, true>(mt) : at_kernel2<128, false>(mt);
 }
 int at_smem(int head_dim) { return head_dim == 64 ? AtGeom<64>::kSmem : AtGeom<128>::kSmem; }
-
-cudaError_t encode_cache(CUtensorMap *map, const void *base, const AttnArgs &a) {
-  const AttnMapEncodeFn enc = attn_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t page = 1ull << a.page_shift, row = 2ull * a.head_dim;
-  const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, page, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_pages};
-  const cuuint64_t strides[3] = {row, row * page, row * page * a.kv_heads};
-  const cuuint32_t box[4] = {64, 16, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult e = enc(map, a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                         const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
 }  // namespace
 
 cudaError_t attn_tree_setup(int head_dim, int f16) {
@@ -619,22 +598,25 @@ AttnTreeWs attn_tree_ws(int group, int kv_heads, int head_dim, int B, int T, int
   w.tickets = take(4 * (size_t)kv_heads * ((((size_t)T * group + 15) / 16) + B));
   w.stat = take(8 * (size_t)(2 * num_sms) * 32);
   w.part = take(4 * (size_t)(2 * num_sms) * 32 * head_dim);
-  w.total = off;
+  w.wide = attn_wide_ws(off, group, kv_heads, head_dim, B, T, num_sms);
+  w.total = w.wide.total;
   return w;
 }
 
 cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream) {
+  const AttnTreeWs w = attn_tree_ws(a.group, a.kv_heads, a.head_dim, a.B, a.T, num_sms);
+  const long long rows = ((long long)a.T * a.group + a.B - 1) / a.B;   // of a request and kv head, on the average
+  if (rows > kAtMostRows) return launch_attn_wide_tree(a, ws, w.wide, num_sms, stream);
   AtArgs p;
   p.a = a;
-  cudaError_t err = encode_cache(&p.kmap, a.k_cache, a);
-  if (err == cudaSuccess) err = encode_cache(&p.vmap, a.v_cache, a);
+  cudaError_t err = attn_encode_cache(&p.kmap, a.k_cache, a, 16);
+  if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 16);
   if (err != cudaSuccess) return err;
-  const AttnTreeWs w = attn_tree_ws(a.group, a.kv_heads, a.head_dim, a.B, a.T, num_sms);
   p.ctrl = reinterpret_cast<int *>(ws);
   p.tickets = reinterpret_cast<int *>(ws + w.tickets);
   p.stat = reinterpret_cast<float2 *>(ws + w.stat);
   p.part = reinterpret_cast<float *>(ws + w.part);
-  const int mt = (long long)a.T * a.group <= 16LL * a.B ? 1 : 2;   // rows of a request on the average
+  const int mt = rows <= 16 ? 1 : 2;
   at_kernel(a.head_dim, a.f16, mt)<<<num_sms, kAtThreads, at_smem(a.head_dim), stream>>>(p);
   return cudaGetLastError();
 }

@@ -1,0 +1,933 @@
+// attn_wide.cu -- attention on the 5th-generation tensor cores: causal over
+// whole packed prompts (moe_attn_prompt), and over the paged cache when a
+// request brings many query rows (moe_attn_tree; attn_tree.cu has the other
+// calls).
+//
+// The G query heads of a kv head are rows of one matrix: row r = token * G + g
+// of a request, so a key tile serves all of them and short prompts fill the
+// 128-row tensor-core tiles.  An item is (request, kv head, 256 rows): two row
+// tiles of 128 that share every key/value tile of 128 tokens.  With c =
+// softmax_scale * log2(e), per row tile and key tile j:
+//   S = Q K_j^T                                   (tcgen05, both from shared memory)
+//   m' = max(m, max S);  P = 2^(c (S - m'));  l = l 2^(c (m - m')) + sum P
+//   O = O 2^(c (m - m')) + P V_j                  (tcgen05, P from tensor memory)
+// and at the end o = O / l, lse = softmax_scale * m + ln l.  The running maximum
+// that P is taken against moves only when the true one passes it by 2^8 (in P's
+// terms): P then stays below 2^8, which bf16 and f16 hold, l is summed in fp32
+// from the unrounded values, and O (in tensor memory) is hardly ever rescaled.
+// P is rounded to the element type because the tensor cores multiply equal
+// types; O and l stay fp32.
+//
+// One CTA per SM, 12 warps:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row, so the
+//                   maximum and the sum need no exchange between threads;
+//                   also the rare rescaling of O and the epilogue
+//   warp 8          key/value tiles by tensor-map copies (128-byte swizzle)
+//                   into a ring, in the order K0 K1 V0 K2 V1 ..; takes the items
+//   warp 9          MMA issue: S of the next tile is issued with PV of this one,
+//                   so one row tile's softmax runs while the other's MMAs do
+//   warps 10-11     Q rows into swizzled shared memory (cp.async, zero for rows
+//                   past the end); the scan described below
+// Tensor memory: S0, S1 (128 columns each, P over their first 64), O0, O1.
+//
+// A tile past the last token that all rows see holds keys that some rows, or
+// all, may not see.  Their scores are replaced by -infinity, so P is 0; but 0
+// times an infinite or NaN v is NaN, so warps 10-11 scan those tiles' v, zero
+// such elements and note their tokens, and the epilogue adds them to the
+// rows that do see the token.
+//
+// Prompts: items are taken from a counter, those with most key tiles first; an
+// item's length depends on its row tile alone, so with the requests ranked by
+// length the idx-th longest item has a closed form (prompt_item).
+// Cache: the key tiles of all items stand in one line and every CTA takes an
+// equal range of it.  A part of an item goes to the workspace (fp32 O, m, l) and
+// attn_join_kernel joins the parts in the order of the context.  In a part of
+// at most 128 rows the two row tiles are the same rows over alternate key
+// tiles, so that the softmax of one still runs beside the MMAs of the other.
+//
+// Bound: with G = 8, D = 128 and long prompts the tensor pipe (2 x 512 cycles
+// a row tile and key tile); with D = 64 the exponentials.
+#include <math.h>
+#include <string.h>
+
+#include "attn_tc.cuh"
+
+namespace moe {
+
+constexpr int kApThreads = 384;
+constexpr int kApRows = 256, kApTile = 128;      // rows of an item; rows of a row tile, tokens of a key tile
+constexpr int kApRegsSoft = 208, kApRegsRest = 88;
+constexpr int kApWTma = 8, kApWMma = 9, kApWHelp = 10;
+constexpr int kApMaxB = MOE_ATTN_MAX_REQUESTS;
+constexpr float kApSlack = 8.f;                  // log2 of the largest P
+constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache)
+
+template <int D>
+struct ApGeom {
+  static constexpr int kTileBytes = kApTile * D * 2;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024;
+};
+
+struct ApArgs {
+  CUtensorMap kmap, vmap;      // prompt: (64, 1, 128) boxes over [rows][kv_heads][D]; cache: (64, page, 1, 1) over
+                               // [pages][kv_heads][page][D]; 128-byte swizzle
+  AttnArgs a;
+  int *ctrl;                   // workspace control words
+  int magic;                   // ceil(2^16 / group)
+  // cache only
+  int4 *desc;                  // per item: (first, hk, row0, rows), (first CTA, last CTA, its slot, twin)
+  float4 *part;                // [2 * grid][D / 4][256]  O of a part
+  float2 *stat;                // [2 * grid][256]         (m, l)
+};
+
+struct ApItem {
+  int b, hk, row0;             // request (-1: no more items), kv head, first row (of the request's rows)
+  int first;                   // the request's first packed row
+  int tok0, g0;                // fresh token and group place of row0
+  int rows;                    // rows of the item (<= 256)
+  int j0, n;                   // first key tile and number of key tiles
+  int n0, n1;                  // key tiles of the two row tiles
+  int cached;                  // context before the fresh tokens
+  int all, end;                // tokens that every row sees; tokens from `end` on are seen by none
+  int m0;                      // tiles j0 + m0 .. are masked
+  int twin;                    // the second row tile is the first one, over the odd tiles
+  int slot;                    // where the part goes; -1: the item is whole
+};
+
+struct ApSmem {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_clean[3], v_next, sched_full[2], sched_empty[2], drain;
+  uint32_t tmem;
+  int wsum[2][kApThreads / 32];
+  ApItem item[2];
+  uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
+  union {
+    struct {                   // prompts: requests by falling length
+      uint16_t order[kApMaxB];
+      int tiles[kApMaxB];      // 256-row items per kv head of the k-th longest
+      int before[kApMaxB + 1]; // items (per kv head) of row tiles in which fewer than k + 1 requests take part
+    };
+    struct {                   // cache: the line of key tiles
+      long long work[kApMaxB + 1];   // tiles of the requests before
+      int items[kApMaxB];      // items of the requests before
+      int nch[kApMaxB];        // key tiles of an item's context
+    };
+  };
+  long long wsum2[kApThreads / 32];
+};
+
+// The rows of an item, given its row0.
+__device__ __forceinline__ void ap_rows(const ApArgs &p, ApItem &it, int n_fresh) {
+  const AttnArgs &a = p.a;
+  it.rows = (int)min((long long)kApRows, (long long)n_fresh * a.group - it.row0);
+  it.tok0 = it.row0 / a.group;
+  it.g0 = it.row0 - it.tok0 * a.group;
+}
+
+// The idx-th item by falling row tile: row tiles [tiles[k], tiles[k - 1]) have
+// the k longest requests.
+__device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, int idx, ApItem &it) {
+  const AttnArgs &a = p.a;
+  const int e = idx / a.kv_heads;
+  it.hk = idx - e * a.kv_heads;
+  int lo = 0, hi = a.B - 1;                        // largest k with before[k] <= e
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.before[mid] <= e) lo = mid; else hi = mid - 1;
+  }
+  const int k = lo + 1, off = e - s.before[lo];
+  it.row0 = (s.tiles[lo] - 1 - off / k) * kApRows;
+  it.b = s.order[off % k];
+  it.first = __ldg(a.cu + it.b);
+  ap_rows(p, it, min(__ldg(a.cu + it.b + 1), a.T) - it.first);
+  it.n0 = (it.tok0 + (((it.g0 + min(it.rows, kApTile) - 1) * p.magic) >> 16)) / kApTile + 1;
+  it.n1 = it.rows > kApTile ? (it.tok0 + (((it.g0 + it.rows - 1) * p.magic) >> 16)) / kApTile + 1 : 0;
+  it.n = max(it.n0, it.n1);
+  it.j0 = it.cached = it.twin = 0;
+  it.all = it.tok0 + 1;
+  it.end = it.tok0 + kApRows;                      // the causal limit alone cuts
+  it.m0 = it.all / kApTile;
+  it.slot = -1;
+}
+
+// The part of an item that starts at place x of the line of key tiles (x < x1,
+// the end of the CTA's range); returns the place after it.  n = 0: the rows
+// need nothing of it (later tokens than theirs).
+__device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p, long long x, long long x0, long long x1,
+                                                long long total, long long ctas, ApItem &it) {
+  const AttnArgs &a = p.a;
+  int lo = 0, hi = a.B - 1;                        // largest b with work[b] <= x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.work[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  it.b = lo;
+  const int nch = s.nch[lo];
+  const int item = (int)((x - s.work[lo]) / nch);
+  const long long item0 = s.work[lo] + (long long)item * nch, xe = min(x1, item0 + nch);
+  it.first = __ldg(a.cu + lo);
+  const int n = min(__ldg(a.cu + lo + 1), a.T) - it.first;
+  const int tiles = (int)(((long long)n * a.group + kApRows - 1) / kApRows);
+  it.hk = item / tiles;
+  it.row0 = (item - it.hk * tiles) * kApRows;
+  ap_rows(p, it, n);
+  it.cached = max(__ldg(a.cached + lo), 0);
+  const long long lim = min((long long)a.max_pages << a.page_shift, (long long)it.cached + n);
+  const int last = it.tok0 + (((it.g0 + it.rows - 1) * p.magic) >> 16);      // fresh token of the last row
+  it.all = a.tree_mask ? it.cached : it.cached + it.tok0 + 1;
+  it.end = (int)min(lim, (long long)it.cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : last + 1));
+  const int need = (it.end + kApTile - 1) / kApTile;                          // key tiles of this row tile
+  it.j0 = (int)(x - item0);
+  it.n = max(0, min((int)(xe - item0), need) - it.j0);
+  const bool whole = it.j0 == 0 && it.n == need;
+  it.twin = !whole && it.rows <= kApTile;
+  it.slot = whole ? -1 : 2 * blockIdx.x + (x > x0);
+  it.n0 = it.twin ? (it.n + 1) >> 1 : it.n;
+  it.n1 = it.twin ? it.n >> 1 : (it.rows > kApTile ? it.n : 0);
+  it.m0 = max(0, it.all / kApTile - it.j0);
+  if (it.j0 == 0) {
+    // for the join: the CTAs that hold the parts, and the slot of the first one's
+    const int c0 = blockIdx.x, c1 = (int)(((item0 + need) * ctas - 1) / total);
+    if ((threadIdx.x & 31) == 0) {
+      int4 *d = p.desc + 2 * (s.items[lo] + item);
+      d[0] = make_int4(it.first, it.hk, it.row0, it.rows);
+      d[1] = make_int4(c0, whole ? -1 : c1, it.slot, it.twin);
+    }
+  }
+  return xe;
+}
+
+// Bits of the tokens base .. base + 31 (word w of the tile) that a row sees.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+__device__ __forceinline__ uint32_t cache_visible(const AttnArgs &a, const ApItem &it, uint64_t word, int lim, int base,
+                                                  uint32_t held, int w) {
+  uint32_t bits;
+  if (a.tree_mask) {
+    const int f0 = base - it.cached;               // fresh row of the first bit
+    const uint32_t fresh = f0 >= 64 || f0 <= -32 ? 0u : (f0 >= 0 ? (uint32_t)(word >> f0) : (uint32_t)(word << -f0));
+    bits = low_bits(-f0) | fresh;
+  } else {
+    bits = low_bits(it.cached + lim + 1 - base);
+  }
+  bits &= low_bits(it.end - base);
+  const uint32_t pages = a.page_shift == 4 ? ((held >> (2 * w)) & 1u ? 0xFFFFu : 0u) | ((held >> (2 * w)) & 2u ? 0xFFFF0000u : 0u)
+                                           : ((held >> ((32 * w) >> a.page_shift)) & 1u ? ~0u : 0u);
+  return bits & pages;
+}
+
+// Positions in the ring's order K0 K1 V0 K2 V1 .. V[n-1] of an item of n tiles.
+__device__ __forceinline__ int ap_pos_k(int j) { return j ? 2 * j - 1 : 0; }
+__device__ __forceinline__ int ap_pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
+
+template <int D, bool F16, bool PAGED>
+__global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_constant__ ApArgs p) {
+  extern __shared__ uint8_t dsm[];
+  __shared__ ApSmem s;
+  using G = ApGeom<D>;
+  constexpr int kSlots = G::kSlots, kTB = G::kTileBytes, kHalves = D / 64;
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
+  const uint32_t q_smem = smem0, ring = smem0 + 2 * kTB;
+  uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; i++) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.kv_empty[i], 1);
+    }
+    mbar_init(&s.q_full, 64);
+    mbar_init(&s.q_empty, 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.o_done[i], 1);
+      mbar_init(&s.sched_full[i], 1);
+      mbar_init(&s.sched_empty[i], 11);            // 8 softmax warps, MMA warp, 2 helper warps
+    }
+    for (int i = 0; i < 3; i++) mbar_init(&s.v_clean[i], 2);
+    mbar_init(&s.v_next, 1);
+    mbar_init(&s.drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kApWMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  long long total = 0, x0 = 0, x1 = 0, ctas = 0;   // prompt: items; cache: key tiles, and this CTA's range of them
+  if constexpr (PAGED) {
+    int nitems = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kApThreads) {
+      const int b = b0 + tid;
+      int items = 0, nch = 1;
+      if (b < a.B) {
+        const int lo = __ldg(a.cu + b), n = lo < 0 ? 0 : min(__ldg(a.cu + b + 1), a.T) - lo;
+        if (n > 0) {
+          const long long ctx = min((long long)max(__ldg(a.cached + b), 0) + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n),
+                                    (long long)a.max_pages << a.page_shift);
+          items = (int)(((long long)n * a.group + kApRows - 1) / kApRows) * a.kv_heads;
+          nch = (int)((ctx + kApTile - 1) / kApTile);
+        }
+      }
+      const long long v = (long long)items * nch;
+      long long incl = v;
+      int iincl = items;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(kFull, incl, o);
+        const int u = __shfl_up_sync(kFull, iincl, o);
+        if (lane >= o) {
+          incl += t;
+          iincl += u;
+        }
+      }
+      if (lane == 31) {
+        s.wsum2[warp] = incl;
+        s.wsum[0][warp] = iincl;
+      }
+      __syncthreads();
+      long long at = total;
+      int iat = nitems;
+#pragma unroll
+      for (int w = 0; w < kApThreads / 32; w++) {
+        at += w < warp ? s.wsum2[w] : 0;
+        iat += w < warp ? s.wsum[0][w] : 0;
+        total += s.wsum2[w];
+        nitems += s.wsum[0][w];
+      }
+      if (b < a.B) {
+        s.work[b] = at + incl - v;
+        s.items[b] = iat + iincl - items;
+        s.nch[b] = nch;
+      }
+      __syncthreads();
+    }
+    if (tid == 0 && blockIdx.x == 0) p.ctrl[kAttnCtrlItems] = nitems;
+    const long long want = (total + kApMinTiles - 1) / kApMinTiles;
+    ctas = want < (long long)gridDim.x ? want : (long long)gridDim.x;
+    if ((long long)blockIdx.x < ctas) {
+      x0 = total * blockIdx.x / ctas;
+      x1 = total * (blockIdx.x + 1) / ctas;
+    }
+  } else {
+    // requests by falling number of row tiles (equal ones by index), every CTA alike
+    for (int b = tid; b < a.B; b += kApThreads) {
+      const int lo = __ldg(a.cu + b), n = max(0, min(__ldg(a.cu + b + 1), a.T) - lo);
+      s.before[b] = lo < 0 ? 0 : (int)(((long long)n * a.group + kApRows - 1) / kApRows);
+    }
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kApThreads) {
+      const int mine = s.before[b];
+      int rank = 0;
+      for (int o = 0; o < a.B; o++) rank += s.before[o] > mine || (s.before[o] == mine && o < b);
+      s.order[rank] = (uint16_t)b;
+      s.tiles[rank] = mine;
+    }
+    __syncthreads();
+    int items = 0;                                   // per kv head
+    for (int k0 = 0; k0 < a.B; k0 += kApThreads) {
+      const int k = k0 + tid;
+      // row tiles [tiles[k], tiles[k - 1]) hold the k longest requests each
+      const int v = k > 0 && k < a.B ? k * (s.tiles[k - 1] - s.tiles[k]) : 0;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += t;
+      }
+      if (lane == 31) s.wsum[0][warp] = incl;
+      __syncthreads();
+      int at = items;
+#pragma unroll
+      for (int w = 0; w < kApThreads / 32; w++) {
+        at += w < warp ? s.wsum[0][w] : 0;
+        items += s.wsum[0][w];
+      }
+      if (k < a.B) s.before[k] = at + incl;
+      __syncthreads();
+    }
+    total = (long long)(items + a.B * s.tiles[a.B - 1]) * a.kv_heads;   // row tiles that every request has come last
+  }
+  at_fence_before();
+  __syncthreads();
+  at_fence_after();
+  const uint32_t tb = s.tmem;
+  const float c = a.scale * 1.44269504088896340736f;
+  if constexpr (PAGED) pdl_launch_dependents();    // the join's CTAs take the SMs as they fall free, and wait
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kApRegsSoft));
+    const int h = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tb + lanes + 128u * h, to = tb + lanes + 256u + 128u * h;
+    uint32_t ns = 0;                               // tiles of this half so far
+    bool ok = true;
+    for (int i = 0;; i++) {
+      if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) {
+        atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+        break;
+      }
+      const ApItem it = s.item[i & 1];
+      if (it.b < 0) break;
+      const int nt = h ? it.n1 : it.n0;
+      const int ri = PAGED && it.twin ? tid & 127 : tid & 255;                  // row of the item
+      const bool real = ri < it.rows;
+      const int x = it.g0 + min(ri, it.rows - 1), dt = (x * p.magic) >> 16;
+      const int lim = it.tok0 + dt;                // the row's token: of the prompt, or among the fresh ones
+      uint64_t word = 0;
+      if constexpr (PAGED)
+        if (a.tree_mask) word = __ldg(a.tree_mask + it.first + lim);
+      float m = -INFINITY;                         // the maximum that P is taken against
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int j = 0; j < nt; j++, ns++) {
+        const int jl = PAGED && it.twin ? 2 * j + h : j, tok0 = (it.j0 + jl) * kApTile;
+        bool masked;
+        uint32_t held = 0;                         // pages of the tile that are in the cache
+        if constexpr (PAGED) {
+          const int np = kApTile >> a.page_shift, col = (tok0 >> a.page_shift) + lane;
+          const int id = lane < np && col < a.max_pages ? __ldg(a.block_table + (size_t)it.b * a.max_pages + col) : -1;
+          held = __ballot_sync(kFull, (unsigned)id < (unsigned)a.num_pages);
+          masked = jl >= it.m0 || held != (1u << np) - 1u;
+        } else {
+          masked = __any_sync(kFull, tok0 + kApTile - 1 > lim);
+        }
+        if (!mbar_wait_bounded(&s.s_full[h], ns & 1u)) {
+          atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+          ok = false;
+          break;
+        }
+        at_fence_after();
+        float v[128];
+#pragma unroll
+        for (int q = 0; q < 4; q++) at_ld32(ts + 32u * q, v + 32 * q);
+        at_wait_ld();
+        if (masked) {
+          if constexpr (PAGED) {
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+              const uint32_t bits = cache_visible(a, it, word, lim, tok0 + 32 * w, held, w);
+#pragma unroll
+              for (int e = 0; e < 32; e++) v[32 * w + e] = (bits >> e) & 1u ? v[32 * w + e] : -INFINITY;
+            }
+          } else {
+            const int vis = lim - tok0;
+#pragma unroll
+            for (int q = 0; q < 128; q++) v[q] = q > vis ? -INFINITY : v[q];
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          mx[q] = fmaxf(v[32 * q], v[32 * q + 1]);
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) mx[q] = at_max3(mx[q], v[32 * q + e], v[32 * q + e + 1]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(kFull, (top - m) * c > kApSlack)) {
+          const float m1 = fmaxf(m, top), f = m1 == -INFINITY ? 1.f : at_exp2((m - m1) * c);
+          m = m1;
+          l2.x *= f;
+          l2.y *= f;
+          if (!mbar_wait_bounded(&s.o_done[h], (ns - 1u) & 1u)) {
+            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+            ok = false;
+            break;
+          }
+          at_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; q++) {
+            float o[32];
+            at_ld32(to + 32u * q, o);
+            at_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e++) o[e] *= f;
+            at_st32(to + 32u * q, o);
+          }
+          at_wait_st();
+        }
+        const float mc = m == -INFINITY ? 0.f : -m * c;
+        const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            float2 t = ffma2(make_float2(v[32 * q + 2 * e], v[32 * q + 2 * e + 1]), c2, mc2);
+            t.x = at_exp2(t.x);
+            t.y = at_exp2(t.y);
+            sum[e & 1] = at_add2(sum[e & 1], t);
+            pk[e] = at_pack<F16>(t.x, t.y);
+          }
+          at_st16(ts + 16u * q, pk);
+        }
+        l2 = at_add2(l2, at_add2(sum[0], sum[1]));
+        at_wait_st();
+        at_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[h]);
+      }
+      if (!ok) break;
+      const float l = l2.x + l2.y;
+      if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (tid & 255)] = make_float2(m, l);
+      if (nt > 0) {
+        // ---------------------------------------------------------- epilogue
+        if (!mbar_wait_bounded(&s.o_done[h], (ns - 1u) & 1u)) {
+          atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+          break;
+        }
+        at_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int t = it.first + lim, hq = it.hk * a.group + x - dt * a.group;
+        uint32_t anybad = 0;
+#pragma unroll
+        for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
+        uint16_t *dst = a.out.p + (long long)t * a.out.row + (long long)hq * a.out.head;
+#pragma unroll 1
+        for (int q = 0; q < D / 32; q++) {
+          float o[32];
+          at_ld32(to + 32u * q, o);
+          at_wait_ld();
+          if (anybad) {
+            for (int w = 0; w < 12; w++) {
+              uint32_t bits = s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
+              for (; bits; bits &= bits - 1) {
+                const int tl = it.m0 + (w >> 2);   // tile of the part
+                if (PAGED && it.twin && (tl & 1) != h) continue;
+                const int tok = (it.j0 + tl) * kApTile + 32 * (w & 3) + __ffs(bits) - 1;
+                const uint16_t *vp;
+                if constexpr (PAGED) {
+                  const int f = tok - it.cached;
+                  if (tok >= it.end || !(a.tree_mask ? f < 64 && ((word >> (f & 63)) & 1) : f <= lim)) continue;
+                  const long long page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (tok >> a.page_shift));
+                  vp = a.v_cache + (((page * a.kv_heads + it.hk) << a.page_shift) + (tok & ((1 << a.page_shift) - 1))) * D + 32 * q;
+                } else {
+                  if (tok > lim) continue;
+                  vp = a.v.p + (long long)(it.first + tok) * a.v.row + (long long)it.hk * a.v.head + 32 * q;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e++) {
+                  const float u = at_value<F16>(__ldg(vp + e));
+                  if (!isfinite(u)) o[e] += u;
+                }
+              }
+            }
+          }
+          if (PAGED && it.slot >= 0) {
+            // [element / 4][row]: the 32 rows of a warp side by side
+            float4 *part = p.part + ((size_t)it.slot * (D / 4) + 8 * q) * kApRows + (tid & 255);
+#pragma unroll
+            for (int e = 0; e < 8; e++) part[e * kApRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (real) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              uint4 w;
+              w.x = at_pack<F16>(o[8 * e] * inv, o[8 * e + 1] * inv);
+              w.y = at_pack<F16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+              w.z = at_pack<F16>(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+              w.w = at_pack<F16>(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+              *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * e) = w;
+            }
+          }
+        }
+        at_fence_before();
+        if (a.lse && real && it.slot < 0) a.lse[(size_t)t * a.q_heads + hq] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApRegsRest));
+    if (warp == kApWTma) {
+      // ---------------------------------------------------------- items and key/value tiles
+      // over the cache every lane copies a page of the tile; else lane 0 the whole tile
+      if (PAGED || lane == 0) {
+        int pos = 0;
+        long long next = PAGED ? x0 : blockIdx.x;
+        bool ok = true;
+        for (int i = 0; ok; i++) {
+          ApItem it;
+          it.b = -1;
+          if constexpr (PAGED) {
+            while (next < x1) {
+              next = cache_part(s, p, next, x0, x1, total, ctas, it);
+              if (it.n > 0) break;
+              it.b = -1;
+            }
+          } else if (next < total) {
+            prompt_item(s, p, (int)next, it);
+          }
+          if (i >= 2 && !mbar_wait_bounded(&s.sched_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u)) {
+            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+            break;
+          }
+          if (lane == 0) {
+            s.item[i & 1] = it;
+            mbar_arrive(&s.sched_full[i & 1]);
+          }
+          if (it.b < 0) break;
+          if (!PAGED) next = gridDim.x + atomicAdd(p.ctrl + kAttnCtrlNext, 1);
+          const int n = it.n;
+          for (int q = 0; q < 2 * n; q++, pos++) {
+            // K0 K1 V0 K2 V1 .. K[n-1] V[n-2] V[n-1]
+            const bool isk = q < 2 * n - 1 && (q == 0 || (q & 1));
+            const int j = it.j0 + (isk ? (q + 1) >> 1 : (q == 2 * n - 1 ? n - 1 : (q >> 1) - 1));
+            const int slot = pos % kSlots;
+            int page = 0;
+            if constexpr (PAGED) {
+              const int col = (j * kApTile >> a.page_shift) + lane;
+              const int id = lane < kApTile >> a.page_shift && col < a.max_pages
+                                 ? __ldg(a.block_table + (size_t)it.b * a.max_pages + col) : -1;
+              page = (unsigned)id < (unsigned)a.num_pages ? id : a.num_pages;   // past the end: reads zeros
+            }
+            if (pos >= kSlots && !mbar_wait_bounded(&s.kv_empty[slot], (uint32_t)(pos / kSlots - 1) & 1u)) {
+              atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)kTB);
+            if constexpr (PAGED) {
+              __syncwarp();
+              if (lane < kApTile >> a.page_shift)
+                for (int hf = 0; hf < kHalves; hf++)
+                  at_tma_4d(ring + slot * kTB + hf * (kApTile * 128) + ((uint32_t)lane << (a.page_shift + 7)),
+                            isk ? &p.kmap : &p.vmap, 64 * hf, 0, it.hk, page, &s.kv_full[slot]);
+            } else {
+              for (int hf = 0; hf < kHalves; hf++)
+                at_tma_3d(ring + slot * kTB + hf * (kApTile * 128), isk ? &p.kmap : &p.vmap, 64 * hf, it.hk,
+                          it.first + j * kApTile, &s.kv_full[slot]);
+            }
+          }
+        }
+        // copies in flight land before the CTA ends
+        for (int q = (pos > kSlots ? pos - kSlots : 0); q < pos; q++)
+          mbar_wait_bounded(&s.kv_full[q % kSlots], (uint32_t)(q / kSlots) & 1u);
+        if (!PAGED) {
+          // the last CTA to have taken its last item leaves the counters at zero
+          __threadfence();
+          if (atomicAdd(p.ctrl + kAttnCtrlDone, 1) == (int)gridDim.x - 1) {
+            p.ctrl[kAttnCtrlNext] = 0;
+            p.ctrl[kAttnCtrlDone] = 0;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == kApWMma) {
+      // ---------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        constexpr uint32_t id_s = at_idesc(F16, kApTile, false), id_o = at_idesc(F16, D, true);
+        int base = 0;
+        uint32_t clean[3] = {0, 0, 0}, np[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+          if (ok && !mbar_wait_bounded(bar, parity)) {
+            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+            ok = false;
+          }
+          return ok;
+        };
+        auto wait_kv = [&](int pos) { return wait(&s.kv_full[pos % kSlots], (uint32_t)(pos / kSlots) & 1u); };
+        auto issue_s = [&](int h, uint32_t q, int pos) {
+          const int slot = pos % kSlots;
+#pragma unroll
+          for (int k = 0; k < D / 16; k++) {
+            const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32);
+            at_mma_ss(tb + 128u * h, at_desc(q + off, 16), at_desc(ring + slot * kTB + off, 16), id_s, k > 0);
+          }
+          at_commit(&s.s_full[h]);
+        };
+        auto issue_o = [&](int h, int pos, bool add) {
+          const int slot = pos % kSlots;
+#pragma unroll
+          for (int k = 0; k < kApTile / 16; k++)
+            at_mma_ts(tb + 256u + 128u * h, tb + 128u * h + 8u * k, at_desc(ring + slot * kTB + 2048u * k, kApTile * 128),
+                      id_o, (uint32_t)(add || k > 0));
+          at_commit(&s.o_done[h]);
+        };
+        for (int i = 0; ok; i++) {
+          if (!wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+          const ApItem it = s.item[i & 1];
+          if (it.b < 0) break;
+          const int n = it.n;
+          const bool twin = PAGED && it.twin;
+          const uint32_t q1 = twin ? q_smem : q_smem + kTB;
+          if (!wait(&s.q_full, (uint32_t)i & 1u) || !wait_kv(base)) break;
+          at_fence_after();
+          issue_s(0, q_smem, base);
+          if (!twin && it.n1 > 0) issue_s(1, q1, base);
+          at_commit(&s.kv_empty[base % kSlots]);
+          if (twin && n > 1) {
+            if (!wait_kv(base + 1)) break;
+            at_fence_after();
+            issue_s(1, q1, base + 1);
+            at_commit(&s.kv_empty[(base + 1) % kSlots]);
+          }
+          const int ahead = twin ? 2 : 1;          // the S issued with PV of tile j is that of tile j + ahead
+          if (n <= ahead) at_commit(&s.q_empty);
+          for (int j = 0; j < n; j++) {
+            const int pk = base + ap_pos_k(j + ahead), pv = base + ap_pos_v(j, n);
+            const bool next = j + ahead < n;
+            // in the order of the ring, but for K1 of a pair of row tiles
+            if (!twin && next && !wait_kv(pk)) break;
+            if (!wait_kv(pv)) break;
+            if (j >= it.m0) {
+              const int z = j - it.m0;             // 0, 1 or 2: a constant index in each case
+              const uint32_t ph = z == 0 ? clean[0]++ : (z == 1 ? clean[1]++ : clean[2]++);
+              if (!wait(&s.v_clean[z], ph & 1u)) break;
+            }
+            if (j + 1 == n) mbar_arrive(&s.v_next);   // the next item's scans may signal
+            if (twin && next && !wait_kv(pk)) break;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              if (twin ? (j & 1) == h : j < (h ? it.n1 : it.n0)) {
+                if (!wait(&s.p_full[h], np[h]++ & 1u)) break;
+                at_fence_after();
+                issue_o(h, pv, j >= ahead);
+                if (twin ? next : j + 1 < (h ? it.n1 : it.n0)) issue_s(h, h ? q1 : q_smem, pk);
+              }
+            }
+            if (!ok) break;
+            at_commit(&s.kv_empty[pv % kSlots]);
+            if (next) at_commit(&s.kv_empty[pk % kSlots]);
+            if (j + ahead + 1 == n) at_commit(&s.q_empty);
+          }
+          base += 2 * n;
+          mbar_arrive(&s.sched_empty[i & 1]);
+        }
+        // every MMA issued has completed before tensor memory is released
+        at_commit(&s.drain);
+        mbar_wait_bounded(&s.drain, 0u);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- Q rows, and the scan of masked tiles' v
+      const int ht = tid - 32 * kApWHelp;
+      int base = 0;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+        const ApItem it = s.item[i & 1];
+        if (it.b < 0) break;
+        const int n = it.n;
+        if (lane < 12) s.bad[i & 1][warp - kApWHelp][lane >> 2][lane & 3] = 0u;
+        __syncwarp();
+        if (i > 0 && !mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u)) break;
+        constexpr int kChunks = D / 8;
+        const int ch = ht % kChunks, top = it.rows > kApTile ? kApRows : kApTile;
+        const uint32_t qd = q_smem + (uint32_t)(ch >> 3) * (kApTile * 128);
+        for (int r = ht / kChunks; r < top; r += 64 / kChunks) {
+          const int x = it.g0 + r, dt = (x * p.magic) >> 16;
+          const uint16_t *src = a.q.p + (long long)(it.first + it.tok0 + dt) * a.q.row +
+                                (long long)(it.hk * a.group + x - dt * a.group) * a.q.head + 8 * ch;
+          const int rr = r & (kApTile - 1);
+          at_cp16(qd + (r >= kApTile ? kTB : 0) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), r < it.rows ? src : a.q.p,
+                  r < it.rows);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        at_fence_async();
+        mbar_arrive(&s.q_full);
+        // the MMA warp has seen this item's predecessor's scans: a barrier is
+        // never a phase ahead of its reader
+        if (i > 0 && !mbar_wait_bounded(&s.v_next, (uint32_t)(i - 1) & 1u)) break;
+        for (int j = it.m0; j < n; j++) {
+          const int pv = base + ap_pos_v(j, n), slot = pv % kSlots;
+          if (!mbar_wait_bounded(&s.kv_full[slot], (uint32_t)(pv / kSlots) & 1u)) {
+            ok = false;
+            break;
+          }
+          uint8_t *tile = generic0 + 2 * kTB + slot * kTB;
+          const int r0 = max(0, it.all - (it.j0 + j) * kApTile);      // earlier tokens are seen by every row
+          for (int hf = 0; hf < kHalves; hf++)
+            for (int e = r0 * 8 + ht; e < kApTile * 8; e += 64) {
+              uint4 *at = reinterpret_cast<uint4 *>(tile + hf * (kApTile * 128)) + e;
+              const uint4 w = *at;
+              const uint32_t f[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
+              if (f[0] | f[1] | f[2] | f[3]) {
+                uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int z = 0; z < 4; z++) u[z] &= ~(((f[z] >> 15) & 0x00010001u) * 0xFFFFu);
+                *at = make_uint4(u[0], u[1], u[2], u[3]);
+                atomicOr(&s.bad[i & 1][warp - kApWHelp][j - it.m0][(e >> 3) >> 5], 1u << ((e >> 3) & 31));
+              }
+            }
+          at_fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.v_clean[j - it.m0]);
+        }
+        base += 2 * n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
+      }
+    }
+  }
+  at_fence_before();
+  __syncthreads();
+  if (warp == kApWMma) {
+    at_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512) : "memory");
+  }
+}
+
+// Joins the parts of the items that several CTAs took, in the order of the
+// context: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A CTA takes 32
+// rows of an item; a thread one row and D / 8 of its elements, so that a warp
+// reads 32 rows side by side.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) attn_join_kernel(const ApArgs p) {
+  const AttnArgs &a = p.a;
+  pdl_wait();
+  if (blockIdx.x >= (unsigned)__ldcg(p.ctrl + kAttnCtrlItems)) return;
+  const int4 d0 = __ldcg(p.desc + 2 * blockIdx.x), d1 = __ldcg(p.desc + 2 * blockIdx.x + 1);
+  const int first = d0.x, hk = d0.y, row0 = d0.z, rows = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), dg = threadIdx.x >> 5;
+  if (c1 < 0 || r >= rows) return;
+  const float c = a.scale * 1.44269504088896340736f;
+  constexpr int N = D / 32;                        // float4 of a thread
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int k = c0; k <= c1; k++) {
+    const size_t at = (size_t)(k == c0 ? slot0 : 2 * k) * kApRows + r;
+    top = fmaxf(top, __ldcg(&p.stat[at].x));
+    if (twin) top = fmaxf(top, __ldcg(&p.stat[at + kApTile].x));
+  }
+  float sum = 0.f;
+  float4 acc[N];
+#pragma unroll
+  for (int e = 0; e < N; e++) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int slot, int row) {
+    const float2 st = __ldcg(&p.stat[(size_t)slot * kApRows + row]);
+    if (st.y == 0.f) return;                       // a part in which the row sees nothing (it may hold no O)
+    const float f = at_exp2((st.x - top) * c);
+    sum = fmaf(st.y, f, sum);
+    const float4 *src = p.part + ((size_t)slot * (D / 4) + N * dg) * kApRows + row;
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+      const float4 u = __ldcg(src + e * kApRows);
+      acc[e].x = fmaf(u.x, f, acc[e].x);
+      acc[e].y = fmaf(u.y, f, acc[e].y);
+      acc[e].z = fmaf(u.z, f, acc[e].z);
+      acc[e].w = fmaf(u.w, f, acc[e].w);
+    }
+  };
+#pragma unroll 2
+  for (int k = c0; k <= c1; k++) {
+    const int slot = k == c0 ? slot0 : 2 * k;
+    add(slot, r);
+    if (twin) add(slot, r + kApTile);
+  }
+  const int rr = row0 + r, i = rr / a.group, hq = hk * a.group + rr - i * a.group;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t *dst = a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + 4 * N * dg;
+#pragma unroll
+  for (int e = 0; e < N; e++)
+    *reinterpret_cast<uint2 *>(dst + 4 * e) =
+        make_uint2(at_pack<F16>(acc[e].x * inv, acc[e].y * inv), at_pack<F16>(acc[e].z * inv, acc[e].w * inv));
+  if (a.lse && dg == 0) a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+}
+
+namespace {
+typedef void (*ApKernel)(const ApArgs);
+template <bool PAGED>
+ApKernel ap_kernel(int head_dim, int f16) {
+  if (head_dim == 64) return f16 ? attn_wide_kernel<64, true, PAGED> : attn_wide_kernel<64, false, PAGED>;
+  return f16 ? attn_wide_kernel<128, true, PAGED> : attn_wide_kernel<128, false, PAGED>;
+}
+ApKernel ap_join(int head_dim, int f16) {
+  if (head_dim == 64) return f16 ? attn_join_kernel<64, true> : attn_join_kernel<64, false>;
+  return f16 ? attn_join_kernel<128, true> : attn_join_kernel<128, false>;
+}
+int ap_smem(int head_dim) { return head_dim == 64 ? ApGeom<64>::kSmem : ApGeom<128>::kSmem; }
+
+cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, int head_dim, int f16) {
+  const AttnMapEncodeFn enc = attn_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)r.head * 2, (cuuint64_t)r.row * 2};
+  const cuuint32_t box[3] = {64, 1, kApTile};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult e = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, strides,
+                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// Items at most: every request may end inside a row tile.
+long long wide_items(int group, int kv_heads, int B, int T) {
+  return (((long long)T * group + kApRows - 1) / kApRows + B) * kv_heads;
+}
+}  // namespace
+
+cudaError_t attn_wide_setup(int head_dim, int f16) {
+  for (int i = 0; i < 2; i++) {
+    const ApKernel k = i ? ap_kernel<true>(head_dim, f16) : ap_kernel<false>(head_dim, f16);
+    cudaFuncAttributes at;
+    cudaError_t err = cudaFuncGetAttributes(&at, k);
+    if (err != cudaSuccess) return err;
+    // the register shares of the warpgroups have to fit what the CTA is launched with
+    if (at.numRegs * kApThreads < kApRegsSoft * 256 + kApRegsRest * 128) return cudaErrorInvalidConfiguration;
+    err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ap_smem(head_dim));
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+AttnWideWs attn_wide_ws(size_t off, int group, int kv_heads, int head_dim, int B, int T, int num_sms) {
+  AttnWideWs w;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  w.desc = take(32 * (size_t)wide_items(group, kv_heads, B, T));
+  w.stat = take(8 * (size_t)(2 * num_sms) * kApRows);
+  w.part = take(4 * (size_t)(2 * num_sms) * kApRows * head_dim);
+  w.total = off;
+  return w;
+}
+
+cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaStream_t stream) {
+  ApArgs p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  p.ctrl = ctrl;
+  p.magic = (65536 + a.group - 1) / a.group;
+  cudaError_t err = encode_rows(&p.kmap, a.k, a.T, a.kv_heads, a.head_dim, a.f16);
+  if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, a.head_dim, a.f16);
+  if (err != cudaSuccess) return err;
+  const long long items = wide_items(a.group, a.kv_heads, a.B, a.T);
+  const int grid = (int)(items < num_sms ? items : num_sms);
+  ap_kernel<false>(a.head_dim, a.f16)<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWideWs &w, int num_sms, cudaStream_t stream) {
+  ApArgs p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  p.ctrl = reinterpret_cast<int *>(ws);
+  p.magic = (65536 + a.group - 1) / a.group;
+  p.desc = reinterpret_cast<int4 *>(ws + w.desc);
+  p.stat = reinterpret_cast<float2 *>(ws + w.stat);
+  p.part = reinterpret_cast<float4 *>(ws + w.part);
+  cudaError_t err = attn_encode_cache(&p.kmap, a.k_cache, a, 1 << a.page_shift);
+  if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 1 << a.page_shift);
+  if (err != cudaSuccess) return err;
+  ap_kernel<true>(a.head_dim, a.f16)<<<num_sms, kApThreads, ap_smem(a.head_dim), stream>>>(p);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)wide_items(a.group, a.kv_heads, a.B, a.T), kApRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ap_join(a.head_dim, a.f16), p);
+}
+
+}  // namespace moe
