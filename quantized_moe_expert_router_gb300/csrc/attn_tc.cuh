@@ -13,7 +13,15 @@ namespace moe {
 
 __device__ __forceinline__ void at_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void at_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Wait for this thread's tensor-memory loads into r.  The empty statements make
+// the registers depend on the wait: without them the compiler may move their
+// first uses, which depend on the load instructions alone, before it.
+template <int N>
+__device__ __forceinline__ void at_wait_ld(float (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i++) asm volatile("" : "+f"(r[i])::"memory");
+}
 __device__ __forceinline__ void at_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of this warp's 32 tensor-memory lanes into r[0..31]; complete
@@ -48,6 +56,31 @@ __device__ __forceinline__ void at_st32(uint32_t taddr, const float *r) {
       : "memory");
 }
 
+// 32 columns of 16 of this warp's tensor-memory lanes as fragments: of columns
+// 8 i + 2 (lane & 3), + 1, row lane / 4 in r[4 i], r[4 i + 1] and row lane / 4 + 8
+// in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void at_ld_frag(uint32_t taddr, float *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Word i of lane q of a quad <-> word q of lane i.
+__device__ __forceinline__ void at_quad_transpose(uint32_t (&w)[4], int q) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t got = __shfl_xor_sync(kFull, (q & 1) ? w[i] : w[i + 1], 1);
+    if (q & 1) w[i] = got; else w[i + 1] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const uint32_t got = __shfl_xor_sync(kFull, (q & 2) ? w[i] : w[i + 2], 2);
+    if (q & 2) w[i] = got; else w[i + 2] = got;
+  }
+}
+
 // Shared-memory descriptors of tiles of 128-byte rows under the 128-byte
 // swizzle (16-byte piece c of row r at piece c ^ (r & 7); 8 rows = 1024 bytes).
 //   K-major (rows are M or N, the row's elements are K): 8-row groups 1024
@@ -78,6 +111,12 @@ __device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// True in one lane of the warp.
+__device__ __forceinline__ bool at_elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ void at_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))

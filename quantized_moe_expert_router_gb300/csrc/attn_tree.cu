@@ -43,19 +43,17 @@ struct AtArgs {
   CUtensorMap kmap, vmap;      // (64, 16, 1, 1) boxes over [pages][kv_heads][page_size][D]
   AttnArgs a;
   int *ctrl;                   // workspace control words
-  int *tickets;                // per item: parts done; zero between calls
+  int *tickets;                // per CTA that holds an item's first part: parts done; zero between calls
   float *part;                 // [2 * grid][rows][D]
   float2 *stat;                // [2 * grid][rows]  (m, l)
+  int magic;                   // ceil(2^16 / group)
 };
 
 struct AtSmem {
   uint64_t full[kAtWarps][kAtStages];
   long long work[kAtMaxB + 1]; // chunks of the requests before
-  int items[kAtMaxB];          // items of the requests before
-  int nch[kAtMaxB];            // chunks of an item
-  int tiles[kAtMaxB];          // row tiles of a kv head
-  int wsum[kAtWarps];
-  long long wsum2[kAtWarps];
+  int first[kAtMaxB], n[kAtMaxB], cached[kAtMaxB];   // first packed row, fresh rows, cached tokens
+  long long wsum[kAtWarps];
   float2 stat[kAtWarps][32];   // (m, l) by warp and row
   int last;
 };
@@ -93,33 +91,53 @@ __device__ __forceinline__ void at_ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// A place in the line of chunks.
+// x / d for 0 <= x, 0 < d: the 64-bit division is a long software routine.
+__device__ __forceinline__ long long at_div(long long x, long long d) {
+  return (x | d) >> 32 ? x / d : (long long)((uint32_t)x / (uint32_t)d);
+}
+
+// A place in the line of chunks: request, kv head, row tile, chunk; innermost
+// last, so that the row tiles of a kv head read the same keys one after another.
 struct AtPos {
-  int b, item, chunk;          // request, item of the request (kv head * row tiles + row tile), chunk
+  int b, hk, rt, chunk;
+  int tiles, nch;              // row tiles of the request, chunks of its context
 };
-__device__ __forceinline__ AtPos at_pos(const AtSmem &s, int B, long long x) {
-  int lo = 0, hi = B - 1;                          // largest b with work[b] <= x: the later ones of equals have no chunks before x
+template <int TOK, int ROWS>
+__device__ __forceinline__ void at_request(const AtSmem &s, const AttnArgs &a, AtPos &p) {
+  const int n = s.n[p.b];
+  p.tiles = (int)(((long long)n * a.group + ROWS - 1) / ROWS);
+  p.nch = (int)((min((long long)s.cached[p.b] + n, (long long)a.max_pages << a.page_shift) + TOK - 1) / TOK);
+}
+template <int TOK, int ROWS>
+__device__ __forceinline__ AtPos at_pos(const AtSmem &s, const AttnArgs &a, long long x) {
+  int lo = 0, hi = a.B - 1;                        // largest b with work[b] <= x: requests without rows have no chunks
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (s.work[mid] <= x) lo = mid; else hi = mid - 1;
   }
-  const long long off = x - s.work[lo];
   AtPos p;
   p.b = lo;
-  p.item = (int)(off / s.nch[lo]);
-  p.chunk = (int)(off - (long long)p.item * s.nch[lo]);
+  at_request<TOK, ROWS>(s, a, p);
+  const long long off = x - s.work[lo];
+  const int item = (int)at_div(off, p.nch);
+  p.chunk = (int)(off - (long long)item * p.nch);
+  p.hk = item / p.tiles;
+  p.rt = item - p.hk * p.tiles;
   return p;
 }
 // `step` chunks on (a place that exists).
-__device__ __forceinline__ void at_advance(const AtSmem &s, AtPos &p, int step) {
+template <int TOK, int ROWS>
+__device__ __forceinline__ void at_advance(const AtSmem &s, const AttnArgs &a, AtPos &p, int step) {
   p.chunk += step;
-  while (p.chunk >= s.nch[p.b]) {
-    p.chunk -= s.nch[p.b];
-    p.item++;
-    if (s.work[p.b] + (long long)p.item * s.nch[p.b] == s.work[p.b + 1]) {
-      p.item = 0;
-      p.b++;
-      while (s.work[p.b + 1] == s.work[p.b]) p.b++;   // requests without rows
+  while (p.chunk >= p.nch) {
+    p.chunk -= p.nch;
+    if (++p.rt == p.tiles) {
+      p.rt = 0;
+      if (++p.hk == a.kv_heads) {
+        p.hk = 0;
+        do p.b++; while (s.n[p.b] == 0);
+        at_request<TOK, ROWS>(s, a, p);
+      }
     }
   }
 }
@@ -146,69 +164,57 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
   }
   // the line of chunks, every CTA alike
   long long total = 0;
-  int nitems = 0;
   for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
     const int b = b0 + tid;
-    int tiles = 0, nch = 1;
+    long long v = 0;
     if (b < a.B) {
-      const int lo = __ldg(a.cu + b), n = lo < 0 ? 0 : min(__ldg(a.cu + b + 1), a.T) - lo;
-      const long long ctx = min((long long)max(__ldg(a.cached + b), 0) + max(n, 0), (long long)a.max_pages << a.page_shift);
-      if (n > 0) {
-        tiles = (int)(((long long)n * a.group + kRows - 1) / kRows);
-        nch = (int)((ctx + kTok - 1) / kTok);
-      }
+      const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1), cached = max(__ldg(a.cached + b), 0);
+      s.first[b] = lo;
+      s.n[b] = lo < 0 ? 0 : max(0, min(hi, a.T) - lo);
+      s.cached[b] = cached;
+      AtPos q;
+      q.b = b;
+      at_request<kTok, kRows>(s, a, q);
+      v = (long long)q.tiles * a.kv_heads * q.nch;
     }
-    const int items = tiles * a.kv_heads;
-    const long long v = (long long)items * nch;
     long long incl = v;
-    int iincl = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(kFull, incl, o);
-      const int u = __shfl_up_sync(kFull, iincl, o);
-      if (lane >= o) {
-        incl += t;
-        iincl += u;
-      }
+      const long long u = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += u;
     }
-    if (lane == 31) {
-      s.wsum2[warp] = incl;
-      s.wsum[warp] = iincl;
-    }
+    if (lane == 31) s.wsum[warp] = incl;
     __syncthreads();
     long long at = total;
-    int iat = nitems;
 #pragma unroll
     for (int w = 0; w < kAtWarps; w++) {
-      at += w < warp ? s.wsum2[w] : 0;
-      iat += w < warp ? s.wsum[w] : 0;
-      total += s.wsum2[w];
-      nitems += s.wsum[w];
+      at += w < warp ? s.wsum[w] : 0;
+      total += s.wsum[w];
     }
-    if (b < a.B) {
-      s.work[b] = at + incl - v;
-      s.items[b] = iat + iincl - items;
-      s.nch[b] = nch;
-      s.tiles[b] = tiles;
-    }
+    if (b < a.B) s.work[b] = at + incl - v;
     __syncthreads();
   }
-  if (tid == 0) s.work[a.B] = total;
-  __syncthreads();
-  const long long want = (total + kAtMinChunks - 1) / kAtMinChunks;
-  const long long ctas = want < (long long)gridDim.x ? want : (long long)gridDim.x;   // CTAs with a range
-  if ((long long)blockIdx.x >= ctas) return;
-  const long long x0 = total * blockIdx.x / ctas, x1 = total * (blockIdx.x + 1) / ctas;
+  // CTA i of `ctas` takes chunks start(i) .. start(i + 1): per or per + 1 of them
+  const int ctas = (int)min((total + kAtMinChunks - 1) / kAtMinChunks, (long long)gridDim.x);
+  if ((int)blockIdx.x >= ctas) return;
+  const long long per = at_div(total, ctas), rem = total - per * ctas;
+  auto start = [&](long long i) { return i * per + min(i, rem); };
+  auto cta_of = [&](long long x) {
+    const long long big = rem * (per + 1);
+    return (int)(x < big ? at_div(x, per + 1) : rem + at_div(x - big, per));
+  };
+  const long long x0 = start(blockIdx.x), x1 = start(blockIdx.x + 1);
 
   const float c = a.scale * 1.44269504088896340736f;
   bool ok = true;                                  // no wait of this warp has run out
   // the warp's chunks: x0 + warp, + 8, ..; `xp` is the next to be copied
+  AtPos sp = at_pos<kTok, kRows>(s, a, x0);
   long long xp = x0 + warp;
-  AtPos pp = {0, 0, 0};
-  if (xp < x1) pp = at_pos(s, a.B, xp);
+  AtPos pp = sp;
+  if (xp < x1) at_advance<kTok, kRows>(s, a, pp, warp);
   uint32_t kp = 0, kc = 0;                         // chunks copied, consumed
   auto issue = [&]() {
-    const int hk = pp.item / s.tiles[pp.b], stage = kp % kAtStages;
+    const int stage = kp % kAtStages;
     if (lane == 0) {
       uint64_t *bar = &s.full[warp][stage];
       const uint32_t dst = ring + stage * kAtStageBytes;
@@ -221,30 +227,47 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
         const int place = tok & ((1 << a.page_shift) - 1);
 #pragma unroll
         for (int hf = 0; hf < kHalves; hf++) {
-          at_tma_4d(dst + (k * kHalves + hf) * 2048, &p.kmap, 64 * hf, place, hk, page, bar);
-          at_tma_4d(dst + kAtStageBytes / 2 + (k * kHalves + hf) * 2048, &p.vmap, 64 * hf, place, hk, page, bar);
+          at_tma_4d(dst + (k * kHalves + hf) * 2048, &p.kmap, 64 * hf, place, pp.hk, page, bar);
+          at_tma_4d(dst + kAtStageBytes / 2 + (k * kHalves + hf) * 2048, &p.vmap, 64 * hf, place, pp.hk, page, bar);
         }
       }
     }
     kp++;
     xp += kAtWarps;
-    if (xp < x1) at_advance(s, pp, kAtWarps);
+    if (xp < x1) at_advance<kTok, kRows>(s, a, pp, kAtWarps);
   };
   for (int i = 0; i < kAtStages && xp < x1; i++) issue();
 
   long long xc = x0 + warp, xs = x0;               // the warp's next chunk; start of the part
-  AtPos sp = at_pos(s, a.B, x0);
   int nparts = 0;
   while (xs < x1) {
     // ---------------------------------------------------------------- a part of one item
-    const int b = sp.b, nch = s.nch[b];
-    const long long item0 = s.work[b] + (long long)sp.item * nch;   // the item's place in the line
+    const int b = sp.b, nch = sp.nch, hk = sp.hk, row0 = sp.rt * kRows;
+    const long long item0 = xs - sp.chunk;         // the item's place in the line
     const long long xe = min(x1, item0 + nch);
-    const int hk = sp.item / s.tiles[b], row0 = (sp.item - hk * s.tiles[b]) * kRows;
-    const int first = __ldg(a.cu + b), n = min(__ldg(a.cu + b + 1), a.T) - first;
-    const int cached = max(__ldg(a.cached + b), 0);
+    const int first = s.first[b], n = s.n[b], cached = s.cached[b];
     const int ctx = (int)min((long long)cached + n, (long long)a.max_pages << a.page_shift);
     const int rows = (int)min((long long)kRows, (long long)n * a.group - row0);
+    const int i0 = row0 / a.group, g0 = row0 - i0 * a.group;
+    // fresh row and query head of row r of the item
+    auto row_of = [&](int r, int &i, int &hq) {
+      const int dt = ((g0 + r) * p.magic) >> 16;
+      i = i0 + dt;
+      hq = hk * a.group + g0 + r - dt * a.group;
+    };
+    // o, m and l of a row -> the result: elements col .. col + N - 1
+    auto emit = [&](int r, int col, float top, float sum, const float *acc) {
+      int i, hq;
+      row_of(r, i, hq);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint16_t *dst = a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + col;
+#pragma unroll
+      for (int e = 0; e < D / 64; e++)
+        *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_pack<F16>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                                                             at_pack<F16>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
+      if (a.lse && col == 0)
+        a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+    };
 
     uint32_t qf[MT][D / 16][4];
     uint64_t word[MT][2];                          // tree: the row's word; else bits unused and the row's place in `lim`
@@ -253,8 +276,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
       for (int z = 0; z < 2; z++) {
-        const int r = 16 * mt + g + 8 * z, rr = row0 + min(r, rows - 1);
-        const int i = rr / a.group, hq = hk * a.group + rr - i * a.group;
+        const int r = 16 * mt + g + 8 * z;
+        int i, hq;
+        row_of(min(r, rows - 1), i, hq);
         const uint16_t *src = a.q.p + (long long)(first + i) * a.q.row + (long long)hq * a.q.head;
         const bool real = r < rows;
 #pragma unroll
@@ -485,15 +509,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
           }
         }
         if (entire) {
-          const int rr = row0 + r32, i = rr / a.group, hq = hk * a.group + rr - i * a.group;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          uint16_t *dst = a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + col;
-#pragma unroll
-          for (int e = 0; e < N / 4; e++)
-            *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_pack<F16>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
-                                                                 at_pack<F16>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
-          if (a.lse && (tid & 15) == 0)
-            a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+          emit(r32, col, top, sum, acc);
         } else {
           float4 *dst = reinterpret_cast<float4 *>(p.part + ((size_t)slot * kRows + r32) * D + col);
 #pragma unroll
@@ -504,59 +520,68 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
       __syncthreads();
     }
     if (!entire) {
-      // the CTAs that hold the item's chunks; the last to arrive joins their parts
-      const int c0 = (int)(((item0 + 1) * ctas - 1) / total), c1 = (int)(((item0 + nch) * ctas - 1) / total);
-      __threadfence();
-      __syncthreads();
+      // the CTAs that hold the item's chunks; the last to arrive joins their
+      // parts.  A CTA's first part is in its slot 0, and CTA c0's is not its
+      // first unless the item starts with the CTA's range.
+      const int c0 = xs == item0 ? (int)blockIdx.x : cta_of(item0);
+      const int c1 = xe == item0 + nch ? (int)blockIdx.x : cta_of(item0 + nch - 1);
+      const int slot0 = 2 * c0 + (start(c0) < item0);
       if (tid == 0) {
-        int *ticket = p.tickets + s.items[b] + sp.item;
-        s.last = atomicAdd(ticket, 1) == c1 - c0;
-        if (s.last) *ticket = 0;
+        // release: the CTA's parts, ordered before by the barrier; acquire: the others'
+        int got;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(got) : "l"(p.tickets + c0) : "memory");
+        s.last = got == c1 - c0;
+        if (got == c1 - c0) p.tickets[c0] = 0;
       }
       __syncthreads();
       if (s.last) {
-        __threadfence();
         constexpr int N = D / 16;
         const int col = (tid & 15) * N;
-        for (int r = tid >> 4; r < rows; r += 16) {
-          float top = -INFINITY, sum = 0.f, acc[N];
+        for (int r = tid >> 4; r < kRows; r += 16) {
+          const bool real = r < rows;
+          // the 16 threads of a row look at a part's statistics each
+          float top = -INFINITY;
+          for (int k = c0 + (tid & 15); k <= c1; k += 16)
+            if (real) top = fmaxf(top, __ldcg(&p.stat[(size_t)(k == c0 ? slot0 : 2 * k) * kRows + r].x));
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+          if (!real) continue;
+          float sum = 0.f, acc[N];
 #pragma unroll
           for (int e = 0; e < N; e++) acc[e] = 0.f;
-          // a CTA's first part is in its slot 0; the item's start lies inside CTA c0's range unless it is that range's start
-          const int off0 = total * c0 / ctas < item0 ? 1 : 0;
-          for (int k = c0; k <= c1; k++)
-            top = fmaxf(top, __ldcg(&p.stat[(size_t)(2 * k + (k == c0 ? off0 : 0)) * kRows + r].x));
-#pragma unroll 4
-          for (int k = c0; k <= c1; k++) {
-            const size_t at = (size_t)(2 * k + (k == c0 ? off0 : 0)) * kRows + r;
-            const float2 st = __ldcg(&p.stat[at]);
-            const float f = st.x == -INFINITY ? 0.f : at_exp2((st.x - top) * c);
-            sum = fmaf(st.y, f, sum);
-            const float4 *src = reinterpret_cast<const float4 *>(p.part + at * D + col);
+          // eight parts at a time, so that their loads wait together
+          for (int k0 = c0; k0 <= c1; k0 += 8) {
+            float2 st[8];
+            float4 u[8][N / 4];
 #pragma unroll
-            for (int e = 0; e < N / 4; e++) {
-              const float4 u = __ldcg(src + e);
-              acc[4 * e] = fmaf(u.x, f, acc[4 * e]);
-              acc[4 * e + 1] = fmaf(u.y, f, acc[4 * e + 1]);
-              acc[4 * e + 2] = fmaf(u.z, f, acc[4 * e + 2]);
-              acc[4 * e + 3] = fmaf(u.w, f, acc[4 * e + 3]);
+            for (int z = 0; z < 8; z++) {
+              const int k = min(k0 + z, c1);
+              const size_t at = (size_t)(k == c0 ? slot0 : 2 * k) * kRows + r;
+              st[z] = __ldcg(&p.stat[at]);
+#pragma unroll
+              for (int e = 0; e < N / 4; e++) u[z][e] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + col) + e);
+            }
+#pragma unroll
+            for (int z = 0; z < 8; z++) {
+              if (k0 + z > c1) break;
+              const float f = st[z].x == -INFINITY ? 0.f : at_exp2((st[z].x - top) * c);
+              sum = fmaf(st[z].y, f, sum);
+#pragma unroll
+              for (int e = 0; e < N / 4; e++) {
+                acc[4 * e] = fmaf(u[z][e].x, f, acc[4 * e]);
+                acc[4 * e + 1] = fmaf(u[z][e].y, f, acc[4 * e + 1]);
+                acc[4 * e + 2] = fmaf(u[z][e].z, f, acc[4 * e + 2]);
+                acc[4 * e + 3] = fmaf(u[z][e].w, f, acc[4 * e + 3]);
+              }
             }
           }
-          const int rr = row0 + r, i = rr / a.group, hq = hk * a.group + rr - i * a.group;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          uint16_t *dst = a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + col;
-#pragma unroll
-          for (int e = 0; e < N / 4; e++)
-            *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_pack<F16>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
-                                                                 at_pack<F16>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
-          if (a.lse && (tid & 15) == 0)
-            a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+          emit(r, col, top, sum, acc);
         }
         __syncthreads();
       }
     }
     xs = xe;
-    if (xs < x1) at_advance(s, sp, (int)(xe - (item0 + sp.chunk)));
+    if (xs < x1) at_advance<kTok, kRows>(s, a, sp, nch - sp.chunk);
   }
   // copies in flight (after a wait ran out) land before the CTA ends
   if (!ok)
@@ -594,8 +619,7 @@ AttnTreeWs attn_tree_ws(int group, int kv_heads, int head_dim, int B, int T, int
     off = (off + bytes + 255) / 256 * 256;
     return at;
   };
-  // items at most: of 16 rows, and every request may end inside one
-  w.tickets = take(4 * (size_t)kv_heads * ((((size_t)T * group + 15) / 16) + B));
+  w.tickets = take(4 * (size_t)num_sms);
   w.stat = take(8 * (size_t)(2 * num_sms) * 32);
   w.part = take(4 * (size_t)(2 * num_sms) * 32 * head_dim);
   w.wide = attn_wide_ws(off, group, kv_heads, head_dim, B, T, num_sms);
@@ -609,6 +633,7 @@ cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaSt
   if (rows > kAtMostRows) return launch_attn_wide_tree(a, ws, w.wide, num_sms, stream);
   AtArgs p;
   p.a = a;
+  p.magic = (65536 + a.group - 1) / a.group;
   cudaError_t err = attn_encode_cache(&p.kmap, a.k_cache, a, 16);
   if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 16);
   if (err != cudaSuccess) return err;

@@ -97,7 +97,7 @@ struct ApItem {
 
 struct ApSmem {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_clean[3], v_next, sched_full[2], sched_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int wsum[2][kApThreads / 32];
   ApItem item[2];
@@ -182,7 +182,7 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
   it.n = max(0, min((int)(xe - item0), need) - it.j0);
   const bool whole = it.j0 == 0 && it.n == need;
   it.twin = !whole && it.rows <= kApTile;
-  it.slot = whole ? -1 : 2 * blockIdx.x + (x > x0);
+  it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > x0);
   it.n0 = it.twin ? (it.n + 1) >> 1 : it.n;
   it.n1 = it.twin ? it.n >> 1 : (it.rows > kApTile ? it.n : 0);
   it.m0 = max(0, it.all / kApTile - it.j0);
@@ -200,8 +200,10 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
 
 // Bits of the tokens base .. base + 31 (word w of the tile) that a row sees.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
-__device__ __forceinline__ uint32_t cache_visible(const AttnArgs &a, const ApItem &it, uint64_t word, int lim, int base,
-                                                  uint32_t held, int w) {
+template <bool PAGED>
+__device__ __forceinline__ uint32_t visible_bits(const AttnArgs &a, const ApItem &it, uint64_t word, int lim, int base,
+                                                 uint32_t held, int w) {
+  if constexpr (!PAGED) return low_bits(lim + 1 - base);
   uint32_t bits;
   if (a.tree_mask) {
     const int f0 = base - it.cached;               // fresh row of the first bit
@@ -216,8 +218,30 @@ __device__ __forceinline__ uint32_t cache_visible(const AttnArgs &a, const ApIte
   return bits & pages;
 }
 
-// Positions in the ring's order K0 K1 V0 K2 V1 .. V[n-1] of an item of n tiles.
-__device__ __forceinline__ int ap_pos_k(int j) { return j ? 2 * j - 1 : 0; }
+// exp2(c v + mc) of 32 scores: P as 16 packed words, and its sum added to acc.
+template <bool F16>
+__device__ __forceinline__ void ap_weights(const float *v, float2 c2, float2 mc2, uint32_t *pk, float2 (&acc)[2]) {
+#pragma unroll
+  for (int e = 0; e < 16; e++) {
+    float2 t = ffma2(make_float2(v[2 * e], v[2 * e + 1]), c2, mc2);
+    t.x = at_exp2(t.x);
+    t.y = at_exp2(t.y);
+    acc[e & 1] = at_add2(acc[e & 1], t);
+    pk[e] = at_pack<F16>(t.x, t.y);
+  }
+}
+__device__ __forceinline__ float ap_max(const float (&v)[128]) {
+  float mx[4];
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    mx[q] = fmaxf(v[32 * q], v[32 * q + 1]);
+#pragma unroll
+    for (int e = 2; e < 32; e += 2) mx[q] = at_max3(mx[q], v[32 * q + e], v[32 * q + e + 1]);
+  }
+  return at_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+}
+
+// Position of V[j] in the ring order K0 K1 V0 K2 V1 .. V[n-1] of an item of n tiles.
 __device__ __forceinline__ int ap_pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
 
 template <int D, bool F16, bool PAGED>
@@ -246,10 +270,18 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       mbar_init(&s.sched_full[i], 1);
       mbar_init(&s.sched_empty[i], 11);            // 8 softmax warps, MMA warp, 2 helper warps
     }
-    for (int i = 0; i < 3; i++) mbar_init(&s.v_clean[i], 2);
+    for (int i = 0; i < 3; i++) {
+      mbar_init(&s.v_posted[0][i], 1);
+      mbar_init(&s.v_posted[1][i], 1);
+      mbar_init(&s.v_clean[i], 2);
+    }
     mbar_init(&s.v_next, 1);
     mbar_init(&s.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 32 * kApWTma) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.vmap)) : "memory");
   }
   if (warp == kApWMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
@@ -403,29 +435,18 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         float v[128];
 #pragma unroll
         for (int q = 0; q < 4; q++) at_ld32(ts + 32u * q, v + 32 * q);
-        at_wait_ld();
+        at_wait_ld(v);
         if (masked) {
-          if constexpr (PAGED) {
 #pragma unroll
-            for (int w = 0; w < 4; w++) {
-              const uint32_t bits = cache_visible(a, it, word, lim, tok0 + 32 * w, held, w);
+          for (int w = 0; w < 4; w++) {
+            const uint32_t bits = visible_bits<PAGED>(a, it, word, lim, tok0 + 32 * w, held, w);
+            if (__any_sync(kFull, bits != ~0u)) {
 #pragma unroll
               for (int e = 0; e < 32; e++) v[32 * w + e] = (bits >> e) & 1u ? v[32 * w + e] : -INFINITY;
             }
-          } else {
-            const int vis = lim - tok0;
-#pragma unroll
-            for (int q = 0; q < 128; q++) v[q] = q > vis ? -INFINITY : v[q];
           }
         }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          mx[q] = fmaxf(v[32 * q], v[32 * q + 1]);
-#pragma unroll
-          for (int e = 2; e < 32; e += 2) mx[q] = at_max3(mx[q], v[32 * q + e], v[32 * q + e + 1]);
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = ap_max(v);
         if (j == 0) {
           m = top;
         } else if (__any_sync(kFull, (top - m) * c > kApSlack)) {
@@ -443,7 +464,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           for (int q = 0; q < D / 32; q++) {
             float o[32];
             at_ld32(to + 32u * q, o);
-            at_wait_ld();
+            at_wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 32; e++) o[e] *= f;
             at_st32(to + 32u * q, o);
@@ -456,14 +477,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
 #pragma unroll
         for (int q = 0; q < 4; q++) {
           uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; e++) {
-            float2 t = ffma2(make_float2(v[32 * q + 2 * e], v[32 * q + 2 * e + 1]), c2, mc2);
-            t.x = at_exp2(t.x);
-            t.y = at_exp2(t.y);
-            sum[e & 1] = at_add2(sum[e & 1], t);
-            pk[e] = at_pack<F16>(t.x, t.y);
-          }
+          ap_weights<F16>(v + 32 * q, c2, mc2, pk, sum);
           at_st16(ts + 16u * q, pk);
         }
         l2 = at_add2(l2, at_add2(sum[0], sum[1]));
@@ -482,18 +496,15 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           break;
         }
         at_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int t = it.first + lim, hq = it.hk * a.group + x - dt * a.group;
         uint32_t anybad = 0;
 #pragma unroll
         for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
-        uint16_t *dst = a.out.p + (long long)t * a.out.row + (long long)hq * a.out.head;
+        if (anybad) {
 #pragma unroll 1
-        for (int q = 0; q < D / 32; q++) {
-          float o[32];
-          at_ld32(to + 32u * q, o);
-          at_wait_ld();
-          if (anybad) {
+          for (int q = 0; q < D / 32; q++) {
+            float o[32];
+            at_ld32(to + 32u * q, o);
+            at_wait_ld(o);
             for (int w = 0; w < 12; w++) {
               uint32_t bits = s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
               for (; bits; bits &= bits - 1) {
@@ -517,26 +528,63 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                 }
               }
             }
+            __syncwarp();
+            at_st32(to + 32u * q, o);
           }
-          if (PAGED && it.slot >= 0) {
-            // [element / 4][row]: the 32 rows of a warp side by side
-            float4 *part = p.part + ((size_t)it.slot * (D / 4) + 8 * q) * kApRows + (tid & 255);
+          at_wait_st();
+        }
+        if (PAGED && it.slot >= 0) {
+          // [element / 4][row]: the 32 rows of a warp side by side
+          float4 *part = p.part + (size_t)it.slot * (D / 4) * kApRows + (tid & 255);
+#pragma unroll 1
+          for (int q = 0; q < D / 32; q++) {
+            float o[32];
+            at_ld32(to + 32u * q, o);
+            at_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 8; e++) part[e * kApRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else if (real) {
+            for (int e = 0; e < 8; e++)
+              part[(8 * q + e) * kApRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        } else {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int hq = it.hk * a.group + x - dt * a.group;
+          if (a.lse && real)
+            a.lse[(size_t)(it.first + lim) * a.q_heads + hq] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+          // A lane's row at a time would touch 32 lines a store; with the
+          // fragment shape a quad holds 32 elements of a row (pairs 2 q4 of each
+          // 8), and a transpose within the quad gives each lane 16 bytes of 64.
+          const int qg = lane >> 2, q4 = lane & 3;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-              uint4 w;
-              w.x = at_pack<F16>(o[8 * e] * inv, o[8 * e + 1] * inv);
-              w.y = at_pack<F16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
-              w.z = at_pack<F16>(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
-              w.w = at_pack<F16>(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
-              *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * e) = w;
+          for (int rb = 0; rb < 2; rb++) {
+            float iv[2];
+            uint16_t *dst[2];
+            bool wr[2];
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+              const int rl = 16 * rb + 8 * z + qg, r = (ri & ~31) + rl;
+              iv[z] = __shfl_sync(kFull, inv, rl);
+              wr[z] = r < it.rows;
+              const int xr = it.g0 + r, dr = (xr * p.magic) >> 16;
+              dst[z] = a.out.p + (long long)(it.first + it.tok0 + dr) * a.out.row +
+                       (long long)(it.hk * a.group + xr - dr * a.group) * a.out.head + 8 * q4;
+            }
+#pragma unroll
+            for (int cb = 0; cb < D / 32; cb++) {
+              float o[16];
+              at_ld_frag(to + ((uint32_t)(16 * rb) << 16) + 32u * cb, o);
+              at_wait_ld(o);
+#pragma unroll
+              for (int z = 0; z < 2; z++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[e] = at_pack<F16>(o[4 * e + 2 * z] * iv[z], o[4 * e + 2 * z + 1] * iv[z]);
+                at_quad_transpose(w, q4);
+                if (wr[z]) *reinterpret_cast<uint4 *>(dst[z] + 32 * cb) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
           }
         }
         at_fence_before();
-        if (a.lse && real && it.slot < 0) a.lse[(size_t)t * a.q_heads + hq] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
@@ -590,7 +638,12 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
               ok = false;
               break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)kTB);
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)kTB);
+              // the scan may wait for this tile now: before, the barrier may still
+              // be in an earlier phase, which a wait cannot tell from this one
+              if (!isk && j - it.j0 >= it.m0) mbar_arrive(&s.v_posted[i & 1][j - it.j0 - it.m0]);
+            }
             if constexpr (PAGED) {
               __syncwarp();
               if (lane < kApTile >> a.page_shift)
@@ -619,95 +672,125 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       __syncwarp();
     } else if (warp == kApWMma) {
       // ---------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        constexpr uint32_t id_s = at_idesc(F16, kApTile, false), id_o = at_idesc(F16, D, true);
-        int base = 0;
-        uint32_t clean[3] = {0, 0, 0}, np[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-          if (ok && !mbar_wait_bounded(bar, parity)) {
-            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-            ok = false;
-          }
-          return ok;
-        };
-        auto wait_kv = [&](int pos) { return wait(&s.kv_full[pos % kSlots], (uint32_t)(pos / kSlots) & 1u); };
-        auto issue_s = [&](int h, uint32_t q, int pos) {
-          const int slot = pos % kSlots;
+      // The whole warp goes through the loop, so that what the instructions take
+      // (descriptors, tensor-memory columns) stays in uniform registers and costs
+      // one addition; one elected lane issues.
+      constexpr uint32_t id_s = at_idesc(F16, kApTile, false), id_o = at_idesc(F16, D, true);
+      const uint32_t tu = __shfl_sync(kFull, tb, 0);
+      const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring, kApTile * 128);
+      int slot = 0;                                // ring slot and phase of the next position
+      uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait_bounded(bar, parity)) {
+          if (lane == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+          ok = false;
+        }
+        ok = __all_sync(kFull, ok);
+        return ok;
+      };
+      // the next position of the ring: its slot, once it is full
+      auto take = [&]() {
+        const int at = slot;
+        wait(&s.kv_full[at], phase);
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        return at;
+      };
+      auto issue_s = [&](int h, int q, int at) {   // S of row tile h: Q of row tile q, K in slot `at`
+        const uint64_t da = dq0 + (uint64_t)(q * (kTB >> 4)), db = dk0 + (uint64_t)(at * (kTB >> 4));
+        if (at_elect()) {
 #pragma unroll
           for (int k = 0; k < D / 16; k++) {
-            const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32);
-            at_mma_ss(tb + 128u * h, at_desc(q + off, 16), at_desc(ring + slot * kTB + off, 16), id_s, k > 0);
+            const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32) >> 4;
+            at_mma_ss(tu + 128u * h, da + off, db + off, id_s, k > 0);
           }
           at_commit(&s.s_full[h]);
-        };
-        auto issue_o = [&](int h, int pos, bool add) {
-          const int slot = pos % kSlots;
+        }
+        __syncwarp();
+      };
+      auto issue_o = [&](int h, int at, bool add) {     // O of row tile h (+)= P V, V in slot `at`
+        const uint64_t db = dv0 + (uint64_t)(at * (kTB >> 4));
+        if (at_elect()) {
 #pragma unroll
           for (int k = 0; k < kApTile / 16; k++)
-            at_mma_ts(tb + 256u + 128u * h, tb + 128u * h + 8u * k, at_desc(ring + slot * kTB + 2048u * k, kApTile * 128),
-                      id_o, (uint32_t)(add || k > 0));
+            at_mma_ts(tu + 256u + 128u * h, tu + 128u * h + 8u * k, db + (uint64_t)(128u * k), id_o, (uint32_t)(add || k > 0));
           at_commit(&s.o_done[h]);
-        };
-        for (int i = 0; ok; i++) {
-          if (!wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
-          const ApItem it = s.item[i & 1];
-          if (it.b < 0) break;
-          const int n = it.n;
-          const bool twin = PAGED && it.twin;
-          const uint32_t q1 = twin ? q_smem : q_smem + kTB;
-          if (!wait(&s.q_full, (uint32_t)i & 1u) || !wait_kv(base)) break;
-          at_fence_after();
-          issue_s(0, q_smem, base);
-          if (!twin && it.n1 > 0) issue_s(1, q1, base);
-          at_commit(&s.kv_empty[base % kSlots]);
-          if (twin && n > 1) {
-            if (!wait_kv(base + 1)) break;
-            at_fence_after();
-            issue_s(1, q1, base + 1);
-            at_commit(&s.kv_empty[(base + 1) % kSlots]);
-          }
-          const int ahead = twin ? 2 : 1;          // the S issued with PV of tile j is that of tile j + ahead
-          if (n <= ahead) at_commit(&s.q_empty);
-          for (int j = 0; j < n; j++) {
-            const int pk = base + ap_pos_k(j + ahead), pv = base + ap_pos_v(j, n);
-            const bool next = j + ahead < n;
-            // in the order of the ring, but for K1 of a pair of row tiles
-            if (!twin && next && !wait_kv(pk)) break;
-            if (!wait_kv(pv)) break;
-            if (j >= it.m0) {
-              const int z = j - it.m0;             // 0, 1 or 2: a constant index in each case
-              const uint32_t ph = z == 0 ? clean[0]++ : (z == 1 ? clean[1]++ : clean[2]++);
-              if (!wait(&s.v_clean[z], ph & 1u)) break;
-            }
-            if (j + 1 == n) mbar_arrive(&s.v_next);   // the next item's scans may signal
-            if (twin && next && !wait_kv(pk)) break;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              if (twin ? (j & 1) == h : j < (h ? it.n1 : it.n0)) {
-                if (!wait(&s.p_full[h], np[h]++ & 1u)) break;
-                at_fence_after();
-                issue_o(h, pv, j >= ahead);
-                if (twin ? next : j + 1 < (h ? it.n1 : it.n0)) issue_s(h, h ? q1 : q_smem, pk);
-              }
-            }
-            if (!ok) break;
-            at_commit(&s.kv_empty[pv % kSlots]);
-            if (next) at_commit(&s.kv_empty[pk % kSlots]);
-            if (j + ahead + 1 == n) at_commit(&s.q_empty);
-          }
-          base += 2 * n;
-          mbar_arrive(&s.sched_empty[i & 1]);
         }
-        // every MMA issued has completed before tensor memory is released
-        at_commit(&s.drain);
-        mbar_wait_bounded(&s.drain, 0u);
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t *bar) {
+        if (at_elect()) at_commit(bar);
+        __syncwarp();
+      };
+      for (int i = 0; ok; i++) {
+        if (!wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+        const ApItem &im = s.item[i & 1];
+        if (__shfl_sync(kFull, im.b, 0) < 0) break;
+        const int n = __shfl_sync(kFull, im.n, 0), m0 = __shfl_sync(kFull, im.m0, 0);
+        const int n0 = __shfl_sync(kFull, im.n0, 0), n1 = __shfl_sync(kFull, im.n1, 0);
+        const bool twin = PAGED && __shfl_sync(kFull, im.twin, 0);
+        if (!wait(&s.q_full, (uint32_t)i & 1u)) break;
+        const int k0 = take();
+        if (!ok) break;
+        at_fence_after();
+        issue_s(0, 0, k0);
+        if (!twin && n1 > 0) issue_s(1, 1, k0);
+        commit(&s.kv_empty[k0]);
+        int kn = 0;                                // slot of the K that goes with PV of tile j
+        if (n > 1) {
+          kn = take();
+          if (!ok) break;
+          if (twin) {
+            at_fence_after();
+            issue_s(1, 0, kn);
+            commit(&s.kv_empty[kn]);
+          }
+        }
+        const int ahead = twin ? 2 : 1;            // the S issued with PV of tile j is that of tile j + ahead
+        if (n <= ahead) commit(&s.q_empty);
+        // ring order: K0 K1 V0 K2 V1 ..; of two row tiles K[j + 1] is taken before V[j], of twins after it
+        for (int j = 0; j < n; j++) {
+          const bool next = j + ahead < n;
+          if (!twin && j > 0 && next) kn = take();
+          const int v = take();
+          if (twin && next) kn = take();
+          if (j >= m0) {
+            const int z = j - m0;                  // 0, 1 or 2; a phase bit each
+            if (!wait(&s.v_clean[z], (clean >> z) & 1u)) break;
+            clean ^= 1u << z;
+          }
+          if (j + 1 == n && lane == 0) mbar_arrive(&s.v_next);   // the next item's scans may signal
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            if (twin ? (j & 1) == h : j < (h ? n1 : n0)) {
+              uint32_t &np = h ? np1 : np0;
+              if (!wait(&s.p_full[h], np)) break;
+              np ^= 1u;
+              at_fence_after();
+              issue_o(h, v, j >= ahead);
+              if (twin ? next : j + 1 < (h ? n1 : n0)) issue_s(h, twin ? 0 : h, kn);
+            }
+          }
+          if (!ok) break;
+          commit(&s.kv_empty[v]);
+          if (next) commit(&s.kv_empty[kn]);
+          if (j + ahead + 1 == n) commit(&s.q_empty);
+        }
+        if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
+      // every MMA issued has completed before tensor memory is released
+      commit(&s.drain);
+      mbar_wait_bounded(&s.drain, 0u);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- Q rows, and the scan of masked tiles' v
       const int ht = tid - 32 * kApWHelp;
       int base = 0;
+      uint32_t posted[3] = {0u, 0u, 0u};
       bool ok = true;
       for (int i = 0; ok; i++) {
         if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
@@ -717,16 +800,28 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         if (lane < 12) s.bad[i & 1][warp - kApWHelp][lane >> 2][lane & 3] = 0u;
         __syncwarp();
         if (i > 0 && !mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u)) break;
-        constexpr int kChunks = D / 8;
-        const int ch = ht % kChunks, top = it.rows > kApTile ? kApRows : kApTile;
+        // a thread copies 16-byte piece `ch` of every kStep-th row; the row's token
+        // and head follow by addition
+        constexpr int kChunks = D / 8, kStep = 64 / kChunks;
+        const int ch = ht % kChunks, r0 = ht / kChunks, top = it.rows > kApTile ? kApRows : kApTile;
+        const int dtok = (kStep * p.magic) >> 16, dg = kStep - dtok * a.group;
+        const long long adv = dtok * a.q.row + dg * a.q.head, wrap = a.q.row - a.group * a.q.head;
+        const int x0q = it.g0 + r0, t0q = (x0q * p.magic) >> 16;
+        int gq = x0q - t0q * a.group;
+        const uint16_t *src = a.q.p + (long long)(it.first + it.tok0 + t0q) * a.q.row +
+                              (long long)(it.hk * a.group + gq) * a.q.head + 8 * ch;
         const uint32_t qd = q_smem + (uint32_t)(ch >> 3) * (kApTile * 128);
-        for (int r = ht / kChunks; r < top; r += 64 / kChunks) {
-          const int x = it.g0 + r, dt = (x * p.magic) >> 16;
-          const uint16_t *src = a.q.p + (long long)(it.first + it.tok0 + dt) * a.q.row +
-                                (long long)(it.hk * a.group + x - dt * a.group) * a.q.head + 8 * ch;
+#pragma unroll 4
+        for (int r = r0; r < top; r += kStep) {
           const int rr = r & (kApTile - 1);
           at_cp16(qd + (r >= kApTile ? kTB : 0) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), r < it.rows ? src : a.q.p,
                   r < it.rows);
+          src += adv;
+          gq += dg;
+          if (gq >= a.group) {
+            gq -= a.group;
+            src += wrap;
+          }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         at_fence_async();
@@ -735,11 +830,16 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         // never a phase ahead of its reader
         if (i > 0 && !mbar_wait_bounded(&s.v_next, (uint32_t)(i - 1) & 1u)) break;
         for (int j = it.m0; j < n; j++) {
-          const int pv = base + ap_pos_v(j, n), slot = pv % kSlots;
-          if (!mbar_wait_bounded(&s.kv_full[slot], (uint32_t)(pv / kSlots) & 1u)) {
+          const int pv = base + ap_pos_v(j, n), slot = pv % kSlots, z = j - it.m0;
+          const uint32_t ph = z == 0 ? posted[0] : (z == 1 ? posted[1] : posted[2]);   // by item parity: bit i & 1
+          if (!mbar_wait_bounded(&s.v_posted[i & 1][z], (ph >> (i & 1)) & 1u) ||
+              !mbar_wait_bounded(&s.kv_full[slot], (uint32_t)(pv / kSlots) & 1u)) {
             ok = false;
             break;
           }
+          if (z == 0) posted[0] ^= 1u << (i & 1);
+          else if (z == 1) posted[1] ^= 1u << (i & 1);
+          else posted[2] ^= 1u << (i & 1);
           uint8_t *tile = generic0 + 2 * kTB + slot * kTB;
           const int r0 = max(0, it.all - (it.j0 + j) * kApTile);      // earlier tokens are seen by every row
           for (int hf = 0; hf < kHalves; hf++)

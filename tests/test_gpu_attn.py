@@ -164,6 +164,18 @@ def test_prompt_large_scores():
     ref.check(out, lse, prompt_ref(q, k, v, [n], d ** -0.5))
 
 
+@pytest.mark.parametrize("hk,g,d,lengths", [(1, 12, 64, [1000, 7]), (2, 8, 64, [1500]), (1, 3, 128, [900, 300])])
+def test_prompt_fresh_data_every_call(hk, g, d, lengths):
+    """Other values in every call: what an earlier call left in shared memory is of no use.  The key tiles of the long
+    requests go round the ring more than once before their masked tiles come."""
+    T, dt = sum(lengths), torch.float16
+    attn = moe.Attention(hk * g, hk, d, 16, 1, 1, dt)
+    for rep in range(8):
+        q, k, v = (randn((T, h, d), dt, 50 + 3 * rep + i, 1.5 if i == 0 else 1.0) for i, h in enumerate((hk * g, hk, hk)))
+        want = prompt_ref(q, k, v, lengths, d ** -0.5)
+        ref.check(*run_prompt(attn, q, k, v, lengths), want, f"call {rep}")
+
+
 def test_prompt_scale_and_slope():
     """A small softmax_scale: near-uniform weights; v of large magnitude."""
     d, n, dt = 64, 333, torch.float16
