@@ -51,7 +51,7 @@ struct AttnArgs {
 };
 // First 256 bytes of the workspace: zero between calls, but for the flags.
 constexpr int kAttnCtrlBytes = 256;
-constexpr int kAttnCtrlNext = 0, kAttnCtrlDone = 1, kAttnCtrlFlags = 2, kAttnCtrlItems = 3;   // ints
+constexpr int kAttnCtrlNext = 0, kAttnCtrlDone = 1, kAttnCtrlFlags = 2;   // ints
 
 // Byte offsets of moe_attn_tree's workspace (after the control words): that of
 // the calls with many rows per request, and all of it.
@@ -64,11 +64,11 @@ struct AttnTreeWs {
 };
 // Opt-in shared memory of the tcgen05 kernels (idempotent).
 cudaError_t attn_wide_setup(int head_dim, int f16);
-AttnWideWs attn_wide_ws(size_t off, int group, int kv_heads, int head_dim, int B, int T, int num_sms);
+AttnWideWs attn_wide_ws(size_t off, int head_dim, int num_sms);
 cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaStream_t stream);
 cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWideWs &w, int num_sms, cudaStream_t stream);
 
-AttnTreeWs attn_tree_ws(int group, int kv_heads, int head_dim, int B, int T, int num_sms);
+AttnTreeWs attn_tree_ws(int head_dim, int num_sms);
 cudaError_t attn_tree_setup(int head_dim, int f16);
 cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream);
 

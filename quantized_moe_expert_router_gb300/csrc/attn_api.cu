@@ -64,9 +64,7 @@ AttnArgs attn_args(const moe_attn &L, int B, int T) {
   return a;
 }
 
-size_t attn_ws_bytes(const moe_attn &L, int B, int T) {
-  return attn_tree_ws(L.cfg.q_heads / L.cfg.kv_heads, L.cfg.kv_heads, L.cfg.head_dim, B, T, L.num_sms).total;
-}
+size_t attn_ws_bytes(const moe_attn &L) { return attn_tree_ws(L.cfg.head_dim, L.num_sms).total; }
 
 }  // namespace
 
@@ -110,7 +108,7 @@ moe_status moe_attn_destroy(moe_attn_t attn) {
 moe_status moe_attn_workspace_bytes(moe_attn_t attn, int num_requests, int num_rows, size_t *bytes) {
   if (!attn || !bytes || !counts_ok(num_requests, num_rows)) return MOE_ERR_INVALID_ARG;
   if (num_requests > MOE_ATTN_MAX_REQUESTS || num_rows > MOE_ATTN_MAX_ROWS) return MOE_ERR_UNSUPPORTED_SHAPE;
-  *bytes = attn_ws_bytes(*attn, num_requests, num_rows);
+  *bytes = attn_ws_bytes(*attn);
   return MOE_OK;
 }
 
@@ -180,7 +178,7 @@ moe_status moe_attn_prompt(moe_attn_t attn, int num_requests, int num_rows, cons
       !row_view(v, num_rows, a.kv_heads, a.head_dim, &a.v) || !row_view(out, num_rows, a.q_heads, a.head_dim, &a.out) ||
       !words(cu) || !given(ws) || !lse_ok(lse))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < attn_ws_bytes(*attn, num_requests, num_rows)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < attn_ws_bytes(*attn)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   a.cu = cu;
   a.lse = lse;
   DeviceGuard g(attn->device);
@@ -200,7 +198,7 @@ moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const 
       !words(cu) || !words(cached) || !words(block_table) || !given(k_cache) || !given(v_cache) || !given(ws) ||
       (tree_mask && !aligned8(tree_mask)) || !lse_ok(lse))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < attn_ws_bytes(*attn, num_requests, num_rows)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < attn_ws_bytes(*attn)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   a.cu = cu;
   a.cached = cached;
   a.block_table = block_table;

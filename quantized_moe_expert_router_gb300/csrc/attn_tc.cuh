@@ -176,6 +176,103 @@ __device__ __forceinline__ float at_value(uint16_t v) {
   else return __uint_as_float((uint32_t)v << 16);
 }
 
+// x / d for 0 <= x, 0 < d: the 64-bit division is a long software routine.
+__device__ __forceinline__ long long at_div(long long x, long long d) {
+  return (x | d) >> 32 ? x / d : (long long)((uint32_t)x / (uint32_t)d);
+}
+
+// The share of a CTA in the line of units (chunks or key tiles) of all items.
+// work[b]: units of the requests before b; request b has items(b) items of
+// nch(b) units each.  Two ways to cut the line:
+//   parts   every item in equal parts of `len` units, a CTA each, when there are
+//           CTAs enough for a `len` of at most `extra` units above the mean: a CTA
+//           then sets up, joins and stores one part only;
+//   even    CTA i takes units [total i / ctas, total (i + 1) / ctas), whatever
+//           items they belong to: long and short items together, many items.
+struct AtShare {
+  long long x0, x1;            // this CTA's units
+  long long per, rem;          // even: units of a CTA, and CTAs with one more
+  int ctas;
+  int c0, c1;                  // parts (len > 0): the CTAs of the item's first and last part
+  int len;
+  __device__ __forceinline__ long long start(long long i) const { return i * per + min(i, rem); }
+  __device__ __forceinline__ int cta_of(long long x) const {
+    const long long big = rem * (per + 1);
+    return (int)(x < big ? at_div(x, per + 1) : rem + at_div(x - big, per));
+  }
+  // CTAs that hold the first and the last unit of an item of this CTA
+  __device__ __forceinline__ void ctas_of(long long item0, long long last, int &a, int &b) const {
+    if (len) {
+      a = c0;
+      b = c1;
+    } else {
+      a = item0 >= x0 ? (int)blockIdx.x : cta_of(item0);
+      b = last < x1 ? (int)blockIdx.x : cta_of(last);
+    }
+  }
+  // where CTA a, which holds the item's first unit, keeps its part: a CTA's first part is in its slot 0
+  __device__ __forceinline__ int first_slot(int a, long long item0) const { return 2 * a + (!len && start(a) < item0); }
+};
+// All threads of the CTA (NW warps) call this; `scratch` is NW x 32 ints.
+template <int NW, typename Items, typename Nch>
+__device__ __forceinline__ AtShare at_share(const long long *work, int B, long long total, int nitems, int min_len, int extra,
+                                            int (*scratch)[32], Items items, Nch nch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grid = gridDim.x, me = blockIdx.x;
+  AtShare r;
+  r.x0 = r.x1 = 0;
+  r.c0 = r.c1 = r.len = 0;
+  r.ctas = (int)min((total + min_len - 1) / min_len, (long long)grid);
+  if (total == 0) return r;
+  const long long mean = at_div(total + grid - 1, grid);
+  if (nitems <= grid && mean < (1 << 28)) {
+    // the smallest len of 32 candidates that does with the CTAs there are
+    const int len0 = max(min_len, (int)mean), step = (extra + 30) / 31, len = len0 + lane * step;
+    int parts = 0;
+    for (int b = warp; b < B; b += NW) parts += items(b) * ((nch(b) + len - 1) / len);
+    scratch[warp][lane] = parts;
+    __syncthreads();
+    parts = 0;
+#pragma unroll
+    for (int w = 0; w < NW; w++) parts += scratch[w][lane];
+    const unsigned fits = __ballot_sync(kFull, parts <= grid);
+    if (fits) {
+      r.len = len0 + (__ffs(fits) - 1) * step;
+      int before = 0;
+      for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane, n = b < B ? nch(b) : 1, per_item = (n + r.len - 1) / r.len;
+        const int v = b < B ? items(b) * per_item : 0;
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(kFull, incl, o);
+          if (lane >= o) incl += t;
+        }
+        const int at = me - before - (incl - v);   // place among the request's parts
+        const unsigned mine = __ballot_sync(kFull, at >= 0 && at < v);
+        if (mine) {
+          const int src = __ffs(mine) - 1, pi = __shfl_sync(kFull, per_item, src), place = __shfl_sync(kFull, at, src);
+          const int nn = __shfl_sync(kFull, n, src), item = place / pi, k = place - item * pi;
+          const long long item0 = work[b0 + src] + (long long)item * nn;
+          r.x0 = item0 + (long long)k * r.len;
+          r.x1 = min(r.x0 + r.len, item0 + nn);
+          r.c0 = me - k;
+          r.c1 = r.c0 + pi - 1;
+          break;
+        }
+        before += __shfl_sync(kFull, incl, 31);
+      }
+      return r;
+    }
+  }
+  r.per = at_div(total, r.ctas);
+  r.rem = total - r.per * r.ctas;
+  if (me < r.ctas) {
+    r.x0 = r.start(me);
+    r.x1 = r.start(me + 1);
+  }
+  return r;
+}
+
 using AttnMapEncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
 inline AttnMapEncodeFn attn_map_encoder() {
   static AttnMapEncodeFn fn = []() -> AttnMapEncodeFn {

@@ -35,6 +35,7 @@ constexpr int kAtThreads = 256, kAtWarps = 8;
 constexpr int kAtStages = 2;
 constexpr int kAtStageBytes = 8192;
 constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least: one per warp costs no more time than one
+constexpr int kAtExtra = 31;                     // chunks above the mean that are cheaper than a second part in a CTA
 constexpr int kAtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kAtSlack = 8.f;
 constexpr int kAtMostRows = 32;                  // mean rows of a request and kv head; more go to attn_wide.cu
@@ -54,6 +55,8 @@ struct AtSmem {
   long long work[kAtMaxB + 1]; // chunks of the requests before
   int first[kAtMaxB], n[kAtMaxB], cached[kAtMaxB];   // first packed row, fresh rows, cached tokens
   long long wsum[kAtWarps];
+  int wsum2[kAtWarps];
+  int cand[kAtWarps][32];
   float2 stat[kAtWarps][32];   // (m, l) by warp and row
   int last;
 };
@@ -91,11 +94,6 @@ __device__ __forceinline__ void at_ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// x / d for 0 <= x, 0 < d: the 64-bit division is a long software routine.
-__device__ __forceinline__ long long at_div(long long x, long long d) {
-  return (x | d) >> 32 ? x / d : (long long)((uint32_t)x / (uint32_t)d);
-}
-
 // A place in the line of chunks: request, kv head, row tile, chunk; innermost
 // last, so that the row tiles of a kv head read the same keys one after another.
 struct AtPos {
@@ -164,9 +162,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
   }
   // the line of chunks, every CTA alike
   long long total = 0;
+  int nitems = 0;
   for (int b0 = 0; b0 < a.B; b0 += kAtThreads) {
     const int b = b0 + tid;
     long long v = 0;
+    int items = 0;
     if (b < a.B) {
       const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1), cached = max(__ldg(a.cached + b), 0);
       s.first[b] = lo;
@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
       AtPos q;
       q.b = b;
       at_request<kTok, kRows>(s, a, q);
-      v = (long long)q.tiles * a.kv_heads * q.nch;
+      items = q.tiles * a.kv_heads;
+      v = (long long)items * q.nch;
     }
     long long incl = v;
 #pragma unroll
@@ -183,27 +184,38 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
       const long long u = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += u;
     }
-    if (lane == 31) s.wsum[warp] = incl;
+    items = __reduce_add_sync(kFull, items);
+    if (lane == 31) {
+      s.wsum[warp] = incl;
+      s.wsum2[warp] = items;
+    }
     __syncthreads();
     long long at = total;
 #pragma unroll
     for (int w = 0; w < kAtWarps; w++) {
       at += w < warp ? s.wsum[w] : 0;
       total += s.wsum[w];
+      nitems += s.wsum2[w];
     }
     if (b < a.B) s.work[b] = at + incl - v;
     __syncthreads();
   }
-  // CTA i of `ctas` takes chunks start(i) .. start(i + 1): per or per + 1 of them
-  const int ctas = (int)min((total + kAtMinChunks - 1) / kAtMinChunks, (long long)gridDim.x);
-  if ((int)blockIdx.x >= ctas) return;
-  const long long per = at_div(total, ctas), rem = total - per * ctas;
-  auto start = [&](long long i) { return i * per + min(i, rem); };
-  auto cta_of = [&](long long x) {
-    const long long big = rem * (per + 1);
-    return (int)(x < big ? at_div(x, per + 1) : rem + at_div(x - big, per));
-  };
-  const long long x0 = start(blockIdx.x), x1 = start(blockIdx.x + 1);
+  const AtShare share = at_share<kAtWarps>(
+      s.work, a.B, total, nitems, kAtMinChunks, kAtExtra, s.cand,
+      [&](int b) {
+        AtPos q;
+        q.b = b;
+        at_request<kTok, kRows>(s, a, q);
+        return q.tiles * a.kv_heads;
+      },
+      [&](int b) {
+        AtPos q;
+        q.b = b;
+        at_request<kTok, kRows>(s, a, q);
+        return q.nch;
+      });
+  const long long x0 = share.x0, x1 = share.x1;
+  if (x0 >= x1) return;
 
   const float c = a.scale * 1.44269504088896340736f;
   bool ok = true;                                  // no wait of this warp has run out
@@ -461,7 +473,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
       if (ok && xp < x1) issue();
     }
 
-    // ------------------------------------------------------------ the warps join, in warp order
+    // ------------------------------------------------------------ join
+    // Eight sources of 16 rows at a time, in shared memory: first the warps, in
+    // warp order; then, in the CTA that finishes the item's last part, the
+    // parts in the order of the context.  One loop for both, so that the second
+    // runs instructions that are at hand.
     const bool entire = xs == item0 && xe == item0 + nch;
     const int slot = 2 * blockIdx.x + (nparts > 0);
     nparts++;
@@ -474,41 +490,77 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
         v += __shfl_xor_sync(kFull, v, 2);
         if (q4 == 0) s.stat[warp][16 * mt + g + 8 * z] = make_float2(m[mt][z], v);
       }
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++) {
-      float *mine = join + warp * (16 * G::kLd);
-#pragma unroll
-      for (int d = 0; d < D / 8; d++)
-#pragma unroll
-        for (int z = 0; z < 2; z++)
-          *reinterpret_cast<float2 *>(mine + (g + 8 * z) * G::kLd + 8 * d + 2 * q4) =
-              make_float2(o[mt][d][2 * z], o[mt][d][2 * z + 1]);
-      __syncthreads();
-      // 16 threads a row, D / 16 elements each
-      constexpr int N = D / 16;
+    int c0 = 0, c1 = 0, slot0 = 0;                 // the CTAs that hold the item's first and last chunk
+    bool parts = false;
+    for (int mt = 0, k0 = 0;;) {
+      constexpr int N = D / 16;                    // 16 threads a row, N elements each
       const int r = tid >> 4, col = (tid & 15) * N, r32 = 16 * mt + r;
-      if (r32 < rows) {
-        float top = -INFINITY, sum = 0.f, acc[N];
+      float top = -INFINITY, sum = 0.f, acc[N];
 #pragma unroll
-        for (int e = 0; e < N; e++) acc[e] = 0.f;
+      for (int e = 0; e < N; e++) acc[e] = 0.f;
+      for (;;) {
+        float *mine = join + warp * (16 * G::kLd);
+        if (!parts) {
 #pragma unroll
-        for (int w = 0; w < kAtWarps; w++) top = fmaxf(top, s.stat[w][r32].x);
+          for (int q = 0; q < MT; q++)
+            if (q == mt)
 #pragma unroll
-        for (int w = 0; w < kAtWarps; w++) {
-          const float2 st = s.stat[w][r32];
-          const float f = st.x == -INFINITY ? 0.f : at_exp2((st.x - top) * c);
-          sum = fmaf(st.y, f, sum);
-          const float4 *src = reinterpret_cast<const float4 *>(join + w * (16 * G::kLd) + r * G::kLd + col);
+              for (int e = 0; e < D / 8; e++)
 #pragma unroll
-          for (int e = 0; e < N / 4; e++) {
-            const float4 u = src[e];
-            acc[4 * e] = fmaf(u.x, f, acc[4 * e]);
-            acc[4 * e + 1] = fmaf(u.y, f, acc[4 * e + 1]);
-            acc[4 * e + 2] = fmaf(u.z, f, acc[4 * e + 2]);
-            acc[4 * e + 3] = fmaf(u.w, f, acc[4 * e + 3]);
+                for (int z = 0; z < 2; z++)
+                  *reinterpret_cast<float2 *>(mine + (g + 8 * z) * G::kLd + 8 * e + 2 * q4) =
+                      make_float2(o[q][e][2 * z], o[q][e][2 * z + 1]);
+        } else {
+          const int k = k0 + warp;
+          const size_t at = (size_t)(k == c0 ? slot0 : 2 * k) * kRows + 16 * mt;
+          const int rr = min(16, rows - 16 * mt);
+          if (lane < 16) {
+            float2 st = make_float2(-INFINITY, 0.f);
+            if (k <= c1 && lane < rr) st = __ldcg(p.stat + at + lane);
+            s.stat[warp][16 * mt + lane] = st;
+          }
+          if (k <= c1) {
+            constexpr int kPer = 128 / D;          // rows of a warp's load
+#pragma unroll 4
+            for (int q = lane / (D / 4); q < rr; q += kPer) {
+              const int e = 4 * (lane % (D / 4));
+              *reinterpret_cast<float4 *>(mine + q * G::kLd + e) =
+                  __ldcg(reinterpret_cast<const float4 *>(p.part + (at + q) * D + e));
+            }
           }
         }
-        if (entire) {
+        __syncthreads();
+        if (r32 < rows) {
+          float t1 = top;
+#pragma unroll
+          for (int w = 0; w < kAtWarps; w++) t1 = fmaxf(t1, s.stat[w][r32].x);
+          const float f0 = top == -INFINITY ? 1.f : at_exp2((top - t1) * c);
+          top = t1;
+          sum *= f0;
+#pragma unroll
+          for (int e = 0; e < N; e++) acc[e] *= f0;
+#pragma unroll 2
+          for (int w = 0; w < kAtWarps; w++) {
+            const float2 st = s.stat[w][r32];
+            if (st.y == 0.f) continue;             // a source in which the row sees nothing, or none
+            const float f = at_exp2((st.x - top) * c);
+            sum = fmaf(st.y, f, sum);
+            const float4 *src = reinterpret_cast<const float4 *>(join + w * (16 * G::kLd) + r * G::kLd + col);
+#pragma unroll
+            for (int e = 0; e < N / 4; e++) {
+              const float4 u = src[e];
+              acc[4 * e] = fmaf(u.x, f, acc[4 * e]);
+              acc[4 * e + 1] = fmaf(u.y, f, acc[4 * e + 1]);
+              acc[4 * e + 2] = fmaf(u.z, f, acc[4 * e + 2]);
+              acc[4 * e + 3] = fmaf(u.w, f, acc[4 * e + 3]);
+            }
+          }
+        }
+        if (!parts || (k0 += kAtWarps) > c1) break;
+        __syncthreads();                           // the buffer is read
+      }
+      if (r32 < rows) {
+        if (parts || entire) {
           emit(r32, col, top, sum, acc);
         } else {
           float4 *dst = reinterpret_cast<float4 *>(p.part + ((size_t)slot * kRows + r32) * D + col);
@@ -518,67 +570,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
         }
       }
       __syncthreads();
-    }
-    if (!entire) {
-      // the CTAs that hold the item's chunks; the last to arrive joins their
-      // parts.  A CTA's first part is in its slot 0, and CTA c0's is not its
-      // first unless the item starts with the CTA's range.
-      const int c0 = xs == item0 ? (int)blockIdx.x : cta_of(item0);
-      const int c1 = xe == item0 + nch ? (int)blockIdx.x : cta_of(item0 + nch - 1);
-      const int slot0 = 2 * c0 + (start(c0) < item0);
+      if (++mt < MT) {
+        k0 = c0;
+        continue;
+      }
+      if (parts || entire) break;
+      share.ctas_of(item0, item0 + nch - 1, c0, c1);
+      slot0 = share.first_slot(c0, item0);
       if (tid == 0) {
-        // release: the CTA's parts, ordered before by the barrier; acquire: the others'
+        // release: the CTA's part, ordered before by the barrier; acquire: the others'
         int got;
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(got) : "l"(p.tickets + c0) : "memory");
         s.last = got == c1 - c0;
         if (got == c1 - c0) p.tickets[c0] = 0;
       }
       __syncthreads();
-      if (s.last) {
-        constexpr int N = D / 16;
-        const int col = (tid & 15) * N;
-        for (int r = tid >> 4; r < kRows; r += 16) {
-          const bool real = r < rows;
-          // the 16 threads of a row look at a part's statistics each
-          float top = -INFINITY;
-          for (int k = c0 + (tid & 15); k <= c1; k += 16)
-            if (real) top = fmaxf(top, __ldcg(&p.stat[(size_t)(k == c0 ? slot0 : 2 * k) * kRows + r].x));
-#pragma unroll
-          for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-          if (!real) continue;
-          float sum = 0.f, acc[N];
-#pragma unroll
-          for (int e = 0; e < N; e++) acc[e] = 0.f;
-          // eight parts at a time, so that their loads wait together
-          for (int k0 = c0; k0 <= c1; k0 += 8) {
-            float2 st[8];
-            float4 u[8][N / 4];
-#pragma unroll
-            for (int z = 0; z < 8; z++) {
-              const int k = min(k0 + z, c1);
-              const size_t at = (size_t)(k == c0 ? slot0 : 2 * k) * kRows + r;
-              st[z] = __ldcg(&p.stat[at]);
-#pragma unroll
-              for (int e = 0; e < N / 4; e++) u[z][e] = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + col) + e);
-            }
-#pragma unroll
-            for (int z = 0; z < 8; z++) {
-              if (k0 + z > c1) break;
-              const float f = st[z].x == -INFINITY ? 0.f : at_exp2((st[z].x - top) * c);
-              sum = fmaf(st[z].y, f, sum);
-#pragma unroll
-              for (int e = 0; e < N / 4; e++) {
-                acc[4 * e] = fmaf(u[z][e].x, f, acc[4 * e]);
-                acc[4 * e + 1] = fmaf(u[z][e].y, f, acc[4 * e + 1]);
-                acc[4 * e + 2] = fmaf(u[z][e].z, f, acc[4 * e + 2]);
-                acc[4 * e + 3] = fmaf(u[z][e].w, f, acc[4 * e + 3]);
-              }
-            }
-          }
-          emit(r, col, top, sum, acc);
-        }
-        __syncthreads();
-      }
+      if (!s.last) break;
+      parts = true;
+      mt = 0;
+      k0 = c0;
     }
     xs = xe;
     if (xs < x1) at_advance<kTok, kRows>(s, a, sp, nch - sp.chunk);
@@ -611,7 +621,7 @@ cudaError_t attn_tree_setup(int head_dim, int f16) {
   return cudaSuccess;
 }
 
-AttnTreeWs attn_tree_ws(int group, int kv_heads, int head_dim, int B, int T, int num_sms) {
+AttnTreeWs attn_tree_ws(int head_dim, int num_sms) {
   AttnTreeWs w;
   size_t off = kAttnCtrlBytes;
   auto take = [&](size_t bytes) {
@@ -622,13 +632,13 @@ AttnTreeWs attn_tree_ws(int group, int kv_heads, int head_dim, int B, int T, int
   w.tickets = take(4 * (size_t)num_sms);
   w.stat = take(8 * (size_t)(2 * num_sms) * 32);
   w.part = take(4 * (size_t)(2 * num_sms) * 32 * head_dim);
-  w.wide = attn_wide_ws(off, group, kv_heads, head_dim, B, T, num_sms);
+  w.wide = attn_wide_ws(off, head_dim, num_sms);
   w.total = w.wide.total;
   return w;
 }
 
 cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream) {
-  const AttnTreeWs w = attn_tree_ws(a.group, a.kv_heads, a.head_dim, a.B, a.T, num_sms);
+  const AttnTreeWs w = attn_tree_ws(a.head_dim, num_sms);
   const long long rows = ((long long)a.T * a.group + a.B - 1) / a.B;   // of a request and kv head, on the average
   if (rows > kAtMostRows) return launch_attn_wide_tree(a, ws, w.wide, num_sms, stream);
   AtArgs p;

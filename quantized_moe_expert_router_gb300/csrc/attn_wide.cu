@@ -26,8 +26,8 @@
 //                   into a ring, in the order K0 K1 V0 K2 V1 ..; takes the items
 //   warp 9          MMA issue: S of the next tile is issued with PV of this one,
 //                   so one row tile's softmax runs while the other's MMAs do
-//   warps 10-11     Q rows into swizzled shared memory (cp.async, zero for rows
-//                   past the end); the scan described below
+//   warps 10-11     Q rows into swizzled shared memory (tensor-map boxes where the
+//                   group divides a row tile, else cp.async); the scan below
 // Tensor memory: S0, S1 (128 columns each, P over their first 64), O0, O1.
 //
 // A tile past the last token that all rows see holds keys that some rows, or
@@ -39,8 +39,8 @@
 // Prompts: items are taken from a counter, those with most key tiles first; an
 // item's length depends on its row tile alone, so with the requests ranked by
 // length the idx-th longest item has a closed form (prompt_item).
-// Cache: the key tiles of all items stand in one line and every CTA takes an
-// equal range of it.  A part of an item goes to the workspace (fp32 O, m, l) and
+// Cache: the key tiles of all items stand in one line that the CTAs share
+// (at_share).  A part of an item goes to the workspace (fp32 O, m, l) and
 // attn_join_kernel joins the parts in the order of the context.  In a part of
 // at most 128 rows the two row tiles are the same rows over alternate key
 // tiles, so that the softmax of one still runs beside the MMAs of the other.
@@ -61,6 +61,7 @@ constexpr int kApWTma = 8, kApWMma = 9, kApWHelp = 10;
 constexpr int kApMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kApSlack = 8.f;                  // log2 of the largest P
 constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache)
+constexpr int kApExtra = 6;                      // key tiles above the mean that are cheaper than a second part in a CTA
 
 template <int D>
 struct ApGeom {
@@ -72,11 +73,14 @@ struct ApGeom {
 struct ApArgs {
   CUtensorMap kmap, vmap;      // prompt: (64, 1, 128) boxes over [rows][kv_heads][D]; cache: (64, page, 1, 1) over
                                // [pages][kv_heads][page][D]; 128-byte swizzle
+  CUtensorMap qmap;            // (64, group, 128 / group) boxes over [rows][q_heads][D], for groups that divide 128
   AttnArgs a;
   int *ctrl;                   // workspace control words
   int magic;                   // ceil(2^16 / group)
+  int q_boxes;                 // qmap is there
   // cache only
-  int4 *desc;                  // per item: (first, hk, row0, rows), (first CTA, last CTA, its slot, twin)
+  int4 *desc;                  // per CTA, of the item whose first part it holds and others the rest:
+                               // (first, hk, row0, rows), (first CTA, last CTA, its slot, twin)
   float4 *part;                // [2 * grid][D / 4][256]  O of a part
   float2 *stat;                // [2 * grid][256]         (m, l)
 };
@@ -110,12 +114,22 @@ struct ApSmem {
     };
     struct {                   // cache: the line of key tiles
       long long work[kApMaxB + 1];   // tiles of the requests before
-      int items[kApMaxB];      // items of the requests before
-      int nch[kApMaxB];        // key tiles of an item's context
+      int first[kApMaxB], n[kApMaxB], cached[kApMaxB];   // first packed row, fresh rows, cached tokens
+      int cand[kApThreads / 32][32];
     };
   };
   long long wsum2[kApThreads / 32];
 };
+
+// Of a request of n fresh rows over the cache: items of a kv head, and key
+// tiles that its rows may see.
+__device__ __forceinline__ int cache_tiles(const AttnArgs &a, int n) {
+  return (int)(((long long)n * a.group + kApRows - 1) / kApRows);
+}
+__device__ __forceinline__ int cache_nch(const AttnArgs &a, int n, int cached) {
+  const long long ctx = min((long long)cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n), (long long)a.max_pages << a.page_shift);
+  return (int)((ctx + kApTile - 1) / kApTile);
+}
 
 // The rows of an item, given its row0.
 __device__ __forceinline__ void ap_rows(const ApArgs &p, ApItem &it, int n_fresh) {
@@ -151,11 +165,10 @@ __device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, in
   it.slot = -1;
 }
 
-// The part of an item that starts at place x of the line of key tiles (x < x1,
-// the end of the CTA's range); returns the place after it.  n = 0: the rows
-// need nothing of it (later tokens than theirs).
-__device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p, long long x, long long x0, long long x1,
-                                                long long total, long long ctas, ApItem &it) {
+// The part of an item that starts at place x of the line of key tiles, up to
+// the end of the CTA's share; returns the place after it.  n = 0: the rows need
+// nothing of it (later tokens than theirs).
+__device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p, long long x, const AtShare &share, ApItem &it) {
   const AttnArgs &a = p.a;
   int lo = 0, hi = a.B - 1;                        // largest b with work[b] <= x
   while (lo < hi) {
@@ -163,16 +176,14 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
     if (s.work[mid] <= x) lo = mid; else hi = mid - 1;
   }
   it.b = lo;
-  const int nch = s.nch[lo];
-  const int item = (int)((x - s.work[lo]) / nch);
-  const long long item0 = s.work[lo] + (long long)item * nch, xe = min(x1, item0 + nch);
-  it.first = __ldg(a.cu + lo);
-  const int n = min(__ldg(a.cu + lo + 1), a.T) - it.first;
-  const int tiles = (int)(((long long)n * a.group + kApRows - 1) / kApRows);
+  it.first = s.first[lo];
+  it.cached = s.cached[lo];
+  const int n = s.n[lo], tiles = cache_tiles(a, n), nch = cache_nch(a, n, it.cached);
+  const int item = (int)at_div(x - s.work[lo], nch);
+  const long long item0 = s.work[lo] + (long long)item * nch, xe = min(share.x1, item0 + nch);
   it.hk = item / tiles;
   it.row0 = (item - it.hk * tiles) * kApRows;
   ap_rows(p, it, n);
-  it.cached = max(__ldg(a.cached + lo), 0);
   const long long lim = min((long long)a.max_pages << a.page_shift, (long long)it.cached + n);
   const int last = it.tok0 + (((it.g0 + it.rows - 1) * p.magic) >> 16);      // fresh token of the last row
   it.all = a.tree_mask ? it.cached : it.cached + it.tok0 + 1;
@@ -182,17 +193,20 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
   it.n = max(0, min((int)(xe - item0), need) - it.j0);
   const bool whole = it.j0 == 0 && it.n == need;
   it.twin = !whole && it.rows <= kApTile;
-  it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > x0);
+  it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > share.x0);
   it.n0 = it.twin ? (it.n + 1) >> 1 : it.n;
   it.n1 = it.twin ? it.n >> 1 : (it.rows > kApTile ? it.n : 0);
   it.m0 = max(0, it.all / kApTile - it.j0);
-  if (it.j0 == 0) {
-    // for the join: the CTAs that hold the parts, and the slot of the first one's
-    const int c0 = blockIdx.x, c1 = (int)(((item0 + need) * ctas - 1) / total);
+  if (!whole && it.j0 == 0) {
+    // for the join, at the CTA that holds the first part: the last part of a
+    // CTA's share, so that there is one at most
+    int c0, c1;
+    share.ctas_of(item0, item0 + need - 1, c0, c1);
+    if (share.len) c1 = c0 + (need - 1) / share.len;
     if ((threadIdx.x & 31) == 0) {
-      int4 *d = p.desc + 2 * (s.items[lo] + item);
+      int4 *d = p.desc + 2 * blockIdx.x;
       d[0] = make_int4(it.first, it.hk, it.row0, it.rows);
-      d[1] = make_int4(c0, whole ? -1 : c1, it.slot, it.twin);
+      d[1] = make_int4(c0, c1, it.slot, it.twin);
     }
   }
   return xe;
@@ -256,93 +270,83 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   const uint32_t q_smem = smem0, ring = smem0 + 2 * kTB;
   uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
 
-  if (tid == 0) {
-    for (int i = 0; i < kSlots; i++) {
-      mbar_init(&s.kv_full[i], 1);
-      mbar_init(&s.kv_empty[i], 1);
+  if (warp == 0) {
+    // a barrier a lane: one lane would take some 25 cycles for each of them
+    if (lane < kSlots) {
+      mbar_init(&s.kv_full[lane], 1);
+      mbar_init(&s.kv_empty[lane], 1);
     }
-    mbar_init(&s.q_full, 64);
-    mbar_init(&s.q_empty, 1);
-    for (int i = 0; i < 2; i++) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 4);
-      mbar_init(&s.o_done[i], 1);
-      mbar_init(&s.sched_full[i], 1);
-      mbar_init(&s.sched_empty[i], 11);            // 8 softmax warps, MMA warp, 2 helper warps
+    if (lane < 2) {
+      mbar_init(&s.s_full[lane], 1);
+      mbar_init(&s.p_full[lane], 4);
+      mbar_init(&s.o_done[lane], 1);
+      mbar_init(&s.sched_full[lane], 1);
+      mbar_init(&s.sched_empty[lane], 11);         // 8 softmax warps, MMA warp, 2 helper warps
+    } else if (lane < 5) {
+      mbar_init(&s.v_posted[0][lane - 2], 1);
+      mbar_init(&s.v_posted[1][lane - 2], 1);
+      mbar_init(&s.v_clean[lane - 2], 2);
+    } else if (lane == 5) {
+      mbar_init(&s.q_full, p.q_boxes ? 1 : 64);
+      mbar_init(&s.q_empty, 1);
+      mbar_init(&s.v_next, 1);
+      mbar_init(&s.drain, 1);
     }
-    for (int i = 0; i < 3; i++) {
-      mbar_init(&s.v_posted[0][i], 1);
-      mbar_init(&s.v_posted[1][i], 1);
-      mbar_init(&s.v_clean[i], 2);
-    }
-    mbar_init(&s.v_next, 1);
-    mbar_init(&s.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid == 32 * kApWTma) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.vmap)) : "memory");
+    if (p.q_boxes) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
   }
   if (warp == kApWMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  long long total = 0, x0 = 0, x1 = 0, ctas = 0;   // prompt: items; cache: key tiles, and this CTA's range of them
+  long long total = 0;                             // prompt: items; cache: key tiles
+  AtShare share = {};
   if constexpr (PAGED) {
     int nitems = 0;
     for (int b0 = 0; b0 < a.B; b0 += kApThreads) {
       const int b = b0 + tid;
-      int items = 0, nch = 1;
+      int items = 0;
+      long long v = 0;
       if (b < a.B) {
-        const int lo = __ldg(a.cu + b), n = lo < 0 ? 0 : min(__ldg(a.cu + b + 1), a.T) - lo;
-        if (n > 0) {
-          const long long ctx = min((long long)max(__ldg(a.cached + b), 0) + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n),
-                                    (long long)a.max_pages << a.page_shift);
-          items = (int)(((long long)n * a.group + kApRows - 1) / kApRows) * a.kv_heads;
-          nch = (int)((ctx + kApTile - 1) / kApTile);
-        }
+        const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1), cached = max(__ldg(a.cached + b), 0);
+        const int n = lo < 0 ? 0 : max(0, min(hi, a.T) - lo);
+        s.first[b] = lo;
+        s.n[b] = n;
+        s.cached[b] = cached;
+        items = cache_tiles(a, n) * a.kv_heads;
+        v = (long long)items * cache_nch(a, n, cached);
       }
-      const long long v = (long long)items * nch;
       long long incl = v;
-      int iincl = items;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long t = __shfl_up_sync(kFull, incl, o);
-        const int u = __shfl_up_sync(kFull, iincl, o);
-        if (lane >= o) {
-          incl += t;
-          iincl += u;
-        }
+        if (lane >= o) incl += t;
       }
+      items = __reduce_add_sync(kFull, items);
       if (lane == 31) {
         s.wsum2[warp] = incl;
-        s.wsum[0][warp] = iincl;
+        s.wsum[0][warp] = items;
       }
       __syncthreads();
       long long at = total;
-      int iat = nitems;
 #pragma unroll
       for (int w = 0; w < kApThreads / 32; w++) {
         at += w < warp ? s.wsum2[w] : 0;
-        iat += w < warp ? s.wsum[0][w] : 0;
         total += s.wsum2[w];
         nitems += s.wsum[0][w];
       }
-      if (b < a.B) {
-        s.work[b] = at + incl - v;
-        s.items[b] = iat + iincl - items;
-        s.nch[b] = nch;
-      }
+      if (b < a.B) s.work[b] = at + incl - v;
       __syncthreads();
     }
-    if (tid == 0 && blockIdx.x == 0) p.ctrl[kAttnCtrlItems] = nitems;
-    const long long want = (total + kApMinTiles - 1) / kApMinTiles;
-    ctas = want < (long long)gridDim.x ? want : (long long)gridDim.x;
-    if ((long long)blockIdx.x < ctas) {
-      x0 = total * blockIdx.x / ctas;
-      x1 = total * (blockIdx.x + 1) / ctas;
-    }
+    share = at_share<kApThreads / 32>(
+        s.work, a.B, total, nitems, kApMinTiles, kApExtra, s.cand,
+        [&](int b) { return cache_tiles(a, s.n[b]) * a.kv_heads; }, [&](int b) { return cache_nch(a, s.n[b], s.cached[b]); });
+    if (tid == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless cache_part finds it
   } else {
     // requests by falling number of row tiles (equal ones by index), every CTA alike
     for (int b = tid; b < a.B; b += kApThreads) {
@@ -596,14 +600,14 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       // over the cache every lane copies a page of the tile; else lane 0 the whole tile
       if (PAGED || lane == 0) {
         int pos = 0;
-        long long next = PAGED ? x0 : blockIdx.x;
+        long long next = PAGED ? share.x0 : blockIdx.x;
         bool ok = true;
         for (int i = 0; ok; i++) {
           ApItem it;
           it.b = -1;
           if constexpr (PAGED) {
-            while (next < x1) {
-              next = cache_part(s, p, next, x0, x1, total, ctas, it);
+            while (next < share.x1) {
+              next = cache_part(s, p, next, share, it);
               if (it.n > 0) break;
               it.b = -1;
             }
@@ -791,6 +795,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       const int ht = tid - 32 * kApWHelp;
       int base = 0;
       uint32_t posted[3] = {0u, 0u, 0u};
+      int nq = 0;                                  // items whose Q was copied by boxes
       bool ok = true;
       for (int i = 0; ok; i++) {
         if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
@@ -800,32 +805,46 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         if (lane < 12) s.bad[i & 1][warp - kApWHelp][lane >> 2][lane & 3] = 0u;
         __syncwarp();
         if (i > 0 && !mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u)) break;
-        // a thread copies 16-byte piece `ch` of every kStep-th row; the row's token
-        // and head follow by addition
-        constexpr int kChunks = D / 8, kStep = 64 / kChunks;
-        const int ch = ht % kChunks, r0 = ht / kChunks, top = it.rows > kApTile ? kApRows : kApTile;
-        const int dtok = (kStep * p.magic) >> 16, dg = kStep - dtok * a.group;
-        const long long adv = dtok * a.q.row + dg * a.q.head, wrap = a.q.row - a.group * a.q.head;
-        const int x0q = it.g0 + r0, t0q = (x0q * p.magic) >> 16;
-        int gq = x0q - t0q * a.group;
-        const uint16_t *src = a.q.p + (long long)(it.first + it.tok0 + t0q) * a.q.row +
-                              (long long)(it.hk * a.group + gq) * a.q.head + 8 * ch;
-        const uint32_t qd = q_smem + (uint32_t)(ch >> 3) * (kApTile * 128);
-#pragma unroll 4
-        for (int r = r0; r < top; r += kStep) {
-          const int rr = r & (kApTile - 1);
-          at_cp16(qd + (r >= kApTile ? kTB : 0) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), r < it.rows ? src : a.q.p,
-                  r < it.rows);
-          src += adv;
-          gq += dg;
-          if (gq >= a.group) {
-            gq -= a.group;
-            src += wrap;
+        if (p.q_boxes) {
+          // rows token by token, head by head: a box (64, group, 128 / group) is a
+          // row tile; rows past the request's are others' and not stored
+          if (ht == 0) {
+            const int boxes = it.rows > kApTile ? 2 : 1, per = kApTile / a.group;
+            mbar_arrive_expect_tx(&s.q_full, (uint32_t)(boxes * kTB));
+            for (int q = 0; q < boxes; q++)
+              for (int hf = 0; hf < kHalves; hf++)
+                at_tma_3d(q_smem + q * kTB + hf * (kApTile * 128), &p.qmap, 64 * hf, it.hk * a.group, it.first + it.tok0 + q * per,
+                          &s.q_full);
+            nq++;
           }
+        } else {
+          // a thread copies 16-byte piece `ch` of every kStep-th row; the row's token
+          // and head follow by addition
+          constexpr int kChunks = D / 8, kStep = 64 / kChunks;
+          const int ch = ht % kChunks, r0 = ht / kChunks, top = it.rows > kApTile ? kApRows : kApTile;
+          const int dtok = (kStep * p.magic) >> 16, dg = kStep - dtok * a.group;
+          const long long adv = dtok * a.q.row + dg * a.q.head, wrap = a.q.row - a.group * a.q.head;
+          const int x0q = it.g0 + r0, t0q = (x0q * p.magic) >> 16;
+          int gq = x0q - t0q * a.group;
+          const uint16_t *src = a.q.p + (long long)(it.first + it.tok0 + t0q) * a.q.row +
+                                (long long)(it.hk * a.group + gq) * a.q.head + 8 * ch;
+          const uint32_t qd = q_smem + (uint32_t)(ch >> 3) * (kApTile * 128);
+#pragma unroll 4
+          for (int r = r0; r < top; r += kStep) {
+            const int rr = r & (kApTile - 1);
+            at_cp16(qd + (r >= kApTile ? kTB : 0) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), r < it.rows ? src : a.q.p,
+                    r < it.rows);
+            src += adv;
+            gq += dg;
+            if (gq >= a.group) {
+              gq -= a.group;
+              src += wrap;
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          at_fence_async();
+          mbar_arrive(&s.q_full);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        at_fence_async();
-        mbar_arrive(&s.q_full);
         // the MMA warp has seen this item's predecessor's scans: a barrier is
         // never a phase ahead of its reader
         if (i > 0 && !mbar_wait_bounded(&s.v_next, (uint32_t)(i - 1) & 1u)) break;
@@ -863,6 +882,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
+      if (nq > 0) mbar_wait_bounded(&s.q_full, (uint32_t)(nq - 1) & 1u);   // a copy in flight lands before the CTA ends
+      __syncwarp();
     }
   }
   at_fence_before();
@@ -881,44 +902,59 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(256) attn_join_kernel(const ApArgs p) {
   const AttnArgs &a = p.a;
   pdl_wait();
-  if (blockIdx.x >= (unsigned)__ldcg(p.ctrl + kAttnCtrlItems)) return;
   const int4 d0 = __ldcg(p.desc + 2 * blockIdx.x), d1 = __ldcg(p.desc + 2 * blockIdx.x + 1);
   const int first = d0.x, hk = d0.y, row0 = d0.z, rows = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), dg = threadIdx.x >> 5;
   if (c1 < 0 || r >= rows) return;
   const float c = a.scale * 1.44269504088896340736f;
   constexpr int N = D / 32;                        // float4 of a thread
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int k = c0; k <= c1; k++) {
-    const size_t at = (size_t)(k == c0 ? slot0 : 2 * k) * kApRows + r;
-    top = fmaxf(top, __ldcg(&p.stat[at].x));
-    if (twin) top = fmaxf(top, __ldcg(&p.stat[at + kApTile].x));
-  }
-  float sum = 0.f;
+  const int nsrc = (c1 - c0 + 1) << twin;          // twins: two sources a part
+  // source q's row in the parts' buffers
+  auto at_of = [&](int q) {
+    const int k = c0 + (q >> twin);
+    return (size_t)(k == c0 ? slot0 : 2 * k) * kApRows + r + (twin && (q & 1) ? kApTile : 0);
+  };
+  float top = -INFINITY, sum = 0.f;
   float4 acc[N];
 #pragma unroll
   for (int e = 0; e < N; e++) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int slot, int row) {
-    const float2 st = __ldcg(&p.stat[(size_t)slot * kApRows + row]);
-    if (st.y == 0.f) return;                       // a part in which the row sees nothing (it may hold no O)
-    const float f = at_exp2((st.x - top) * c);
-    sum = fmaf(st.y, f, sum);
-    const float4 *src = p.part + ((size_t)slot * (D / 4) + N * dg) * kApRows + row;
+  // four sources at a time, so that their loads wait together
+  for (int q0 = 0; q0 < nsrc; q0 += 4) {
+    float2 st[4];
+    float4 u[4][N];
+#pragma unroll
+    for (int z = 0; z < 4; z++) {
+      const size_t at = at_of(min(q0 + z, nsrc - 1)), slot = at / kApRows, row = at - slot * kApRows;
+      st[z] = __ldcg(p.stat + at);
+#pragma unroll
+      for (int e = 0; e < N; e++) u[z][e] = __ldcg(p.part + (slot * (D / 4) + N * dg + e) * kApRows + row);
+    }
+    float t1 = top;
+#pragma unroll
+    for (int z = 0; z < 4; z++) t1 = fmaxf(t1, st[z].x);
+    const float f0 = top == -INFINITY ? 1.f : at_exp2((top - t1) * c);
+    top = t1;
+    sum *= f0;
 #pragma unroll
     for (int e = 0; e < N; e++) {
-      const float4 u = __ldcg(src + e * kApRows);
-      acc[e].x = fmaf(u.x, f, acc[e].x);
-      acc[e].y = fmaf(u.y, f, acc[e].y);
-      acc[e].z = fmaf(u.z, f, acc[e].z);
-      acc[e].w = fmaf(u.w, f, acc[e].w);
+      acc[e].x *= f0;
+      acc[e].y *= f0;
+      acc[e].z *= f0;
+      acc[e].w *= f0;
     }
-  };
-#pragma unroll 2
-  for (int k = c0; k <= c1; k++) {
-    const int slot = k == c0 ? slot0 : 2 * k;
-    add(slot, r);
-    if (twin) add(slot, r + kApTile);
+#pragma unroll
+    for (int z = 0; z < 4; z++) {
+      if (q0 + z >= nsrc || st[z].y == 0.f) continue;   // a part in which the row sees nothing (it may hold no O)
+      const float f = at_exp2((st[z].x - top) * c);
+      sum = fmaf(st[z].y, f, sum);
+#pragma unroll
+      for (int e = 0; e < N; e++) {
+        acc[e].x = fmaf(u[z][e].x, f, acc[e].x);
+        acc[e].y = fmaf(u[z][e].y, f, acc[e].y);
+        acc[e].z = fmaf(u[z][e].z, f, acc[e].z);
+        acc[e].w = fmaf(u[z][e].w, f, acc[e].w);
+      }
+    }
   }
   const int rr = row0 + r, i = rr / a.group, hq = hk * a.group + rr - i * a.group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -943,21 +979,26 @@ ApKernel ap_join(int head_dim, int f16) {
 }
 int ap_smem(int head_dim) { return head_dim == 64 ? ApGeom<64>::kSmem : ApGeom<128>::kSmem; }
 
-cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, int head_dim, int f16) {
+// Packed rows [T][heads][D] in boxes of 64 elements x `heads_box` heads x `rows_box` rows.
+cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, int heads_box, int rows_box, const AttnArgs &a) {
   const AttnMapEncodeFn enc = attn_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)heads, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)r.head * 2, (cuuint64_t)r.row * 2};
-  const cuuint32_t box[3] = {64, 1, kApTile};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows_box};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult e = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, strides,
+  const CUresult e = enc(map, a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, strides,
                          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-// Items at most: every request may end inside a row tile.
-long long wide_items(int group, int kv_heads, int B, int T) {
-  return (((long long)T * group + kApRows - 1) / kApRows + B) * kv_heads;
+
+// Q rows of whole tokens as boxes, for groups that divide a row tile.
+cudaError_t encode_q(ApArgs *p) {
+  const AttnArgs &a = p->a;
+  p->magic = (65536 + a.group - 1) / a.group;
+  p->q_boxes = kApTile % a.group == 0;
+  return p->q_boxes ? encode_rows(&p->qmap, a.q, a.T, a.q_heads, a.group, kApTile / a.group, a) : cudaSuccess;
 }
 }  // namespace
 
@@ -975,14 +1016,14 @@ cudaError_t attn_wide_setup(int head_dim, int f16) {
   return cudaSuccess;
 }
 
-AttnWideWs attn_wide_ws(size_t off, int group, int kv_heads, int head_dim, int B, int T, int num_sms) {
+AttnWideWs attn_wide_ws(size_t off, int head_dim, int num_sms) {
   AttnWideWs w;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off = (off + bytes + 255) / 256 * 256;
     return at;
   };
-  w.desc = take(32 * (size_t)wide_items(group, kv_heads, B, T));
+  w.desc = take(32 * (size_t)num_sms);
   w.stat = take(8 * (size_t)(2 * num_sms) * kApRows);
   w.part = take(4 * (size_t)(2 * num_sms) * kApRows * head_dim);
   w.total = off;
@@ -994,11 +1035,12 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaSt
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.ctrl = ctrl;
-  p.magic = (65536 + a.group - 1) / a.group;
-  cudaError_t err = encode_rows(&p.kmap, a.k, a.T, a.kv_heads, a.head_dim, a.f16);
-  if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, a.head_dim, a.f16);
+  cudaError_t err = encode_q(&p);
+  if (err == cudaSuccess) err = encode_rows(&p.kmap, a.k, a.T, a.kv_heads, 1, kApTile, a);
+  if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, 1, kApTile, a);
   if (err != cudaSuccess) return err;
-  const long long items = wide_items(a.group, a.kv_heads, a.B, a.T);
+  // items at most: every request may end inside a row tile
+  const long long items = (((long long)a.T * a.group + kApRows - 1) / kApRows + a.B) * a.kv_heads;
   const int grid = (int)(items < num_sms ? items : num_sms);
   ap_kernel<false>(a.head_dim, a.f16)<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
   return cudaGetLastError();
@@ -1009,17 +1051,17 @@ cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWide
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.ctrl = reinterpret_cast<int *>(ws);
-  p.magic = (65536 + a.group - 1) / a.group;
   p.desc = reinterpret_cast<int4 *>(ws + w.desc);
   p.stat = reinterpret_cast<float2 *>(ws + w.stat);
   p.part = reinterpret_cast<float4 *>(ws + w.part);
-  cudaError_t err = attn_encode_cache(&p.kmap, a.k_cache, a, 1 << a.page_shift);
+  cudaError_t err = encode_q(&p);
+  if (err == cudaSuccess) err = attn_encode_cache(&p.kmap, a.k_cache, a, 1 << a.page_shift);
   if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 1 << a.page_shift);
   if (err != cudaSuccess) return err;
   ap_kernel<true>(a.head_dim, a.f16)<<<num_sms, kApThreads, ap_smem(a.head_dim), stream>>>(p);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)wide_items(a.group, a.kv_heads, a.B, a.T), kApRows / 32);
+  cfg.gridDim = dim3((unsigned)num_sms, kApRows / 32);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
