@@ -3,10 +3,10 @@
 // request brings many query rows (moe_attn_tree; attn_tree.cu has the other
 // calls).
 //
-// The G query heads of a kv head are rows of one matrix: row r = token * G + g
-// of a request, so a key tile serves all of them and short prompts fill the
-// 128-row tensor-core tiles.  An item is (request, kv head, 256 rows): two row
-// tiles of 128 that share every key/value tile of 128 tokens.  With c =
+// The G query heads of a kv head are rows of one matrix (row = token * G + head of
+// the group), so a key tile serves all of them and short prompts fill the 128-row
+// tensor-core tiles: a row tile is floor(128 / G) whole tokens.  An item is
+// (request, kv head, two row tiles): they share every key/value tile of 128 tokens.  With c =
 // softmax_scale * log2(e), per row tile and key tile j:
 //   S = Q K_j^T                                   (tcgen05, both from shared memory)
 //   m' = max(m, max S);  P = 2^(c (S - m'));  l = l 2^(c (m - m')) + sum P
@@ -24,15 +24,17 @@
 //                   also the rare rescaling of O and the epilogue
 //   warp 8          key/value tiles by tensor-map copies (128-byte swizzle)
 //                   into a ring, in the order K0 K1 V0 K2 V1 ..; takes the items
-//   warp 9          MMA issue: S of the next tile is issued with PV of this one,
-//                   so one row tile's softmax runs while the other's MMAs do
-//   warps 10-11     Q rows into swizzled shared memory (tensor-map boxes where the
-//                   group divides a row tile, else cp.async); the scan below
+//   warps 9, 10     MMA issue for row tile 0 and 1: S of the next key tile follows
+//                   PV of this one, so one row tile's softmax runs while the
+//                   other's MMAs do.  An issuer's way from one operation to the
+//                   next (barriers, commits) takes some 500 cycles; with an issuer
+//                   each the tensor pipe has the other's work meanwhile
+//   warp 11         Q rows by tensor-map boxes (64, G, tokens); the scan below
 // Tensor memory: S0, S1 (128 columns each, P over their first 64), O0, O1.
 //
 // A tile past the last token that all rows see holds keys that some rows, or
 // all, may not see.  Their scores are replaced by -infinity, so P is 0; but 0
-// times an infinite or NaN v is NaN, so warps 10-11 scan those tiles' v, zero
+// times an infinite or NaN v is NaN, so warp 11 scans those tiles' v, zeroes
 // such elements and note their tokens, and the epilogue adds them to the
 // rows that do see the token.
 //
@@ -57,7 +59,7 @@ namespace moe {
 constexpr int kApThreads = 384;
 constexpr int kApRows = 256, kApTile = 128;      // rows of an item; rows of a row tile, tokens of a key tile
 constexpr int kApRegsSoft = 208, kApRegsRest = 88;
-constexpr int kApWTma = 8, kApWMma = 9, kApWHelp = 10;
+constexpr int kApWTma = 8, kApWMma = 9, kApWHelp = 11;   // MMA warps 9, 10
 constexpr int kApMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kApSlack = 8.f;                  // log2 of the largest P
 constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache)
@@ -73,23 +75,22 @@ struct ApGeom {
 struct ApArgs {
   CUtensorMap kmap, vmap;      // prompt: (64, 1, 128) boxes over [rows][kv_heads][D]; cache: (64, page, 1, 1) over
                                // [pages][kv_heads][page][D]; 128-byte swizzle
-  CUtensorMap qmap;            // (64, group, 128 / group) boxes over [rows][q_heads][D], for groups that divide 128
+  CUtensorMap qmap;            // (64, group, per) boxes over [rows][q_heads][D]
   AttnArgs a;
   int *ctrl;                   // workspace control words
   int magic;                   // ceil(2^16 / group)
-  int q_boxes;                 // qmap is there
+  int per;                     // tokens of a row tile: floor(128 / group)
   // cache only
   int4 *desc;                  // per CTA, of the item whose first part it holds and others the rest:
-                               // (first, hk, row0, rows), (first CTA, last CTA, its slot, twin)
+                               // (first, hk, tok0, toks), (first CTA, last CTA, its slot, twin)
   float4 *part;                // [2 * grid][D / 4][256]  O of a part
   float2 *stat;                // [2 * grid][256]         (m, l)
 };
 
 struct ApItem {
-  int b, hk, row0;             // request (-1: no more items), kv head, first row (of the request's rows)
+  int b, hk;                   // request (-1: no more items), kv head
   int first;                   // the request's first packed row
-  int tok0, g0;                // fresh token and group place of row0
-  int rows;                    // rows of the item (<= 256)
+  int tok0, toks;              // the item's tokens, among the request's fresh ones
   int j0, n;                   // first key tile and number of key tiles
   int n0, n1;                  // key tiles of the two row tiles
   int cached;                  // context before the fresh tokens
@@ -101,15 +102,15 @@ struct ApItem {
 
 struct ApSmem {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, sched_full[2], sched_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, sched_full[2], sched_empty[2], drain[2];
   uint32_t tmem;
   int wsum[2][kApThreads / 32];
   ApItem item[2];
-  uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
+  uint32_t bad[2][3][4];       // by item parity and masked tile: tokens with a non-finite v
   union {
     struct {                   // prompts: requests by falling length
       uint16_t order[kApMaxB];
-      int tiles[kApMaxB];      // 256-row items per kv head of the k-th longest
+      int tiles[kApMaxB];      // items per kv head of the k-th longest
       int before[kApMaxB + 1]; // items (per kv head) of row tiles in which fewer than k + 1 requests take part
     };
     struct {                   // cache: the line of key tiles
@@ -123,20 +124,10 @@ struct ApSmem {
 
 // Of a request of n fresh rows over the cache: items of a kv head, and key
 // tiles that its rows may see.
-__device__ __forceinline__ int cache_tiles(const AttnArgs &a, int n) {
-  return (int)(((long long)n * a.group + kApRows - 1) / kApRows);
-}
+__device__ __forceinline__ int cache_tiles(const ApArgs &p, int n) { return (n + 2 * p.per - 1) / (2 * p.per); }
 __device__ __forceinline__ int cache_nch(const AttnArgs &a, int n, int cached) {
   const long long ctx = min((long long)cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n), (long long)a.max_pages << a.page_shift);
   return (int)((ctx + kApTile - 1) / kApTile);
-}
-
-// The rows of an item, given its row0.
-__device__ __forceinline__ void ap_rows(const ApArgs &p, ApItem &it, int n_fresh) {
-  const AttnArgs &a = p.a;
-  it.rows = (int)min((long long)kApRows, (long long)n_fresh * a.group - it.row0);
-  it.tok0 = it.row0 / a.group;
-  it.g0 = it.row0 - it.tok0 * a.group;
 }
 
 // The idx-th item by falling row tile: row tiles [tiles[k], tiles[k - 1]) have
@@ -151,16 +142,16 @@ __device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, in
     if (s.before[mid] <= e) lo = mid; else hi = mid - 1;
   }
   const int k = lo + 1, off = e - s.before[lo];
-  it.row0 = (s.tiles[lo] - 1 - off / k) * kApRows;
+  it.tok0 = (s.tiles[lo] - 1 - off / k) * 2 * p.per;
   it.b = s.order[off % k];
   it.first = __ldg(a.cu + it.b);
-  ap_rows(p, it, min(__ldg(a.cu + it.b + 1), a.T) - it.first);
-  it.n0 = (it.tok0 + (((it.g0 + min(it.rows, kApTile) - 1) * p.magic) >> 16)) / kApTile + 1;
-  it.n1 = it.rows > kApTile ? (it.tok0 + (((it.g0 + it.rows - 1) * p.magic) >> 16)) / kApTile + 1 : 0;
+  it.toks = min(min(__ldg(a.cu + it.b + 1), a.T) - it.first - it.tok0, 2 * p.per);
+  it.n0 = (it.tok0 + min(it.toks, p.per) - 1) / kApTile + 1;
+  it.n1 = it.toks > p.per ? (it.tok0 + it.toks - 1) / kApTile + 1 : 0;
   it.n = max(it.n0, it.n1);
   it.j0 = it.cached = it.twin = 0;
   it.all = it.tok0 + 1;
-  it.end = it.tok0 + kApRows;                      // the causal limit alone cuts
+  it.end = it.tok0 + it.toks;                      // the causal limit alone cuts
   it.m0 = it.all / kApTile;
   it.slot = -1;
 }
@@ -178,24 +169,23 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
   it.b = lo;
   it.first = s.first[lo];
   it.cached = s.cached[lo];
-  const int n = s.n[lo], tiles = cache_tiles(a, n), nch = cache_nch(a, n, it.cached);
+  const int n = s.n[lo], tiles = cache_tiles(p, n), nch = cache_nch(a, n, it.cached);
   const int item = (int)at_div(x - s.work[lo], nch);
   const long long item0 = s.work[lo] + (long long)item * nch, xe = min(share.x1, item0 + nch);
   it.hk = item / tiles;
-  it.row0 = (item - it.hk * tiles) * kApRows;
-  ap_rows(p, it, n);
+  it.tok0 = (item - it.hk * tiles) * 2 * p.per;
+  it.toks = min(n - it.tok0, 2 * p.per);
   const long long lim = min((long long)a.max_pages << a.page_shift, (long long)it.cached + n);
-  const int last = it.tok0 + (((it.g0 + it.rows - 1) * p.magic) >> 16);      // fresh token of the last row
   it.all = a.tree_mask ? it.cached : it.cached + it.tok0 + 1;
-  it.end = (int)min(lim, (long long)it.cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : last + 1));
+  it.end = (int)min(lim, (long long)it.cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : it.tok0 + it.toks));
   const int need = (it.end + kApTile - 1) / kApTile;                          // key tiles of this row tile
   it.j0 = (int)(x - item0);
   it.n = max(0, min((int)(xe - item0), need) - it.j0);
   const bool whole = it.j0 == 0 && it.n == need;
-  it.twin = !whole && it.rows <= kApTile;
+  it.twin = !whole && it.toks <= p.per;
   it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > share.x0);
   it.n0 = it.twin ? (it.n + 1) >> 1 : it.n;
-  it.n1 = it.twin ? it.n >> 1 : (it.rows > kApTile ? it.n : 0);
+  it.n1 = it.twin ? it.n >> 1 : (it.toks > p.per ? it.n : 0);
   it.m0 = max(0, it.all / kApTile - it.j0);
   if (!whole && it.j0 == 0) {
     // for the join, at the CTA that holds the first part: the last part of a
@@ -205,7 +195,7 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
     if (share.len) c1 = c0 + (need - 1) / share.len;
     if ((threadIdx.x & 31) == 0) {
       int4 *d = p.desc + 2 * blockIdx.x;
-      d[0] = make_int4(it.first, it.hk, it.row0, it.rows);
+      d[0] = make_int4(it.first, it.hk, it.tok0, it.toks);
       d[1] = make_int4(c0, c1, it.slot, it.twin);
     }
   }
@@ -274,30 +264,30 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     // a barrier a lane: one lane would take some 25 cycles for each of them
     if (lane < kSlots) {
       mbar_init(&s.kv_full[lane], 1);
-      mbar_init(&s.kv_empty[lane], 1);
+      mbar_init(&s.kv_empty[lane], 2);             // both MMA warps
     }
     if (lane < 2) {
       mbar_init(&s.s_full[lane], 1);
       mbar_init(&s.p_full[lane], 4);
       mbar_init(&s.o_done[lane], 1);
       mbar_init(&s.sched_full[lane], 1);
-      mbar_init(&s.sched_empty[lane], 11);         // 8 softmax warps, MMA warp, 2 helper warps
+      mbar_init(&s.sched_empty[lane], 11);         // 8 softmax warps, 2 MMA warps, warp 11
+      mbar_init(&s.drain[lane], 1);
     } else if (lane < 5) {
       mbar_init(&s.v_posted[0][lane - 2], 1);
       mbar_init(&s.v_posted[1][lane - 2], 1);
-      mbar_init(&s.v_clean[lane - 2], 2);
+      mbar_init(&s.v_clean[lane - 2], 1);
     } else if (lane == 5) {
-      mbar_init(&s.q_full, p.q_boxes ? 1 : 64);
-      mbar_init(&s.q_empty, 1);
-      mbar_init(&s.v_next, 1);
-      mbar_init(&s.drain, 1);
+      mbar_init(&s.q_full, 1);
+      mbar_init(&s.q_empty, 2);
+      mbar_init(&s.v_next, 2);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid == 32 * kApWTma) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.vmap)) : "memory");
-    if (p.q_boxes) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
   }
   if (warp == kApWMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
@@ -318,7 +308,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         s.first[b] = lo;
         s.n[b] = n;
         s.cached[b] = cached;
-        items = cache_tiles(a, n) * a.kv_heads;
+        items = cache_tiles(p, n) * a.kv_heads;
         v = (long long)items * cache_nch(a, n, cached);
       }
       long long incl = v;
@@ -345,13 +335,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     }
     share = at_share<kApThreads / 32>(
         s.work, a.B, total, nitems, kApMinTiles, kApExtra, s.cand,
-        [&](int b) { return cache_tiles(a, s.n[b]) * a.kv_heads; }, [&](int b) { return cache_nch(a, s.n[b], s.cached[b]); });
+        [&](int b) { return cache_tiles(p, s.n[b]) * a.kv_heads; }, [&](int b) { return cache_nch(a, s.n[b], s.cached[b]); });
     if (tid == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless cache_part finds it
   } else {
     // requests by falling number of row tiles (equal ones by index), every CTA alike
     for (int b = tid; b < a.B; b += kApThreads) {
       const int lo = __ldg(a.cu + b), n = max(0, min(__ldg(a.cu + b + 1), a.T) - lo);
-      s.before[b] = lo < 0 ? 0 : (int)(((long long)n * a.group + kApRows - 1) / kApRows);
+      s.before[b] = lo < 0 ? 0 : (n + 2 * p.per - 1) / (2 * p.per);
     }
     __syncthreads();
     for (int b = tid; b < a.B; b += kApThreads) {
@@ -409,10 +399,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       const ApItem it = s.item[i & 1];
       if (it.b < 0) break;
       const int nt = h ? it.n1 : it.n0;
-      const int ri = PAGED && it.twin ? tid & 127 : tid & 255;                  // row of the item
-      const bool real = ri < it.rows;
-      const int x = it.g0 + min(ri, it.rows - 1), dt = (x * p.magic) >> 16;
-      const int lim = it.tok0 + dt;                // the row's token: of the prompt, or among the fresh ones
+      const int r = tid & 127, dt = (r * p.magic) >> 16;                        // row of the row tile, its token there
+      const int tl = (PAGED && it.twin ? 0 : h * p.per) + dt;                   // token of the item
+      const bool real = dt < p.per && tl < it.toks;
+      const int lim = it.tok0 + min(tl, it.toks - 1);   // the row's token: of the prompt, or among the fresh ones
       uint64_t word = 0;
       if constexpr (PAGED)
         if (a.tree_mask) word = __ldg(a.tree_mask + it.first + lim);
@@ -502,7 +492,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         at_fence_after();
         uint32_t anybad = 0;
 #pragma unroll
-        for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
+        for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][w >> 2][w & 3];
         if (anybad) {
 #pragma unroll 1
           for (int q = 0; q < D / 32; q++) {
@@ -510,11 +500,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             at_ld32(to + 32u * q, o);
             at_wait_ld(o);
             for (int w = 0; w < 12; w++) {
-              uint32_t bits = s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
-              for (; bits; bits &= bits - 1) {
-                const int tl = it.m0 + (w >> 2);   // tile of the part
-                if (PAGED && it.twin && (tl & 1) != h) continue;
-                const int tok = (it.j0 + tl) * kApTile + 32 * (w & 3) + __ffs(bits) - 1;
+              for (uint32_t bits = s.bad[i & 1][w >> 2][w & 3]; bits; bits &= bits - 1) {
+                const int jl = it.m0 + (w >> 2);   // tile of the part
+                if (PAGED && it.twin && (jl & 1) != h) continue;
+                const int tok = (it.j0 + jl) * kApTile + 32 * (w & 3) + __ffs(bits) - 1;
                 const uint16_t *vp;
                 if constexpr (PAGED) {
                   const int f = tok - it.cached;
@@ -551,7 +540,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
         } else {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          const int hq = it.hk * a.group + x - dt * a.group;
+          const int hq = it.hk * a.group + r - dt * a.group;
           if (a.lse && real)
             a.lse[(size_t)(it.first + lim) * a.q_heads + hq] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
           // A lane's row at a time would touch 32 lines a store; with the
@@ -565,12 +554,12 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             bool wr[2];
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-              const int rl = 16 * rb + 8 * z + qg, r = (ri & ~31) + rl;
+              const int rl = 16 * rb + 8 * z + qg, rr = (r & ~31) + rl, dr = (rr * p.magic) >> 16;
+              const int tr = tl - dt + dr;         // token of the item (not twins: they are parts)
               iv[z] = __shfl_sync(kFull, inv, rl);
-              wr[z] = r < it.rows;
-              const int xr = it.g0 + r, dr = (xr * p.magic) >> 16;
-              dst[z] = a.out.p + (long long)(it.first + it.tok0 + dr) * a.out.row +
-                       (long long)(it.hk * a.group + xr - dr * a.group) * a.out.head + 8 * q4;
+              wr[z] = dr < p.per && tr < it.toks;
+              dst[z] = a.out.p + (long long)(it.first + it.tok0 + tr) * a.out.row +
+                       (long long)(it.hk * a.group + rr - dr * a.group) * a.out.head + 8 * q4;
             }
 #pragma unroll
             for (int cb = 0; cb < D / 32; cb++) {
@@ -674,16 +663,17 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
       }
       __syncwarp();
-    } else if (warp == kApWMma) {
+    } else if (warp < kApWHelp) {
       // ---------------------------------------------------------- MMA issue
       // The whole warp goes through the loop, so that what the instructions take
       // (descriptors, tensor-memory columns) stays in uniform registers and costs
       // one addition; one elected lane issues.
       constexpr uint32_t id_s = at_idesc(F16, kApTile, false), id_o = at_idesc(F16, D, true);
-      const uint32_t tu = __shfl_sync(kFull, tb, 0);
+      const int h = __shfl_sync(kFull, warp, 0) - kApWMma;   // the warp's row tile
+      const uint32_t tu = __shfl_sync(kFull, tb, 0), sc = tu + 128u * h, oc = tu + 256u + 128u * h;
       const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring, kApTile * 128);
       int slot = 0;                                // ring slot and phase of the next position
-      uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;
+      uint32_t phase = 0, clean = 0, np = 0;
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok && !mbar_wait_bounded(bar, parity)) {
@@ -703,149 +693,106 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
         return at;
       };
-      auto issue_s = [&](int h, int q, int at) {   // S of row tile h: Q of row tile q, K in slot `at`
-        const uint64_t da = dq0 + (uint64_t)(q * (kTB >> 4)), db = dk0 + (uint64_t)(at * (kTB >> 4));
-        if (at_elect()) {
+      auto issue_s = [&](uint64_t da, int at) {    // S = Q K: by the elected lane, K in slot `at`
+        const uint64_t db = dk0 + (uint64_t)(at * (kTB >> 4));
 #pragma unroll
-          for (int k = 0; k < D / 16; k++) {
-            const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32) >> 4;
-            at_mma_ss(tu + 128u * h, da + off, db + off, id_s, k > 0);
-          }
-          at_commit(&s.s_full[h]);
+        for (int k = 0; k < D / 16; k++) {
+          const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32) >> 4;
+          at_mma_ss(sc, da + off, db + off, id_s, k > 0);
         }
-        __syncwarp();
-      };
-      auto issue_o = [&](int h, int at, bool add) {     // O of row tile h (+)= P V, V in slot `at`
-        const uint64_t db = dv0 + (uint64_t)(at * (kTB >> 4));
-        if (at_elect()) {
-#pragma unroll
-          for (int k = 0; k < kApTile / 16; k++)
-            at_mma_ts(tu + 256u + 128u * h, tu + 128u * h + 8u * k, db + (uint64_t)(128u * k), id_o, (uint32_t)(add || k > 0));
-          at_commit(&s.o_done[h]);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t *bar) {
-        if (at_elect()) at_commit(bar);
-        __syncwarp();
+        at_commit(&s.s_full[h]);
       };
       for (int i = 0; ok; i++) {
         if (!wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
         const ApItem &im = s.item[i & 1];
         if (__shfl_sync(kFull, im.b, 0) < 0) break;
         const int n = __shfl_sync(kFull, im.n, 0), m0 = __shfl_sync(kFull, im.m0, 0);
-        const int n0 = __shfl_sync(kFull, im.n0, 0), n1 = __shfl_sync(kFull, im.n1, 0);
+        const int nh = __shfl_sync(kFull, h ? im.n1 : im.n0, 0);
+        const int end = __shfl_sync(kFull, im.end - im.j0 * kApTile, 0);   // tokens of the part from here on are seen by none
         const bool twin = PAGED && __shfl_sync(kFull, im.twin, 0);
+        const uint64_t da = dq0 + (uint64_t)((twin ? 0 : h) * (kTB >> 4));
+        const int ahead = twin ? 2 : 1;            // S of tile j + ahead follows PV of tile j
         if (!wait(&s.q_full, (uint32_t)i & 1u)) break;
-        const int k0 = take();
-        if (!ok) break;
-        at_fence_after();
-        issue_s(0, 0, k0);
-        if (!twin && n1 > 0) issue_s(1, 1, k0);
-        commit(&s.kv_empty[k0]);
-        int kn = 0;                                // slot of the K that goes with PV of tile j
-        if (n > 1) {
-          kn = take();
+        // K0, and for twins K1, one each
+        for (int j = 0; j < ahead && j < n; j++) {
+          const int at = take();
           if (!ok) break;
-          if (twin) {
-            at_fence_after();
-            issue_s(1, 0, kn);
-            commit(&s.kv_empty[kn]);
+          at_fence_after();
+          if (at_elect()) {
+            if (twin ? j == h : nh > 0) issue_s(da, at);
+            at_commit(&s.kv_empty[at]);
+            if (j + 1 == n) at_commit(&s.q_empty);
           }
+          __syncwarp();
         }
-        const int ahead = twin ? 2 : 1;            // the S issued with PV of tile j is that of tile j + ahead
-        if (n <= ahead) commit(&s.q_empty);
-        // ring order: K0 K1 V0 K2 V1 ..; of two row tiles K[j + 1] is taken before V[j], of twins after it
-        for (int j = 0; j < n; j++) {
-          const bool next = j + ahead < n;
-          if (!twin && j > 0 && next) kn = take();
+        // ring order: K0 K1 V0 K2 V1 ..; of two row tiles K[j + 1] is taken before V[j], of twins K[j + 2] after it
+        for (int j = 0; j < n && ok; j++) {
+          const bool next = j + ahead < n, mine = twin ? (j & 1) == h : j < nh;
+          int kn = 0;
+          if (!twin && next) kn = take();
           const int v = take();
           if (twin && next) kn = take();
           if (j >= m0) {
             const int z = j - m0;                  // 0, 1 or 2; a phase bit each
-            if (!wait(&s.v_clean[z], (clean >> z) & 1u)) break;
+            if (mine) wait(&s.v_clean[z], (clean >> z) & 1u);
             clean ^= 1u << z;
           }
           if (j + 1 == n && lane == 0) mbar_arrive(&s.v_next);   // the next item's scans may signal
           if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            if (twin ? (j & 1) == h : j < (h ? n1 : n0)) {
-              uint32_t &np = h ? np1 : np0;
-              if (!wait(&s.p_full[h], np)) break;
-              np ^= 1u;
-              at_fence_after();
-              issue_o(h, v, j >= ahead);
-              if (twin ? next : j + 1 < (h ? n1 : n0)) issue_s(h, twin ? 0 : h, kn);
-            }
+          const bool more = twin ? next : j + 1 < nh;
+          const uint64_t db = dv0 + (uint64_t)(v * (kTB >> 4));
+          const uint32_t add = j >= ahead;
+          const int left = end - j * kApTile;      // tokens of the tile that some row sees
+          if (mine) {
+            if (!wait(&s.p_full[h], np)) break;
+            np ^= 1u;
+            at_fence_after();
           }
-          if (!ok) break;
-          commit(&s.kv_empty[v]);
-          if (next) commit(&s.kv_empty[kn]);
-          if (j + ahead + 1 == n) commit(&s.q_empty);
+          if (at_elect()) {
+            if (mine) {
+#pragma unroll
+              for (int k = 0; k < kApTile / 16; k++)
+                if (16 * k < left) at_mma_ts(oc, sc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+              at_commit(&s.o_done[h]);
+              if (more) issue_s(da, kn);
+            }
+            at_commit(&s.kv_empty[v]);
+            if (next) at_commit(&s.kv_empty[kn]);
+            if (j + ahead + 1 == n) at_commit(&s.q_empty);
+          }
+          __syncwarp();
         }
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
       // every MMA issued has completed before tensor memory is released
-      commit(&s.drain);
-      mbar_wait_bounded(&s.drain, 0u);
+      if (at_elect()) at_commit(&s.drain[h]);
+      mbar_wait_bounded(&s.drain[h], 0u);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- Q rows, and the scan of masked tiles' v
-      const int ht = tid - 32 * kApWHelp;
-      int base = 0;
       uint32_t posted[3] = {0u, 0u, 0u};
-      int nq = 0;                                  // items whose Q was copied by boxes
+      int base = 0, nq = 0;                        // nq: items whose Q has been copied
       bool ok = true;
       for (int i = 0; ok; i++) {
         if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
         const ApItem it = s.item[i & 1];
         if (it.b < 0) break;
         const int n = it.n;
-        if (lane < 12) s.bad[i & 1][warp - kApWHelp][lane >> 2][lane & 3] = 0u;
+        if (lane < 12) s.bad[i & 1][lane >> 2][lane & 3] = 0u;
         __syncwarp();
         if (i > 0 && !mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u)) break;
-        if (p.q_boxes) {
-          // rows token by token, head by head: a box (64, group, 128 / group) is a
-          // row tile; rows past the request's are others' and not stored
-          if (ht == 0) {
-            const int boxes = it.rows > kApTile ? 2 : 1, per = kApTile / a.group;
-            mbar_arrive_expect_tx(&s.q_full, (uint32_t)(boxes * kTB));
-            for (int q = 0; q < boxes; q++)
-              for (int hf = 0; hf < kHalves; hf++)
-                at_tma_3d(q_smem + q * kTB + hf * (kApTile * 128), &p.qmap, 64 * hf, it.hk * a.group, it.first + it.tok0 + q * per,
-                          &s.q_full);
-            nq++;
-          }
-        } else {
-          // a thread copies 16-byte piece `ch` of every kStep-th row; the row's token
-          // and head follow by addition
-          constexpr int kChunks = D / 8, kStep = 64 / kChunks;
-          const int ch = ht % kChunks, r0 = ht / kChunks, top = it.rows > kApTile ? kApRows : kApTile;
-          const int dtok = (kStep * p.magic) >> 16, dg = kStep - dtok * a.group;
-          const long long adv = dtok * a.q.row + dg * a.q.head, wrap = a.q.row - a.group * a.q.head;
-          const int x0q = it.g0 + r0, t0q = (x0q * p.magic) >> 16;
-          int gq = x0q - t0q * a.group;
-          const uint16_t *src = a.q.p + (long long)(it.first + it.tok0 + t0q) * a.q.row +
-                                (long long)(it.hk * a.group + gq) * a.q.head + 8 * ch;
-          const uint32_t qd = q_smem + (uint32_t)(ch >> 3) * (kApTile * 128);
-#pragma unroll 4
-          for (int r = r0; r < top; r += kStep) {
-            const int rr = r & (kApTile - 1);
-            at_cp16(qd + (r >= kApTile ? kTB : 0) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), r < it.rows ? src : a.q.p,
-                    r < it.rows);
-            src += adv;
-            gq += dg;
-            if (gq >= a.group) {
-              gq -= a.group;
-              src += wrap;
-            }
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          at_fence_async();
-          mbar_arrive(&s.q_full);
+        // a box (64, group, per) is a row tile; rows past the item's tokens are
+        // others' or zeros, rows past the box what was there: none is stored
+        if (lane == 0) {
+          const int boxes = it.toks > p.per ? 2 : 1;
+          mbar_arrive_expect_tx(&s.q_full, (uint32_t)(boxes * p.per * a.group * D * 2));
+          for (int q = 0; q < boxes; q++)
+            for (int hf = 0; hf < kHalves; hf++)
+              at_tma_3d(q_smem + q * kTB + hf * (kApTile * 128), &p.qmap, 64 * hf, it.hk * a.group, it.first + it.tok0 + q * p.per,
+                        &s.q_full);
         }
-        // the MMA warp has seen this item's predecessor's scans: a barrier is
+        nq++;
+        // the MMA warps have seen this item's predecessor's scans: a barrier is
         // never a phase ahead of its reader
         if (i > 0 && !mbar_wait_bounded(&s.v_next, (uint32_t)(i - 1) & 1u)) break;
         for (int j = it.m0; j < n; j++) {
@@ -860,23 +807,26 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           else if (z == 1) posted[1] ^= 1u << (i & 1);
           else posted[2] ^= 1u << (i & 1);
           uint8_t *tile = generic0 + 2 * kTB + slot * kTB;
-          const int r0 = max(0, it.all - (it.j0 + j) * kApTile);      // earlier tokens are seen by every row
+          // earlier tokens are seen by every row; PV leaves out the groups of 16 past the last one that is seen
+          const int r0 = max(0, it.all - (it.j0 + j) * kApTile);
+          const int r1 = min(kApTile, (it.end - (it.j0 + j) * kApTile + 15) & ~15);
           for (int hf = 0; hf < kHalves; hf++)
-            for (int e = r0 * 8 + ht; e < kApTile * 8; e += 64) {
+#pragma unroll 4
+            for (int e = r0 * 8 + lane; e < r1 * 8; e += 32) {
               uint4 *at = reinterpret_cast<uint4 *>(tile + hf * (kApTile * 128)) + e;
               const uint4 w = *at;
               const uint32_t f[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
               if (f[0] | f[1] | f[2] | f[3]) {
                 uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int z = 0; z < 4; z++) u[z] &= ~(((f[z] >> 15) & 0x00010001u) * 0xFFFFu);
+                for (int w = 0; w < 4; w++) u[w] &= ~(((f[w] >> 15) & 0x00010001u) * 0xFFFFu);
                 *at = make_uint4(u[0], u[1], u[2], u[3]);
-                atomicOr(&s.bad[i & 1][warp - kApWHelp][j - it.m0][(e >> 3) >> 5], 1u << ((e >> 3) & 31));
+                atomicOr(&s.bad[i & 1][z][(e >> 3) >> 5], 1u << ((e >> 3) & 31));
               }
             }
           at_fence_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.v_clean[j - it.m0]);
+          if (lane == 0) mbar_arrive(&s.v_clean[z]);
         }
         base += 2 * n;
         __syncwarp();
@@ -903,9 +853,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const ApArgs p) {
   const AttnArgs &a = p.a;
   pdl_wait();
   const int4 d0 = __ldcg(p.desc + 2 * blockIdx.x), d1 = __ldcg(p.desc + 2 * blockIdx.x + 1);
-  const int first = d0.x, hk = d0.y, row0 = d0.z, rows = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
+  const int first = d0.x, hk = d0.y, tok0 = d0.z, toks = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), dg = threadIdx.x >> 5;
-  if (c1 < 0 || r >= rows) return;
+  const int rt = r & (kApTile - 1), dt = (rt * p.magic) >> 16, tl = (r / kApTile) * p.per + dt;   // as in the kernel above
+  if (c1 < 0 || dt >= p.per || tl >= toks) return;
   const float c = a.scale * 1.44269504088896340736f;
   constexpr int N = D / 32;                        // float4 of a thread
   const int nsrc = (c1 - c0 + 1) << twin;          // twins: two sources a part
@@ -956,7 +907,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const ApArgs p) {
       }
     }
   }
-  const int rr = row0 + r, i = rr / a.group, hq = hk * a.group + rr - i * a.group;
+  const int i = tok0 + tl, hq = hk * a.group + rt - dt * a.group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t *dst = a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + 4 * N * dg;
 #pragma unroll
@@ -993,12 +944,12 @@ cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, in
   return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Q rows of whole tokens as boxes, for groups that divide a row tile.
+// Row tiles of whole tokens, and their Q as boxes.
 cudaError_t encode_q(ApArgs *p) {
   const AttnArgs &a = p->a;
   p->magic = (65536 + a.group - 1) / a.group;
-  p->q_boxes = kApTile % a.group == 0;
-  return p->q_boxes ? encode_rows(&p->qmap, a.q, a.T, a.q_heads, a.group, kApTile / a.group, a) : cudaSuccess;
+  p->per = kApTile / a.group;
+  return encode_rows(&p->qmap, a.q, a.T, a.q_heads, a.group, p->per, a);
 }
 }  // namespace
 
@@ -1040,7 +991,7 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaSt
   if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, 1, kApTile, a);
   if (err != cudaSuccess) return err;
   // items at most: every request may end inside a row tile
-  const long long items = (((long long)a.T * a.group + kApRows - 1) / kApRows + a.B) * a.kv_heads;
+  const long long items = ((a.T + 2 * p.per - 1) / (2 * p.per) + a.B) * (long long)a.kv_heads;
   const int grid = (int)(items < num_sms ? items : num_sms);
   ap_kernel<false>(a.head_dim, a.f16)<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
   return cudaGetLastError();
