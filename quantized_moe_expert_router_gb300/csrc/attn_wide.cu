@@ -19,22 +19,24 @@
 // types; O and l stay fp32.
 //
 // One CTA per SM, 12 warps:
-//   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row, so the
+//   warp 0          key/value tiles by tensor-map copies (128-byte swizzle)
+//                   into a ring of stages: the key tile that S needs next with the
+//                   value tile that PV needs; takes the items
+//   warp 1          MMA issue: S of the next tile follows PV of this one, so one
+//                   row tile's softmax runs while the other's MMAs do.  The tensor
+//                   pipe's queue covers some 250 cycles of the issuer's way from
+//                   one operation to the next, hence one stage, one barrier and
+//                   few commits a tile (and not an issuer per row tile: their
+//                   MMAs mix, and each change of accumulator costs)
+//   warps 2-3       Q rows by tensor-map boxes (64, G, tokens); the scan below
+//   warps 4-7, 8-11 softmax of row tile 0 and 1: a thread owns a row, so the
 //                   maximum and the sum need no exchange between threads;
 //                   also the rare rescaling of O and the epilogue
-//   warp 8          key/value tiles by tensor-map copies (128-byte swizzle)
-//                   into a ring, in the order K0 K1 V0 K2 V1 ..; takes the items
-//   warps 9, 10     MMA issue for row tile 0 and 1: S of the next key tile follows
-//                   PV of this one, so one row tile's softmax runs while the
-//                   other's MMAs do.  An issuer's way from one operation to the
-//                   next (barriers, commits) takes some 500 cycles; with an issuer
-//                   each the tensor pipe has the other's work meanwhile
-//   warp 11         Q rows by tensor-map boxes (64, G, tokens); the scan below
 // Tensor memory: S0, S1 (128 columns each, P over their first 64), O0, O1.
 //
 // A tile past the last token that all rows see holds keys that some rows, or
 // all, may not see.  Their scores are replaced by -infinity, so P is 0; but 0
-// times an infinite or NaN v is NaN, so warp 11 scans those tiles' v, zeroes
+// times an infinite or NaN v is NaN, so warps 2-3 scan those tiles' v, zero
 // such elements and note their tokens, and the epilogue adds them to the
 // rows that do see the token.
 //
@@ -59,7 +61,7 @@ namespace moe {
 constexpr int kApThreads = 384;
 constexpr int kApRows = 256, kApTile = 128;      // rows of an item; rows of a row tile, tokens of a key tile
 constexpr int kApRegsSoft = 208, kApRegsRest = 88;
-constexpr int kApWTma = 8, kApWMma = 9, kApWHelp = 11;   // MMA warps 9, 10
+constexpr int kApWTma = 0, kApWMma = 1, kApWHelp = 2, kApWSoft = 4;
 constexpr int kApMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kApSlack = 8.f;                  // log2 of the largest P
 constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache)
@@ -68,8 +70,8 @@ constexpr int kApExtra = 6;                      // key tiles above the mean tha
 template <int D>
 struct ApGeom {
   static constexpr int kTileBytes = kApTile * D * 2;
-  static constexpr int kSlots = D == 128 ? 4 : 8;
-  static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024;
+  static constexpr int kStages = D == 128 ? 2 : 4; // of a key and a value tile
+  static constexpr int kSmem = 2 * kTileBytes + kStages * 2 * kTileBytes + 1024;
 };
 
 struct ApArgs {
@@ -101,12 +103,13 @@ struct ApItem {
 };
 
 struct ApSmem {
-  uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, sched_full[2], sched_empty[2], drain[2];
+  uint64_t kv_full[4], kv_empty[4];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int wsum[2][kApThreads / 32];
   ApItem item[2];
-  uint32_t bad[2][3][4];       // by item parity and masked tile: tokens with a non-finite v
+  int v_pos[2][3];             // by item parity: stages of the masked value tiles, counted from the CTA's start
+  uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
   union {
     struct {                   // prompts: requests by falling length
       uint16_t order[kApMaxB];
@@ -245,15 +248,12 @@ __device__ __forceinline__ float ap_max(const float (&v)[128]) {
   return at_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
 }
 
-// Position of V[j] in the ring order K0 K1 V0 K2 V1 .. V[n-1] of an item of n tiles.
-__device__ __forceinline__ int ap_pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
-
 template <int D, bool F16, bool PAGED>
 __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_constant__ ApArgs p) {
   extern __shared__ uint8_t dsm[];
   __shared__ ApSmem s;
   using G = ApGeom<D>;
-  constexpr int kSlots = G::kSlots, kTB = G::kTileBytes, kHalves = D / 64;
+  constexpr int kStages = G::kStages, kTB = G::kTileBytes, kHalves = D / 64;
   const AttnArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
@@ -262,25 +262,25 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
 
   if (warp == 0) {
     // a barrier a lane: one lane would take some 25 cycles for each of them
-    if (lane < kSlots) {
+    if (lane < kStages) {
       mbar_init(&s.kv_full[lane], 1);
-      mbar_init(&s.kv_empty[lane], 2);             // both MMA warps
+      mbar_init(&s.kv_empty[lane], 1);
     }
     if (lane < 2) {
       mbar_init(&s.s_full[lane], 1);
       mbar_init(&s.p_full[lane], 4);
       mbar_init(&s.o_done[lane], 1);
       mbar_init(&s.sched_full[lane], 1);
-      mbar_init(&s.sched_empty[lane], 11);         // 8 softmax warps, 2 MMA warps, warp 11
-      mbar_init(&s.drain[lane], 1);
+      mbar_init(&s.sched_empty[lane], 11);         // 8 softmax warps, MMA warp, 2 helper warps
     } else if (lane < 5) {
       mbar_init(&s.v_posted[0][lane - 2], 1);
       mbar_init(&s.v_posted[1][lane - 2], 1);
-      mbar_init(&s.v_clean[lane - 2], 1);
+      mbar_init(&s.v_clean[lane - 2], 2);
     } else if (lane == 5) {
       mbar_init(&s.q_full, 1);
-      mbar_init(&s.q_empty, 2);
-      mbar_init(&s.v_next, 2);
+      mbar_init(&s.q_empty, 1);
+      mbar_init(&s.v_next, 1);
+      mbar_init(&s.drain, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -383,13 +383,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   const float c = a.scale * 1.44269504088896340736f;
   if constexpr (PAGED) pdl_launch_dependents();    // the join's CTAs take the SMs as they fall free, and wait
 
-  if (warp < 8) {
+  if (warp >= kApWSoft) {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kApRegsSoft));
-    const int h = warp >> 2;
+    const int h = (warp - kApWSoft) >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tb + lanes + 128u * h, to = tb + lanes + 256u + 128u * h;
-    uint32_t ns = 0;                               // tiles of this half so far
+    uint32_t ns = 0, ni = 0;                       // key tiles of this row tile, and items with any, so far
     bool ok = true;
     for (int i = 0;; i++) {
       if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) {
@@ -448,12 +448,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           m = m1;
           l2.x *= f;
           l2.y *= f;
-          if (!mbar_wait_bounded(&s.o_done[h], (ns - 1u) & 1u)) {
-            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-            ok = false;
-            break;
-          }
-          at_fence_after();
+          // PV of the tile before is done: S of this one was issued behind it
 #pragma unroll 1
           for (int q = 0; q < D / 32; q++) {
             float o[32];
@@ -482,17 +477,17 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       }
       if (!ok) break;
       const float l = l2.x + l2.y;
-      if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (tid & 255)] = make_float2(m, l);
+      if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (kApTile * h + (tid & 127))] = make_float2(m, l);
       if (nt > 0) {
         // ---------------------------------------------------------- epilogue
-        if (!mbar_wait_bounded(&s.o_done[h], (ns - 1u) & 1u)) {
+        if (!mbar_wait_bounded(&s.o_done[h], ni++ & 1u)) {
           atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
           break;
         }
         at_fence_after();
         uint32_t anybad = 0;
 #pragma unroll
-        for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][w >> 2][w & 3];
+        for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
         if (anybad) {
 #pragma unroll 1
           for (int q = 0; q < D / 32; q++) {
@@ -500,7 +495,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             at_ld32(to + 32u * q, o);
             at_wait_ld(o);
             for (int w = 0; w < 12; w++) {
-              for (uint32_t bits = s.bad[i & 1][w >> 2][w & 3]; bits; bits &= bits - 1) {
+              uint32_t bits = s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
+              for (; bits; bits &= bits - 1) {
                 const int jl = it.m0 + (w >> 2);   // tile of the part
                 if (PAGED && it.twin && (jl & 1) != h) continue;
                 const int tok = (it.j0 + jl) * kApTile + 32 * (w & 3) + __ffs(bits) - 1;
@@ -528,7 +524,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
         if (PAGED && it.slot >= 0) {
           // [element / 4][row]: the 32 rows of a warp side by side
-          float4 *part = p.part + (size_t)it.slot * (D / 4) * kApRows + (tid & 255);
+          float4 *part = p.part + (size_t)it.slot * (D / 4) * kApRows + (kApTile * h + (tid & 127));
 #pragma unroll 1
           for (int q = 0; q < D / 32; q++) {
             float o[32];
@@ -613,46 +609,57 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
           if (it.b < 0) break;
           if (!PAGED) next = gridDim.x + atomicAdd(p.ctrl + kAttnCtrlNext, 1);
-          const int n = it.n;
-          for (int q = 0; q < 2 * n; q++, pos++) {
-            // K0 K1 V0 K2 V1 .. K[n-1] V[n-2] V[n-1]
-            const bool isk = q < 2 * n - 1 && (q == 0 || (q & 1));
-            const int j = it.j0 + (isk ? (q + 1) >> 1 : (q == 2 * n - 1 ? n - 1 : (q >> 1) - 1));
-            const int slot = pos % kSlots;
-            int page = 0;
+          // stage q: K[q] and V[q - ahead], as far as they are there
+          const int n = it.n, ahead = PAGED && it.twin ? 2 : 1;
+          for (int q = 0; q < n + ahead; q++) {
+            if (q >= n && q < ahead) continue;
+            const int slot = pos % kStages;
+            int page[2] = {0, 0};
             if constexpr (PAGED) {
-              const int col = (j * kApTile >> a.page_shift) + lane;
-              const int id = lane < kApTile >> a.page_shift && col < a.max_pages
-                                 ? __ldg(a.block_table + (size_t)it.b * a.max_pages + col) : -1;
-              page = (unsigned)id < (unsigned)a.num_pages ? id : a.num_pages;   // past the end: reads zeros
+#pragma unroll
+              for (int z = 0; z < 2; z++) {
+                const int col = ((it.j0 + q - z * ahead) * kApTile >> a.page_shift) + lane;
+                const bool here = (z ? q >= ahead : q < n) && lane < kApTile >> a.page_shift && col < a.max_pages;
+                const int id = here ? __ldg(a.block_table + (size_t)it.b * a.max_pages + col) : -1;
+                page[z] = (unsigned)id < (unsigned)a.num_pages ? id : a.num_pages;   // past the end: reads zeros
+              }
             }
-            if (pos >= kSlots && !mbar_wait_bounded(&s.kv_empty[slot], (uint32_t)(pos / kSlots - 1) & 1u)) {
+            if (pos >= kStages && !mbar_wait_bounded(&s.kv_empty[slot], (uint32_t)(pos / kStages - 1) & 1u)) {
               atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
               ok = false;
               break;
             }
             if (lane == 0) {
-              mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)kTB);
-              // the scan may wait for this tile now: before, the barrier may still
+              mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)(kTB * ((q < n) + (q >= ahead))));
+              // the scan may wait for this stage now: before, the barrier may still
               // be in an earlier phase, which a wait cannot tell from this one
-              if (!isk && j - it.j0 >= it.m0) mbar_arrive(&s.v_posted[i & 1][j - it.j0 - it.m0]);
+              if (q - ahead >= it.m0) {
+                s.v_pos[i & 1][q - ahead - it.m0] = pos;
+                mbar_arrive(&s.v_posted[i & 1][q - ahead - it.m0]);
+              }
             }
-            if constexpr (PAGED) {
-              __syncwarp();
-              if (lane < kApTile >> a.page_shift)
-                for (int hf = 0; hf < kHalves; hf++)
-                  at_tma_4d(ring + slot * kTB + hf * (kApTile * 128) + ((uint32_t)lane << (a.page_shift + 7)),
-                            isk ? &p.kmap : &p.vmap, 64 * hf, 0, it.hk, page, &s.kv_full[slot]);
-            } else {
-              for (int hf = 0; hf < kHalves; hf++)
-                at_tma_3d(ring + slot * kTB + hf * (kApTile * 128), isk ? &p.kmap : &p.vmap, 64 * hf, it.hk,
-                          it.first + j * kApTile, &s.kv_full[slot]);
+            if constexpr (PAGED) __syncwarp();
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+              if (!(z ? q >= ahead : q < n)) continue;
+              const uint32_t dst = ring + (2 * slot + z) * kTB;
+              for (int hf = 0; hf < kHalves; hf++) {
+                if constexpr (PAGED) {
+                  if (lane < kApTile >> a.page_shift)
+                    at_tma_4d(dst + hf * (kApTile * 128) + ((uint32_t)lane << (a.page_shift + 7)), z ? &p.vmap : &p.kmap, 64 * hf, 0,
+                              it.hk, page[z], &s.kv_full[slot]);
+                } else {
+                  at_tma_3d(dst + hf * (kApTile * 128), z ? &p.vmap : &p.kmap, 64 * hf, it.hk,
+                            it.first + (it.j0 + q - z * ahead) * kApTile, &s.kv_full[slot]);
+                }
+              }
             }
+            pos++;
           }
         }
         // copies in flight land before the CTA ends
-        for (int q = (pos > kSlots ? pos - kSlots : 0); q < pos; q++)
-          mbar_wait_bounded(&s.kv_full[q % kSlots], (uint32_t)(q / kSlots) & 1u);
+        for (int q = (pos > kStages ? pos - kStages : 0); q < pos; q++)
+          mbar_wait_bounded(&s.kv_full[q % kStages], (uint32_t)(q / kStages) & 1u);
         if (!PAGED) {
           // the last CTA to have taken its last item leaves the counters at zero
           __threadfence();
@@ -663,17 +670,16 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
       }
       __syncwarp();
-    } else if (warp < kApWHelp) {
+    } else if (warp == kApWMma) {
       // ---------------------------------------------------------- MMA issue
       // The whole warp goes through the loop, so that what the instructions take
       // (descriptors, tensor-memory columns) stays in uniform registers and costs
       // one addition; one elected lane issues.
       constexpr uint32_t id_s = at_idesc(F16, kApTile, false), id_o = at_idesc(F16, D, true);
-      const int h = __shfl_sync(kFull, warp, 0) - kApWMma;   // the warp's row tile
-      const uint32_t tu = __shfl_sync(kFull, tb, 0), sc = tu + 128u * h, oc = tu + 256u + 128u * h;
-      const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring, kApTile * 128);
-      int slot = 0;                                // ring slot and phase of the next position
-      uint32_t phase = 0, clean = 0, np = 0;
+      const uint32_t tu = __shfl_sync(kFull, tb, 0);
+      const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring + kTB, kApTile * 128);
+      int slot = 0;                                // next stage and its phase
+      uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok && !mbar_wait_bounded(bar, parity)) {
@@ -683,22 +689,18 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         ok = __all_sync(kFull, ok);
         return ok;
       };
-      // the next position of the ring: its slot, once it is full
-      auto take = [&]() {
-        const int at = slot;
-        wait(&s.kv_full[at], phase);
-        if (++slot == kSlots) {
+      auto next_stage = [&]() {
+        if (++slot == kStages) {
           slot = 0;
           phase ^= 1u;
         }
-        return at;
       };
-      auto issue_s = [&](uint64_t da, int at) {    // S = Q K: by the elected lane, K in slot `at`
-        const uint64_t db = dk0 + (uint64_t)(at * (kTB >> 4));
+      auto issue_s = [&](int h, int q) {           // S of row tile h = Q of row tile q K: by the elected lane
+        const uint64_t da = dq0 + (uint64_t)(q * (kTB >> 4)), db = dk0 + (uint64_t)(slot * (2 * kTB >> 4));
 #pragma unroll
         for (int k = 0; k < D / 16; k++) {
           const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32) >> 4;
-          at_mma_ss(sc, da + off, db + off, id_s, k > 0);
+          at_mma_ss(tu + 128u * h, da + off, db + off, id_s, k > 0);
         }
         at_commit(&s.s_full[h]);
       };
@@ -707,83 +709,89 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const ApItem &im = s.item[i & 1];
         if (__shfl_sync(kFull, im.b, 0) < 0) break;
         const int n = __shfl_sync(kFull, im.n, 0), m0 = __shfl_sync(kFull, im.m0, 0);
-        const int nh = __shfl_sync(kFull, h ? im.n1 : im.n0, 0);
+        const int n0 = __shfl_sync(kFull, im.n0, 0), n1 = __shfl_sync(kFull, im.n1, 0);
         const int end = __shfl_sync(kFull, im.end - im.j0 * kApTile, 0);   // tokens of the part from here on are seen by none
         const bool twin = PAGED && __shfl_sync(kFull, im.twin, 0);
-        const uint64_t da = dq0 + (uint64_t)((twin ? 0 : h) * (kTB >> 4));
         const int ahead = twin ? 2 : 1;            // S of tile j + ahead follows PV of tile j
         if (!wait(&s.q_full, (uint32_t)i & 1u)) break;
-        // K0, and for twins K1, one each
         for (int j = 0; j < ahead && j < n; j++) {
-          const int at = take();
-          if (!ok) break;
+          if (!wait(&s.kv_full[slot], phase)) break;
           at_fence_after();
           if (at_elect()) {
-            if (twin ? j == h : nh > 0) issue_s(da, at);
-            at_commit(&s.kv_empty[at]);
+            if (twin) {
+              issue_s(j, 0);
+            } else {
+              issue_s(0, 0);
+              if (n1 > 0) issue_s(1, 1);
+            }
+            at_commit(&s.kv_empty[slot]);
             if (j + 1 == n) at_commit(&s.q_empty);
           }
           __syncwarp();
+          next_stage();
         }
-        // ring order: K0 K1 V0 K2 V1 ..; of two row tiles K[j + 1] is taken before V[j], of twins K[j + 2] after it
         for (int j = 0; j < n && ok; j++) {
-          const bool next = j + ahead < n, mine = twin ? (j & 1) == h : j < nh;
-          int kn = 0;
-          if (!twin && next) kn = take();
-          const int v = take();
-          if (twin && next) kn = take();
+          if (!wait(&s.kv_full[slot], phase)) break;
           if (j >= m0) {
             const int z = j - m0;                  // 0, 1 or 2; a phase bit each
-            if (mine) wait(&s.v_clean[z], (clean >> z) & 1u);
+            if (!wait(&s.v_clean[z], (clean >> z) & 1u)) break;
             clean ^= 1u << z;
           }
           if (j + 1 == n && lane == 0) mbar_arrive(&s.v_next);   // the next item's scans may signal
-          if (!ok) break;
-          const bool more = twin ? next : j + 1 < nh;
-          const uint64_t db = dv0 + (uint64_t)(v * (kTB >> 4));
-          const uint32_t add = j >= ahead;
           const int left = end - j * kApTile;      // tokens of the tile that some row sees
-          if (mine) {
-            if (!wait(&s.p_full[h], np)) break;
-            np ^= 1u;
-            at_fence_after();
-          }
-          if (at_elect()) {
-            if (mine) {
+          const uint64_t db = dv0 + (uint64_t)(slot * (2 * kTB >> 4));
+          const uint32_t add = j >= ahead;
 #pragma unroll
-              for (int k = 0; k < kApTile / 16; k++)
-                if (16 * k < left) at_mma_ts(oc, sc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
-              at_commit(&s.o_done[h]);
-              if (more) issue_s(da, kn);
+          for (int h = 0; h < 2; h++) {
+            const int nh = h ? n1 : n0;
+            if (twin ? (j & 1) == h : j < nh) {
+              uint32_t &np = h ? np1 : np0;
+              const bool more = twin ? j + 2 < n : j + 1 < nh;
+              if (!wait(&s.p_full[h], np)) break;
+              np ^= 1u;
+              at_fence_after();
+              if (at_elect()) {
+#pragma unroll
+                for (int k = 0; k < kApTile / 16; k++)
+                  if (16 * k < left)
+                    at_mma_ts(tu + 256u + 128u * h, tu + 128u * h + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                if (more) issue_s(h, twin ? 0 : h);
+                else at_commit(&s.o_done[h]);      // the row tile's last
+              }
+              __syncwarp();
             }
-            at_commit(&s.kv_empty[v]);
-            if (next) at_commit(&s.kv_empty[kn]);
+          }
+          if (!ok) break;
+          if (at_elect()) {
+            at_commit(&s.kv_empty[slot]);
             if (j + ahead + 1 == n) at_commit(&s.q_empty);
           }
           __syncwarp();
+          next_stage();
         }
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
       // every MMA issued has completed before tensor memory is released
-      if (at_elect()) at_commit(&s.drain[h]);
-      mbar_wait_bounded(&s.drain[h], 0u);
+      if (at_elect()) at_commit(&s.drain);
+      mbar_wait_bounded(&s.drain, 0u);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- Q rows, and the scan of masked tiles' v
+      const int ht = tid - 32 * kApWHelp;
       uint32_t posted[3] = {0u, 0u, 0u};
-      int base = 0, nq = 0;                        // nq: items whose Q has been copied
+      int nq = 0;                                  // items whose Q has been copied
       bool ok = true;
       for (int i = 0; ok; i++) {
         if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
         const ApItem it = s.item[i & 1];
         if (it.b < 0) break;
         const int n = it.n;
-        if (lane < 12) s.bad[i & 1][lane >> 2][lane & 3] = 0u;
+        if (lane < 12) s.bad[i & 1][warp - kApWHelp][lane >> 2][lane & 3] = 0u;
         __syncwarp();
         if (i > 0 && !mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u)) break;
         // a box (64, group, per) is a row tile; rows past the item's tokens are
         // others' or zeros, rows past the box what was there: none is stored
-        if (lane == 0) {
+        if (ht == 0) {
           const int boxes = it.toks > p.per ? 2 : 1;
           mbar_arrive_expect_tx(&s.q_full, (uint32_t)(boxes * p.per * a.group * D * 2));
           for (int q = 0; q < boxes; q++)
@@ -792,27 +800,31 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                         &s.q_full);
         }
         nq++;
-        // the MMA warps have seen this item's predecessor's scans: a barrier is
+        // the MMA warp has seen this item's predecessor's scans: a barrier is
         // never a phase ahead of its reader
         if (i > 0 && !mbar_wait_bounded(&s.v_next, (uint32_t)(i - 1) & 1u)) break;
         for (int j = it.m0; j < n; j++) {
-          const int pv = base + ap_pos_v(j, n), slot = pv % kSlots, z = j - it.m0;
+          const int z = j - it.m0;
           const uint32_t ph = z == 0 ? posted[0] : (z == 1 ? posted[1] : posted[2]);   // by item parity: bit i & 1
-          if (!mbar_wait_bounded(&s.v_posted[i & 1][z], (ph >> (i & 1)) & 1u) ||
-              !mbar_wait_bounded(&s.kv_full[slot], (uint32_t)(pv / kSlots) & 1u)) {
+          if (!mbar_wait_bounded(&s.v_posted[i & 1][z], (ph >> (i & 1)) & 1u)) {
+            ok = false;
+            break;
+          }
+          const int pos = s.v_pos[i & 1][z], slot = pos % kStages;
+          if (!mbar_wait_bounded(&s.kv_full[slot], (uint32_t)(pos / kStages) & 1u)) {
             ok = false;
             break;
           }
           if (z == 0) posted[0] ^= 1u << (i & 1);
           else if (z == 1) posted[1] ^= 1u << (i & 1);
           else posted[2] ^= 1u << (i & 1);
-          uint8_t *tile = generic0 + 2 * kTB + slot * kTB;
+          uint8_t *tile = generic0 + 2 * kTB + (2 * slot + 1) * kTB;
           // earlier tokens are seen by every row; PV leaves out the groups of 16 past the last one that is seen
           const int r0 = max(0, it.all - (it.j0 + j) * kApTile);
           const int r1 = min(kApTile, (it.end - (it.j0 + j) * kApTile + 15) & ~15);
           for (int hf = 0; hf < kHalves; hf++)
 #pragma unroll 4
-            for (int e = r0 * 8 + lane; e < r1 * 8; e += 32) {
+            for (int e = r0 * 8 + ht; e < r1 * 8; e += 64) {
               uint4 *at = reinterpret_cast<uint4 *>(tile + hf * (kApTile * 128)) + e;
               const uint4 w = *at;
               const uint32_t f[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
@@ -821,14 +833,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
 #pragma unroll
                 for (int w = 0; w < 4; w++) u[w] &= ~(((f[w] >> 15) & 0x00010001u) * 0xFFFFu);
                 *at = make_uint4(u[0], u[1], u[2], u[3]);
-                atomicOr(&s.bad[i & 1][z][(e >> 3) >> 5], 1u << ((e >> 3) & 31));
+                atomicOr(&s.bad[i & 1][warp - kApWHelp][z][(e >> 3) >> 5], 1u << ((e >> 3) & 31));
               }
             }
           at_fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.v_clean[z]);
         }
-        base += 2 * n;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
