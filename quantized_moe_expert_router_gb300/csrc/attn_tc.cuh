@@ -176,9 +176,19 @@ __device__ __forceinline__ float at_value(uint16_t v) {
   else return __uint_as_float((uint32_t)v << 16);
 }
 
-// x / d for 0 <= x, 0 < d: the 64-bit division is a long software routine.
+// x / d for 0 <= x, 0 < d.  Up to 2^22 by a reciprocal, whose quotient is off by
+// one at most there, put right by the remainder: a fifth of the latency of the
+// integer division, which the start of a short call would pay several times in
+// a row (and the 64-bit one is a longer routine still).
+__device__ __forceinline__ int at_idiv(int x, int d) {
+  if ((x | d) >> 22) return x / d;
+  int q = (int)(__int2float_rn(x) * __frcp_rn(__int2float_rn(d)));
+  const int r = x - q * d;
+  q += (r >= d) - (r < 0);
+  return q;
+}
 __device__ __forceinline__ long long at_div(long long x, long long d) {
-  return (x | d) >> 32 ? x / d : (long long)((uint32_t)x / (uint32_t)d);
+  return (x | d) >> 31 ? x / d : (long long)at_idiv((int)x, (int)d);
 }
 
 // The share of a CTA in the line of units (chunks or key tiles) of all items.
@@ -228,7 +238,7 @@ __device__ __forceinline__ AtShare at_share(const long long *work, int B, long l
     // the smallest len of 32 candidates that does with the CTAs there are
     const int len0 = max(min_len, (int)mean), step = (extra + 30) / 31, len = len0 + lane * step;
     int parts = 0;
-    for (int b = warp; b < B; b += NW) parts += items(b) * ((nch(b) + len - 1) / len);
+    for (int b = warp; b < B; b += NW) parts += items(b) * at_idiv(nch(b) + len - 1, len);
     scratch[warp][lane] = parts;
     __syncthreads();
     parts = 0;
@@ -239,7 +249,7 @@ __device__ __forceinline__ AtShare at_share(const long long *work, int B, long l
       r.len = len0 + (__ffs(fits) - 1) * step;
       int before = 0;
       for (int b0 = 0; b0 < B; b0 += 32) {
-        const int b = b0 + lane, n = b < B ? nch(b) : 1, per_item = (n + r.len - 1) / r.len;
+        const int b = b0 + lane, n = b < B ? nch(b) : 1, per_item = at_idiv(n + r.len - 1, r.len);
         const int v = b < B ? items(b) * per_item : 0;
         int incl = v;
 #pragma unroll
@@ -251,7 +261,7 @@ __device__ __forceinline__ AtShare at_share(const long long *work, int B, long l
         const unsigned mine = __ballot_sync(kFull, at >= 0 && at < v);
         if (mine) {
           const int src = __ffs(mine) - 1, pi = __shfl_sync(kFull, per_item, src), place = __shfl_sync(kFull, at, src);
-          const int nn = __shfl_sync(kFull, n, src), item = place / pi, k = place - item * pi;
+          const int nn = __shfl_sync(kFull, n, src), item = at_idiv(place, pi), k = place - item * pi;
           const long long item0 = work[b0 + src] + (long long)item * nn;
           r.x0 = item0 + (long long)k * r.len;
           r.x1 = min(r.x0 + r.len, item0 + nn);

@@ -119,7 +119,7 @@ __device__ __forceinline__ AtPos at_pos(const AtSmem &s, const AttnArgs &a, long
   const long long off = x - s.work[lo];
   const int item = (int)at_div(off, p.nch);
   p.chunk = (int)(off - (long long)item * p.nch);
-  p.hk = item / p.tiles;
+  p.hk = at_idiv(item, p.tiles);
   p.rt = item - p.hk * p.tiles;
   return p;
 }
@@ -155,9 +155,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
   uint8_t *const gring = gen0 + warp * (kAtStages * kAtStageBytes);
   float *const join = reinterpret_cast<float *>(gen0 + kAtWarps * kAtStages * kAtStageBytes);
 
-  if (tid == 0) {
-    for (int w = 0; w < kAtWarps; w++)
-      for (int i = 0; i < kAtStages; i++) mbar_init(&s.full[w][i], 1);
+  if (tid < kAtWarps * kAtStages) {
+    mbar_init(&s.full[0][0] + tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // the line of chunks, every CTA alike
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tree_kernel(const __grid_c
     const int first = s.first[b], n = s.n[b], cached = s.cached[b];
     const int ctx = (int)min((long long)cached + n, (long long)a.max_pages << a.page_shift);
     const int rows = (int)min((long long)kRows, (long long)n * a.group - row0);
-    const int i0 = row0 / a.group, g0 = row0 - i0 * a.group;
+    const int i0 = at_idiv(row0, a.group), g0 = row0 - i0 * a.group;
     // fresh row and query head of row r of the item
     auto row_of = [&](int r, int &i, int &hq) {
       const int dt = ((g0 + r) * p.magic) >> 16;

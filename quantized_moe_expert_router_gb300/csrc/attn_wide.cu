@@ -63,6 +63,7 @@ constexpr int kApRows = 256, kApTile = 128;      // rows of an item; rows of a r
 constexpr int kApRegsSoft = 208, kApRegsRest = 88;
 constexpr int kApWTma = 0, kApWMma = 1, kApWHelp = 2, kApWSoft = 4;
 constexpr int kApMaxB = MOE_ATTN_MAX_REQUESTS;
+constexpr int kApMaxSms = 1024;                  // CTAs of the wide kernel at most
 constexpr float kApSlack = 8.f;                  // log2 of the largest P
 constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache)
 constexpr int kApExtra = 6;                      // key tiles above the mean that are cheaper than a second part in a CTA
@@ -127,7 +128,7 @@ struct ApSmem {
 
 // Of a request of n fresh rows over the cache: items of a kv head, and key
 // tiles that its rows may see.
-__device__ __forceinline__ int cache_tiles(const ApArgs &p, int n) { return (n + 2 * p.per - 1) / (2 * p.per); }
+__device__ __forceinline__ int cache_tiles(const ApArgs &p, int n) { return at_idiv(n + 2 * p.per - 1, 2 * p.per); }
 __device__ __forceinline__ int cache_nch(const AttnArgs &a, int n, int cached) {
   const long long ctx = min((long long)cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n), (long long)a.max_pages << a.page_shift);
   return (int)((ctx + kApTile - 1) / kApTile);
@@ -137,7 +138,7 @@ __device__ __forceinline__ int cache_nch(const AttnArgs &a, int n, int cached) {
 // the k longest requests.
 __device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, int idx, ApItem &it) {
   const AttnArgs &a = p.a;
-  const int e = idx / a.kv_heads;
+  const int e = at_idiv(idx, a.kv_heads);
   it.hk = idx - e * a.kv_heads;
   int lo = 0, hi = a.B - 1;                        // largest k with before[k] <= e
   while (lo < hi) {
@@ -145,8 +146,9 @@ __device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, in
     if (s.before[mid] <= e) lo = mid; else hi = mid - 1;
   }
   const int k = lo + 1, off = e - s.before[lo];
-  it.tok0 = (s.tiles[lo] - 1 - off / k) * 2 * p.per;
-  it.b = s.order[off % k];
+  const int lvl = at_idiv(off, k);
+  it.tok0 = (s.tiles[lo] - 1 - lvl) * 2 * p.per;
+  it.b = s.order[off - lvl * k];
   it.first = __ldg(a.cu + it.b);
   it.toks = min(min(__ldg(a.cu + it.b + 1), a.T) - it.first - it.tok0, 2 * p.per);
   it.n0 = (it.tok0 + min(it.toks, p.per) - 1) / kApTile + 1;
@@ -175,7 +177,7 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
   const int n = s.n[lo], tiles = cache_tiles(p, n), nch = cache_nch(a, n, it.cached);
   const int item = (int)at_div(x - s.work[lo], nch);
   const long long item0 = s.work[lo] + (long long)item * nch, xe = min(share.x1, item0 + nch);
-  it.hk = item / tiles;
+  it.hk = at_idiv(item, tiles);
   it.tok0 = (item - it.hk * tiles) * 2 * p.per;
   it.toks = min(n - it.tok0, 2 * p.per);
   const long long lim = min((long long)a.max_pages << a.page_shift, (long long)it.cached + n);
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     // requests by falling number of row tiles (equal ones by index), every CTA alike
     for (int b = tid; b < a.B; b += kApThreads) {
       const int lo = __ldg(a.cu + b), n = max(0, min(__ldg(a.cu + b + 1), a.T) - lo);
-      s.before[b] = lo < 0 ? 0 : (n + 2 * p.per - 1) / (2 * p.per);
+      s.before[b] = lo < 0 ? 0 : at_idiv(n + 2 * p.per - 1, 2 * p.per);
     }
     __syncthreads();
     for (int b = tid; b < a.B; b += kApThreads) {
@@ -751,10 +753,14 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
               np ^= 1u;
               at_fence_after();
               if (at_elect()) {
+                const uint32_t oc = tu + 256u + 128u * h, pc = tu + 128u * h;
+                if (left >= kApTile) {
 #pragma unroll
-                for (int k = 0; k < kApTile / 16; k++)
-                  if (16 * k < left)
-                    at_mma_ts(tu + 256u + 128u * h, tu + 128u * h + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  for (int k = 0; k < kApTile / 16; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                } else {
+#pragma unroll 1
+                  for (int k = 0; 16 * k < left; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                }
                 if (more) issue_s(h, twin ? 0 : h);
                 else at_commit(&s.o_done[h]);      // the row tile's last
               }
@@ -855,19 +861,14 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   }
 }
 
-// Joins the parts of the items that several CTAs took, in the order of the
-// context: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A CTA takes 32
-// rows of an item; a thread one row and D / 8 of its elements, so that a warp
-// reads 32 rows side by side.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) attn_join_kernel(const ApArgs p) {
+__device__ __forceinline__ void join_rows(const ApArgs &p, int which, int group) {
   const AttnArgs &a = p.a;
-  pdl_wait();
-  const int4 d0 = __ldcg(p.desc + 2 * blockIdx.x), d1 = __ldcg(p.desc + 2 * blockIdx.x + 1);
+  const int4 d0 = __ldcg(p.desc + 2 * which), d1 = __ldcg(p.desc + 2 * which + 1);
   const int first = d0.x, hk = d0.y, tok0 = d0.z, toks = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
-  const int r = blockIdx.y * 32 + (threadIdx.x & 31), dg = threadIdx.x >> 5;
+  const int r = group * 32 + (threadIdx.x & 31), dg = threadIdx.x >> 5;
   const int rt = r & (kApTile - 1), dt = (rt * p.magic) >> 16, tl = (r / kApTile) * p.per + dt;   // as in the kernel above
-  if (c1 < 0 || dt >= p.per || tl >= toks) return;
+  if (dt >= p.per || tl >= toks) return;
   const float c = a.scale * 1.44269504088896340736f;
   constexpr int N = D / 32;                        // float4 of a thread
   const int nsrc = (c1 - c0 + 1) << twin;          // twins: two sources a part
@@ -928,14 +929,42 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const ApArgs p) {
   if (a.lse && dg == 0) a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
 }
 
+// Joins the parts of the items that several CTAs took, in the order of the
+// context: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A CTA takes 32
+// rows of an item at a time; a thread one row and D / 8 of its elements, so that a
+// warp reads 32 rows side by side.  The items to join are few and anywhere among
+// the CTAs' descriptions: every CTA looks all of them over and takes its share.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ApArgs p, int sms) {
+  __shared__ int16_t list[kApMaxSms];
+  __shared__ int count;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int k0 = 0; k0 < sms; k0 += 32) {
+      const bool has = k0 + lane < sms && __ldcg(&p.desc[2 * (k0 + lane) + 1].y) >= 0;
+      const unsigned mask = __ballot_sync(kFull, has);
+      if (has) list[n + __popc(mask & ((1u << lane) - 1u))] = (int16_t)(k0 + lane);
+      n += __popc(mask);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  for (int unit = blockIdx.x; unit < count * (kApRows / 32); unit += gridDim.x)
+    join_rows<D, F16>(p, list[unit / (kApRows / 32)], unit % (kApRows / 32));
+}
+
+
 namespace {
 typedef void (*ApKernel)(const ApArgs);
+typedef void (*ApJoin)(const ApArgs, int);
 template <bool PAGED>
 ApKernel ap_kernel(int head_dim, int f16) {
   if (head_dim == 64) return f16 ? attn_wide_kernel<64, true, PAGED> : attn_wide_kernel<64, false, PAGED>;
   return f16 ? attn_wide_kernel<128, true, PAGED> : attn_wide_kernel<128, false, PAGED>;
 }
-ApKernel ap_join(int head_dim, int f16) {
+ApJoin ap_join(int head_dim, int f16) {
   if (head_dim == 64) return f16 ? attn_join_kernel<64, true> : attn_join_kernel<64, false>;
   return f16 ? attn_join_kernel<128, true> : attn_join_kernel<128, false>;
 }
@@ -1020,10 +1049,11 @@ cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWide
   if (err == cudaSuccess) err = attn_encode_cache(&p.kmap, a.k_cache, a, 1 << a.page_shift);
   if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 1 << a.page_shift);
   if (err != cudaSuccess) return err;
+  if (num_sms > kApMaxSms) num_sms = kApMaxSms;
   ap_kernel<true>(a.head_dim, a.f16)<<<num_sms, kApThreads, ap_smem(a.head_dim), stream>>>(p);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_sms, kApRows / 32);
+  cfg.gridDim = dim3((unsigned)(2 * num_sms));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -1031,7 +1061,7 @@ cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWide
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ap_join(a.head_dim, a.f16), p);
+  return cudaLaunchKernelEx(&cfg, ap_join(a.head_dim, a.f16), p, num_sms);
 }
 
 }  // namespace moe
