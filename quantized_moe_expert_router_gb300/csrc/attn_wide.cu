@@ -861,100 +861,80 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   }
 }
 
-template <int D, bool F16>
-__device__ __forceinline__ void join_rows(const ApArgs &p, int which, int group) {
-  const AttnArgs &a = p.a;
-  const int4 d0 = __ldcg(p.desc + 2 * which), d1 = __ldcg(p.desc + 2 * which + 1);
-  const int first = d0.x, hk = d0.y, tok0 = d0.z, toks = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
-  const int r = group * 32 + (threadIdx.x & 31), dg = threadIdx.x >> 5;
-  const int rt = r & (kApTile - 1), dt = (rt * p.magic) >> 16, tl = (r / kApTile) * p.per + dt;   // as in the kernel above
-  if (dt >= p.per || tl >= toks) return;
-  const float c = a.scale * 1.44269504088896340736f;
-  constexpr int N = D / 32;                        // float4 of a thread
-  const int nsrc = (c1 - c0 + 1) << twin;          // twins: two sources a part
-  // source q's row in the parts' buffers
-  auto at_of = [&](int q) {
-    const int k = c0 + (q >> twin);
-    return (size_t)(k == c0 ? slot0 : 2 * k) * kApRows + r + (twin && (q & 1) ? kApTile : 0);
-  };
-  float top = -INFINITY, sum = 0.f;
-  float4 acc[N];
-#pragma unroll
-  for (int e = 0; e < N; e++) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // four sources at a time, so that their loads wait together
-  for (int q0 = 0; q0 < nsrc; q0 += 4) {
-    float2 st[4];
-    float4 u[4][N];
-#pragma unroll
-    for (int z = 0; z < 4; z++) {
-      const size_t at = at_of(min(q0 + z, nsrc - 1)), slot = at / kApRows, row = at - slot * kApRows;
-      st[z] = __ldcg(p.stat + at);
-#pragma unroll
-      for (int e = 0; e < N; e++) u[z][e] = __ldcg(p.part + (slot * (D / 4) + N * dg + e) * kApRows + row);
-    }
-    float t1 = top;
-#pragma unroll
-    for (int z = 0; z < 4; z++) t1 = fmaxf(t1, st[z].x);
-    const float f0 = top == -INFINITY ? 1.f : at_exp2((top - t1) * c);
-    top = t1;
-    sum *= f0;
-#pragma unroll
-    for (int e = 0; e < N; e++) {
-      acc[e].x *= f0;
-      acc[e].y *= f0;
-      acc[e].z *= f0;
-      acc[e].w *= f0;
-    }
-#pragma unroll
-    for (int z = 0; z < 4; z++) {
-      if (q0 + z >= nsrc || st[z].y == 0.f) continue;   // a part in which the row sees nothing (it may hold no O)
-      const float f = at_exp2((st[z].x - top) * c);
-      sum = fmaf(st[z].y, f, sum);
-#pragma unroll
-      for (int e = 0; e < N; e++) {
-        acc[e].x = fmaf(u[z][e].x, f, acc[e].x);
-        acc[e].y = fmaf(u[z][e].y, f, acc[e].y);
-        acc[e].z = fmaf(u[z][e].z, f, acc[e].z);
-        acc[e].w = fmaf(u[z][e].w, f, acc[e].w);
-      }
-    }
-  }
-  const int i = tok0 + tl, hq = hk * a.group + rt - dt * a.group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t *dst = a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + 4 * N * dg;
-#pragma unroll
-  for (int e = 0; e < N; e++)
-    *reinterpret_cast<uint2 *>(dst + 4 * e) =
-        make_uint2(at_pack<F16>(acc[e].x * inv, acc[e].y * inv), at_pack<F16>(acc[e].z * inv, acc[e].w * inv));
-  if (a.lse && dg == 0) a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
-}
-
 // Joins the parts of the items that several CTAs took, in the order of the
-// context: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A CTA takes 32
-// rows of an item at a time; a thread one row and D / 8 of its elements, so that a
-// warp reads 32 rows side by side.  The items to join are few and anywhere among
-// the CTAs' descriptions: every CTA looks all of them over and takes its share.
+// context: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A unit is 1024 / D
+// rows of an item, a thread one row and four of its elements, so that 8 or 16
+// rows are read side by side and a long context's many parts are spread over as
+// many CTAs as there are.  The items to join are few and anywhere among the CTAs'
+// descriptions: every CTA looks all of them over and takes its units.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ApArgs p, int sms) {
-  __shared__ int16_t list[kApMaxSms];
-  __shared__ int count;
-  const int lane = threadIdx.x & 31;
+  __shared__ unsigned masks[kApMaxSms / 32];
+  constexpr int kUnit = 1024 / D, kUnits = kApRows / kUnit;
+  const AttnArgs &a = p.a;
+  const int tid = threadIdx.x, words = (sms + 31) / 32;
   pdl_wait();
-  if (threadIdx.x < 32) {
-    int n = 0;
-    for (int k0 = 0; k0 < sms; k0 += 32) {
-      const bool has = k0 + lane < sms && __ldcg(&p.desc[2 * (k0 + lane) + 1].y) >= 0;
-      const unsigned mask = __ballot_sync(kFull, has);
-      if (has) list[n + __popc(mask & ((1u << lane) - 1u))] = (int16_t)(k0 + lane);
-      n += __popc(mask);
-    }
-    if (lane == 0) count = n;
+  for (int k = tid; k < 32 * words; k += 256) {
+    const unsigned mask = __ballot_sync(kFull, k < sms && __ldcg(&p.desc[2 * k + 1].y) >= 0);
+    if ((tid & 31) == 0) masks[k >> 5] = mask;
   }
   __syncthreads();
-  for (int unit = blockIdx.x; unit < count * (kApRows / 32); unit += gridDim.x)
-    join_rows<D, F16>(p, list[unit / (kApRows / 32)], unit % (kApRows / 32));
+  int count = 0;
+  for (int w = 0; w < words; w++) count += __popc(masks[w]);
+  const float c = a.scale * 1.44269504088896340736f;
+  for (int unit = blockIdx.x; unit < count * kUnits; unit += gridDim.x) {
+    // the unit's item: the description of the (unit / kUnits)-th set bit
+    int left = unit / kUnits, w = 0;
+    while (left >= __popc(masks[w])) left -= __popc(masks[w++]);
+    unsigned bits = masks[w];
+    for (; left > 0; left--) bits &= bits - 1;
+    const int which = 32 * w + __ffs(bits) - 1;
+    const int4 d0 = __ldcg(p.desc + 2 * which), d1 = __ldcg(p.desc + 2 * which + 1);
+    const int first = d0.x, hk = d0.y, tok0 = d0.z, toks = d0.w, c0 = d1.x, c1 = d1.y, slot0 = d1.z, twin = d1.w;
+    const int r = unit % kUnits * kUnit + tid % kUnit, d4 = tid / kUnit;
+    const int rt = r & (kApTile - 1), dt = (rt * p.magic) >> 16, tl = (r / kApTile) * p.per + dt;   // as in the kernel above
+    if (dt >= p.per || tl >= toks) continue;
+    const int nsrc = (c1 - c0 + 1) << twin;        // twins: two sources a part, 128 rows apart
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < nsrc; q0 += 8) {         // eight sources at a time, so that their loads wait together
+      float2 st[8];
+      float4 u[8];
+      float t1 = top;
+#pragma unroll
+      for (int z = 0; z < 8; z++) {
+        const int q = min(q0 + z, nsrc - 1), k = c0 + (q >> twin), slot = k == c0 ? slot0 : 2 * k;
+        const int row = r + (twin && (q & 1) ? kApTile : 0);
+        st[z] = __ldcg(p.stat + (size_t)slot * kApRows + row);
+        u[z] = __ldcg(p.part + ((size_t)slot * (D / 4) + d4) * kApRows + row);
+      }
+#pragma unroll
+      for (int z = 0; z < 8; z++) t1 = fmaxf(t1, st[z].x);
+      const float f0 = top == t1 ? 1.f : at_exp2((top - t1) * c);
+      top = t1;
+      sum *= f0;
+      acc.x *= f0;
+      acc.y *= f0;
+      acc.z *= f0;
+      acc.w *= f0;
+#pragma unroll
+      for (int z = 0; z < 8; z++) {
+        if (q0 + z >= nsrc || st[z].y == 0.f) continue;   // a part in which the row sees nothing (it may hold no O)
+        const float f = at_exp2((st[z].x - t1) * c);
+        sum = fmaf(st[z].y, f, sum);
+        acc.x = fmaf(u[z].x, f, acc.x);
+        acc.y = fmaf(u[z].y, f, acc.y);
+        acc.z = fmaf(u[z].z, f, acc.z);
+        acc.w = fmaf(u[z].w, f, acc.w);
+      }
+    }
+    const int i = tok0 + tl, hq = hk * a.group + rt - dt * a.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(a.out.p + (long long)(first + i) * a.out.row + (long long)hq * a.out.head + 4 * d4) =
+        make_uint2(at_pack<F16>(acc.x * inv, acc.y * inv), at_pack<F16>(acc.z * inv, acc.w * inv));
+    if (a.lse && d4 == 0) a.lse[(size_t)(first + i) * a.q_heads + hq] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+  }
 }
-
 
 namespace {
 typedef void (*ApKernel)(const ApArgs);
