@@ -41,7 +41,13 @@ constexpr int kAtStageBytes = 8192;
 constexpr int kAtRows = 16;                      // rows of an item
 constexpr int kAtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kAtSlack = 8.f;
-constexpr int kAtMostRows = 32;                  // mean rows of a request and kv head; more go to attn_wide.cu
+// Mean rows of a request and kv head up to which the calls stay here, for
+// contexts of any length, and for such that L2 keeps (every row tile of 16 rows
+// reads the context again).  bf16, D = 128, us here and in attn_wide.cu:
+//   32 rows, 1 request of 8000: 16.4, 21.5;    64 rows, 1 of 30000 (123 MB): 66, 44;
+//   64 rows, 2 of 4000: 13.6, 19.6;            128 rows, 2 of 30000 (35 MB): 20.0, 34.4
+constexpr int kAtMostRows = 32, kAtMostRowsL2 = 128;
+constexpr long long kAtL2Bytes = 64LL << 20;
 constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least: one per warp costs no more time than one
 constexpr int kAtExtra = 31;                     // chunks above the mean that are cheaper than a second part in a CTA
 
@@ -903,7 +909,10 @@ AttnTreeWs attn_tree_ws(int head_dim, int num_sms) {
 cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream) {
   const AttnTreeWs w = attn_tree_ws(a.head_dim, num_sms);
   const long long rows = ((long long)a.T * a.group + a.B - 1) / a.B;   // of a request and kv head, on the average
-  if (rows > kAtMostRows) return launch_attn_wide_tree(a, ws, w.wide, num_sms, stream);
+  // keys and values of contexts as long as the block table's rows
+  const long long most = ((long long)a.max_pages << a.page_shift) * a.B * a.kv_heads * a.head_dim * 4;
+  if (rows > (most <= kAtL2Bytes ? kAtMostRowsL2 : kAtMostRows))
+    return launch_attn_wide_tree(a, ws, w.wide, num_sms, stream);
   AtArgs p;
   p.a = a;
   p.magic = (65536 + a.group - 1) / a.group;
