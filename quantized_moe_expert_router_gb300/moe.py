@@ -8,6 +8,7 @@ raises if ``_lib/libmoe.so`` is missing: there is no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import threading
@@ -413,19 +414,22 @@ def moe_attn_get_device_status(attn: Attention, ws: torch.Tensor, stream=None) -
     return f.value
 
 
-# The calls below run once or more per step and layer, so their checks are kept
-# to a few attribute reads per tensor; what went wrong is found out only then.
+# The calls below run once or more per step and layer, so what they look at is
+# written out: dtype, number of elements, contiguity and device of each array, in
+# one condition.  What went wrong is found out only then (_attn_refuse).
 
 _pack_rows = struct.Struct("@Pqq").pack         # a moe_attn_rows
 
 
-def _attn_words(fn, name, t, dtype, shape, device):
-    """Address of a contiguous tensor of this dtype and shape on cuda:device."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{fn}: {name} is {t.dtype}, not {dtype}")
-    raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)} on {t.device} is not a contiguous {shape} on cuda:{device}")
+def _attn_refuse(fn, dev, *arrays):
+    """Raise for the first of (name, tensor, dtype, shape) that is not a contiguous tensor like that on cuda:dev."""
+    for name, t, dtype, shape in arrays:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+        if t.numel() != math.prod(shape) or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)} on {t.device} is not a contiguous {shape} on cuda:{dev}")
 
 
 def _attn_rows(fn, name, attn, t, shape):
@@ -439,38 +443,60 @@ def _attn_rows(fn, name, attn, t, shape):
                      f"last axis on cuda:{attn.device}")
 
 
-def _raw_stream(attn, stream):
-    return torch._C._cuda_getCurrentRawStream(attn.device) if stream is None else stream.cuda_stream
+def _attn_caches(fn, attn, k_cache, v_cache):
+    dt, shape, dev = attn.dtype, attn.cache_shape, attn.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype is not dt:
+            raise TypeError(f"{fn}: {name} is {t.dtype}, not {dt}")
+        if t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)} on {t.device} is not a contiguous {shape} on cuda:{dev}")
 
 
 def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
                 stream=None) -> None:
     """Block table entries, row offsets, slots, positions and (from parents)
     tree masks of one step; int32 tensors, tree_mask int64."""
-    fn, dev, i32, w = "moe_kv_plan", attn.device, torch.int32, _attn_words
-    B, T, F = cached.shape[0], slots.shape[0], free_pages.shape[0]
-    rows, reqs = (T,), (B,)
+    dev, i32, B, T, F = attn.device, torch.int32, cached.numel(), slots.numel(), free_pages.numel()
+    if (cached.dtype is not i32 or not cached.is_contiguous() or cached.get_device() != dev
+            or fresh.dtype is not i32 or fresh.numel() != B or not fresh.is_contiguous() or fresh.get_device() != dev
+            or free_pages.dtype is not i32 or not free_pages.is_contiguous() or free_pages.get_device() != dev
+            or block_table.dtype is not i32 or block_table.shape != (B, attn.max_pages) or not block_table.is_contiguous()
+            or block_table.get_device() != dev
+            or cu.dtype is not i32 or cu.numel() != B + 1 or not cu.is_contiguous() or cu.get_device() != dev
+            or slots.dtype is not i32 or not slots.is_contiguous() or slots.get_device() != dev
+            or positions.dtype is not i32 or positions.numel() != T or not positions.is_contiguous() or positions.get_device() != dev
+            or info.dtype is not i32 or info.numel() != 4 or not info.is_contiguous() or info.get_device() != dev
+            or parents is not None and (parents.dtype is not i32 or parents.numel() != T or not parents.is_contiguous()
+                                        or parents.get_device() != dev)
+            or tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.numel() != T
+                                          or not tree_mask.is_contiguous() or tree_mask.get_device() != dev)):
+        _attn_refuse("moe_kv_plan", dev, ("cached", cached, i32, (B,)), ("fresh", fresh, i32, (B,)), ("free_pages", free_pages, i32, (F,)),
+                     ("block_table", block_table, i32, (B, attn.max_pages)), ("cu", cu, i32, (B + 1,)), ("slots", slots, i32, (T,)),
+                     ("positions", positions, i32, (T,)), ("info", info, i32, (4,)), ("parents", parents, i32, (T,)),
+                     ("tree_mask", tree_mask, torch.int64, (T,)))
+        raise ValueError(f"moe_kv_plan: block_table has shape {tuple(block_table.shape)}, not {(B, attn.max_pages)}")
     status = _lib.moe_kv_plan(
-        attn.handle, B, T, w(fn, "cached", cached, i32, reqs, dev), w(fn, "fresh", fresh, i32, reqs, dev),
-        w(fn, "free_pages", free_pages, i32, (F,), dev), F,
-        None if parents is None else w(fn, "parents", parents, i32, rows, dev),
-        w(fn, "block_table", block_table, i32, (B, attn.max_pages), dev), w(fn, "cu", cu, i32, (B + 1,), dev),
-        w(fn, "slots", slots, i32, rows, dev), w(fn, "positions", positions, i32, rows, dev),
-        None if tree_mask is None else w(fn, "tree_mask", tree_mask, torch.int64, rows, dev),
-        w(fn, "info", info, i32, (4,), dev), _raw_stream(attn, stream))
+        attn.handle, B, T, cached.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(), F,
+        None if parents is None else parents.data_ptr(), block_table.data_ptr(), cu.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(), info.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
-        _check(fn, status)
+        _check("moe_kv_plan", status)
 
 
 def moe_kv_append(attn, k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Write k and v rows [rows][kv_heads][head_dim] to their slots (negative: skipped)."""
-    fn, dev, T = "moe_kv_append", attn.device, slots.shape[0]
-    shape = (T, attn.kv_heads, attn.head_dim)
+    fn, dev, dt, T = "moe_kv_append", attn.device, attn.dtype, slots.numel()
+    shape, cs = (T, attn.kv_heads, attn.head_dim), attn.cache_shape
+    if slots.dtype is not torch.int32 or not slots.is_contiguous() or slots.get_device() != dev:
+        _attn_refuse(fn, dev, ("slots", slots, torch.int32, (T,)))
+    if (k_cache.dtype is not dt or k_cache.shape != cs or not k_cache.is_contiguous() or k_cache.get_device() != dev
+            or v_cache.dtype is not dt or v_cache.shape != cs or not v_cache.is_contiguous() or v_cache.get_device() != dev):
+        _attn_caches(fn, attn, k_cache, v_cache)
     status = _lib.moe_kv_append(
-        attn.handle, T, _attn_rows(fn, "k", attn, k, shape), _attn_rows(fn, "v", attn, v, shape),
-        _attn_words(fn, "slots", slots, torch.int32, (T,), dev),
-        _attn_words(fn, "k_cache", k_cache, attn.dtype, attn.cache_shape, dev),
-        _attn_words(fn, "v_cache", v_cache, attn.dtype, attn.cache_shape, dev), _raw_stream(attn, stream))
+        attn.handle, T, _attn_rows(fn, "k", attn, k, shape), _attn_rows(fn, "v", attn, v, shape), slots.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)
 
@@ -479,14 +505,18 @@ def moe_attn_prompt(attn, q, k, v, cu, out, ws, lse=None, stream=None) -> None:
     """Causal attention over packed prompts: q, out [rows][q_heads][head_dim],
     k, v [rows][kv_heads][head_dim], cu int32 [requests + 1], lse fp32
     [rows][q_heads]."""
-    fn, dev, T, n = "moe_attn_prompt", attn.device, q.shape[0], cu.shape[0]
-    qs, ks = (T, attn.q_heads, attn.head_dim), (T, attn.kv_heads, attn.head_dim)
+    fn, dev, T, n = "moe_attn_prompt", attn.device, q.shape[0], cu.numel()
+    hq = attn.q_heads
+    qs, ks = (T, hq, attn.head_dim), (T, attn.kv_heads, attn.head_dim)
+    if (cu.dtype is not torch.int32 or not cu.is_contiguous() or cu.get_device() != dev
+            or lse is not None and (lse.dtype is not torch.float32 or lse.numel() != T * hq or not lse.is_contiguous()
+                                    or lse.get_device() != dev)):
+        _attn_refuse(fn, dev, ("cu", cu, torch.int32, (n,)), ("lse", lse, torch.float32, (T, hq)))
     status = _lib.moe_attn_prompt(
         attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), _attn_rows(fn, "k", attn, k, ks),
-        _attn_rows(fn, "v", attn, v, ks), _attn_words(fn, "cu", cu, torch.int32, (n,), dev),
-        _attn_rows(fn, "out", attn, out, qs),
-        None if lse is None else _attn_words(fn, "lse", lse, torch.float32, (T, attn.q_heads), dev),
-        ws.data_ptr(), ws.nbytes, _raw_stream(attn, stream))
+        _attn_rows(fn, "v", attn, v, ks), cu.data_ptr(), _attn_rows(fn, "out", attn, out, qs),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)
 
@@ -496,15 +526,28 @@ def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, t
     """Attention of the step's rows over the cache: all cached tokens of the
     row's request, and its fresh rows as the row's word of tree_mask (int64)
     says, or up to the row itself without one."""
-    fn, dev, i32, w, T, n = "moe_attn_tree", attn.device, torch.int32, _attn_words, q.shape[0], cu.shape[0]
-    qs = (T, attn.q_heads, attn.head_dim)
+    fn, dev, i32, dt, T, n = "moe_attn_tree", attn.device, torch.int32, attn.dtype, q.shape[0], cu.numel()
+    hq, cs = attn.q_heads, attn.cache_shape
+    qs = (T, hq, attn.head_dim)
+    if (cu.dtype is not i32 or not cu.is_contiguous() or cu.get_device() != dev
+            or cached.dtype is not i32 or cached.numel() != n - 1 or not cached.is_contiguous() or cached.get_device() != dev
+            or block_table.dtype is not i32 or block_table.shape != (n - 1, attn.max_pages) or not block_table.is_contiguous()
+            or block_table.get_device() != dev
+            or tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.numel() != T
+                                          or not tree_mask.is_contiguous() or tree_mask.get_device() != dev)
+            or lse is not None and (lse.dtype is not torch.float32 or lse.numel() != T * hq or not lse.is_contiguous()
+                                    or lse.get_device() != dev)):
+        _attn_refuse(fn, dev, ("cu", cu, i32, (n,)), ("cached", cached, i32, (n - 1,)),
+                     ("block_table", block_table, i32, (n - 1, attn.max_pages)), ("tree_mask", tree_mask, torch.int64, (T,)),
+                     ("lse", lse, torch.float32, (T, hq)))
+        raise ValueError(f"{fn}: block_table has shape {tuple(block_table.shape)}, not {(n - 1, attn.max_pages)}")
+    if (k_cache.dtype is not dt or k_cache.shape != cs or not k_cache.is_contiguous() or k_cache.get_device() != dev
+            or v_cache.dtype is not dt or v_cache.shape != cs or not v_cache.is_contiguous() or v_cache.get_device() != dev):
+        _attn_caches(fn, attn, k_cache, v_cache)
     status = _lib.moe_attn_tree(
-        attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), w(fn, "cu", cu, i32, (n,), dev),
-        w(fn, "cached", cached, i32, (n - 1,), dev), w(fn, "block_table", block_table, i32, (n - 1, attn.max_pages), dev),
-        None if tree_mask is None else w(fn, "tree_mask", tree_mask, torch.int64, (T,), dev),
-        w(fn, "k_cache", k_cache, attn.dtype, attn.cache_shape, dev),
-        w(fn, "v_cache", v_cache, attn.dtype, attn.cache_shape, dev), _attn_rows(fn, "out", attn, out, qs),
-        None if lse is None else w(fn, "lse", lse, torch.float32, (T, attn.q_heads), dev),
-        ws.data_ptr(), ws.nbytes, _raw_stream(attn, stream))
+        attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), cu.data_ptr(), cached.data_ptr(), block_table.data_ptr(),
+        None if tree_mask is None else tree_mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _attn_rows(fn, "out", attn, out, qs), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)
