@@ -653,3 +653,17 @@ def test_refusals():
     moe.moe_kv_append(attn, k[:0], k[:0], slots[:0], cache, cache)
     torch.cuda.synchronize()
     assert (cache == 0).all()
+
+
+def test_example_runs_the_operators_together():
+    """The serving loop around the MoE layer: stepwise, paged attention equals the whole sequences'.  Both sides round
+    P and the result to bf16: 2 (u A + u |o|) on each, with A at most max |v| and v of unit variance."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_step.py")
+    spec = importlib.util.spec_from_file_location("paged_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    off, largest = example.main(4)
+    assert largest > 0.1
+    assert off <= 4 * 2 * 2.0 ** -8 * 5.0
