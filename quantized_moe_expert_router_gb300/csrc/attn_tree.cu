@@ -127,7 +127,8 @@ __device__ __forceinline__ void at_table(AtTable &s, const AttnArgs &a, long lon
     long long v = 0;
     int items = 0;
     if (b < a.B) {
-      const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1), cached = max(__ldg(a.cached + b), 0);
+      const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1);
+      const int cached = min(max(__ldg(a.cached + b), 0), a.max_pages << a.page_shift);   // no sum with rows passes 2^31
       s.first[b] = lo;
       s.n[b] = lo < 0 ? 0 : max(0, min(hi, a.T) - lo);
       s.cached[b] = cached;

@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       int items = 0;
       long long v = 0;
       if (b < a.B) {
-        const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1), cached = max(__ldg(a.cached + b), 0);
+        const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1);
+        const int cached = min(max(__ldg(a.cached + b), 0), a.max_pages << a.page_shift);   // no sum with rows passes 2^31
         const int n = lo < 0 ? 0 : max(0, min(hi, a.T) - lo);
         s.first[b] = lo;
         s.n[b] = n;
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           // fragment shape a quad holds 32 elements of a row (pairs 2 q4 of each
           // 8), and a transpose within the quad gives each lane 16 bytes of 64.
           const int qg = lane >> 2, q4 = lane & 3;
-#pragma unroll
+#pragma unroll 1
           for (int rb = 0; rb < 2; rb++) {
             float iv[2];
             uint16_t *dst[2];
@@ -685,9 +686,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok && !mbar_wait_bounded(bar, parity)) {
-          if (lane == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+          atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
           ok = false;
         }
+      };
+      // The lanes go on or end together.  With a wait that S or PV stands behind, the
+      // vote comes after the issue: the lanes meet at the election anyway.
+      auto all_ok = [&]() {
         ok = __all_sync(kFull, ok);
         return ok;
       };
@@ -707,7 +712,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         at_commit(&s.s_full[h]);
       };
       for (int i = 0; ok; i++) {
-        if (!wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+        wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
+        if (!all_ok()) break;
         const ApItem &im = s.item[i & 1];
         if (__shfl_sync(kFull, im.b, 0) < 0) break;
         const int n = __shfl_sync(kFull, im.n, 0), m0 = __shfl_sync(kFull, im.m0, 0);
@@ -715,9 +721,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const int end = __shfl_sync(kFull, im.end - im.j0 * kApTile, 0);   // tokens of the part from here on are seen by none
         const bool twin = PAGED && __shfl_sync(kFull, im.twin, 0);
         const int ahead = twin ? 2 : 1;            // S of tile j + ahead follows PV of tile j
-        if (!wait(&s.q_full, (uint32_t)i & 1u)) break;
+        wait(&s.q_full, (uint32_t)i & 1u);
         for (int j = 0; j < ahead && j < n; j++) {
-          if (!wait(&s.kv_full[slot], phase)) break;
+          wait(&s.kv_full[slot], phase);
+          if (!all_ok()) break;
           at_fence_after();
           if (at_elect()) {
             if (twin) {
@@ -733,13 +740,16 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           next_stage();
         }
         for (int j = 0; j < n && ok; j++) {
-          if (!wait(&s.kv_full[slot], phase)) break;
+          wait(&s.kv_full[slot], phase);
           if (j >= m0) {
             const int z = j - m0;                  // 0, 1 or 2; a phase bit each
-            if (!wait(&s.v_clean[z], (clean >> z) & 1u)) break;
+            wait(&s.v_clean[z], (clean >> z) & 1u);
             clean ^= 1u << z;
           }
-          if (j + 1 == n && lane == 0) mbar_arrive(&s.v_next);   // the next item's scans may signal
+          if (j + 1 == n) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.v_next); // the next item's scans may signal
+          }
           const int left = end - j * kApTile;      // tokens of the tile that some row sees
           const uint64_t db = dv0 + (uint64_t)(slot * (2 * kTB >> 4));
           const uint32_t add = j >= ahead;
@@ -749,10 +759,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             if (twin ? (j & 1) == h : j < nh) {
               uint32_t &np = h ? np1 : np0;
               const bool more = twin ? j + 2 < n : j + 1 < nh;
-              if (!wait(&s.p_full[h], np)) break;
+              wait(&s.p_full[h], np);
               np ^= 1u;
               at_fence_after();
-              if (at_elect()) {
+              if (at_elect() && ok) {
                 const uint32_t oc = tu + 256u + 128u * h, pc = tu + 128u * h;
                 if (left >= kApTile) {
 #pragma unroll
@@ -763,16 +773,15 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                 }
                 if (more) issue_s(h, twin ? 0 : h);
                 else at_commit(&s.o_done[h]);      // the row tile's last
+                if (twin || h || n1 == 0) {        // and the tile's last
+                  at_commit(&s.kv_empty[slot]);
+                  if (j + ahead + 1 == n) at_commit(&s.q_empty);
+                }
               }
-              __syncwarp();
+              if (!all_ok()) break;
             }
           }
           if (!ok) break;
-          if (at_elect()) {
-            at_commit(&s.kv_empty[slot]);
-            if (j + ahead + 1 == n) at_commit(&s.q_empty);
-          }
-          __syncwarp();
           next_stage();
         }
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);

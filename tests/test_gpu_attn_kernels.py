@@ -200,3 +200,29 @@ def test_one_workspace_for_all_kernels():
             q = k.repeat(1, 2, 1)
             moe.moe_attn_prompt(c.attn, q, k, k, ints([0, 300]), torch.empty_like(q), ws)
             assert moe.moe_attn_get_device_status(c.attn, ws) == 0
+
+
+@pytest.mark.parametrize("fresh,extra", [([1], 0), ([1] * 24, 0), ([40], 0), ([9], 4200)])
+@pytest.mark.parametrize("cached", [1 << 20, 2 ** 31 - 1])
+def test_lengths_past_the_block_table(fresh, extra, cached):
+    """A request that claims more tokens than its row of the block table has: its rows see the table's tokens, whose
+    missing pages count for nothing."""
+    n = 200
+    c = Cache(8, 8, 128, 16, torch.bfloat16, [n] * len(fresh), [0] * len(fresh), seed=170, extra_cols=extra)
+    T = sum(fresh)
+    cu = ints([0] + np.cumsum(fresh).tolist())
+    q = torch.randn((T, 8, 128), generator=gen(171), device=DEV).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((T, 8), dtype=torch.float32, device=DEV)
+    # the page that holds the context's last tokens holds NaN behind them: fill it up with zero rows
+    for b in range(len(fresh)):
+        pg = int(c.table[b, n // 16])
+        c.k[pg, :, n % 16:] = 0
+        c.v[pg, :, n % 16:] = 0
+        c.rows[b] = [torch.cat([x, torch.zeros((16 - n % 16, 8, 128), dtype=x.dtype, device=DEV)]) for x in c.rows[b]]
+    ws = moe.alloc_attn_workspace(c.attn, len(fresh), T)
+    moe.moe_attn_tree(c.attn, q, cu, ints([cached] * len(fresh)), c.table, c.k, c.v, out, ws, lse=lse)
+    torch.cuda.synchronize()
+    vis = [torch.ones((f, 208), dtype=torch.bool, device=DEV) for f in fresh]
+    parts = [ref.attend(x, *c.rows[b], vis[b], 128 ** -0.5) for b, x in enumerate(q.split(fresh))]
+    ref.check(out, lse, [torch.cat([p[i] for p in parts]) for i in range(4)])
+    assert moe.moe_attn_get_device_status(c.attn, ws) == 0
