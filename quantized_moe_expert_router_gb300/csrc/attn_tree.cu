@@ -41,13 +41,15 @@ constexpr int kAtStageBytes = 8192;
 constexpr int kAtRows = 16;                      // rows of an item
 constexpr int kAtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr float kAtSlack = 8.f;
-// Mean rows of a request and kv head up to which the calls stay here, for
-// contexts of any length, and for such that L2 keeps (every row tile of 16 rows
-// reads the context again).  bf16, D = 128, us here and in attn_wide.cu:
-//   32 rows, 1 request of 8000: 16.4, 21.5;    64 rows, 1 of 30000 (123 MB): 66, 44;
-//   64 rows, 2 of 4000: 13.6, 19.6;            128 rows, 2 of 30000 (35 MB): 20.0, 34.4
-constexpr int kAtMostRows = 32, kAtMostRowsL2 = 128;
-constexpr long long kAtL2Bytes = 64LL << 20;
+// Calls that stay here and not on attn_wide.cu, whose tiles of 128 rows read the
+// context once for all of them: up to kAtMostRows rows of a request and kv head on
+// the average, and more while the contexts, as long as the block table's rows,
+// are at most kAtMostChunks chunks a warp with each of the row tiles of 16.  bf16,
+// D = 128, 4 kv heads, us here and there (chunks a warp):
+//   32 rows, 1 request of 8000: 16.4, 21.5 (3.3);    256 rows, 1 of 500: 12.3, 16.2 (1.9)
+//   128 rows, 1 of 4000: 16.4, 18.1 (6.6);           192 rows: 18.6, 18.0 (10);     256 rows: 22.6, 18.0 (13)
+//   64 rows, 1 of 30000: 31.7, 28.9 (25);            128 rows: 53.3, 29.4 (49)
+constexpr int kAtMostRows = 32, kAtMostChunks = 10;
 constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least: one per warp costs no more time than one
 constexpr int kAtExtra = 31;                     // chunks above the mean that are cheaper than a second part in a CTA
 
@@ -910,9 +912,9 @@ AttnTreeWs attn_tree_ws(int head_dim, int num_sms) {
 cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream) {
   const AttnTreeWs w = attn_tree_ws(a.head_dim, num_sms);
   const long long rows = ((long long)a.T * a.group + a.B - 1) / a.B;   // of a request and kv head, on the average
-  // keys and values of contexts as long as the block table's rows
-  const long long most = ((long long)a.max_pages << a.page_shift) * a.B * a.kv_heads * a.head_dim * 4;
-  if (rows > (most <= kAtL2Bytes ? kAtMostRowsL2 : kAtMostRows))
+  const long long items = (long long)a.B * a.kv_heads * ((rows + kAtRows - 1) / kAtRows);
+  const long long most = ((long long)a.max_pages << a.page_shift) * a.head_dim / 2048;   // chunks of a context
+  if (rows > kAtMostRows && items * most > (long long)kAtMostChunks * kAtWarps * num_sms)
     return launch_attn_wide_tree(a, ws, w.wide, num_sms, stream);
   AtArgs p;
   p.a = a;
@@ -924,7 +926,7 @@ cudaError_t launch_attn_tree(const AttnArgs &a, uint8_t *ws, int num_sms, cudaSt
   p.tickets = reinterpret_cast<int *>(ws + w.tickets);
   p.stat = reinterpret_cast<float2 *>(ws + w.stat);
   p.part = reinterpret_cast<float *>(ws + w.part);
-  const bool many = (long long)a.B * a.kv_heads * ((rows + kAtRows - 1) / kAtRows) > num_sms;
+  const bool many = items > num_sms;
   at_kernel(a.head_dim, a.f16, many)<<<num_sms, kAtThreads, at_smem(a.head_dim), stream>>>(p);
   return cudaGetLastError();
 }

@@ -912,10 +912,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       float t1 = top;
 #pragma unroll
       for (int z = 0; z < 8; z++) {
-        const int q = min(q0 + z, nsrc - 1), k = c0 + (q >> twin), slot = k == c0 ? slot0 : 2 * k;
+        const int q = q0 + z, k = c0 + (q >> twin), slot = k == c0 ? slot0 : 2 * k;
         const int row = r + (twin && (q & 1) ? kApTile : 0);
-        st[z] = __ldcg(p.stat + (size_t)slot * kApRows + row);
-        u[z] = __ldcg(p.part + ((size_t)slot * (D / 4) + d4) * kApRows + row);
+        st[z] = make_float2(-INFINITY, 0.f);
+        if (q < nsrc) {
+          st[z] = __ldcg(p.stat + (size_t)slot * kApRows + row);
+          u[z] = __ldcg(p.part + ((size_t)slot * (D / 4) + d4) * kApRows + row);
+        }
       }
 #pragma unroll
       for (int z = 0; z < 8; z++) t1 = fmaxf(t1, st[z].x);
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       acc.w *= f0;
 #pragma unroll
       for (int z = 0; z < 8; z++) {
-        if (q0 + z >= nsrc || st[z].y == 0.f) continue;   // a part in which the row sees nothing (it may hold no O)
+        if (st[z].y == 0.f) continue;              // a part in which the row sees nothing (it may hold no O), or none
         const float f = at_exp2((st[z].x - t1) * c);
         sum = fmaf(st[z].y, f, sum);
         acc.x = fmaf(u[z].x, f, acc.x);

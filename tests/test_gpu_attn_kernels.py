@@ -146,6 +146,8 @@ WIDE = [   # kv heads, group, D, page, cached, rows; block tables for contexts p
     (1, 12, 128, 32, [2000, 31], [10, 4], 2100),                         # 12 does not divide 128
     (1, 1, 128, 16, [30000], [64], 8200),                                # one item over all CTAs
     (2, 4, 64, 16, [1500], [200], 2),                                    # no mask above 64 rows: a prompt's next part
+    (2, 4, 64, 16, [1500], [200], 600),                                  # the same with a long block table
+    (1, 3, 128, 128, [5, 700], [300, 65], 300),
     (4, 16, 128, 16, ragged(40, 300, 20), [9] * 40, 2),                  # more items than CTAs, whole and shared ones
     (8, 8, 64, 32, ragged(24, 700, 21), [33] * 24, 2),
 ]
