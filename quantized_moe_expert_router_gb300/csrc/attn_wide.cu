@@ -43,11 +43,13 @@
 // Prompts: items are taken from a counter, those with most key tiles first; an
 // item's length depends on its row tile alone, so with the requests ranked by
 // length the idx-th longest item has a closed form (prompt_item).
+// Few prompts: items are single row tiles, and the two row tiles are the same rows
+// over alternate key tiles (twins), joined through shared memory.
 // Cache: the key tiles of all items stand in one line that the CTAs share
 // (at_share).  A part of an item goes to the workspace (fp32 O, m, l) and
-// attn_join_kernel joins the parts in the order of the context.  In a part of
-// at most 128 rows the two row tiles are the same rows over alternate key
-// tiles, so that the softmax of one still runs beside the MMAs of the other.
+// attn_join_kernel joins the parts in the order of the context.  Parts of at most
+// 128 rows are twins too, so that the softmax of one still runs beside the MMAs of
+// the other.
 //
 // Bound: with G = 8, D = 128 and long prompts the tensor pipe (2 x 512 cycles
 // a row tile and key tile); with D = 64 the exponentials.
@@ -83,6 +85,7 @@ struct ApArgs {
   int *ctrl;                   // workspace control words
   int magic;                   // ceil(2^16 / group)
   int per;                     // tokens of a row tile: floor(128 / group)
+  int span;                    // prompts: tokens of an item, per (twins) or 2 * per
   // cache only
   int4 *desc;                  // per CTA, of the item whose first part it holds and others the rest:
                                // (first, hk, tok0, toks), (first CTA, last CTA, its slot, twin)
@@ -105,11 +108,12 @@ struct ApItem {
 
 struct ApSmem {
   uint64_t kv_full[4], kv_empty[4];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, sched_full[2], sched_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, x_full, sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int wsum[2][kApThreads / 32];
   ApItem item[2];
   int v_pos[2][3];             // by item parity: stages of the masked value tiles, counted from the CTA's start
+  float2 stat[kApTile];        // prompts: (m, l) of the second twin
   uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
   union {
     struct {                   // prompts: requests by falling length
@@ -147,14 +151,15 @@ __device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, in
   }
   const int k = lo + 1, off = e - s.before[lo];
   const int lvl = at_idiv(off, k);
-  it.tok0 = (s.tiles[lo] - 1 - lvl) * 2 * p.per;
+  it.tok0 = (s.tiles[lo] - 1 - lvl) * p.span;
   it.b = s.order[off - lvl * k];
   it.first = __ldg(a.cu + it.b);
-  it.toks = min(min(__ldg(a.cu + it.b + 1), a.T) - it.first - it.tok0, 2 * p.per);
-  it.n0 = (it.tok0 + min(it.toks, p.per) - 1) / kApTile + 1;
-  it.n1 = it.toks > p.per ? (it.tok0 + it.toks - 1) / kApTile + 1 : 0;
-  it.n = max(it.n0, it.n1);
-  it.j0 = it.cached = it.twin = 0;
+  it.toks = min(min(__ldg(a.cu + it.b + 1), a.T) - it.first - it.tok0, p.span);
+  it.n = (it.tok0 + it.toks - 1) / kApTile + 1;
+  it.twin = p.span == p.per;
+  it.n0 = it.twin ? (it.n + 1) >> 1 : (it.tok0 + min(it.toks, p.per) - 1) / kApTile + 1;
+  it.n1 = it.twin ? it.n >> 1 : (it.toks > p.per ? it.n : 0);
+  it.j0 = it.cached = 0;
   it.all = it.tok0 + 1;
   it.end = it.tok0 + it.toks;                      // the causal limit alone cuts
   it.m0 = it.all / kApTile;
@@ -250,7 +255,8 @@ __device__ __forceinline__ float ap_max(const float (&v)[128]) {
   return at_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
 }
 
-template <int D, bool F16, bool PAGED>
+// TWINS: prompts whose items are one row tile each, over alternate key tiles.
+template <int D, bool F16, bool PAGED, bool TWINS>
 __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_constant__ ApArgs p) {
   extern __shared__ uint8_t dsm[];
   __shared__ ApSmem s;
@@ -282,6 +288,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       mbar_init(&s.q_full, 1);
       mbar_init(&s.q_empty, 1);
       mbar_init(&s.v_next, 1);
+      mbar_init(&s.x_full, 4);
       mbar_init(&s.drain, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     // requests by falling number of row tiles (equal ones by index), every CTA alike
     for (int b = tid; b < a.B; b += kApThreads) {
       const int lo = __ldg(a.cu + b), n = max(0, min(__ldg(a.cu + b + 1), a.T) - lo);
-      s.before[b] = lo < 0 ? 0 : at_idiv(n + 2 * p.per - 1, 2 * p.per);
+      s.before[b] = lo < 0 ? 0 : at_idiv(n + p.span - 1, p.span);
     }
     __syncthreads();
     for (int b = tid; b < a.B; b += kApThreads) {
@@ -403,7 +410,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       if (it.b < 0) break;
       const int nt = h ? it.n1 : it.n0;
       const int r = tid & 127, dt = (r * p.magic) >> 16;                        // row of the row tile, its token there
-      const int tl = (PAGED && it.twin ? 0 : h * p.per) + dt;                   // token of the item
+      const bool twin = PAGED ? it.twin : TWINS;
+      const int tl = (twin ? 0 : h * p.per) + dt;                               // token of the item
       const bool real = dt < p.per && tl < it.toks;
       const int lim = it.tok0 + min(tl, it.toks - 1);   // the row's token: of the prompt, or among the fresh ones
       uint64_t word = 0;
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       float m = -INFINITY;                         // the maximum that P is taken against
       float2 l2 = make_float2(0.f, 0.f);
       for (int j = 0; j < nt; j++, ns++) {
-        const int jl = PAGED && it.twin ? 2 * j + h : j, tok0 = (it.j0 + jl) * kApTile;
+        const int jl = twin ? 2 * j + h : j, tok0 = (it.j0 + jl) * kApTile;
         bool masked;
         uint32_t held = 0;                         // pages of the tile that are in the cache
         if constexpr (PAGED) {
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
         const float top = ap_max(v);
         if (j == 0) {
-          m = top;
+          m = real ? top : INFINITY;               // rows of no token hold anything: P = 0, and no say in the vote below
         } else if (__any_sync(kFull, (top - m) * c > kApSlack)) {
           const float m1 = fmaxf(m, top), f = m1 == -INFINITY ? 1.f : at_exp2((m - m1) * c);
           m = m1;
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&s.p_full[h]);
       }
       if (!ok) break;
-      const float l = l2.x + l2.y;
+      float l = l2.x + l2.y;
       if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (kApTile * h + (tid & 127))] = make_float2(m, l);
       if (nt > 0) {
         // ---------------------------------------------------------- epilogue
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
               uint32_t bits = s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
               for (; bits; bits &= bits - 1) {
                 const int jl = it.m0 + (w >> 2);   // tile of the part
-                if (PAGED && it.twin && (jl & 1) != h) continue;
+                if (twin && (jl & 1) != h) continue;
                 const int tok = (it.j0 + jl) * kApTile + 32 * (w & 3) + __ffs(bits) - 1;
                 const uint16_t *vp;
                 if constexpr (PAGED) {
@@ -525,7 +533,55 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
           at_wait_st();
         }
-        if (PAGED && it.slot >= 0) {
+        if (TWINS && it.n1 > 0) {
+          // The second twin's O, m and l go to the first through shared memory, in the
+          // place of Q: with twins a CTA has one item, and its S are done.
+          float4 *const x = reinterpret_cast<float4 *>(generic0) + (tid & 127);   // [element / 4][row]
+          float f0 = 1.f, f1 = 0.f;
+          if (h) {
+            s.stat[tid & 127] = make_float2(m, l);
+          } else {
+            if (!mbar_wait_bounded(&s.x_full, 0u)) {
+              atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+              break;
+            }
+            const float2 other = s.stat[tid & 127];
+            const float top = fmaxf(m, other.x);
+            f0 = m == top ? 1.f : at_exp2((m - top) * c);
+            f1 = other.x == top ? 1.f : at_exp2((other.x - top) * c);
+            m = top;
+            l = l * f0 + other.y * f1;
+          }
+#pragma unroll 1
+          for (int q = 0; q < D / 32; q++) {
+            float o[32];
+            at_ld32(to + 32u * q, o);
+            at_wait_ld(o);
+            if (h) {
+#pragma unroll
+              for (int e = 0; e < 8; e++) x[(8 * q + e) * kApTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; e++) {
+                const float4 w = x[(8 * q + e) * kApTile];
+                o[4 * e] = o[4 * e] * f0 + w.x * f1;
+                o[4 * e + 1] = o[4 * e + 1] * f0 + w.y * f1;
+                o[4 * e + 2] = o[4 * e + 2] * f0 + w.z * f1;
+                o[4 * e + 3] = o[4 * e + 3] * f0 + w.w * f1;
+              }
+              at_st32(to + 32u * q, o);
+            }
+          }
+          if (h) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.x_full);
+          } else {
+            at_wait_st();
+          }
+        }
+        if (TWINS && h) {
+          // the first twin stores
+        } else if (PAGED && it.slot >= 0) {
           // [element / 4][row]: the 32 rows of a warp side by side
           float4 *part = p.part + (size_t)it.slot * (D / 4) * kApRows + (kApTile * h + (tid & 127));
 #pragma unroll 1
@@ -613,7 +669,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           if (it.b < 0) break;
           if (!PAGED) next = gridDim.x + atomicAdd(p.ctrl + kAttnCtrlNext, 1);
           // stage q: K[q] and V[q - ahead], as far as they are there
-          const int n = it.n, ahead = PAGED && it.twin ? 2 : 1;
+          const int n = it.n, ahead = (PAGED ? it.twin : TWINS) ? 2 : 1;
           for (int q = 0; q < n + ahead; q++) {
             if (q >= n && q < ahead) continue;
             const int slot = pos % kStages;
@@ -719,7 +775,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const int n = __shfl_sync(kFull, im.n, 0), m0 = __shfl_sync(kFull, im.m0, 0);
         const int n0 = __shfl_sync(kFull, im.n0, 0), n1 = __shfl_sync(kFull, im.n1, 0);
         const int end = __shfl_sync(kFull, im.end - im.j0 * kApTile, 0);   // tokens of the part from here on are seen by none
-        const bool twin = PAGED && __shfl_sync(kFull, im.twin, 0);
+        const bool twin = PAGED ? __shfl_sync(kFull, im.twin, 0) : TWINS;
         const int ahead = twin ? 2 : 1;            // S of tile j + ahead follows PV of tile j
         wait(&s.q_full, (uint32_t)i & 1u);
         for (int j = 0; j < ahead && j < n; j++) {
@@ -951,10 +1007,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 namespace {
 typedef void (*ApKernel)(const ApArgs);
 typedef void (*ApJoin)(const ApArgs, int);
-template <bool PAGED>
+template <bool PAGED, bool TWINS>
 ApKernel ap_kernel(int head_dim, int f16) {
-  if (head_dim == 64) return f16 ? attn_wide_kernel<64, true, PAGED> : attn_wide_kernel<64, false, PAGED>;
-  return f16 ? attn_wide_kernel<128, true, PAGED> : attn_wide_kernel<128, false, PAGED>;
+  if (head_dim == 64) return f16 ? attn_wide_kernel<64, true, PAGED, TWINS> : attn_wide_kernel<64, false, PAGED, TWINS>;
+  return f16 ? attn_wide_kernel<128, true, PAGED, TWINS> : attn_wide_kernel<128, false, PAGED, TWINS>;
 }
 ApJoin ap_join(int head_dim, int f16) {
   if (head_dim == 64) return f16 ? attn_join_kernel<64, true> : attn_join_kernel<64, false>;
@@ -986,8 +1042,8 @@ cudaError_t encode_q(ApArgs *p) {
 }  // namespace
 
 cudaError_t attn_wide_setup(int head_dim, int f16) {
-  for (int i = 0; i < 2; i++) {
-    const ApKernel k = i ? ap_kernel<true>(head_dim, f16) : ap_kernel<false>(head_dim, f16);
+  const ApKernel kernels[3] = {ap_kernel<false, false>(head_dim, f16), ap_kernel<false, true>(head_dim, f16), ap_kernel<true, false>(head_dim, f16)};
+  for (const ApKernel k : kernels) {
     cudaFuncAttributes at;
     cudaError_t err = cudaFuncGetAttributes(&at, k);
     if (err != cudaSuccess) return err;
@@ -1022,10 +1078,15 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaSt
   if (err == cudaSuccess) err = encode_rows(&p.kmap, a.k, a.T, a.kv_heads, 1, kApTile, a);
   if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, 1, kApTile, a);
   if (err != cudaSuccess) return err;
-  // items at most: every request may end inside a row tile
-  const long long items = ((a.T + 2 * p.per - 1) / (2 * p.per) + a.B) * (long long)a.kv_heads;
+  // Items at most: every request may end inside one.  Where row tiles are as few as
+  // CTAs, an item is one row tile and the softmax warps of the other take every second
+  // of its key tiles (us with twins, without): 1 prompt of 512, 8 kv heads of 4, D = 128
+  // 12.2, 13.5; of 2000, 1 kv head of 8 21.2, 29.5; of 1000, 8 of 2, D = 64 12.1, 15.6.
+  auto items_of = [&](int span) { return (a.T + (long long)a.B * (span - 1)) / span * a.kv_heads; };
+  p.span = items_of(p.per) <= num_sms ? p.per : 2 * p.per;
+  const long long items = items_of(p.span);
   const int grid = (int)(items < num_sms ? items : num_sms);
-  ap_kernel<false>(a.head_dim, a.f16)<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
+  (p.span == p.per ? ap_kernel<false, true> : ap_kernel<false, false>)(a.head_dim, a.f16)<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1042,7 +1103,7 @@ cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWide
   if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 1 << a.page_shift);
   if (err != cudaSuccess) return err;
   if (num_sms > kApMaxSms) num_sms = kApMaxSms;
-  ap_kernel<true>(a.head_dim, a.f16)<<<num_sms, kApThreads, ap_smem(a.head_dim), stream>>>(p);
+  ap_kernel<true, false>(a.head_dim, a.f16)<<<num_sms, kApThreads, ap_smem(a.head_dim), stream>>>(p);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * num_sms));

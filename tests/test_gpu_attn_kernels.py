@@ -1,5 +1,6 @@
-"""moe_attn_tree on the shapes that choose among its kernels (few items, many
-items, many rows per request), against the definition in 64 bits with the
+"""The attention calls on the shapes that choose among their kernels (prompts of
+many and few row tiles; trees of few items, many items, many rows per request),
+against the definition in 64 bits with the
 bounds of ``attn_ref``."""
 import math
 
@@ -9,7 +10,7 @@ import torch
 
 import attn_ref as ref
 from quantized_moe_expert_router_gb300 import moe
-from test_gpu_attn import Cache, built, gen, ints, random_words  # noqa: F401  (built: the module's build fixture)
+from test_gpu_attn import Cache, built, gen, ints, offsets, prompt_ref, randn, random_words, run_prompt  # noqa: F401  (built: the module's build fixture)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -37,6 +38,62 @@ def poison(c, words, row, bad):
                 sees[lo + row + 1] = True
         lo += f
     return words, sees
+
+
+# ---------------------------------------------------------------- prompts of more row tiles than SMs, and of fewer
+
+PROMPTS = [   # kv heads, group, D, lengths
+    (40, 1, 64, [129, 1, 0, 513, 300, 64]), (24, 2, 128, [129, 1, 0, 513, 300]), (8, 12, 128, [10, 11, 21, 250]),
+    (4, 32, 64, [200, 3, 57]), (2, 128, 128, [33, 90]), (32, 3, 64, [42, 43, 84, 85, 400]),                       # pairs of row tiles
+    (1, 1, 64, [128, 129, 256, 257, 900]), (4, 4, 128, [640]), (1, 8, 128, [2000]), (2, 7, 64, [1, 18, 19, 400]),  # single ones
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_prompt_items_parity(dt, case):
+    hk, g, d, lengths = PROMPTS[case]
+    T, dt = sum(lengths), TYPES[dt]
+    attn = moe.Attention(hk * g, hk, d, 16, 1, 1, dt)
+    for rep in range(2):
+        q, k, v = (randn((T, h, d), dt, 300 + 10 * rep + i, 1.5 if i == 0 else 1.0) for i, h in enumerate((hk * g, hk, hk)))
+        out, lse = run_prompt(attn, q, k, v, lengths)
+        ref.check(out, lse, prompt_ref(q, k, v, lengths, d ** -0.5))
+    a = run_prompt(attn, q, k, v, lengths)
+    assert torch.equal(a[0], out) and torch.equal(a[1], lse)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("hk,d", [(40, 64), (24, 128), (2, 64), (2, 128)])
+def test_prompt_items_unseen_rows(hk, d, bad):
+    """Everything from a row of each request on is poisoned: the rows before stay exact."""
+    lengths, last, dt = [300, 129, 700], [170, 128, 515], torch.bfloat16
+    attn = moe.Attention(2 * hk, hk, d, 16, 1, 1, dt)
+    T, cu = sum(lengths), offsets(lengths).tolist()
+    q, k, v = (randn((T, h, d), dt, 340 + i) for i, h in enumerate((2 * hk, hk, hk)))
+    want = prompt_ref(q, k, v, lengths, d ** -0.5)
+    for lo, n, at in zip(cu, lengths, last):
+        for x in (q, k, v):
+            x[lo + at:lo + n] = bad
+    out, _ = run_prompt(attn, q, k, v, lengths)
+    for lo, n, at in zip(cu, lengths, last):
+        ref.check(out[lo:lo + at], None, [w[lo:lo + at] for w in want])
+        assert torch.isnan(out[lo + at:lo + n].float()).all()
+
+
+@pytest.mark.parametrize("hk,d", [(40, 64), (24, 128), (2, 64), (2, 128)])
+@pytest.mark.parametrize("at", [0, 127, 128, 300])
+def test_prompt_items_infinite_value_reaches_the_rows_that_see_it(hk, d, at):
+    n, dt = 600, torch.float16
+    attn = moe.Attention(2 * hk, hk, d, 16, 1, 1, dt)
+    q, k, v = (randn((n, h, d), dt, 350 + i) for i, h in enumerate((2 * hk, hk, hk)))
+    want = prompt_ref(q, k, v, [n], d ** -0.5)
+    v[at, :, 5] = math.inf
+    out, _ = run_prompt(attn, q, k, v, [n])
+    ref.check(out[:at], None, [w[:at] for w in want])
+    assert (out[at:, :, 5] == math.inf).all()
+    keep = [e for e in range(d) if e != 5]
+    ref.check(out[:, :, keep], None, [want[0][:, :, keep], want[1], want[2][:, :, keep], want[3]])
 
 
 # ---------------------------------------------------------------- many items: requests x kv heads x row tiles above the SMs
