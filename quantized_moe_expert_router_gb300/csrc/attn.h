@@ -28,7 +28,7 @@ struct KvPlanArgs {
   uint64_t *tree_mask;
   int B, T, num_free, max_pages, num_pages, page_shift;
 };
-cudaError_t launch_kv_plan(const KvPlanArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t stream);
 
 struct KvAppendArgs {
   RowView k, v;

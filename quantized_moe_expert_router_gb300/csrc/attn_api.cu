@@ -144,7 +144,7 @@ moe_status moe_kv_plan(moe_attn_t attn, int num_requests, int num_rows, const in
   a.tree_mask = tree_mask;
   a.B = num_requests; a.T = num_rows; a.num_free = num_free;
   a.max_pages = attn->cfg.max_pages; a.num_pages = attn->cfg.num_pages; a.page_shift = attn->page_shift;
-  return cuda_status(launch_kv_plan(a, attn->num_sms, stream));
+  return cuda_status(launch_kv_plan(a, stream));
 }
 
 moe_status moe_kv_append(moe_attn_t attn, int num_rows, const moe_attn_rows *k, const moe_attn_rows *v,

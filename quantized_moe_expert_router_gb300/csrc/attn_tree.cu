@@ -21,6 +21,9 @@
 //                     line; an item that lies in it is stored from the registers,
 //                     and only the first and the last one of a warp are joined,
 //                     when all warps are done.
+// us in the few and the many kernel, bf16, D = 128, 8 kv heads of 4: 64 requests of
+// a row at 500 34.7, 16.4 (512 items); 20 at 500 17.0, 12.5 (160); 18 at 500 10.8,
+// 12.7 (144); 8 of up to 8 rows at up to 4000 16.8, 20.5; 1 row at 1000 8.0, 10.7.
 // Parts of an item in several CTAs go to the workspace, and the CTA that finishes
 // its last part (a counter per item) joins them: no second launch.  All joins
 // go in the order of the context, so the result does not depend on timing.
@@ -29,6 +32,13 @@
 // is multiplied by P = 0, so v past the context is zeroed in shared memory,
 // and a drafted row's v that is infinite or NaN is added to the rows that see
 // it and then zeroed.
+//
+// Bound: long contexts by HBM: 16 requests of a row at up to 100000 tokens, 8 kv
+// heads of 8, read 2.8 GB in 407 us, 6.9 TB/s (a plain copy has 6.8).  Short ones by
+// the latencies of one call: 1 row at 1000 takes 8.2 us for 4 MB (launch 2 us,
+// lengths, page numbers, first keys, a warp's one or two chunks, the two joins); 8
+// requests of 2 to 8 drafted rows at 500 to 4000 take 17 us for 58 MB, the longest
+// with two row tiles that each read the chunks.
 #include <math.h>
 
 #include "attn_tc.cuh"
@@ -50,8 +60,7 @@ constexpr float kAtSlack = 8.f;
 //   128 rows, 1 of 4000: 16.4, 18.1 (6.6);           192 rows: 18.6, 18.0 (10);     256 rows: 22.6, 18.0 (13)
 //   64 rows, 1 of 30000: 31.7, 28.9 (25);            128 rows: 53.3, 29.4 (49)
 constexpr int kAtMostRows = 32, kAtMostChunks = 10;
-constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least: one per warp costs no more time than one
-constexpr int kAtExtra = 31;                     // chunks above the mean that are cheaper than a second part in a CTA
+constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least, one a warp: 1 row at 1000, us with 4, 8, 16: 8.8, 8.0, 9.0
 
 struct AtArgs {
   CUtensorMap kmap, vmap;      // (64, 16, 1, 1) boxes over [pages][kv_heads][page_size][D]
@@ -565,7 +574,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_few_kernel(const __grid_co
     return q;
   };
   const AtShare share =
-      at_share<kAtWarps>(s.t.work, a.B, total, nitems, kAtMinChunks, kAtExtra, s.cand,
+      at_share<kAtWarps>(s.t.work, a.B, total, nitems, kAtMinChunks, s.cand,
                          [&](int b) { return request(b).tiles * a.kv_heads; }, [&](int b) { return request(b).nch; });
   const long long x0 = share.x0, x1 = share.x1;
   if (x0 >= x1) return;

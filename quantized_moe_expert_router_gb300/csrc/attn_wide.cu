@@ -51,8 +51,16 @@
 // 128 rows are twins too, so that the softmax of one still runs beside the MMAs of
 // the other.
 //
-// Bound: with G = 8, D = 128 and long prompts the tensor pipe (2 x 512 cycles
-// a row tile and key tile); with D = 64 the exponentials.
+// Bound, D = 128: the tensor pipe.  S and PV of a row tile and key tile take it 1025
+// cycles when nothing else runs; beside the copies that write the same shared memory
+// some 1250, and 100 to 150 pass until the next product's P is seen.  16384 tokens (2
+// kv heads of 8): 632 us, 1740 TFLOP/s, where a library product has 1900; 4 x 4096 (4
+// of 8): 347 us, 1580; 512 (8 of 4): 12.1 us, a chain of launch, two key tiles a twin
+// and the store.  D = 64: one product behind the other; the pipe takes 525 cycles, the
+// exponentials 512 and the way from P to the next S the rest of 1140: 8192 tokens (4
+// of 8) 262 us, 1050 TFLOP/s; 17 prompts of 62 to 1501 (8 of 3) 44 us.  A third S
+// buffer with S three products ahead measured the same (267, 48).  Over the cache,
+// 4 requests of 16 to 64 rows at 1125 to 9000 (4 of 8): 27 us, the join's 6 among them.
 #include <math.h>
 #include <string.h>
 
@@ -67,8 +75,8 @@ constexpr int kApWTma = 0, kApWMma = 1, kApWHelp = 2, kApWSoft = 4;
 constexpr int kApMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr int kApMaxSms = 1024;                  // CTAs of the wide kernel at most
 constexpr float kApSlack = 8.f;                  // log2 of the largest P
-constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache)
-constexpr int kApExtra = 6;                      // key tiles above the mean that are cheaper than a second part in a CTA
+constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least (cache); us with 2, 6, 10: 512 rows at 9000 30.3, 30.3,
+                                                 // 32.9; 64 rows of 2 requests at 4000 19.6, 20.2, 21.7
 
 template <int D>
 struct ApGeom {
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       __syncthreads();
     }
     share = at_share<kApThreads / 32>(
-        s.work, a.B, total, nitems, kApMinTiles, kApExtra, s.cand,
+        s.work, a.B, total, nitems, kApMinTiles, s.cand,
         [&](int b) { return cache_tiles(p, s.n[b]) * a.kv_heads; }, [&](int b) { return cache_nch(a, s.n[b], s.cached[b]); });
     if (tid == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless cache_part finds it
   } else {
@@ -931,7 +939,9 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
 // rows of an item, a thread one row and four of its elements, so that 8 or 16
 // rows are read side by side and a long context's many parts are spread over as
 // many CTAs as there are.  The items to join are few and anywhere among the CTAs'
-// descriptions: every CTA looks all of them over and takes its units.
+// descriptions: every CTA looks all of them over and takes its units.  Latency bound:
+// the parts (19 MB for the 4 requests above, from L2) take some 6 us behind the kernel
+// above, which their bytes alone would in 3; more CTAs or more registers gave nothing.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ApArgs p, int sms) {
   __shared__ unsigned masks[kApMaxSms / 32];
