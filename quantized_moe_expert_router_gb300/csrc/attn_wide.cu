@@ -55,8 +55,8 @@
 // cycles when nothing else runs; beside the copies that write the same shared memory
 // some 1250, and 100 to 150 pass until the next product's P is seen.  16384 tokens (2
 // kv heads of 8): 632 us, 1740 TFLOP/s, where a library product has 1900; 4 x 4096 (4
-// of 8): 347 us, 1580; 512 (8 of 4): 12.1 us, a chain of launch, two key tiles a twin
-// and the store.  D = 64: one product behind the other; the pipe takes 525 cycles, the
+// of 8): 347 us, 1580; 512 (8 of 4): 11.5 us, a chain of launch (2 us), items and first
+// copies (3), two key tiles a twin (5) and the store.  D = 64: one product behind the other; the pipe takes 525 cycles, the
 // exponentials 512 and the way from P to the next S the rest of 1140: 8192 tokens (4
 // of 8) 262 us, 1050 TFLOP/s; 17 prompts of 62 to 1501 (8 of 3) 44 us.  A third S
 // buffer with S three products ahead measured the same (267, 48).  Over the cache,
@@ -116,12 +116,12 @@ struct ApItem {
 
 struct ApSmem {
   uint64_t kv_full[4], kv_empty[4];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, x_full, sched_full[2], sched_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, x_full[2], sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int wsum[2][kApThreads / 32];
   ApItem item[2];
   int v_pos[2][3];             // by item parity: stages of the masked value tiles, counted from the CTA's start
-  float2 stat[kApTile];        // prompts: (m, l) of the second twin
+  float2 stat[2][kApTile];     // (m, l) of the twins of a prompt
   uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
   union {
     struct {                   // prompts: requests by falling length
@@ -276,6 +276,12 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   const uint32_t q_smem = smem0, ring = smem0 + 2 * kTB;
   uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
 
+  // the first lengths: on their way while the barriers are set up
+  int lo0 = 0, hi0 = 0;
+  if (!PAGED && tid < a.B) {
+    lo0 = __ldg(a.cu + tid);
+    hi0 = __ldg(a.cu + tid + 1);
+  }
   if (warp == 0) {
     // a barrier a lane: one lane would take some 25 cycles for each of them
     if (lane < kStages) {
@@ -296,12 +302,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       mbar_init(&s.q_full, 1);
       mbar_init(&s.q_empty, 1);
       mbar_init(&s.v_next, 1);
-      mbar_init(&s.x_full, 4);
+      mbar_init(&s.x_full[0], 4);
+      mbar_init(&s.x_full[1], 4);
       mbar_init(&s.drain, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 32 * kApWTma) {
+  if (tid == 32 * kApWHelp) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.vmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   } else {
     // requests by falling number of row tiles (equal ones by index), every CTA alike
     for (int b = tid; b < a.B; b += kApThreads) {
-      const int lo = __ldg(a.cu + b), n = max(0, min(__ldg(a.cu + b + 1), a.T) - lo);
+      const int lo = b == tid ? lo0 : __ldg(a.cu + b), n = max(0, min(b == tid ? hi0 : __ldg(a.cu + b + 1), a.T) - lo);
       s.before[b] = lo < 0 ? 0 : at_idiv(n + p.span - 1, p.span);
     }
     __syncthreads();
@@ -541,55 +548,51 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
           at_wait_st();
         }
-        if (TWINS && it.n1 > 0) {
-          // The second twin's O, m and l go to the first through shared memory, in the
-          // place of Q: with twins a CTA has one item, and its S are done.
-          float4 *const x = reinterpret_cast<float4 *>(generic0) + (tid & 127);   // [element / 4][row]
-          float f0 = 1.f, f1 = 0.f;
-          if (h) {
-            s.stat[tid & 127] = make_float2(m, l);
-          } else {
-            if (!mbar_wait_bounded(&s.x_full, 0u)) {
-              atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-              break;
-            }
-            const float2 other = s.stat[tid & 127];
-            const float top = fmaxf(m, other.x);
-            f0 = m == top ? 1.f : at_exp2((m - top) * c);
-            f1 = other.x == top ? 1.f : at_exp2((other.x - top) * c);
-            m = top;
-            l = l * f0 + other.y * f1;
-          }
+        const bool halves = TWINS && it.n1 > 0;
+        if (halves) {
+          // Each twin gives the other the O of half of the columns, through shared memory
+          // in the place of Q: a CTA has one item then, and its S are done.
+          constexpr int kHalf = D / 2;
+          float4 *const x = reinterpret_cast<float4 *>(generic0) + (tid & 127);   // [giver][element / 4 of the half][row]
+          s.stat[h][tid & 127] = make_float2(m, l);
 #pragma unroll 1
-          for (int q = 0; q < D / 32; q++) {
+          for (int q = 0; q < kHalf / 32; q++) {
             float o[32];
-            at_ld32(to + 32u * q, o);
+            at_ld32(to + (uint32_t)(kHalf * (h ^ 1) + 32 * q), o);
             at_wait_ld(o);
-            if (h) {
 #pragma unroll
-              for (int e = 0; e < 8; e++) x[(8 * q + e) * kApTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            } else {
+            for (int e = 0; e < 8; e++)
+              x[(kHalf / 4 * h + 8 * q + e) * kApTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.x_full[h]);
+          if (!mbar_wait_bounded(&s.x_full[h ^ 1], 0u)) {
+            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+            break;
+          }
+          const float2 other = s.stat[h ^ 1][tid & 127];
+          const float top = fmaxf(m, other.x);
+          const float f0 = m == top ? 1.f : at_exp2((m - top) * c), f1 = other.x == top ? 1.f : at_exp2((other.x - top) * c);
+          m = top;
+          l = h ? other.y * f1 + l * f0 : l * f0 + other.y * f1;
+#pragma unroll 1
+          for (int q = 0; q < kHalf / 32; q++) {
+            float o[32];
+            at_ld32(to + (uint32_t)(kHalf * h + 32 * q), o);
+            at_wait_ld(o);
 #pragma unroll
-              for (int e = 0; e < 8; e++) {
-                const float4 w = x[(8 * q + e) * kApTile];
-                o[4 * e] = o[4 * e] * f0 + w.x * f1;
-                o[4 * e + 1] = o[4 * e + 1] * f0 + w.y * f1;
-                o[4 * e + 2] = o[4 * e + 2] * f0 + w.z * f1;
-                o[4 * e + 3] = o[4 * e + 3] * f0 + w.w * f1;
-              }
-              at_st32(to + 32u * q, o);
+            for (int e = 0; e < 8; e++) {
+              const float4 w = x[(kHalf / 4 * (h ^ 1) + 8 * q + e) * kApTile];
+              o[4 * e] = o[4 * e] * f0 + w.x * f1;
+              o[4 * e + 1] = o[4 * e + 1] * f0 + w.y * f1;
+              o[4 * e + 2] = o[4 * e + 2] * f0 + w.z * f1;
+              o[4 * e + 3] = o[4 * e + 3] * f0 + w.w * f1;
             }
+            at_st32(to + (uint32_t)(kHalf * h + 32 * q), o);
           }
-          if (h) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.x_full);
-          } else {
-            at_wait_st();
-          }
+          at_wait_st();
         }
-        if (TWINS && h) {
-          // the first twin stores
-        } else if (PAGED && it.slot >= 0) {
+        if (PAGED && it.slot >= 0) {
           // [element / 4][row]: the 32 rows of a warp side by side
           float4 *part = p.part + (size_t)it.slot * (D / 4) * kApRows + (kApTile * h + (tid & 127));
 #pragma unroll 1
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         } else {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const int hq = it.hk * a.group + r - dt * a.group;
-          if (a.lse && real)
+          if (a.lse && real && !(TWINS && h))
             a.lse[(size_t)(it.first + lim) * a.q_heads + hq] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
           // A lane's row at a time would touch 32 lines a store; with the
           // fragment shape a quad holds 32 elements of a row (pairs 2 q4 of each
@@ -625,17 +628,25 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                        (long long)(it.hk * a.group + rr - dr * a.group) * a.out.head + 8 * q4;
             }
 #pragma unroll
-            for (int cb = 0; cb < D / 32; cb++) {
-              float o[16];
+            for (int cz = 0; cz < D / 32; cz += 2) {   // blocks of 32 columns, two loads at a time; of twins their half
+              const int blocks = halves ? D / 64 : D / 32, cb = (halves ? D / 64 * h : 0) + cz;
+              if (cz >= blocks) break;
+              float o[32];
               at_ld_frag(to + ((uint32_t)(16 * rb) << 16) + 32u * cb, o);
+              if (cz + 1 < blocks) at_ld_frag(to + ((uint32_t)(16 * rb) << 16) + 32u * (cb + 1), o + 16);
               at_wait_ld(o);
 #pragma unroll
-              for (int z = 0; z < 2; z++) {
-                uint32_t w[4];
+              for (int y = 0; y < 2; y++) {
+                if (cz + y >= blocks) break;
 #pragma unroll
-                for (int e = 0; e < 4; e++) w[e] = at_pack<F16>(o[4 * e + 2 * z] * iv[z], o[4 * e + 2 * z + 1] * iv[z]);
-                at_quad_transpose(w, q4);
-                if (wr[z]) *reinterpret_cast<uint4 *>(dst[z] + 32 * cb) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int z = 0; z < 2; z++) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int e = 0; e < 4; e++)
+                    w[e] = at_pack<F16>(o[16 * y + 4 * e + 2 * z] * iv[z], o[16 * y + 4 * e + 2 * z + 1] * iv[z]);
+                  at_quad_transpose(w, q4);
+                  if (wr[z]) *reinterpret_cast<uint4 *>(dst[z] + 32 * (cb + y)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
               }
             }
           }
@@ -675,7 +686,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             mbar_arrive(&s.sched_full[i & 1]);
           }
           if (it.b < 0) break;
-          if (!PAGED) next = gridDim.x + atomicAdd(p.ctrl + kAttnCtrlNext, 1);
+          if (TWINS) next = total;                 // a CTA an item
+          else if (!PAGED) next = gridDim.x + atomicAdd(p.ctrl + kAttnCtrlNext, 1);
           // stage q: K[q] and V[q - ahead], as far as they are there
           const int n = it.n, ahead = (PAGED ? it.twin : TWINS) ? 2 : 1;
           for (int q = 0; q < n + ahead; q++) {
@@ -727,7 +739,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         // copies in flight land before the CTA ends
         for (int q = (pos > kStages ? pos - kStages : 0); q < pos; q++)
           mbar_wait_bounded(&s.kv_full[q % kStages], (uint32_t)(q / kStages) & 1u);
-        if (!PAGED) {
+        if (!PAGED && !TWINS) {
           // the last CTA to have taken its last item leaves the counters at zero
           __threadfence();
           if (atomicAdd(p.ctrl + kAttnCtrlDone, 1) == (int)gridDim.x - 1) {
@@ -1091,7 +1103,7 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaSt
   // Items at most: every request may end inside one.  Where row tiles are as few as
   // CTAs, an item is one row tile and the softmax warps of the other take every second
   // of its key tiles (us with twins, without): 1 prompt of 512, 8 kv heads of 4, D = 128
-  // 12.2, 13.5; of 2000, 1 kv head of 8 21.2, 29.5; of 1000, 8 of 2, D = 64 12.1, 15.6.
+  // 11.5, 13.5; of 2000, 1 kv head of 8 20.3, 29.5; of 1000, 8 of 2, D = 64 11.5, 15.6.
   auto items_of = [&](int span) { return (a.T + (long long)a.B * (span - 1)) / span * a.kv_heads; };
   p.span = items_of(p.per) <= num_sms ? p.per : 2 * p.per;
   const long long items = items_of(p.span);
