@@ -285,3 +285,12 @@ def test_lengths_past_the_block_table(fresh, extra, cached):
     parts = [ref.attend(x, *c.rows[b], vis[b], 128 ** -0.5) for b, x in enumerate(q.split(fresh))]
     ref.check(out, lse, [torch.cat([p[i] for p in parts]) for i in range(4)])
     assert moe.moe_attn_get_device_status(c.attn, ws) == 0
+
+
+def test_workspace_elsewhere_is_refused():
+    c = Cache(4, 2, 64, 16, torch.bfloat16, [20], [1], seed=180)
+    out, ws = torch.empty_like(c.q), moe.alloc_attn_workspace(c.attn, 1, 1).cpu()
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        moe.moe_attn_tree(c.attn, c.q, c.cu, c.cached, c.table, c.k, c.v, out, ws)
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        moe.moe_attn_prompt(c.attn, c.q, c.q[:, :2], c.q[:, :2], c.cu, out, ws)
