@@ -35,8 +35,8 @@
 //
 // Bound: long contexts by HBM: 16 requests of a row at up to 100000 tokens, 8 kv
 // heads of 8, read 2.8 GB in 407 us, 6.9 TB/s (a plain copy has 6.8).  Short ones by
-// the latencies of one call: 1 row at 1000 takes 8.2 us for 4 MB (launch 2 us,
-// lengths, page numbers, first keys, a warp's one or two chunks, the two joins); 8
+// the latencies of one call: 1 row at 1000 takes 7.9 us for 4 MB (launch 1.5,
+// lengths and shares 2, page numbers and keys 2, a warp's chunk 0.8, the two joins 1.5); 8
 // requests of 2 to 8 drafted rows at 500 to 4000 take 17 us for 58 MB, the longest
 // with two row tiles that each read the chunks.
 #include <math.h>
@@ -124,8 +124,9 @@ __device__ __forceinline__ void at_ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 template <int TOK>
 __device__ __forceinline__ void at_request(const AtTable &s, const AttnArgs &a, AtPos &p) {
   const int n = s.n[p.b];
-  p.tiles = (int)(((long long)n * a.group + kAtRows - 1) / kAtRows);
-  p.nch = (int)((min((long long)s.cached[p.b] + n, (long long)a.max_pages << a.page_shift) + TOK - 1) / TOK);
+  // rows <= 2^20 x 128; the block table's tokens <= 2^30, and `cached` is at most that
+  p.tiles = (n * a.group + kAtRows - 1) / kAtRows;
+  p.nch = (min(s.cached[p.b] + n, a.max_pages << a.page_shift) + TOK - 1) / TOK;
 }
 // Fills in the table; every CTA does the same.  All threads; ends with a barrier.
 template <int TOK>
@@ -212,7 +213,7 @@ struct AtItem {
     const int row0 = p.rt * kAtRows;
     first = s.first[p.b];
     hk = p.hk;
-    rows = (int)min((long long)kAtRows, (long long)s.n[p.b] * a.group - row0);
+    rows = min(kAtRows, s.n[p.b] * a.group - row0);
     i0 = at_idiv(row0, a.group);
     g0 = row0 - i0 * a.group;
   }
@@ -258,7 +259,7 @@ struct AtSums {
     const int g = (threadIdx.x & 31) >> 2, q4 = threadIdx.x & 3;
     b = request;
     cached = s.cached[b];
-    ctx = (int)min((long long)cached + s.n[b], (long long)a.max_pages << a.page_shift);
+    ctx = min(cached + s.n[b], a.max_pages << a.page_shift);
 #pragma unroll
     for (int z = 0; z < 2; z++) {
       const int r = g + 8 * z;

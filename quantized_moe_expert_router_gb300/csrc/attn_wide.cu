@@ -142,8 +142,8 @@ struct ApSmem {
 // tiles that its rows may see.
 __device__ __forceinline__ int cache_tiles(const ApArgs &p, int n) { return at_idiv(n + 2 * p.per - 1, 2 * p.per); }
 __device__ __forceinline__ int cache_nch(const AttnArgs &a, int n, int cached) {
-  const long long ctx = min((long long)cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n), (long long)a.max_pages << a.page_shift);
-  return (int)((ctx + kApTile - 1) / kApTile);
+  const int ctx = min(cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n), a.max_pages << a.page_shift);
+  return (ctx + kApTile - 1) / kApTile;
 }
 
 // The idx-th item by falling row tile: row tiles [tiles[k], tiles[k - 1]) have
@@ -193,9 +193,9 @@ __device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p
   it.hk = at_idiv(item, tiles);
   it.tok0 = (item - it.hk * tiles) * 2 * p.per;
   it.toks = min(n - it.tok0, 2 * p.per);
-  const long long lim = min((long long)a.max_pages << a.page_shift, (long long)it.cached + n);
+  const int lim = min(a.max_pages << a.page_shift, it.cached + n);
   it.all = a.tree_mask ? it.cached : it.cached + it.tok0 + 1;
-  it.end = (int)min(lim, (long long)it.cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : it.tok0 + it.toks));
+  it.end = min(lim, it.cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : it.tok0 + it.toks));
   const int need = (it.end + kApTile - 1) / kApTile;                          // key tiles of this row tile
   it.j0 = (int)(x - item0);
   it.n = max(0, min((int)(xe - item0), need) - it.j0);
