@@ -28,7 +28,7 @@
 //                   one operation to the next, hence one stage, one barrier and
 //                   few commits a tile (and not an issuer per row tile: their
 //                   MMAs mix, and each change of accumulator costs)
-//   warps 2-3       Q rows by tensor-map boxes (64, G, tokens); the scan below
+//   warps 2-3       the scan below; warp 2 also Q rows by tensor-map boxes (64, G, tokens)
 //   warps 4-7, 8-11 softmax of row tile 0 and 1: a thread owns a row, so the
 //                   maximum and the sum need no exchange between threads;
 //                   also the rare rescaling of O and the epilogue
@@ -39,6 +39,24 @@
 // times an infinite or NaN v is NaN, so warps 2-3 scan those tiles' v, zero
 // such elements and note their tokens, and the epilogue adds them to the
 // rows that do see the token.
+//
+// A wait knows its phase by parity alone, so no barrier may be two phases on when
+// a waiter looks (it would wait for the next phase of that parity, or for ever).
+// What keeps each from it:
+//   sched_full    (item parity) item i + 2 is posted when sched_empty has all 11 arrivals
+//                 of item i, each after that warp's last use of the item
+//   kv_full       the stage is filled again after kv_empty, which the MMA warp commits
+//                 after its own wait, and behind v_clean, which both helper warps
+//                 give after theirs; v_posted says that the phase before is over
+//   kv_empty      the copy warp waits before each filling; no lane copies before all
+//                 lanes have passed
+//   q_full        filled again by warp 2 behind q_empty, behind the MMA warp's wait
+//   q_empty       waited for by warp 2 alone, whose lanes meet before the next Q is
+//                 copied, and without that Q there is no next commit
+//   v_posted, v_clean   (item parity) used again two items on, behind sched_empty
+//   s_full, p_full, o_done   S, P and O of a row tile go to and fro between the MMA
+//                 warp and the four softmax warps, which all arrive on p_full
+// (tests/attn_barriers.py runs these roles with any one of them held back.)
 //
 // Prompts: items are taken from a counter, those with most key tiles first; an
 // item's length depends on its row tile alone, so with the requests ranked by
@@ -116,7 +134,7 @@ struct ApItem {
 
 struct ApSmem {
   uint64_t kv_full[4], kv_empty[4];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[3], v_next, x_full[2], sched_full[2], sched_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[2][3], x_full[2], sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int wsum[2][kApThreads / 32];
   ApItem item[2];
@@ -297,11 +315,11 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     } else if (lane < 5) {
       mbar_init(&s.v_posted[0][lane - 2], 1);
       mbar_init(&s.v_posted[1][lane - 2], 1);
-      mbar_init(&s.v_clean[lane - 2], 2);
+      mbar_init(&s.v_clean[0][lane - 2], 2);       // both helper warps
+      mbar_init(&s.v_clean[1][lane - 2], 2);
     } else if (lane == 5) {
       mbar_init(&s.q_full, 1);
       mbar_init(&s.q_empty, 1);
-      mbar_init(&s.v_next, 1);
       mbar_init(&s.x_full[0], 4);
       mbar_init(&s.x_full[1], 4);
       mbar_init(&s.drain, 1);
@@ -511,16 +529,20 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           break;
         }
         at_fence_after();
+        // words of the masked tiles that this row tile's PV waited for: the others may be of an
+        // earlier item, or not complete yet
+        const int wend = 4 * ((twin ? it.n : nt) - it.m0);
         uint32_t anybad = 0;
 #pragma unroll
-        for (int w = 0; w < 12; w++) anybad |= s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
+        for (int w = 0; w < 12; w++)
+          if (w < wend && !(twin && ((it.m0 + (w >> 2)) & 1) != h)) anybad |= s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
         if (anybad) {
 #pragma unroll 1
           for (int q = 0; q < D / 32; q++) {
             float o[32];
             at_ld32(to + 32u * q, o);
             at_wait_ld(o);
-            for (int w = 0; w < 12; w++) {
+            for (int w = 0; w < wend; w++) {
               uint32_t bits = s.bad[i & 1][0][w >> 2][w & 3] | s.bad[i & 1][1][w >> 2][w & 3];
               for (; bits; bits &= bits - 1) {
                 const int jl = it.m0 + (w >> 2);   // tile of the part
@@ -758,7 +780,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       const uint32_t tu = __shfl_sync(kFull, tb, 0);
       const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring + kTB, kApTile * 128);
       int slot = 0;                                // next stage and its phase
-      uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;
+      uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;   // clean: a phase bit per item parity and masked tile
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok && !mbar_wait_bounded(bar, parity)) {
@@ -818,13 +840,9 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         for (int j = 0; j < n && ok; j++) {
           wait(&s.kv_full[slot], phase);
           if (j >= m0) {
-            const int z = j - m0;                  // 0, 1 or 2; a phase bit each
-            wait(&s.v_clean[z], (clean >> z) & 1u);
-            clean ^= 1u << z;
-          }
-          if (j + 1 == n) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.v_next); // the next item's scans may signal
+            const int z = j - m0, bit = 3 * (i & 1) + z;   // z: 0, 1 or 2
+            wait(&s.v_clean[i & 1][z], (clean >> bit) & 1u);
+            clean ^= 1u << bit;
           }
           const int left = end - j * kApTile;      // tokens of the tile that some row sees
           const uint64_t db = dv0 + (uint64_t)(slot * (2 * kTB >> 4));
@@ -879,7 +897,9 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const int n = it.n;
         if (lane < 12) s.bad[i & 1][warp - kApWHelp][lane >> 2][lane & 3] = 0u;
         __syncwarp();
-        if (i > 0 && !mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u)) break;
+        // warp 3 has no part in Q: were it to wait here, the MMA warp could be done with the
+        // next Q before it looks
+        if (warp == kApWHelp && i > 0 && !__all_sync(kFull, mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u))) break;
         // a box (64, group, per) is a row tile; rows past the item's tokens are
         // others' or zeros, rows past the box what was there: none is stored
         if (ht == 0) {
@@ -891,9 +911,6 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                         &s.q_full);
         }
         nq++;
-        // the MMA warp has seen this item's predecessor's scans: a barrier is
-        // never a phase ahead of its reader
-        if (i > 0 && !mbar_wait_bounded(&s.v_next, (uint32_t)(i - 1) & 1u)) break;
         for (int j = it.m0; j < n; j++) {
           const int z = j - it.m0;
           const uint32_t ph = z == 0 ? posted[0] : (z == 1 ? posted[1] : posted[2]);   // by item parity: bit i & 1
@@ -929,12 +946,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             }
           at_fence_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.v_clean[z]);
+          if (lane == 0) mbar_arrive(&s.v_clean[i & 1][z]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
-      if (nq > 0) mbar_wait_bounded(&s.q_full, (uint32_t)(nq - 1) & 1u);   // a copy in flight lands before the CTA ends
+      // a copy in flight lands before the CTA ends
+      if (warp == kApWHelp && nq > 0) mbar_wait_bounded(&s.q_full, (uint32_t)(nq - 1) & 1u);
       __syncwarp();
     }
   }
