@@ -370,8 +370,13 @@ typedef struct {
   int32_t max_pages;      /* entries of a block-table row (its stride) */
   int32_t dtype;          /* MOE_ATTN_BF16 or MOE_ATTN_F16 */
   float softmax_scale;    /* multiplies q . k (finite, > 0); 1 / sqrt(head_dim) as a rule */
-  uint32_t flags;         /* must be 0 */
+  uint32_t flags;         /* MOE_ATTN_TEST_STALL, or 0 */
 } moe_attn_config;
+
+/* Test hook: the copies of keys and values wait for bytes that never come, with a limit
+ * of 20 ms.  moe_attn_prompt and moe_attn_tree then return invalid outputs and raise
+ * MOE_FLAG_TIMEOUT. */
+#define MOE_ATTN_TEST_STALL 0x80000000u
 
 /* Per-row vectors [rows][heads][head_dim]: element (t, h, d) is at
  * data + t * row_stride + h * head_stride + d (strides in elements, positive

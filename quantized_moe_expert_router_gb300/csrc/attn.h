@@ -48,6 +48,8 @@ struct AttnArgs {
   float *lse;                 // [T][q_heads] or null
   int B, T, q_heads, kv_heads, group, head_dim, page_shift, max_pages, num_pages, f16;
   float scale;
+  unsigned stall;             // bytes that a copy's barrier expects and that never come (MOE_ATTN_TEST_STALL); else 0
+  unsigned long long wait_ns; // limit of a device wait
 };
 // First 256 bytes of the workspace: zero between calls, but for the flags.
 constexpr int kAttnCtrlBytes = 256;

@@ -61,6 +61,9 @@ AttnArgs attn_args(const moe_attn &L, int B, int T) {
   a.num_pages = L.cfg.num_pages;
   a.f16 = L.cfg.dtype == MOE_ATTN_F16;
   a.scale = L.cfg.softmax_scale;
+  const bool stall = L.cfg.flags & MOE_ATTN_TEST_STALL;
+  a.stall = stall ? 16 : 0;
+  a.wait_ns = stall ? 20000000ull : 2000000000ull;
   return a;
 }
 
@@ -72,7 +75,7 @@ extern "C" {
 
 moe_status moe_attn_create(const moe_attn_config *cfg, int device, moe_attn_t *out) {
   if (!cfg || !out || device < 0) return MOE_ERR_INVALID_ARG;
-  if (cfg->flags || !(cfg->softmax_scale > 0.f) || !isfinite(cfg->softmax_scale)) return MOE_ERR_INVALID_ARG;
+  if ((cfg->flags & ~MOE_ATTN_TEST_STALL) || !(cfg->softmax_scale > 0.f) || !isfinite(cfg->softmax_scale)) return MOE_ERR_INVALID_ARG;
   if (cfg->dtype != MOE_ATTN_BF16 && cfg->dtype != MOE_ATTN_F16) return MOE_ERR_INVALID_ARG;
   if (cfg->kv_heads < 1 || cfg->q_heads < cfg->kv_heads || cfg->q_heads % cfg->kv_heads ||
       cfg->q_heads / cfg->kv_heads > 128 || cfg->q_heads > 1024)

@@ -191,6 +191,14 @@ __device__ __forceinline__ long long at_div(long long x, long long d) {
   return (x | d) >> 31 ? x / d : (long long)at_idiv((int)x, (int)d);
 }
 
+// A bounded wait of a whole warp, which goes on or gives up together (what follows are
+// instructions of whole warps).
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, const AttnArgs &a, int *ctrl) {
+  const bool ok = __all_sync(kFull, mbar_wait_bounded(bar, parity, a.wait_ns));
+  if (!ok && (threadIdx.x & 31) == 0) atomicOr(ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+  return ok;
+}
+
 // The share of a CTA in the line of units (chunks or key tiles) of all items.
 // work[b]: units of the requests before b; request b has items(b) items of
 // nch(b) units each.  Two ways to cut the line:

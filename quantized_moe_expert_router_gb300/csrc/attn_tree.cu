@@ -230,7 +230,7 @@ template <int D>
 __device__ __forceinline__ void at_copy(const AtArgs &g, const AtPos &p, uint32_t dst, uint64_t *bar) {
   constexpr int kTok = AtGeom<D>::kTok, kHalves = D / 64;
   const AttnArgs &a = g.a;
-  mbar_arrive_expect_tx(bar, kAtStageBytes);
+  mbar_arrive_expect_tx(bar, kAtStageBytes + a.stall);
 #pragma unroll
   for (int k = 0; k < kTok / 16; k++) {
     const int tok = p.chunk * kTok + 16 * k, col = tok >> a.page_shift;
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_few_kernel(const __grid_co
       const int stage = kc % kAtStages, ch = (int)(xc - item0);
       bool held[AtSums<D, F16>::kBlocks];
       w.pages(a, ch, held);
-      if (ok && !mbar_wait_bounded(&s.full[warp][stage], (kc / kAtStages) & 1u)) {
+      if (ok && !mbar_wait_bounded(&s.full[warp][stage], (kc / kAtStages) & 1u, a.wait_ns)) {
         atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
         ok = false;
       }
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_few_kernel(const __grid_co
   // copies in flight (after a wait ran out) land before the CTA ends
   if (!ok)
     for (uint32_t k = kp > kAtStages ? kp - kAtStages : 0; k < kp; k++)
-      mbar_wait_bounded(&s.full[warp][k % kAtStages], (k / kAtStages) & 1u);
+      mbar_wait_bounded(&s.full[warp][k % kAtStages], (k / kAtStages) & 1u, a.wait_ns);
 }
 
 // ----------------------------------------------------------------- many items
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_many_kernel(const __grid_c
         const int stage = kc % kAtStages;
         bool held[AtSums<D, F16>::kBlocks];
         w.pages(a, ch, held);
-        if (ok && !mbar_wait_bounded(&s.full[warp][stage], (kc / kAtStages) & 1u)) {
+        if (ok && !mbar_wait_bounded(&s.full[warp][stage], (kc / kAtStages) & 1u, a.wait_ns)) {
           atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
           ok = false;
         }
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_many_kernel(const __grid_c
     // copies in flight (after a wait ran out) land before the CTA ends
     if (!ok)
       for (uint32_t k = kp > kAtStages ? kp - kAtStages : 0; k < kp; k++)
-        mbar_wait_bounded(&s.full[warp][k % kAtStages], (k / kAtStages) & 1u);
+        mbar_wait_bounded(&s.full[warp][k % kAtStages], (k / kAtStages) & 1u, a.wait_ns);
   }
   __syncthreads();
 

@@ -435,10 +435,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     uint32_t ns = 0, ni = 0;                       // key tiles of this row tile, and items with any, so far
     bool ok = true;
     for (int i = 0;; i++) {
-      if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) {
-        atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-        break;
-      }
+      if (!at_wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u, a, p.ctrl)) break;
       const ApItem it = s.item[i & 1];
       if (it.b < 0) break;
       const int nt = h ? it.n1 : it.n0;
@@ -464,11 +461,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         } else {
           masked = __any_sync(kFull, tok0 + kApTile - 1 > lim);
         }
-        if (!mbar_wait_bounded(&s.s_full[h], ns & 1u)) {
-          atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-          ok = false;
-          break;
-        }
+        ok = at_wait(&s.s_full[h], ns & 1u, a, p.ctrl);
+        if (!ok) break;
         at_fence_after();
         float v[128];
 #pragma unroll
@@ -524,10 +518,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (kApTile * h + (tid & 127))] = make_float2(m, l);
       if (nt > 0) {
         // ---------------------------------------------------------- epilogue
-        if (!mbar_wait_bounded(&s.o_done[h], ni++ & 1u)) {
-          atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-          break;
-        }
+        if (!at_wait(&s.o_done[h], ni++ & 1u, a, p.ctrl)) break;
         at_fence_after();
         // words of the masked tiles that this row tile's PV waited for: the others may be of an
         // earlier item, or not complete yet
@@ -588,10 +579,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.x_full[h]);
-          if (!mbar_wait_bounded(&s.x_full[h ^ 1], 0u)) {
-            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-            break;
-          }
+          if (!at_wait(&s.x_full[h ^ 1], 0u, a, p.ctrl)) break;
           const float2 other = s.stat[h ^ 1][tid & 127];
           const float top = fmaxf(m, other.x);
           const float f0 = m == top ? 1.f : at_exp2((m - top) * c), f1 = other.x == top ? 1.f : at_exp2((other.x - top) * c);
@@ -687,6 +675,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         int pos = 0;
         long long next = PAGED ? share.x0 : blockIdx.x;
         bool ok = true;
+        // over the cache the warp waits as one; else lane 0 is alone
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+          if constexpr (PAGED) return at_wait(bar, parity, a, p.ctrl);
+          const bool got = mbar_wait_bounded(bar, parity, a.wait_ns);
+          if (!got) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+          return got;
+        };
         for (int i = 0; ok; i++) {
           ApItem it;
           it.b = -1;
@@ -699,10 +694,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           } else if (next < total) {
             prompt_item(s, p, (int)next, it);
           }
-          if (i >= 2 && !mbar_wait_bounded(&s.sched_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u)) {
-            atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-            break;
-          }
+          if (i >= 2 && !wait(&s.sched_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u)) break;
           if (lane == 0) {
             s.item[i & 1] = it;
             mbar_arrive(&s.sched_full[i & 1]);
@@ -725,13 +717,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                 page[z] = (unsigned)id < (unsigned)a.num_pages ? id : a.num_pages;   // past the end: reads zeros
               }
             }
-            if (pos >= kStages && !mbar_wait_bounded(&s.kv_empty[slot], (uint32_t)(pos / kStages - 1) & 1u)) {
-              atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-              ok = false;
-              break;
-            }
+            if (pos >= kStages) ok = wait(&s.kv_empty[slot], (uint32_t)(pos / kStages - 1) & 1u);
+            if (!ok) break;
             if (lane == 0) {
-              mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)(kTB * ((q < n) + (q >= ahead))));
+              mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)(kTB * ((q < n) + (q >= ahead))) + a.stall);
               // the scan may wait for this stage now: before, the barrier may still
               // be in an earlier phase, which a wait cannot tell from this one
               if (q - ahead >= it.m0) {
@@ -760,7 +749,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
         // copies in flight land before the CTA ends
         for (int q = (pos > kStages ? pos - kStages : 0); q < pos; q++)
-          mbar_wait_bounded(&s.kv_full[q % kStages], (uint32_t)(q / kStages) & 1u);
+          mbar_wait_bounded(&s.kv_full[q % kStages], (uint32_t)(q / kStages) & 1u, a.wait_ns);
         if (!PAGED && !TWINS) {
           // the last CTA to have taken its last item leaves the counters at zero
           __threadfence();
@@ -783,7 +772,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;   // clean: a phase bit per item parity and masked tile
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait_bounded(bar, parity)) {
+        if (ok && !mbar_wait_bounded(bar, parity, a.wait_ns)) {
           atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
           ok = false;
         }
@@ -882,7 +871,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       }
       // every MMA issued has completed before tensor memory is released
       if (at_elect()) at_commit(&s.drain);
-      mbar_wait_bounded(&s.drain, 0u);
+      mbar_wait_bounded(&s.drain, 0u, a.wait_ns);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- Q rows, and the scan of masked tiles' v
@@ -891,7 +880,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       int nq = 0;                                  // items whose Q has been copied
       bool ok = true;
       for (int i = 0; ok; i++) {
-        if (!mbar_wait_bounded(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+        if (!at_wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u, a, p.ctrl)) break;
         const ApItem it = s.item[i & 1];
         if (it.b < 0) break;
         const int n = it.n;
@@ -899,7 +888,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         __syncwarp();
         // warp 3 has no part in Q: were it to wait here, the MMA warp could be done with the
         // next Q before it looks
-        if (warp == kApWHelp && i > 0 && !__all_sync(kFull, mbar_wait_bounded(&s.q_empty, (uint32_t)(i - 1) & 1u))) break;
+        if (warp == kApWHelp && i > 0 && !at_wait(&s.q_empty, (uint32_t)(i - 1) & 1u, a, p.ctrl)) break;
         // a box (64, group, per) is a row tile; rows past the item's tokens are
         // others' or zeros, rows past the box what was there: none is stored
         if (ht == 0) {
@@ -914,15 +903,11 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         for (int j = it.m0; j < n; j++) {
           const int z = j - it.m0;
           const uint32_t ph = z == 0 ? posted[0] : (z == 1 ? posted[1] : posted[2]);   // by item parity: bit i & 1
-          if (!mbar_wait_bounded(&s.v_posted[i & 1][z], (ph >> (i & 1)) & 1u)) {
-            ok = false;
-            break;
-          }
+          ok = at_wait(&s.v_posted[i & 1][z], (ph >> (i & 1)) & 1u, a, p.ctrl);
+          if (!ok) break;
           const int pos = s.v_pos[i & 1][z], slot = pos % kStages;
-          if (!mbar_wait_bounded(&s.kv_full[slot], (uint32_t)(pos / kStages) & 1u)) {
-            ok = false;
-            break;
-          }
+          ok = at_wait(&s.kv_full[slot], (uint32_t)(pos / kStages) & 1u, a, p.ctrl);
+          if (!ok) break;
           if (z == 0) posted[0] ^= 1u << (i & 1);
           else if (z == 1) posted[1] ^= 1u << (i & 1);
           else posted[2] ^= 1u << (i & 1);
@@ -952,7 +937,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
       // a copy in flight lands before the CTA ends
-      if (warp == kApWHelp && nq > 0) mbar_wait_bounded(&s.q_full, (uint32_t)(nq - 1) & 1u);
+      if (warp == kApWHelp && nq > 0) mbar_wait_bounded(&s.q_full, (uint32_t)(nq - 1) & 1u, a.wait_ns);
       __syncwarp();
     }
   }

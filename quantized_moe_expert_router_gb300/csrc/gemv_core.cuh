@@ -62,14 +62,17 @@ __device__ __forceinline__ unsigned long long global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Bounded wait for the phase with `parity` to complete; false on expiry.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity) {
+// Bounded wait for the phase with `parity` to complete; false on expiry.  The
+// clock is read after every try that failed: a try suspends the warp for as long as
+// the hardware likes (3.9 us measured on GB300, with any time hint), so that a count
+// of tries bounds nothing.
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity, unsigned long long limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  for (uint32_t it = 1;; it++) {
+  do {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) return false;
-  }
+  } while (global_ns() - t0 <= limit_ns);
+  return false;
 }
 __device__ __forceinline__ void bulk_copy_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
                                               uint64_t pol) {

@@ -34,6 +34,7 @@ CONFIG_GROUPED_ABOVE_8 = 0x2            # the grouped tcgen05 path for every cal
 CONFIG_W4A4 = 0x4                       # activations quantized to NVFP4 with each matrix's input scale
 ACT_BF16, ACT_F32 = 0, 1                # source types of moe_quantize_nvfp4
 ATTN_BF16, ATTN_F16 = 0, 1              # element types of an Attention
+ATTN_TEST_STALL = 0x80000000            # test hook: the attention's bounded waits run out
 KV_FLAG_LENGTH = 0x1                    # moe_kv_plan's info[3]: a negative length, or more rows than given
 KV_FLAG_TABLE = 0x2                     # a context longer than a block-table row
 KV_FLAG_PAGES = 0x4                     # free pages ran out, or a page id is out of range
@@ -371,13 +372,13 @@ class Attention:
     given."""
 
     def __init__(self, q_heads, kv_heads, head_dim, page_size, num_pages, max_pages, dtype=torch.bfloat16,
-                 softmax_scale=None, device=0):
+                 softmax_scale=None, device=0, flags=0):
         if dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"Attention: unsupported dtype {dtype}")
         lib = load_library()
         scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
         self.cfg = moe_attn_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_pages,
-                                   ATTN_F16 if dtype == torch.float16 else ATTN_BF16, scale, 0)
+                                   ATTN_F16 if dtype == torch.float16 else ATTN_BF16, scale, flags)
         self.dtype, self.device = dtype, device
         self.q_heads, self.kv_heads, self.head_dim, self.max_pages = q_heads, kv_heads, head_dim, max_pages
         self.cache_shape = (num_pages, kv_heads, page_size, head_dim)

@@ -76,3 +76,11 @@ def test_reference_roundoff_is_that_of_the_types():
     for dt, u in ref.U.items():
         err = ((x.to(dt).double() - x) / x).abs().max()
         assert abs(float(err) - u / (1 + u)) < 1e-4 * u
+
+
+@pytest.mark.parametrize("flags", [0x80000001, 0x40000000])
+def test_create_knows_one_flag(lib, flags):
+    cfg = moe.moe_attn_config(8, 2, 128, 16, 64, 8, 0, 0.1, flags)
+    out = ctypes.c_void_p()
+    lib.moe_attn_create.argtypes = [ctypes.POINTER(moe.moe_attn_config), ctypes.c_int, ctypes.POINTER(ctypes.c_void_p)]
+    assert lib.moe_attn_create(ctypes.byref(cfg), 0, ctypes.byref(out)) == 1 and not out.value
