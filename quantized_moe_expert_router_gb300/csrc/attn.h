@@ -60,7 +60,7 @@ constexpr int kAttnCtrlNext = 0, kAttnCtrlDone = 1, kAttnCtrlFlags = 2;   // int
 struct AttnWideWs {
   size_t desc, stat, part, total;
 };
-struct AttnTreeWs {
+struct AttnTreeWs {             // up to `stat`: zero between calls, but for the flags
   size_t tickets, stat, part, total;
   AttnWideWs wide;
 };

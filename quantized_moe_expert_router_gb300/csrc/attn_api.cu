@@ -121,7 +121,8 @@ moe_status moe_attn_get_device_status(moe_attn_t attn, void *ws, cudaStream_t st
   if (!g.ok) return MOE_ERR_CUDA;
   int32_t got = 0;
   cudaError_t err = cudaMemcpyAsync(&got, static_cast<int *>(ws) + kAttnCtrlFlags, sizeof(got), cudaMemcpyDeviceToHost, stream);
-  if (err == cudaSuccess) err = cudaMemsetAsync(ws, 0, kAttnCtrlBytes, stream);
+  // the control words and the tickets: what a call has to find at zero
+  if (err == cudaSuccess) err = cudaMemsetAsync(ws, 0, attn_tree_ws(attn->cfg.head_dim, attn->num_sms).stat, stream);
   if (err == cudaSuccess) err = cudaStreamSynchronize(stream);
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   *flags = got;

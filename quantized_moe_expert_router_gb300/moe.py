@@ -409,9 +409,11 @@ def alloc_attn_workspace(attn: Attention, num_requests: int, num_rows: int, devi
 
 
 def moe_attn_get_device_status(attn: Attention, ws: torch.Tensor, stream=None) -> int:
-    f = ctypes.c_int32()
-    _check("moe_attn_get_device_status", load_library().moe_attn_get_device_status(
-        attn.handle, _ptr(ws), _stream(stream), ctypes.byref(f)))
+    fn, f = "moe_attn_get_device_status", ctypes.c_int32()
+    if ws.get_device() != attn.device or not ws.is_contiguous() or ws.nbytes < moe_attn_workspace_bytes(attn, 0, 0):
+        raise ValueError(f"{fn}: ws of {ws.nbytes} bytes on {ws.device} is not a workspace on cuda:{attn.device}")
+    _check(fn, load_library().moe_attn_get_device_status(
+        attn.handle, ws.data_ptr(), _stream(torch.cuda.current_stream(attn.device) if stream is None else stream), ctypes.byref(f)))
     return f.value
 
 

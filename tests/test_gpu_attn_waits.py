@@ -62,3 +62,24 @@ def test_tree_wait_that_runs_out(d, cached, fresh, cols):
         torch.cuda.synchronize()
         ref.check(out, None, c.want())
         assert moe.moe_attn_get_device_status(c.attn, ws) == 0
+
+
+@pytest.mark.parametrize("cached,fresh,cols", [([2000, 3], [1, 5], 2), ([300] * 24, [1] * 24, 2), ([1200, 60], [33, 20], 2100)])
+def test_status_leaves_the_workspace_as_new(cached, fresh, cols):
+    """Whatever a call that did not end left in it: every word that a call has to find at zero is zero."""
+    c = Cache(16, 8, 128, 16, torch.bfloat16, cached, fresh, seed=270, extra_cols=cols)
+    out, ws = torch.empty_like(c.q), moe.alloc_attn_workspace(c.attn, len(fresh), c.T)
+    ws.fill_(255)
+    moe.moe_attn_get_device_status(c.attn, ws)
+    moe.moe_attn_tree(c.attn, c.q, c.cu, c.cached, c.table, c.k, c.v, out, ws)
+    torch.cuda.synchronize()
+    ref.check(out, None, c.want())
+    assert moe.moe_attn_get_device_status(c.attn, ws) == 0
+
+
+def test_status_refuses_what_is_not_a_workspace():
+    attn = moe.Attention(4, 2, 64, 16, 8, 4)
+    ws = moe.alloc_attn_workspace(attn, 1, 1)
+    for bad in (ws[:1024], ws[:16], ws.cpu(), torch.zeros(1, dtype=torch.uint8, device=DEV).expand(ws.numel())):
+        with pytest.raises(ValueError, match="is not a workspace"):
+            moe.moe_attn_get_device_status(attn, bad)
