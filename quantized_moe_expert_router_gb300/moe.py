@@ -435,6 +435,13 @@ def _attn_refuse(fn, dev, *arrays):
             raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)} on {t.device} is not a contiguous {shape} on cuda:{dev}")
 
 
+def _attn_ws(fn, dev, ws):
+    if ws.get_device() != dev:
+        raise ValueError(f"{fn}: ws is on {ws.device}, not on cuda:{dev}")
+    if not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws with strides {ws.stride()} is not contiguous")
+
+
 def _attn_rows(fn, name, attn, t, shape):
     """The moe_attn_rows of [rows][heads][head_dim] with a contiguous last axis and any strides of the others."""
     s = t.stride()
@@ -511,11 +518,12 @@ def moe_attn_prompt(attn, q, k, v, cu, out, ws, lse=None, stream=None) -> None:
     fn, dev, T, n = "moe_attn_prompt", attn.device, q.shape[0], cu.numel()
     hq = attn.q_heads
     qs, ks = (T, hq, attn.head_dim), (T, attn.kv_heads, attn.head_dim)
-    if (cu.dtype is not torch.int32 or not cu.is_contiguous() or cu.get_device() != dev or ws.get_device() != dev
+    if (cu.dtype is not torch.int32 or not cu.is_contiguous() or cu.get_device() != dev
+            or ws.get_device() != dev or not ws.is_contiguous()
             or lse is not None and (lse.dtype is not torch.float32 or lse.numel() != T * hq or not lse.is_contiguous()
                                     or lse.get_device() != dev)):
         _attn_refuse(fn, dev, ("cu", cu, torch.int32, (n,)), ("lse", lse, torch.float32, (T, hq)))
-        raise ValueError(f"{fn}: ws is on {ws.device}, not on cuda:{dev}")
+        _attn_ws(fn, dev, ws)
     status = _lib.moe_attn_prompt(
         attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), _attn_rows(fn, "k", attn, k, ks),
         _attn_rows(fn, "v", attn, v, ks), cu.data_ptr(), _attn_rows(fn, "out", attn, out, qs),
@@ -533,7 +541,8 @@ def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, t
     fn, dev, i32, dt, T, n = "moe_attn_tree", attn.device, torch.int32, attn.dtype, q.shape[0], cu.numel()
     hq, cs = attn.q_heads, attn.cache_shape
     qs = (T, hq, attn.head_dim)
-    if (cu.dtype is not i32 or not cu.is_contiguous() or cu.get_device() != dev or ws.get_device() != dev
+    if (cu.dtype is not i32 or not cu.is_contiguous() or cu.get_device() != dev
+            or ws.get_device() != dev or not ws.is_contiguous()
             or cached.dtype is not i32 or cached.numel() != n - 1 or not cached.is_contiguous() or cached.get_device() != dev
             or block_table.dtype is not i32 or block_table.shape != (n - 1, attn.max_pages) or not block_table.is_contiguous()
             or block_table.get_device() != dev
@@ -544,8 +553,7 @@ def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, t
         _attn_refuse(fn, dev, ("cu", cu, i32, (n,)), ("cached", cached, i32, (n - 1,)),
                      ("block_table", block_table, i32, (n - 1, attn.max_pages)), ("tree_mask", tree_mask, torch.int64, (T,)),
                      ("lse", lse, torch.float32, (T, hq)))
-        if ws.get_device() != dev:
-            raise ValueError(f"{fn}: ws is on {ws.device}, not on cuda:{dev}")
+        _attn_ws(fn, dev, ws)
         raise ValueError(f"{fn}: block_table has shape {tuple(block_table.shape)}, not {(n - 1, attn.max_pages)}")
     if (k_cache.dtype is not dt or k_cache.shape != cs or not k_cache.is_contiguous() or k_cache.get_device() != dev
             or v_cache.dtype is not dt or v_cache.shape != cs or not v_cache.is_contiguous() or v_cache.get_device() != dev):
