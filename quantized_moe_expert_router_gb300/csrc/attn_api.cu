@@ -39,7 +39,7 @@ bool row_view(const moe_attn_rows *r, int rows, int heads, int head_dim, RowView
   if (!r || !given(r->data)) return false;
   v->p = static_cast<uint16_t *>(r->data);
   v->head = heads > 1 ? r->head_stride : head_dim;
-  v->row = rows > 1 ? r->row_stride : v->head * heads;
+  v->row = rows > 1 ? r->row_stride : head_dim;
   for (const long long s : {v->row, v->head})
     if (s <= 0 || s % 8 || s > (1LL << 36)) return false;
   return true;
