@@ -185,21 +185,27 @@ def measured_peaks():
 
 # every source file that goes into a kernel: the .cu and the headers it includes
 KERNEL_SOURCES = {
-    "expert_gemv.cu": ("csrc/expert_gemv.cu", "csrc/gemv_core.cuh", "csrc/moe_internal.cuh", "csrc/kernels.h",
-                       "../include/moe.h"),
-    "grouped.cu": ("csrc/grouped.cu", "csrc/gemv_core.cuh", "csrc/moe_internal.cuh", "csrc/kernels.h",
-                   "../include/moe.h"),
+    "expert_gemv.cu": ("expert_gemv.cu", "gemv_core.cuh", "quant_core.cuh", "moe_internal.cuh", "kernels.h"),
+    "grouped.cu": ("grouped.cu", "gemv_core.cuh", "quant_core.cuh", "moe_internal.cuh", "kernels.h"),
 }
 
 
-def kernel_sources_sha256(kernel_file):
+def kernel_sources_sha256(kernel_file, root=ROOT):
     """sha256 over the kernel's source files (the .cu and its headers, in a
-    fixed order): the key under which an ncu summary stays valid."""
+    fixed order) and over the constants of the public header that they name:
+    the key under which an ncu summary stays valid.  The rest of that header is
+    declarations, which no kernel sees."""
     import hashlib
-    h = hashlib.sha256()
+    h, text = hashlib.sha256(), ""
     for rel in KERNEL_SOURCES[kernel_file]:
-        with open(os.path.join(ROOT, "quantized_moe_expert_router_gb300", rel), "rb") as f:
-            h.update(f.read())
+        with open(os.path.join(root, "quantized_moe_expert_router_gb300", "csrc", rel)) as f:
+            text += f.read()
+    h.update(text.encode())
+    used = set(re.findall(r"\bMOE_\w+", text))
+    with open(os.path.join(root, "include", "moe.h")) as f:
+        for name, value in re.findall(r"^#define (MOE_\w+)[ \t]+([^\s/]+)", f.read(), flags=re.M):
+            if name in used:
+                h.update(f"{name}={value};".encode())
     return h.hexdigest()
 
 
