@@ -76,7 +76,9 @@ def ints(values):
     return torch.tensor(values, dtype=torch.int32, device=DEV)
 
 
-def main(steps=3):
+def main(steps=3, accepted=None):
+    """Runs the loop; returns the largest difference and the largest value.  A list `accepted` is given, by stream, the
+    accepted rows' (q, k, v, stepwise attention)."""
     streams = len(PROMPTS)
     rows_max = sum(PROMPTS)
     block = Block(rows_max)
@@ -131,6 +133,8 @@ def main(steps=3):
                     table[b, have:held] = -1
         fresh = [len(TREE)] * streams
         print(f"step {step}: {rows} rows, contexts {cached}, {int(used[1])} new pages, |y| {float(y.abs().mean()):.4f}")
+    if accepted is not None:
+        accepted += [tuple(torch.cat([r[i] for r in h]) for i in range(4)) for h in history]
     # the same rows by one call over the whole sequences
     q, k, v, got = (torch.cat([torch.cat([r[i] for r in h]) for h in history]) for i in range(4))
     lengths = [sum(r[0].shape[0] for r in h) for h in history]

@@ -79,3 +79,19 @@ def test_bad_values_stay_with_their_item(d):
         ref.check(o[keep], None, [w[keep] for w in want], f"repetition {r}")
         assert (o[2, :, 3] == float("inf")).all() and torch.isfinite(o[2, :, 4:]).all()
     assert moe.moe_attn_get_device_status(c.attn, ws) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cached,fresh,cols", [([0, 9], [4, 5], 2), ([0] * 20 + [50], [2] * 21, 2), ([0, 300], [40, 64], 2100),
+                                               ([0] * 30, [33] * 30, 600)])
+def test_rows_that_see_nothing(d, cached, fresh, cols):
+    """Outputs of 0 and a logarithm of minus infinity, in each kernel; the rows between them as they are."""
+    c = Cache(16, 8, d, 16, torch.bfloat16, cached, fresh, seed=280, extra_cols=cols)
+    words = random_words(fresh, 31)
+    words[::3] = 0
+    want = c.want(words)
+    out, lse = c.run(words)
+    ref.check(out, lse, want)
+    none = torch.isinf(want[1])
+    assert none.any() and (want[1][none] == -float("inf")).all()
+    assert (lse[none] == -float("inf")).all() and (out[none] == 0).all()
