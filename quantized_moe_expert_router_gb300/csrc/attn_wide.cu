@@ -136,7 +136,7 @@ struct ApSmem {
   uint64_t kv_full[4], kv_empty[4];
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[2][3], x_full[2], sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
-  int wsum[2][kApThreads / 32];
+  int wsum[kApThreads / 32];
   ApItem item[2];
   int v_pos[2][3];             // by item parity: stages of the masked value tiles, counted from the CTA's start
   float2 stat[2][kApTile];     // (m, l) of the twins of a prompt
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       items = __reduce_add_sync(kFull, items);
       if (lane == 31) {
         s.wsum2[warp] = incl;
-        s.wsum[0][warp] = items;
+        s.wsum[warp] = items;
       }
       __syncthreads();
       long long at = total;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       for (int w = 0; w < kApThreads / 32; w++) {
         at += w < warp ? s.wsum2[w] : 0;
         total += s.wsum2[w];
-        nitems += s.wsum[0][w];
+        nitems += s.wsum[w];
       }
       if (b < a.B) s.work[b] = at + incl - v;
       __syncthreads();
@@ -406,13 +406,13 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const int t = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += t;
       }
-      if (lane == 31) s.wsum[0][warp] = incl;
+      if (lane == 31) s.wsum[warp] = incl;
       __syncthreads();
       int at = items;
 #pragma unroll
       for (int w = 0; w < kApThreads / 32; w++) {
-        at += w < warp ? s.wsum[0][w] : 0;
-        items += s.wsum[0][w];
+        at += w < warp ? s.wsum[w] : 0;
+        items += s.wsum[w];
       }
       if (k < a.B) s.before[k] = at + incl;
       __syncthreads();
