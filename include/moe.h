@@ -349,7 +349,10 @@ moe_status moe_quantize_nvfp4(const void *src, int32_t src_dtype, int64_t rows, 
  * place p % page_size.  A slot is page * page_size + place.
  * Query head h reads kv head h / (q_heads / kv_heads).
  * Elements are bf16 or f16 (the same in rows, caches and outputs); products
- * are accumulated, and the softmax's maximum and sum kept, in fp32.
+ * are accumulated, and the softmax's maximum and sum kept, in fp32: a score past its
+ * range is infinite (a row whose scores are all -infinity counts as one that sees
+ * nothing), and |v| x 256 x context has to stay below 3e38, since the division
+ * by the sum comes last and weights of up to 256 are summed before it.
  * Nothing here synchronises or allocates: every call can be captured.
  * Rows, caches and the workspace are 16-byte aligned; int32, uint64 and fp32
  * arrays need their own alignment only. */
@@ -362,7 +365,7 @@ typedef struct moe_attn *moe_attn_t;
 #define MOE_ATTN_MAX_TREE 64           /* rows of a drafted tree: bits of a mask word */
 
 typedef struct {
-  int32_t q_heads;        /* a multiple of kv_heads; q_heads / kv_heads <= 128 */
+  int32_t q_heads;        /* a multiple of kv_heads, <= 1024; q_heads / kv_heads <= 128 */
   int32_t kv_heads;       /* >= 1 */
   int32_t head_dim;       /* 64 or 128 */
   int32_t page_size;      /* tokens of a page: 16, 32, 64 or 128 */
@@ -400,13 +403,15 @@ moe_status moe_attn_destroy(moe_attn_t attn);
 
 /* Workspace of moe_attn_prompt and moe_attn_tree for up to num_requests
  * requests and num_rows rows; device memory of the caller, ZERO-FILLED once
- * before its first use.  Concurrent calls need different workspaces. */
+ * before its first use.  It holds parts per SM, whatever the counts: the same for
+ * all of them.  Concurrent calls need different workspaces. */
 moe_status moe_attn_workspace_bytes(moe_attn_t attn, int num_requests, int num_rows, size_t *bytes);
 
 /* Synchronise `stream`, return the flag bits that moe_attn_prompt and
  * moe_attn_tree calls have left in `ws` since the last call (MOE_FLAG_TIMEOUT:
  * a bounded device wait ran out, the outputs of that call are invalid), and
- * leave the workspace as new.  No other call may be in flight on `ws`. */
+ * leave the workspace as new.  `ws` is a whole workspace of this handle; no other
+ * call may be in flight on it. */
 moe_status moe_attn_get_device_status(moe_attn_t attn, void *ws, cudaStream_t stream, int32_t *flags);
 
 /* Block tables and slot maps from the requests' lengths.
@@ -473,8 +478,8 @@ moe_status moe_attn_prompt(moe_attn_t attn, int num_requests, int num_rows, cons
  * does not see, tokens past the context, and tokens whose block-table entry is
  * not in [0, num_pages) have no effect on it, whatever the cache holds there.
  * cached[b] + the fresh rows may not pass max_pages * page_size (tokens past it
- * are not seen).  Results do not depend on timing: the parts of a long context
- * are joined in a fixed order. */
+ * are not seen).  out may not overlap q.  Results do not depend on timing: the parts
+ * of a long context are joined in a fixed order. */
 moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const moe_attn_rows *q, const int32_t *cu,
                          const int32_t *cached, const int32_t *block_table, const uint64_t *tree_mask,
                          const void *k_cache, const void *v_cache, const moe_attn_rows *out, float *lse, void *ws,

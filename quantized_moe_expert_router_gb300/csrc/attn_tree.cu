@@ -59,6 +59,11 @@ constexpr float kAtSlack = 8.f;
 //   32 rows, 1 request of 8000: 16.4, 21.5 (3.3);    256 rows, 1 of 500: 12.3, 16.2 (1.9)
 //   128 rows, 1 of 4000: 16.4, 18.1 (6.6);           192 rows: 18.6, 18.0 (10);     256 rows: 22.6, 18.0 (13)
 //   64 rows, 1 of 30000: 31.7, 28.9 (25);            128 rows: 53.3, 29.4 (49)
+// The rule knows the call's sizes only; the lengths are on the device.  A table that is
+// wider than the contexts counts as long contexts: 256 rows, 1 of 500, in a table of
+// 131072 tokens takes 16.8 there (11.7 here), 8 of them 23.0 (29.5).  A long part of a
+// prompt among single tokens goes by the mean: 256 tokens at 4000 among 255 of one at
+// 1000, 4 heads of 4, 111 (apart 24 + 87); 1024 at 0 among 63, 8 heads of 1, 91 (23 + 47).
 constexpr int kAtMostRows = 32, kAtMostChunks = 10;
 constexpr int kAtMinChunks = 8;                  // chunks of a CTA at least, one a warp: 1 row at 1000, us with 4, 8, 16: 8.8, 8.0, 9.0
 
