@@ -34,8 +34,8 @@
 // it and then zeroed.
 //
 // Bound: long contexts by HBM: 16 requests of a row at up to 100000 tokens, 8 kv
-// heads of 8, read 2.8 GB in 407 us, 6.9 TB/s (a plain copy has 6.8).  Short ones by
-// the latencies of one call: 1 row at 1000 takes 7.9 us for 4 MB (launch 1.5,
+// heads of 8, read 2.8 GB in 405 us, 7.0 TB/s (a plain copy has 6.8).  Short ones by
+// the latencies of one call: 1 row at 1000 takes 8.0 us for 4 MB (9.0 among other calls; launch 1.5,
 // lengths and shares 2, page numbers and keys 2, a warp's chunk 0.8, the two joins 1.5); 8
 // requests of 2 to 8 drafted rows at 500 to 4000 take 17 us for 58 MB, the longest
 // with two row tiles that each read the chunks.

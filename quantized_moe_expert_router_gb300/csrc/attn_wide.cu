@@ -72,13 +72,15 @@
 // Bound, D = 128: the tensor pipe.  S and PV of a row tile and key tile take it 1025
 // cycles when nothing else runs; beside the copies that write the same shared memory
 // some 1250, and 100 to 150 pass until the next product's P is seen.  16384 tokens (2
-// kv heads of 8): 632 us, 1740 TFLOP/s, where a library product has 1900; 4 x 4096 (4
-// of 8): 347 us, 1580; 512 (8 of 4): 11.5 us, a chain of launch (2 us), items and first
+// kv heads of 8): 630 us, 1745 TFLOP/s, where a library product has 1900; 4 x 4096 (4
+// of 8): 350 us, 1570; 512 (8 of 4): 11.9 us, a chain of launch (2 us), items and first
 // copies (3), two key tiles a twin (5) and the store.  D = 64: one product behind the other; the pipe takes 525 cycles, the
 // exponentials 512 and the way from P to the next S the rest of 1140: 8192 tokens (4
-// of 8) 262 us, 1050 TFLOP/s; 17 prompts of 62 to 1501 (8 of 3) 44 us.  A third S
+// of 8) 259 us, 1060 TFLOP/s; 17 prompts of 62 to 1501 (8 of 3) 44 us.  A third S
 // buffer with S three products ahead measured the same (267, 48).  Over the cache,
-// 4 requests of 16 to 64 rows at 1125 to 9000 (4 of 8): 27 us, the join's 6 among them.
+// 4 requests of 16 to 64 rows at 1125 to 9000 (4 of 8): 27 us: launch 2, lengths, shares and
+// first copies 5.4, 6 key tiles a CTA 8.4 (2870 cycles for the 2050 of two row tiles, while
+// the CTAs copy 64 KB each: 7.2 TB/s from L2), the part's store 2.5, the join 6.
 #include <math.h>
 #include <string.h>
 

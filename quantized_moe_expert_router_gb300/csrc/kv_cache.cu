@@ -38,7 +38,7 @@ __device__ __forceinline__ int last_at_most(const int *first, int n, int x) {
 // is a chain of three dependent loads (lengths; a page id; the store), so
 // launch latency bounds it; tree parents are staged in shared memory because
 // walking them in global memory would add one load latency per tree level.
-// 7 requests of drafted trees: 3.3 us; 48 prompts (31190 rows): 2.9 us.
+// 7 requests of drafted trees: 3.4 us; 48 prompts (31190 rows): 3.1 us.
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanArgs a) {
   __shared__ KvPlanSmem s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
