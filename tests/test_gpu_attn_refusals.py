@@ -39,3 +39,5 @@ def test_one_row_with_heads_far_apart():
     moe.moe_attn_tree(attn, q, cu, cached, table, kc, vc, out, moe.alloc_attn_workspace(attn, 1, 1),
                       tree_mask=torch.zeros(1, dtype=torch.int64, device=DEV))
     assert torch.isfinite(out).all()
+    del x, views, q, k, v, t
+    torch.cuda.empty_cache()                                       # 64 GB
