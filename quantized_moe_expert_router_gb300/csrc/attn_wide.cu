@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
               const int blocks = halves ? D / 64 : D / 32, cb = (halves ? D / 64 * h : 0) + cz;
               if (cz >= blocks) break;
               float o[32];
+              __syncwarp();                        // behind stores that some lanes leave out: the loads are the whole warp's
               at_ld_frag(to + ((uint32_t)(16 * rb) << 16) + 32u * cb, o);
               if (cz + 1 < blocks) at_ld_frag(to + ((uint32_t)(16 * rb) << 16) + 32u * (cb + 1), o + 16);
               at_wait_ld(o);
