@@ -485,6 +485,124 @@ moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const 
                          const void *k_cache, const void *v_cache, const moe_attn_rows *out, float *lse, void *ws,
                          size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Rotary positions.  The first `dims` elements of every head are dims / 2 pairs;
+ * pair i, (x, y), of a row at position p becomes
+ *   attn_factor * (x cos a - y sin a, x sin a + y cos a),  a = p * f_i
+ * and the head's other elements stay as they are.  A pair is
+ *   MOE_ROPE_HALF         elements i and i + dims / 2
+ *   MOE_ROPE_INTERLEAVED  elements 2 i and 2 i + 1
+ * The frequencies, w_i = theta^(-2 i / dims), are scaled for contexts longer than the
+ * model was trained on:
+ *   MOE_ROPE_PLAIN   f = w
+ *   MOE_ROPE_LINEAR  f = w / factor
+ *   MOE_ROPE_BASE    theta is multiplied by factor^(dims / (dims - 2))
+ *   MOE_ROPE_YARN    f = r w / factor + (1 - r) w, with r rising linearly from 0 at pair
+ *                    floor(d(high)) (0 at least) to 1 at pair ceil(d(low)) (dims - 1 at most);
+ *                    d(t) = dims / 2 * ln(original / (2 pi t)) / ln(theta) is the pair that makes t turns
+ *                    over the original context.  attn_factor is given apart.
+ *   MOE_ROPE_BANDS   f = s w + (1 - s) w / factor, s = clamp((original w / (2 pi) - low) / (high - low), 0, 1)
+ * Angles are exact at any int32 position (frequencies have 53 bits); sines and
+ * cosines are off by 2^-20 at most, products are fp32, results are rounded once.
+ * Rows whose position is negative (moe_kv_plan gives -1 to rows of no request) are
+ * left out: nothing is written for them. */
+typedef struct moe_rope *moe_rope_t;
+
+#define MOE_ROPE_HALF 0
+#define MOE_ROPE_INTERLEAVED 1
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_BASE 2
+#define MOE_ROPE_YARN 3
+#define MOE_ROPE_BANDS 4
+#define MOE_ROPE_MAX_HEADS 1024
+#define MOE_ROPE_MAX_HEAD_DIM 1024
+
+typedef struct {
+  int32_t dims;           /* elements of a head that turn: a multiple of 16, 16 .. 256 */
+  int32_t layout;         /* MOE_ROPE_HALF or MOE_ROPE_INTERLEAVED */
+  int32_t scaling;        /* MOE_ROPE_PLAIN .. MOE_ROPE_BANDS */
+  int32_t dtype;          /* MOE_ATTN_BF16 or MOE_ATTN_F16 */
+  double theta;           /* finite, > 1 */
+  double factor;          /* finite, >= 1; not looked at with MOE_ROPE_PLAIN */
+  double low, high;       /* MOE_ROPE_YARN (turns over the original context), MOE_ROPE_BANDS: 0 < low < high */
+  int32_t original;       /* tokens of the original context (YARN, BANDS): >= 1 */
+  float attn_factor;      /* multiplies the turned elements: finite, > 0; 1 as a rule */
+  uint32_t flags;         /* 0 */
+} moe_rope_config;
+
+/* A host-side handle (allocates no device memory, asks no device). */
+moe_status moe_rope_create(const moe_rope_config *cfg, int device, moe_rope_t *out);
+moe_status moe_rope_destroy(moe_rope_t rope);
+/* freq: host, [dims / 2] doubles, written: f_i. */
+moe_status moe_rope_frequencies(moe_rope_t rope, double *freq);
+
+/* Turn rows of q and of k (one launch) by positions (device int32 [num_rows]).
+ *   q, q_out   [num_rows][q_heads][head_dim]; k, k_out [num_rows][k_heads][head_dim]
+ * An output is its input itself (same data and strides) or does not overlap the inputs.
+ * head_dim is a multiple of 16, dims .. 1024; heads 0 .. 1024 (0: that array is not
+ * looked at).  To turn another part of the heads than the first, pass a view of it. */
+moe_status moe_rope_apply(moe_rope_t rope, int num_rows, int head_dim, const int32_t *positions, int q_heads,
+                          const moe_attn_rows *q, const moe_attn_rows *q_out, int k_heads, const moe_attn_rows *k,
+                          const moe_attn_rows *k_out, cudaStream_t stream);
+
+/* moe_rope_apply and moe_kv_append in one launch: q turned into q_out, k turned and v
+ * into their slots of the caches (rows whose slot is out of range: q only; rows whose
+ * position is negative: nothing).  rope has the cache's dtype and dims <= head_dim. */
+moe_status moe_rope_append(moe_attn_t attn, moe_rope_t rope, int num_rows, const int32_t *positions, const int32_t *slots,
+                           const moe_attn_rows *q, const moe_attn_rows *q_out, const moe_attn_rows *k,
+                           const moe_attn_rows *v, void *k_cache, void *v_cache, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Latent attention: layers that keep one vector a token, a latent c of 512 elements
+ * and a key part r of 64 that is turned by the position, for all heads.  A head's
+ * key is [K_h c | r] (128 + 64 elements) and its value V_h c (128):
+ *   expanded  moe_latent_prompt: the caller has made K_h c and V_h c of every row (one
+ *             product); causal attention over packed prompts
+ *   absorbed  moe_latent_tree: the caller has multiplied q_h by K_h, and multiplies the
+ *             output by V_h; the rows' keys are the cached vectors themselves and
+ *             their values the latents, so the cache is read once for all heads
+ * A serving step is moe_latent_plan, moe_latent_append, then one of them.
+ * Requests, packed rows, pages, slots, tree masks, element types, alignment, capture
+ * and workspaces are as above; the cache is [num_pages][page_size][576], the latent
+ * first. */
+typedef struct moe_latent *moe_latent_t;
+
+#define MOE_LATENT_MAX_HEADS 128
+
+typedef struct {
+  int32_t heads;          /* 1 .. 128 */
+  int32_t latent_dim;     /* 512 */
+  int32_t rope_dim;       /* 64 */
+  int32_t head_dim;       /* 128: of a head's own key part and of its value */
+  int32_t page_size;      /* tokens of a page: 16, 32, 64 or 128 */
+  int32_t num_pages;      /* pages of the cache: num_pages * page_size < 2^31 */
+  int32_t max_pages;      /* entries of a block-table row (its stride) */
+  int32_t dtype;          /* MOE_ATTN_BF16 or MOE_ATTN_F16 */
+  float softmax_scale;    /* multiplies q . k (finite, > 0); 1 / sqrt(192) as a rule */
+  uint32_t flags;         /* MOE_ATTN_TEST_STALL, or 0 */
+} moe_latent_config;
+
+/* A host-side handle (allocates no device memory). */
+moe_status moe_latent_create(const moe_latent_config *cfg, int device, moe_latent_t *out);
+moe_status moe_latent_destroy(moe_latent_t lat);
+
+/* moe_kv_plan for this cache. */
+moe_status moe_latent_plan(moe_latent_t lat, int num_requests, int num_rows, const int32_t *cached, const int32_t *fresh,
+                           const int32_t *free_pages, int num_free, const int32_t *parents, int32_t *block_table,
+                           int32_t *cu, int32_t *slots, int32_t *positions, uint64_t *tree_mask, int32_t *info,
+                           cudaStream_t stream);
+
+/* Write latent rows into the cache and turn the rotary part of q beside it (one launch):
+ * for every row t with a position >= 0 and a slot in range, c[t] (512) and the turned
+ * k_rope[t] (64; the first `dims` turn) go to slot slots[t].  q, q_out: [num_rows][heads][64] or both
+ * NULL, turned for every row with a position >= 0; q_out is q itself or does not
+ * overlap the inputs.  The head stride of c and k_rope is not looked at.  Slots must
+ * be distinct.  rope has the cache's dtype and dims <= 64. */
+moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, const int32_t *positions, const int32_t *slots,
+                             const moe_attn_rows *c, const moe_attn_rows *k_rope, const moe_attn_rows *q,
+                             const moe_attn_rows *q_out, void *cache, cudaStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *moe_status_string(moe_status status);
 

@@ -6,46 +6,11 @@
 
 #include <new>
 
-#include "attn.h"
+#include "attn_host.h"
 
 using namespace moe;
 
 namespace {
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-bool given(const void *p) { return p && aligned16(p); }
-// Arrays of words: their own alignment (a free list is advanced by a few pages).
-bool words(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
-bool aligned8(const void *p) { return ((uintptr_t)p & 7u) == 0; }
-bool lse_ok(const float *p) { return ((uintptr_t)p & 3u) == 0; }
-
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
-  }
-  ~DeviceGuard() {
-    if (ok && prev >= 0) cudaSetDevice(prev);
-  }
-};
-
-// Checks a row view and fills in the strides of axes of length one.
-bool row_view(const moe_attn_rows *r, int rows, int heads, int head_dim, RowView *v) {
-  if (!r || !given(r->data)) return false;
-  v->p = static_cast<uint16_t *>(r->data);
-  v->head = heads > 1 ? r->head_stride : head_dim;
-  v->row = rows > 1 ? r->row_stride : head_dim;
-  for (const long long s : {v->row, v->head})
-    if (s <= 0 || s % 8 || s > (1LL << 36)) return false;
-  return true;
-}
-
-bool counts_ok(int num_requests, int num_rows) { return num_requests >= 0 && num_rows >= 0; }
 
 AttnArgs attn_args(const moe_attn &L, int B, int T) {
   AttnArgs a;
@@ -81,9 +46,7 @@ moe_status moe_attn_create(const moe_attn_config *cfg, int device, moe_attn_t *o
       cfg->q_heads / cfg->kv_heads > 128 || cfg->q_heads > 1024)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (cfg->head_dim != 64 && cfg->head_dim != 128) return MOE_ERR_UNSUPPORTED_SHAPE;
-  int shift = -1;
-  for (int s = 4; s <= 7; s++)
-    if (cfg->page_size == 1 << s) shift = s;
+  const int shift = page_shift_of(cfg->page_size);
   if (shift < 0 || cfg->num_pages < 1 || cfg->max_pages < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (((long long)cfg->num_pages << shift) >= (1LL << 31) || ((long long)cfg->max_pages << shift) > (1LL << 30))
     return MOE_ERR_UNSUPPORTED_SHAPE;

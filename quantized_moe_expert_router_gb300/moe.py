@@ -39,6 +39,9 @@ KV_FLAG_LENGTH = 0x1                    # moe_kv_plan's info[3]: a negative leng
 KV_FLAG_TABLE = 0x2                     # a context longer than a block-table row
 KV_FLAG_PAGES = 0x4                     # free pages ran out, or a page id is out of range
 KV_FLAG_TREE = 0x8                      # a bad parent, or a tree of more than 64 rows
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1      # pairs (i, i + dims / 2) or (2 i, 2 i + 1)
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_YARN, ROPE_BANDS = range(5)   # scaling of the frequencies
+LATENT_DIM, LATENT_ROPE, LATENT_HEAD = 512, 64, 128   # a cached token's latent and key part; a head's own key part, and value
 
 EXPORTED = (
     "moe_layer_create", "moe_layer_destroy", "moe_packed_bytes", "moe_workspace_bytes",
@@ -48,6 +51,8 @@ EXPORTED = (
     "moe_ffn_pack_weights", "moe_ffn_partial", "moe_ffn_finish", "moe_ffn_forward", "moe_quantize_nvfp4",
     "moe_attn_create", "moe_attn_destroy", "moe_attn_workspace_bytes", "moe_kv_plan", "moe_kv_append",
     "moe_attn_prompt", "moe_attn_tree", "moe_attn_get_device_status",
+    "moe_rope_create", "moe_rope_destroy", "moe_rope_frequencies", "moe_rope_apply", "moe_rope_append",
+    "moe_latent_create", "moe_latent_destroy", "moe_latent_plan", "moe_latent_append",
     "moe_status_string",
 )
 
@@ -85,6 +90,18 @@ class moe_ffn_weights(ctypes.Structure):
 
 class moe_attn_config(ctypes.Structure):
     _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class moe_rope_config(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("original", ctypes.c_int32), ("attn_factor", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class moe_latent_config(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
@@ -132,6 +149,15 @@ def load_library(path: str = LIB_PATH):
             lib.moe_attn_prompt.argtypes = [P, I32, I32, R, R, R, P, R, P, P, SZ, P]
             lib.moe_attn_tree.argtypes = [P, I32, I32, R, P, P, P, P, P, P, R, P, P, SZ, P]
             lib.moe_attn_get_device_status.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_int32)]
+            lib.moe_rope_create.argtypes = [ctypes.POINTER(moe_rope_config), I32, ctypes.POINTER(P)]
+            lib.moe_rope_destroy.argtypes = [P]
+            lib.moe_rope_frequencies.argtypes = [P, P]
+            lib.moe_rope_apply.argtypes = [P, I32, I32, P, I32, R, R, I32, R, R, P]
+            lib.moe_rope_append.argtypes = [P, P, I32, P, P, R, R, R, R, P, P, P]
+            lib.moe_latent_create.argtypes = [ctypes.POINTER(moe_latent_config), I32, ctypes.POINTER(P)]
+            lib.moe_latent_destroy.argtypes = [P]
+            lib.moe_latent_plan.argtypes = lib.moe_kv_plan.argtypes
+            lib.moe_latent_append.argtypes = [P, P, I32, P, P, R, R, R, R, P, P]
             lib.moe_status_string.argtypes = [I32]
             lib.moe_status_string.restype = ctypes.c_char_p
             for name in EXPORTED[:-1]:
@@ -462,10 +488,7 @@ def _attn_caches(fn, attn, k_cache, v_cache):
             raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)} on {t.device} is not a contiguous {shape} on cuda:{dev}")
 
 
-def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
-                stream=None) -> None:
-    """Block table entries, row offsets, slots, positions and (from parents)
-    tree masks of one step; int32 tensors, tree_mask int64."""
+def _plan(fn, call, attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents, tree_mask, stream) -> None:
     dev, i32, B, T, F = attn.device, torch.int32, cached.numel(), slots.numel(), free_pages.numel()
     if (cached.dtype is not i32 or not cached.is_contiguous() or cached.get_device() != dev
             or fresh.dtype is not i32 or fresh.numel() != B or not fresh.is_contiguous() or fresh.get_device() != dev
@@ -480,18 +503,25 @@ def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positio
                                         or parents.get_device() != dev)
             or tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.numel() != T
                                           or not tree_mask.is_contiguous() or tree_mask.get_device() != dev)):
-        _attn_refuse("moe_kv_plan", dev, ("cached", cached, i32, (B,)), ("fresh", fresh, i32, (B,)), ("free_pages", free_pages, i32, (F,)),
+        _attn_refuse(fn, dev, ("cached", cached, i32, (B,)), ("fresh", fresh, i32, (B,)), ("free_pages", free_pages, i32, (F,)),
                      ("block_table", block_table, i32, (B, attn.max_pages)), ("cu", cu, i32, (B + 1,)), ("slots", slots, i32, (T,)),
                      ("positions", positions, i32, (T,)), ("info", info, i32, (4,)), ("parents", parents, i32, (T,)),
                      ("tree_mask", tree_mask, torch.int64, (T,)))
-        raise ValueError(f"moe_kv_plan: block_table has shape {tuple(block_table.shape)}, not {(B, attn.max_pages)}")
-    status = _lib.moe_kv_plan(
+        raise ValueError(f"{fn}: block_table has shape {tuple(block_table.shape)}, not {(B, attn.max_pages)}")
+    status = call(
         attn.handle, B, T, cached.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(), F,
         None if parents is None else parents.data_ptr(), block_table.data_ptr(), cu.data_ptr(), slots.data_ptr(),
         positions.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(), info.data_ptr(),
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
-        _check("moe_kv_plan", status)
+        _check(fn, status)
+
+
+def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
+                stream=None) -> None:
+    """Block table entries, row offsets, slots, positions and (from parents)
+    tree masks of one step; int32 tensors, tree_mask int64."""
+    _plan("moe_kv_plan", _lib.moe_kv_plan, attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents, tree_mask, stream)
 
 
 def moe_kv_append(attn, k, v, slots, k_cache, v_cache, stream=None) -> None:
@@ -562,6 +592,170 @@ def moe_attn_tree(attn, q, cu, cached, block_table, k_cache, v_cache, out, ws, t
         attn.handle, n - 1, T, _attn_rows(fn, "q", attn, q, qs), cu.data_ptr(), cached.data_ptr(), block_table.data_ptr(),
         None if tree_mask is None else tree_mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         _attn_rows(fn, "out", attn, out, qs), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(fn, status)
+
+
+# ------------------------------------------------ rotary positions
+
+class Rope:
+    """Owns one ``moe_rope_t`` handle (host memory only): which elements of a
+    head turn, in which pairs, and the frequencies.  ``scaling`` is one of
+    ROPE_*; ``factor``, ``original`` (tokens of the original context), ``low`` and
+    ``high`` are its parameters, ``attn_factor`` multiplies the turned elements."""
+
+    def __init__(self, dims, theta=10000.0, layout=ROPE_HALF, scaling=ROPE_PLAIN, factor=1.0, original=0, low=1.0, high=32.0,
+                 attn_factor=1.0, dtype=torch.bfloat16, device=0):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"Rope: unsupported dtype {dtype}")
+        lib = load_library()
+        self.cfg = moe_rope_config(dims, layout, scaling, ATTN_F16 if dtype == torch.float16 else ATTN_BF16, theta, factor, low, high,
+                                   original, attn_factor, 0)
+        self.dims, self.dtype, self.device = dims, dtype, device
+        h = ctypes.c_void_p()
+        _check("moe_rope_create", lib.moe_rope_create(ctypes.byref(self.cfg), device, ctypes.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and _lib is not None:
+            _lib.moe_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        self.close()
+
+
+def moe_rope_frequencies(rope: Rope) -> list:
+    """Radians a position, of each pair."""
+    f = (ctypes.c_double * (rope.dims // 2))()
+    _check("moe_rope_frequencies", load_library().moe_rope_frequencies(rope.handle, f))
+    return list(f)
+
+
+def moe_rope_apply(rope, positions, q, q_out, k=None, k_out=None, stream=None) -> None:
+    """Turn q and k [rows][heads][head_dim] by positions (int32 [rows]) into q_out
+    and k_out, each its input itself or an array apart.  Rows at negative
+    positions are left out."""
+    fn, dev, T, d = "moe_rope_apply", rope.device, positions.numel(), q.shape[-1]
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev:
+        _attn_refuse(fn, dev, ("positions", positions, torch.int32, (T,)))
+    if (k is None) != (k_out is None):
+        raise ValueError(f"{fn}: k and k_out go together")
+    qs, hk = (T, q.shape[1], d), 0
+    kv = ko = None
+    if k is not None:
+        hk = k.shape[1]
+        kv, ko = _attn_rows(fn, "k", rope, k, (T, hk, d)), _attn_rows(fn, "k_out", rope, k_out, (T, hk, d))
+    status = _lib.moe_rope_apply(
+        rope.handle, T, d, positions.data_ptr(), qs[1], _attn_rows(fn, "q", rope, q, qs), _attn_rows(fn, "q_out", rope, q_out, qs),
+        hk, kv, ko, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(fn, status)
+
+
+def _same(fn, a, b):
+    """The handles of one call: one device, one element type."""
+    if a.device != b.device:
+        raise ValueError(f"{fn}: handles on cuda:{a.device} and cuda:{b.device}")
+    if a.dtype is not b.dtype:
+        raise TypeError(f"{fn}: handles of {a.dtype} and {b.dtype}")
+
+
+def moe_rope_append(attn, rope, q, k, v, positions, slots, q_out, k_cache, v_cache, stream=None) -> None:
+    """moe_rope_apply of q into q_out and of k, with v, into their slots of the
+    caches, in one launch."""
+    fn, dev, dt, T = "moe_rope_append", attn.device, attn.dtype, positions.numel()
+    _same(fn, attn, rope)
+    qs, ks, cs = (T, attn.q_heads, attn.head_dim), (T, attn.kv_heads, attn.head_dim), attn.cache_shape
+    if (positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev
+            or slots.dtype is not torch.int32 or slots.numel() != T or not slots.is_contiguous() or slots.get_device() != dev):
+        _attn_refuse(fn, dev, ("positions", positions, torch.int32, (T,)), ("slots", slots, torch.int32, (T,)))
+    if (k_cache.dtype is not dt or k_cache.shape != cs or not k_cache.is_contiguous() or k_cache.get_device() != dev
+            or v_cache.dtype is not dt or v_cache.shape != cs or not v_cache.is_contiguous() or v_cache.get_device() != dev):
+        _attn_caches(fn, attn, k_cache, v_cache)
+    status = _lib.moe_rope_append(
+        attn.handle, rope.handle, T, positions.data_ptr(), slots.data_ptr(), _attn_rows(fn, "q", attn, q, qs),
+        _attn_rows(fn, "q_out", attn, q_out, qs), _attn_rows(fn, "k", attn, k, ks), _attn_rows(fn, "v", attn, v, ks),
+        k_cache.data_ptr(), v_cache.data_ptr(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(fn, status)
+
+
+# ------------------------------------------------ latent attention
+
+class LatentAttention:
+    """Owns one ``moe_latent_t`` handle (host memory only): the heads and the
+    geometry of the paged latent cache, [num_pages][page_size][576].
+    ``softmax_scale`` is 1 / sqrt(192) unless given."""
+
+    def __init__(self, heads, page_size, num_pages, max_pages, dtype=torch.bfloat16, softmax_scale=None, device=0, flags=0):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"LatentAttention: unsupported dtype {dtype}")
+        lib = load_library()
+        scale = (LATENT_HEAD + LATENT_ROPE) ** -0.5 if softmax_scale is None else softmax_scale
+        self.cfg = moe_latent_config(heads, LATENT_DIM, LATENT_ROPE, LATENT_HEAD, page_size, num_pages, max_pages,
+                                     ATTN_F16 if dtype == torch.float16 else ATTN_BF16, scale, flags)
+        self.dtype, self.device = dtype, device
+        self.heads, self.max_pages = heads, max_pages
+        self.cache_shape = (num_pages, page_size, LATENT_DIM + LATENT_ROPE)
+        h = ctypes.c_void_p()
+        _check("moe_latent_create", lib.moe_latent_create(ctypes.byref(self.cfg), device, ctypes.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and _lib is not None:
+            _lib.moe_latent_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        self.close()
+
+
+def moe_latent_plan(lat, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
+                    stream=None) -> None:
+    """moe_kv_plan for the latent cache."""
+    _plan("moe_latent_plan", _lib.moe_latent_plan, lat, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents,
+          tree_mask, stream)
+
+
+def _latent_row(fn, name, lat, t, shape):
+    """The moe_attn_rows of [rows][n] with a contiguous last axis and any stride of the rows."""
+    s = t.stride()
+    if t.dtype is lat.dtype and t.shape == shape and s[1] == 1 and t.get_device() == lat.device:
+        return _pack_rows(t.data_ptr(), s[0], 0)
+    if t.dtype is not lat.dtype:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, not {lat.dtype}")
+    raise ValueError(f"{fn}: {name} of shape {tuple(t.shape)}, strides {s}, on {t.device} is not {shape} with a contiguous "
+                     f"last axis on cuda:{lat.device}")
+
+
+def _latent_cache(fn, lat, cache):
+    if cache.dtype is not lat.dtype:
+        raise TypeError(f"{fn}: cache is {cache.dtype}, not {lat.dtype}")
+    if cache.shape != lat.cache_shape or not cache.is_contiguous() or cache.get_device() != lat.device:
+        raise ValueError(f"{fn}: cache of shape {tuple(cache.shape)} on {cache.device} is not a contiguous {lat.cache_shape} on "
+                         f"cuda:{lat.device}")
+
+
+def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_out=None, stream=None) -> None:
+    """Latents c [rows][512] and turned key parts k_rope [rows][64] into their slots
+    of the cache; q [rows][heads][64] (the queries' rotary part) turned into q_out."""
+    fn, dev, T = "moe_latent_append", lat.device, positions.numel()
+    _same(fn, lat, rope)
+    if (positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev
+            or slots.dtype is not torch.int32 or slots.numel() != T or not slots.is_contiguous() or slots.get_device() != dev):
+        _attn_refuse(fn, dev, ("positions", positions, torch.int32, (T,)), ("slots", slots, torch.int32, (T,)))
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{fn}: q and q_out go together")
+    qv = qo = None
+    if q is not None:
+        qs = (T, lat.heads, LATENT_ROPE)
+        qv, qo = _attn_rows(fn, "q", lat, q, qs), _attn_rows(fn, "q_out", lat, q_out, qs)
+    _latent_cache(fn, lat, cache)
+    status = _lib.moe_latent_append(
+        lat.handle, rope.handle, T, positions.data_ptr(), slots.data_ptr(), _latent_row(fn, "c", lat, c, (T, LATENT_DIM)),
+        _latent_row(fn, "k_rope", lat, k_rope, (T, LATENT_ROPE)), qv, qo, cache.data_ptr(),
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)
