@@ -587,6 +587,13 @@ typedef struct {
 moe_status moe_latent_create(const moe_latent_config *cfg, int device, moe_latent_t *out);
 moe_status moe_latent_destroy(moe_latent_t lat);
 
+/* Workspace of the attention calls below, as moe_attn_workspace_bytes: device memory of
+ * the caller, ZERO-FILLED once, one for each call in flight. */
+moe_status moe_latent_workspace_bytes(moe_latent_t lat, int num_requests, int num_rows, size_t *bytes);
+
+/* As moe_attn_get_device_status. */
+moe_status moe_latent_get_device_status(moe_latent_t lat, void *ws, cudaStream_t stream, int32_t *flags);
+
 /* moe_kv_plan for this cache. */
 moe_status moe_latent_plan(moe_latent_t lat, int num_requests, int num_rows, const int32_t *cached, const int32_t *fresh,
                            const int32_t *free_pages, int num_free, const int32_t *parents, int32_t *block_table,
@@ -602,6 +609,23 @@ moe_status moe_latent_plan(moe_latent_t lat, int num_requests, int num_rows, con
 moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, const int32_t *positions, const int32_t *slots,
                              const moe_attn_rows *c, const moe_attn_rows *k_rope, const moe_attn_rows *q,
                              const moe_attn_rows *q_out, void *cache, cudaStream_t stream);
+
+/* Absorbed form, over the cache: for row i of request b and head h
+ *   o[i] = sum_j w_j c_j,  w = softmax_j(softmax_scale * (q[i] . c_j + q_rope[i] . r_j))
+ * over the tokens that moe_attn_tree's row would see (all cached ones, and the fresh
+ * ones that its word of tree_mask, or causality, lets it see).
+ *   q       [num_rows][heads][512]: the head's query times its K_h
+ *   q_rope  [num_rows][heads][64]: turned, as moe_latent_append leaves it
+ *   cache   [num_pages][page_size][576], device
+ *   out     [num_rows][heads][512] (may not overlap the inputs); lse as there
+ * A row that sees nothing gets out = 0 and lse = -infinity; tokens that a row does not
+ * see, tokens past the context and tokens without a valid page have no effect on it,
+ * whatever the cache holds there.  An infinite or NaN element of a latent that a row does
+ * see makes that element of its output NaN.  Results do not depend on timing. */
+moe_status moe_latent_tree(moe_latent_t lat, int num_requests, int num_rows, const moe_attn_rows *q,
+                           const moe_attn_rows *q_rope, const int32_t *cu, const int32_t *cached, const int32_t *block_table,
+                           const uint64_t *tree_mask, const void *cache, const moe_attn_rows *out, float *lse, void *ws,
+                           size_t ws_bytes, cudaStream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *moe_status_string(moe_status status);

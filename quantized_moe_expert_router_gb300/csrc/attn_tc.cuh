@@ -213,6 +213,7 @@ struct AtShare {
   int ctas;
   int c0, c1;                  // parts (len > 0): the CTAs of the item's first and last part
   int len;
+  int me;                      // this CTA
   __device__ __forceinline__ long long start(long long i) const { return i * per + min(i, rem); }
   __device__ __forceinline__ int cta_of(long long x) const {
     const long long big = rem * (per + 1);
@@ -224,19 +225,21 @@ struct AtShare {
       a = c0;
       b = c1;
     } else {
-      a = item0 >= x0 ? (int)blockIdx.x : cta_of(item0);
-      b = last < x1 ? (int)blockIdx.x : cta_of(last);
+      a = item0 >= x0 ? me : cta_of(item0);
+      b = last < x1 ? me : cta_of(last);
     }
   }
   // where CTA a, which holds the item's first unit, keeps its part: a CTA's first part is in its slot 0
   __device__ __forceinline__ int first_slot(int a, long long item0) const { return 2 * a + (!len && start(a) < item0); }
 };
-// All threads of the CTA (NW warps) call this; `scratch` is NW x 32 ints.
+// All threads of the CTA (NW warps) call this; `scratch` is NW x 32 ints.  `grid` and `me`: the CTAs, or groups of
+// them, that share the line, and which of them this is; `above`: parts may be 31 units longer than the mean, or fewer.
 template <int NW, typename Items, typename Nch>
 __device__ __forceinline__ AtShare at_share(const long long *work, int B, long long total, int nitems, int min_len,
-                                            int (*scratch)[32], Items items, Nch nch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grid = gridDim.x, me = blockIdx.x;
+                                            int (*scratch)[32], Items items, Nch nch, int grid, int me, long long above = 31) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   AtShare r;
+  r.me = me;
   r.x0 = r.x1 = 0;
   r.c0 = r.c1 = r.len = 0;
   r.ctas = (int)min((total + min_len - 1) / min_len, (long long)grid);
@@ -252,7 +255,7 @@ __device__ __forceinline__ AtShare at_share(const long long *work, int B, long l
     parts = 0;
 #pragma unroll
     for (int w = 0; w < NW; w++) parts += scratch[w][lane];
-    const unsigned fits = __ballot_sync(kFull, parts <= grid);
+    const unsigned fits = __ballot_sync(kFull, parts <= grid && lane <= above);
     if (fits) {
       r.len = len0 + __ffs(fits) - 1;
       int before = 0;

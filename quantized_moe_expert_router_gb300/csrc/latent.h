@@ -33,5 +33,8 @@ struct LatArgs {
 struct LatWs {
   size_t desc, stat, part, total;
 };
+LatWs lat_ws(int num_sms);
+cudaError_t lat_tree_setup(int f16);     // opt-in shared memory (idempotent)
+cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

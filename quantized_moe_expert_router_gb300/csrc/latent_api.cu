@@ -56,6 +56,23 @@ RopeSeg seg_cache(const RowView &src, uint16_t *cache, long long row, long long 
   return s;
 }
 
+LatArgs lat_args(const moe_latent &L, int B, int T) {
+  LatArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = B;
+  a.T = T;
+  a.heads = L.cfg.heads;
+  a.page_shift = L.page_shift;
+  a.max_pages = L.cfg.max_pages;
+  a.num_pages = L.cfg.num_pages;
+  a.f16 = L.cfg.dtype == MOE_ATTN_F16;
+  a.scale = L.cfg.softmax_scale;
+  const bool stall = L.cfg.flags & MOE_ATTN_TEST_STALL;
+  a.stall = stall ? 16 : 0;
+  a.wait_ns = stall ? 20000000ull : 2000000000ull;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -157,6 +174,7 @@ moe_status moe_latent_create(const moe_latent_config *cfg, int device, moe_laten
   DeviceGuard g(device);
   int sms = 0;
   if (!g.ok || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return MOE_ERR_CUDA;
+  if (lat_tree_setup(cfg->dtype == MOE_ATTN_F16) != cudaSuccess) return MOE_ERR_CUDA;
   moe_latent *l = new (std::nothrow) moe_latent;
   if (!l) return MOE_ERR_OUT_OF_MEMORY;
   l->cfg = *cfg;
@@ -169,6 +187,26 @@ moe_status moe_latent_create(const moe_latent_config *cfg, int device, moe_laten
 
 moe_status moe_latent_destroy(moe_latent_t lat) {
   delete lat;
+  return MOE_OK;
+}
+
+moe_status moe_latent_workspace_bytes(moe_latent_t lat, int num_requests, int num_rows, size_t *bytes) {
+  if (!lat || !bytes || !counts_ok(num_requests, num_rows)) return MOE_ERR_INVALID_ARG;
+  if (num_requests > MOE_ATTN_MAX_REQUESTS || num_rows > MOE_ATTN_MAX_ROWS) return MOE_ERR_UNSUPPORTED_SHAPE;
+  *bytes = lat_ws(lat->num_sms).total;
+  return MOE_OK;
+}
+
+moe_status moe_latent_get_device_status(moe_latent_t lat, void *ws, cudaStream_t stream, int32_t *flags) {
+  if (!lat || !given(ws) || !flags) return MOE_ERR_INVALID_ARG;
+  DeviceGuard g(lat->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  int32_t got = 0;
+  cudaError_t err = cudaMemcpyAsync(&got, static_cast<int *>(ws) + kAttnCtrlFlags, sizeof(got), cudaMemcpyDeviceToHost, stream);
+  if (err == cudaSuccess) err = cudaMemsetAsync(ws, 0, kAttnCtrlBytes, stream);   // what a call has to find at zero
+  if (err == cudaSuccess) err = cudaStreamSynchronize(stream);
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  *flags = got;
   return MOE_OK;
 }
 
@@ -214,6 +252,30 @@ moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, co
   DeviceGuard g(lat->device);
   if (!g.ok) return MOE_ERR_CUDA;
   return cuda_status(launch_rope(&a, stream));
+}
+
+moe_status moe_latent_tree(moe_latent_t lat, int num_requests, int num_rows, const moe_attn_rows *q,
+                           const moe_attn_rows *q_rope, const int32_t *cu, const int32_t *cached, const int32_t *block_table,
+                           const uint64_t *tree_mask, const void *cache, const moe_attn_rows *out, float *lse, void *ws,
+                           size_t ws_bytes, cudaStream_t stream) {
+  if (!lat || !counts_ok(num_requests, num_rows)) return MOE_ERR_INVALID_ARG;
+  if (num_requests > MOE_ATTN_MAX_REQUESTS || num_rows > MOE_ATTN_MAX_ROWS) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (num_rows == 0 || num_requests == 0) return MOE_OK;
+  LatArgs a = lat_args(*lat, num_requests, num_rows);
+  if (!row_view(q, num_rows, a.heads, kLatDim, &a.q) || !row_view(q_rope, num_rows, a.heads, kLatRope, &a.q_rope) ||
+      !row_view(out, num_rows, a.heads, kLatDim, &a.out) || !words(cu) || !words(cached) || !words(block_table) || !given(cache) ||
+      !given(ws) || (tree_mask && !aligned8(tree_mask)) || !lse_ok(lse))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < lat_ws(lat->num_sms).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  a.cu = cu;
+  a.cached = cached;
+  a.block_table = block_table;
+  a.tree_mask = tree_mask;
+  a.cache = static_cast<const uint16_t *>(cache);
+  a.lse = lse;
+  DeviceGuard g(lat->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  return cuda_status(launch_lat_tree(a, static_cast<uint8_t *>(ws), lat->num_sms, stream));
 }
 
 }  // extern "C"

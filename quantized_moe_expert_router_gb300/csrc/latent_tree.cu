@@ -1,0 +1,986 @@
+// latent_tree.cu -- absorbed latent attention over the paged cache on the 5th-generation
+// tensor cores (moe_latent_tree): single tokens, drafted trees or the next part of a prompt.
+//
+// All heads of a token read the same cached vectors (c, r) of 512 + 64 elements, keys and
+// values at once, so a tile of 128 tokens comes once and serves up to 64 query rows (tokens x
+// heads).  Query rows are the N of both products, tokens and latent elements the M:
+//   S^T = K Q^T                 M = 128 tokens, N rows, K = 576: A the tile as it lies, B = Q
+//   m' = max(m, max S);  P = 2^(c (S - m'));  l = l 2^(c (m - m')) + sum P,  c = softmax_scale * log2(e)
+//   O^T = O^T 2^(c (m - m')) + C^T P^T   M = 4 x 128 latent elements, N rows, K = 128 tokens: A the same tile
+//                               transposed (M-major), B = P^T
+// That way few rows cost little (N is 16, 32 or 64), the 512 x N fp32 of O^T fit tensor memory
+// with S^T beside them (5 N of 512 columns; rows as M would take 512 columns for O alone), and the tile is in
+// shared memory once.  The price: both products read A from shared memory at 4 KB a step of 16, so at
+// N = 64 they take 48 cycles a step and not 32.  The maximum of a row goes over tokens, which
+// are lanes; so the maximum that P is taken against moves only when some score passes it by 2^8
+// (in P's terms), one vote of the four warps a tile tells, and the sums stay per lane to the item's end.
+// P is rounded to the element type because the tensor cores multiply equal types; m, l and O are fp32, l
+// is summed from the unrounded values.
+//
+// An item is (request, whole tokens of it, a part of the heads): N rows at most.  More than 64
+// heads are two parts.  One CTA per SM, 12 warps:
+//   warp 0           tiles, 64 elements x a page a copy (128-byte swizzle): four pairs of 128 x 128 elements into a
+//                    ring of 4 or 5, then the key part; takes the items
+//   warp 1           MMA issue
+//   warp 2           Q rows by boxes (64, heads, tokens)
+//   warps 4-7, 8-11  softmax of rows 0 .. N/2 - 1 and N/2 .. N - 1: a thread has a token, and the
+//                    N/2 rows in registers; the rescaling of O and the epilogue, a thread a latent element
+// A pair is free when the products of its 128 latent elements are done, so the next tile comes while
+// this one's values are multiplied.  With N = 64 shared memory is full: P lies where the key part was, which
+// is done when P is written.
+//
+// The tiles of all items stand in one line that the CTAs share (at_share); calls with two items
+// over the same tokens (two parts of the heads, or more tokens than a tile has room for) give each place of
+// the line to two CTAs, which read the same tiles at the same time: the second one from L2.  A
+// part of an item goes to the workspace (fp32 O, m, l); lat_join_kernel joins them in the order of the context.
+//
+// A token that a row does not see has P = 0, but 0 times an infinite or NaN latent is NaN: in
+// tiles with tokens that not every row sees the softmax warps zero such elements after S, note the token, and
+// the epilogue makes these elements NaN in the rows that do see it.
+//
+// A wait knows its phase by parity alone, so no barrier may be two phases on when a waiter looks:
+//   sched_full    (item parity) item i + 2 is posted when sched_empty has all 10 arrivals of item i
+//   kv_full, r_full   filled again behind kv_empty, r_empty, which the MMA warp commits after its own wait and
+//                 behind p_full, which every softmax warp gives after its scan
+//   kv_empty, r_empty   waited for by the copy warp, whose lanes meet before they copy
+//   q_full        filled again behind q_empty; q_empty is waited for by warp 2 alone, and without that Q there is no next
+//   s_full, p_full, o_done   go to and fro between the MMA warp and the softmax warps
+// The softmax warps of a half also meet at a named barrier: a warp whose wait ran out goes on to
+// the next vote, which tells the others, and all four end together.
+#include <limits.h>
+#include <math.h>
+#include <stddef.h>
+#include <string.h>
+
+#include "attn_tc.cuh"
+#include "latent.h"
+
+namespace moe {
+
+constexpr int kLtThreads = 384;
+constexpr int kLtTile = 128;                      // tokens of a tile
+constexpr int kLtWTma = 0, kLtWMma = 1, kLtWQ = 2, kLtWSoft = 4;
+constexpr int kLtChunk = kLtTile * 128, kLtPair = 2 * kLtChunk;   // bytes of 64 and of 128 elements of a tile
+constexpr int kLtBlocks = kLatDim / 128;          // of 128 latent elements
+constexpr int kLtMaxB = MOE_ATTN_MAX_REQUESTS;
+constexpr int kLtMaxSms = 1024;
+constexpr int kLtRows = 64;                       // rows of an item at most
+constexpr int kLtMinTiles = 1;                    // tiles of a CTA at least
+constexpr float kLtSlack = 8.f;                   // log2 of the largest P
+constexpr float kLtUnset = 1e30f;                 // in place of -c m before a row has seen anything: any score passes it
+
+template <int N>
+struct LtGeom {
+  static constexpr bool kAlias = N == 64;         // P in the place of the key part
+  static constexpr int kPairs = N == 64 ? 4 : 5;
+  static constexpr int kRope = kPairs * kLtPair;
+  static constexpr int kP = kAlias ? kRope : kRope + kLtChunk;
+  static constexpr int kQ = kP + (kAlias ? kLtChunk : kLtTile * N * 2);
+  static constexpr int kQChunk = N * 128;         // 64 elements of the rows
+  static constexpr int kSmem = kQ + 9 * kQChunk + 1024;
+};
+
+struct LtArgs {
+  CUtensorMap cmap;            // (64, page) boxes over [num_pages * page][576]
+  CUtensorMap qmap, rmap;      // (64, hh, per) boxes over [T][heads][512] and [T][heads][64]
+  LatArgs a;
+  int *ctrl;
+  int hh, hp;                  // heads of a part, parts
+  int per;                     // tokens of an item
+  int gang;                    // CTAs (1 or 2) to a place of the line
+  int magic;                   // ceil(2^16 / hh)
+  int4 *desc;                  // per CTA, of the item whose first part it holds and others the rest:
+                               // (first, head part, tok0, toks), (first group, last group, its slot, place in the group)
+  float *part;                 // [2 * grid][N][512]  O of a part
+  float2 *stat;                // [2 * grid][N]       (m, l)
+};
+
+struct LtItem {
+  int b;                       // request (-1: no more items)
+  int first, tok0, toks, hpart;
+  int j0, n;                   // first tile and number of tiles
+  int cached, all, end;        // context before the fresh tokens; tokens that every row sees; tokens from `end` on are seen by none
+  int m0;                      // tiles j0 + m0 .. are masked
+  int slot;                    // where the part goes; -1: the item is whole
+};
+
+struct LtSmem {
+  uint64_t kv_full[5], kv_empty[5];
+  uint64_t r_full, r_empty, q_full, q_empty, s_full, p_full, o_done, sched_full[2], sched_empty[2], drain;
+  uint32_t tmem;
+  int fail[2];                 // the vote at which a wait was found to have run out
+  LtItem item[2];
+  uint32_t bad[2][3][4];       // by item parity and masked tile: tokens with a non-finite latent
+  float wmax[2][4][32], wsum[2][4][32];
+  alignas(16) float mc[8][32]; // per softmax warp: -c m of its rows
+  alignas(16) float f[8][32];  // and their factors
+};
+static_assert(offsetof(LtSmem, mc) % 16 == 0 && offsetof(LtSmem, f) % 16 == 0, "read four at a time");
+
+// While the CTA finds its share, in the place of the tiles.
+struct LtSetup {
+  long long work[kLtMaxB + 1];                    // tiles of the requests before
+  int n[kLtMaxB], cached[kLtMaxB];
+  int cand[kLtThreads / 32][32];
+  long long wsum2[kLtThreads / 32];
+  int wsum[kLtThreads / 32];
+};
+
+__device__ __forceinline__ bool lt_wait(uint64_t *bar, uint32_t parity, const LtArgs &p) {
+  const bool ok = __all_sync(kFull, mbar_wait_bounded(bar, parity, p.a.wait_ns));
+  if (!ok && (threadIdx.x & 31) == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+  return ok;
+}
+// True in all of a half's 128 threads when it is in one of them.
+__device__ __forceinline__ bool lt_any(int half, bool x) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\tbarrier.cta.red.or.pred.aligned p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(1 + half), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void lt_sync(int half) {
+  __syncwarp();
+  asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + half) : "memory");
+}
+__device__ __forceinline__ float lt_redmax(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 8, 16 or 32 columns of this warp's 32 tensor-memory lanes.
+template <int C>
+__device__ __forceinline__ void lt_ld(uint32_t at, float (&r)[C]) {
+  if constexpr (C == 32) {
+    at_ld32(at, r);
+  } else if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(at)
+        : "memory");
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(at)
+                 : "memory");
+  }
+  at_wait_ld(r);
+}
+template <int C>
+__device__ __forceinline__ void lt_st(uint32_t at, const float (&r)[C]) {
+  if constexpr (C == 32) {
+    at_st32(at, r);
+  } else if constexpr (C == 16) {
+    at_st16(at, reinterpret_cast<const uint32_t *>(r));
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "f"(r[0]), "f"(r[1]), "f"(r[2]),
+                 "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+  }
+}
+// Sums over the warp's lanes of C values each: of value lane % C.
+template <int C>
+__device__ __forceinline__ float lt_lane_sums(float (&x)[C]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o >= C; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < C; i++) x[i] += __shfl_xor_sync(kFull, x[i], o);
+#pragma unroll
+  for (int o = C / 2; o >= 1; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; i++) {
+      const float got = __shfl_xor_sync(kFull, up ? x[i] : x[i + o], o);
+      x[i] = (up ? x[i + o] : x[i]) + got;
+    }
+  }
+  return x[0];
+}
+
+// Descriptor of P^T: rows of tokens, 2 N bytes under the swizzle of that width (N-major); 8 rows apart.
+template <int N>
+__device__ __forceinline__ uint64_t lt_desc_p(uint32_t addr) {
+  constexpr uint64_t layout = N == 64 ? 2 : (N == 32 ? 4 : 6);
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)((16u * N) >> 4) << 32) | (1ull << 46) | (layout << 61);
+}
+// Place of 16-byte piece c of row k of P^T under that swizzle.
+template <int N>
+__device__ __forceinline__ int lt_p_at(int k, int c) {
+  return k * 2 * N + ((N == 64 ? c ^ (k & 7) : (N == 32 ? c ^ ((k >> 1) & 3) : c ^ ((k >> 2) & 1))) << 4);
+}
+// Instruction descriptor: fp32 accumulator, M = 128, N rows; `at`: A is M-major, `bt`: B is N-major.
+__device__ __forceinline__ constexpr uint32_t lt_idesc(bool f16, int n, bool at, bool bt) { return at_idesc(f16, n, bt) | (at ? 1u << 15 : 0u); }
+
+// Of a request of n fresh rows: items of a place of the line, and tiles that its rows may see.
+__device__ __forceinline__ int lt_groups(const LtArgs &p, int n) { return p.hp * at_idiv(n + p.per - 1, p.per); }
+__device__ __forceinline__ int lt_items(const LtArgs &p, int n) { return p.gang == 2 ? (lt_groups(p, n) + 1) >> 1 : lt_groups(p, n); }
+__device__ __forceinline__ int lt_nch(const LatArgs &a, int n, int cached) {
+  const int ctx = min(cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : n), a.max_pages << a.page_shift);
+  return (ctx + kLtTile - 1) / kLtTile;
+}
+__device__ __forceinline__ void lt_request(const LatArgs &a, int b, int &first, int &n, int &cached) {
+  first = __ldg(a.cu + b);
+  n = first < 0 ? 0 : max(0, min(__ldg(a.cu + b + 1), a.T) - first);
+  cached = min(max(__ldg(a.cached + b), 0), a.max_pages << a.page_shift);       // no sum with rows passes 2^31
+}
+
+// Walks the line of tiles from place x on.
+struct LtCursor {
+  int b, first, n, cached, nch, items;
+  long long work;              // tiles of the requests before b
+  __device__ __forceinline__ void load(const LtArgs &p) {
+    lt_request(p.a, b, first, n, cached);
+    nch = lt_nch(p.a, n, cached);
+    items = lt_items(p, n);
+  }
+  // The part of an item that starts at place x, up to the end of the CTA's share; returns the place after it.
+  // it.n = 0: there is nothing to do here.
+  __device__ __forceinline__ long long part(const LtArgs &p, long long x, const AtShare &share, LtItem &it) {
+    const LatArgs &a = p.a;
+    while (n == 0 || x >= work + (long long)items * nch) {
+      work += (long long)items * nch;
+      b++;
+      load(p);
+    }
+    const int item = (int)at_div(x - work, nch), member = p.gang == 2 ? (int)blockIdx.x & 1 : 0, group = p.gang * item + member;
+    const long long item0 = work + (long long)item * nch, xe = min(share.x1, item0 + nch);
+    const int tg = p.hp == 2 ? group >> 1 : group;
+    it.b = b;
+    it.first = first;
+    it.hpart = p.hp == 2 ? group & 1 : 0;
+    it.tok0 = tg * p.per;
+    it.toks = min(n - it.tok0, p.per);
+    it.n = 0;
+    if (it.toks <= 0) return xe;                   // the place's second item is not there
+    it.cached = cached;
+    const int lim = min(a.max_pages << a.page_shift, cached + n);
+    it.all = a.tree_mask ? cached : cached + it.tok0 + 1;
+    it.end = min(lim, cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : it.tok0 + it.toks));
+    const int need = (it.end + kLtTile - 1) / kLtTile;                           // tiles of these rows
+    it.j0 = (int)(x - item0);
+    it.n = max(0, min((int)(xe - item0), need) - it.j0);
+    const bool whole = it.j0 == 0 && it.n == need;
+    it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > share.x0);
+    it.m0 = max(0, it.all / kLtTile - it.j0);
+    if (!whole && it.j0 == 0) {
+      // for the join, at the CTA that holds the first part: the last part of a CTA's share, so that there is one at most
+      int c0, c1;
+      share.ctas_of(item0, item0 + need - 1, c0, c1);
+      if (share.len) c1 = c0 + (need - 1) / share.len;
+      if ((threadIdx.x & 31) == 0) {
+        int4 *d = p.desc + 2 * blockIdx.x;
+        d[0] = make_int4(it.first, it.hpart, it.tok0, it.toks);
+        d[1] = make_int4(c0, c1, it.slot, member);
+      }
+    }
+    return xe;
+  }
+};
+
+__device__ __forceinline__ void lt_tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <int N, bool F16>
+__global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_constant__ LtArgs p) {
+  extern __shared__ uint8_t dsm[];
+  __shared__ LtSmem s;
+  using G = LtGeom<N>;
+  constexpr int NP = G::kPairs, NC = N / 2;
+  const LatArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
+  uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
+
+  if (warp == 0) {
+    if (lane < NP) {
+      mbar_init(&s.kv_full[lane], 1);
+      mbar_init(&s.kv_empty[lane], 1);
+    } else if (lane == 8) {
+      mbar_init(&s.r_full, 1);
+      mbar_init(&s.r_empty, 1);
+    } else if (lane == 9) {
+      mbar_init(&s.q_full, 1);
+      mbar_init(&s.q_empty, 1);
+    } else if (lane == 10) {
+      mbar_init(&s.s_full, 1);
+      mbar_init(&s.p_full, 8);
+    } else if (lane == 11) {
+      mbar_init(&s.o_done, 1);
+      mbar_init(&s.drain, 1);
+    } else if (lane < 14 && lane >= 12) {
+      mbar_init(&s.sched_full[lane - 12], 1);
+      mbar_init(&s.sched_empty[lane - 12], 10);    // 8 softmax warps, MMA warp, Q warp
+      s.fail[lane - 12] = INT_MAX;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 32 * kLtWQ) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.cmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.rmap)) : "memory");
+  }
+  if (warp == kLtWMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // rows of Q that no box fills
+  for (int i = tid; i < 9 * (N - p.per * p.hh) * 8; i += kLtThreads) {
+    const int row = p.per * p.hh + (i >> 3) / 9, chunk = (i >> 3) % 9;
+    *reinterpret_cast<uint4 *>(generic0 + G::kQ + chunk * G::kQChunk + row * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  // the CTA's share of the line
+  AtShare share;
+  LtCursor cur;
+  {
+    LtSetup &u = *reinterpret_cast<LtSetup *>(generic0);
+    long long total = 0;
+    int nitems = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kLtThreads) {
+      const int b = b0 + tid;
+      int items = 0;
+      long long v = 0;
+      if (b < a.B) {
+        int first, n, cached;
+        lt_request(a, b, first, n, cached);
+        u.n[b] = n;
+        u.cached[b] = cached;
+        items = lt_items(p, n);
+        v = (long long)items * lt_nch(a, n, cached);
+      }
+      long long incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += t;
+      }
+      items = __reduce_add_sync(kFull, items);
+      if (lane == 31) {
+        u.wsum2[warp] = incl;
+        u.wsum[warp] = items;
+      }
+      __syncthreads();
+      long long at = total;
+#pragma unroll
+      for (int w = 0; w < kLtThreads / 32; w++) {
+        at += w < warp ? u.wsum2[w] : 0;
+        total += u.wsum2[w];
+        nitems += u.wsum[w];
+      }
+      if (b < a.B) u.work[b] = at + incl - v;
+      __syncthreads();
+    }
+    const int grid = p.gang == 2 ? (int)gridDim.x >> 1 : (int)gridDim.x, me = p.gang == 2 ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    // A part costs its CTA an epilogue and the join a source, some two tiles' time: equal parts may be longer than
+    // the mean by that, and by a sixteenth.
+    const long long mean = at_div(total + grid - 1, grid);
+    share = at_share<kLtThreads / 32>(
+        u.work, a.B, total, nitems, kLtMinTiles, u.cand, [&](int b) { return lt_items(p, u.n[b]); },
+        [&](int b) { return lt_nch(a, u.n[b], u.cached[b]); }, grid, me, 2 + (mean >> 4));
+    int lo = 0, hi = a.B - 1;                      // largest b with work[b] <= x0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (u.work[mid] <= share.x0) lo = mid; else hi = mid - 1;
+    }
+    cur.b = lo;
+    cur.work = u.work[lo];
+    cur.n = u.n[lo];
+    cur.cached = u.cached[lo];
+    cur.nch = lt_nch(a, cur.n, cur.cached);
+    cur.items = lt_items(p, cur.n);
+    cur.first = __ldg(a.cu + lo);
+    if (tid == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless LtCursor finds it
+  }
+  at_fence_async();                                // what was written here is written again by copies, or read by the MMAs
+  at_fence_before();
+  __syncthreads();
+  at_fence_after();
+  const uint32_t tb = s.tmem;
+  const float c = a.scale * 1.44269504088896340736f;
+  pdl_launch_dependents();                         // the join's CTAs take the SMs as they fall free, and wait
+
+  if (warp >= kLtWSoft) {
+    // ------------------------------------------------------------ softmax
+    const int h = (warp - kLtWSoft) >> 2, w4 = warp & 3, kt = 32 * w4 + lane;   // token of the tile; latent element of a block
+    const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+    const uint32_t ts = tb + lanes + 4u * N + (uint32_t)(h * NC), to = tb + lanes + (uint32_t)(h * NC);
+    float *const mcw = s.mc[warp - kLtWSoft], *const fw = s.f[warp - kLtWSoft];
+    const int cl = lane & (NC - 1), rl = h * NC + cl;                           // the row whose maximum the lane keeps
+    uint32_t ns = 0, ni = 0;                       // tiles and items so far
+    int nv = 0;                                    // votes so far
+    bool ok = true;
+    // 0: nobody says yes; 1: somebody does; 2: a wait has run out, all four warps end here
+    auto vote = [&](bool x) {
+      if (!ok && lane == 0) atomicMin(&s.fail[h], nv);
+      const bool any = lt_any(h, x || !ok);
+      const int r = !any ? 0 : (*reinterpret_cast<volatile int *>(&s.fail[h]) <= nv ? 2 : 1);
+      nv++;
+      return r;
+    };
+    for (int i = 0;; i++) {
+      ok = lt_wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u, p);
+      if (vote(false) == 2) break;
+      const LtItem it = s.item[i & 1];
+      if (it.b < 0) break;
+      const int rows = it.toks * p.hh;
+      const int tl_l = (rl * p.magic) >> 16, head_l = it.hpart * p.hh + rl - tl_l * p.hh;
+      const bool valid_l = rl < rows && head_l < a.heads;
+      float m_l = -INFINITY;                       // the maximum that P is taken against
+      float l[NC];
+#pragma unroll
+      for (int n = 0; n < NC; n++) l[n] = 0.f;
+      if (lane < NC) mcw[lane] = valid_l ? kLtUnset : -kLtUnset;   // rows of no token have no say
+      __syncwarp();
+      bool dead = false;
+      for (int j = 0; j < it.n; j++, ns++) {
+        const int tok = (it.j0 + j) * kLtTile + kt, col = tok >> a.page_shift;
+        const int id = col < a.max_pages ? __ldg(a.block_table + (size_t)it.b * a.max_pages + col) : -1;
+        const bool held = (unsigned)id < (unsigned)a.num_pages;
+        const bool masked = j >= it.m0 || __any_sync(kFull, !held);
+        ok = lt_wait(&s.s_full, ns & 1u, p);
+        at_fence_after();
+        float v[NC];
+        lt_ld(ts, v);
+        if (masked) {
+          // rows that see this token: those of whole tokens
+          uint64_t sees = 0;
+          if (held && tok < it.end) {
+            const uint64_t ones = p.hh == 64 ? ~0ull : (1ull << p.hh) - 1ull;
+            const int f = tok - it.cached;
+            if (f < 0) {
+              sees = ~0ull;
+            } else if (a.tree_mask) {
+              for (int t = 0; t < it.toks; t++)
+                if (f < 64 && (__ldg(a.tree_mask + it.first + it.tok0 + t) >> f) & 1ull) sees |= ones << (t * p.hh);
+            } else {
+              const int t0 = max(0, f - it.tok0);  // rows from this token on
+              sees = t0 * p.hh >= 64 ? 0ull : ~0ull << (t0 * p.hh);
+            }
+          }
+          sees >>= h * NC;
+#pragma unroll
+          for (int n = 0; n < NC; n++) v[n] = (uint32_t)(sees >> n) & 1u ? v[n] : -INFINITY;
+          // the products take tokens in groups of 16, up to the last that some row sees
+          if (ok && j >= it.m0 && tok >= it.all && tok < ((it.end + 15) & ~15)) {
+            const uint32_t pos = 4u * ns + 2u * (uint32_t)h;
+            for (uint32_t q = pos; q < pos + 2; q++) {                         // half of the pairs each
+              const uint32_t slot = q % NP;
+              if (!mbar_try_wait(&s.kv_full[slot], (q / NP) & 1u)) continue;   // has completed: S needed it; orders the copies before the loads
+              for (int e = 0; e < 16; e++) {
+                uint4 *at = reinterpret_cast<uint4 *>(generic0 + slot * kLtPair + (e >> 3) * kLtChunk + kt * 128 + ((e & 7) ^ (kt & 7)) * 16);
+                const uint4 w = *at;
+                const uint32_t g[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
+                if (g[0] | g[1] | g[2] | g[3]) {
+                  uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                  for (int z = 0; z < 4; z++) u[z] &= ~(((g[z] >> 15) & 0x00010001u) * 0xFFFFu);
+                  *at = make_uint4(u[0], u[1], u[2], u[3]);
+                  atomicOr(&s.bad[i & 1][j - it.m0][kt >> 5], 1u << (kt & 31));
+                }
+              }
+            }
+          }
+          __syncwarp();
+        }
+        const float2 c2 = make_float2(c, c);
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NC; n += 4) {
+          const float4 mc = *reinterpret_cast<const float4 *>(mcw + n);
+          const float2 t0 = ffma2(make_float2(v[n], v[n + 1]), c2, make_float2(mc.x, mc.y));
+          const float2 t1 = ffma2(make_float2(v[n + 2], v[n + 3]), c2, make_float2(mc.z, mc.w));
+          top = at_max3(top, t0.x, t0.y);
+          top = at_max3(top, t1.x, t1.y);
+        }
+        const int moved = vote(top > kLtSlack);
+        if (moved == 2) {
+          dead = true;
+          break;
+        }
+        if (moved) {
+          float mine = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < NC; n++) {
+            const float r = lt_redmax(v[n]);
+            if (cl == n) mine = r;
+          }
+          if (lane < NC) s.wmax[h][w4][lane] = mine;
+          lt_sync(h);
+          const float m1 = fmaxf(fmaxf(m_l, fmaxf(s.wmax[h][0][cl], s.wmax[h][1][cl])), fmaxf(s.wmax[h][2][cl], s.wmax[h][3][cl]));
+          const float f = m1 == m_l || m_l == -INFINITY || !valid_l ? 1.f : at_exp2((m_l - m1) * c);
+          m_l = m1;
+          if (lane < NC) {
+            mcw[lane] = valid_l ? (m1 == -INFINITY ? kLtUnset : -m1 * c) : -kLtUnset;
+            fw[lane] = f;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int n = 0; n < NC; n++) l[n] *= fw[n];
+          if (j > 0) {
+            // the products of the tile before are done: S of this one was issued behind them
+#pragma unroll 1
+            for (int b = 0; b < kLtBlocks; b++) {
+              float o[NC];
+              lt_ld(to + (uint32_t)(b * N), o);
+#pragma unroll
+              for (int n = 0; n < NC; n++) o[n] *= fw[n];
+              lt_st(to + (uint32_t)(b * N), o);
+            }
+            at_wait_st();
+          }
+        }
+        uint8_t *const prow = generic0 + G::kP;
+#pragma unroll
+        for (int n = 0; n < NC; n += 8) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 mc = *reinterpret_cast<const float4 *>(mcw + n + e);
+            float2 t0 = ffma2(make_float2(v[n + e], v[n + e + 1]), c2, make_float2(mc.x, mc.y));
+            float2 t1 = ffma2(make_float2(v[n + e + 2], v[n + e + 3]), c2, make_float2(mc.z, mc.w));
+            t0.x = at_exp2(t0.x);
+            t0.y = at_exp2(t0.y);
+            t1.x = at_exp2(t1.x);
+            t1.y = at_exp2(t1.y);
+            l[n + e] += t0.x;
+            l[n + e + 1] += t0.y;
+            l[n + e + 2] += t1.x;
+            l[n + e + 3] += t1.y;
+            pk[e / 2] = at_pack<F16>(t0.x, t0.y);
+            pk[e / 2 + 1] = at_pack<F16>(t1.x, t1.y);
+          }
+          *reinterpret_cast<uint4 *>(prow + lt_p_at<N>(kt, h * (NC / 8) + n / 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        at_fence_async();
+        at_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full);
+      }
+      if (dead) break;
+      // -------------------------------------------------------------- epilogue
+      {
+        const float sum = lt_lane_sums(l);
+        if (lane < NC) s.wsum[h][w4][lane] = sum;
+      }
+      ok = lt_wait(&s.o_done, ni++ & 1u, p);
+      if (vote(false) == 2) break;
+      at_fence_after();
+      const float l_l = (s.wsum[h][0][cl] + s.wsum[h][1][cl]) + (s.wsum[h][2][cl] + s.wsum[h][3][cl]);
+      if (w4 == 0 && lane < NC && valid_l) {
+        if (it.slot >= 0) p.stat[(size_t)it.slot * N + rl] = make_float2(m_l, l_l);
+        else if (a.lse) a.lse[(size_t)(it.first + it.tok0 + tl_l) * a.heads + head_l] = l_l == 0.f ? -INFINITY : m_l * a.scale + logf(l_l);
+      }
+      if (lane < NC) fw[lane] = l_l == 0.f ? 0.f : 1.f / l_l;
+      __syncwarp();
+      uint32_t anybad = 0;
+      const int wend = min(12, 4 * (it.n - it.m0));
+#pragma unroll
+      for (int w = 0; w < 12; w++)
+        if (w < wend) anybad |= s.bad[i & 1][w >> 2][w & 3];
+#pragma unroll 1
+      for (int b = 0; b < kLtBlocks; b++) {
+        float o[NC];
+        lt_ld(to + (uint32_t)(b * N), o);
+        if (anybad) {
+          for (int w = 0; w < wend; w++)
+            for (uint32_t bits = s.bad[i & 1][w >> 2][w & 3]; bits; bits &= bits - 1) {
+              const int tok = (it.j0 + it.m0) * kLtTile + 32 * w + __ffs(bits) - 1, f = tok - it.cached;
+              if (tok >= it.end) continue;
+              const long long page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (tok >> a.page_shift));
+              const long long at = ((page << a.page_shift) + (tok & ((1 << a.page_shift) - 1))) * kLatRow + 128 * b + kt;
+              if (isfinite(at_value<F16>(__ldg(a.cache + at)))) continue;
+#pragma unroll
+              for (int n = 0; n < NC; n++) {
+                const int tl = ((h * NC + n) * p.magic) >> 16;
+                if (tl >= it.toks) continue;
+                const bool sees = f < 0 || (a.tree_mask ? f < 64 && (__ldg(a.tree_mask + it.first + it.tok0 + tl) >> f) & 1ull
+                                                        : f <= it.tok0 + tl);
+                if (sees) o[n] = __int_as_float(0x7FFFFFFF);
+              }
+            }
+          __syncwarp();
+        }
+        if (it.slot >= 0) {
+          float *part = p.part + ((size_t)it.slot * N + h * NC) * kLatDim + 128 * b + kt;
+#pragma unroll
+          for (int n = 0; n < NC; n++)
+            if (h * NC + n < rows) part[(size_t)n * kLatDim] = o[n];
+        } else {
+          // lanes are neighbouring elements: of two rows an even lane stores a pair of the first and an odd one of the second
+#pragma unroll
+          for (int n = 0; n < NC; n += 2) {
+            const float x = o[n] * fw[n], y = o[n + 1] * fw[n + 1];
+            const float got = __shfl_xor_sync(kFull, lane & 1 ? x : y, 1);
+            const uint32_t w = lane & 1 ? at_pack<F16>(got, y) : at_pack<F16>(x, got);
+            const int r = h * NC + n + (lane & 1), tl = (r * p.magic) >> 16, head = it.hpart * p.hh + r - tl * p.hh;
+            if (r < rows && head < a.heads)
+              *reinterpret_cast<uint32_t *>(a.out.p + (long long)(it.first + it.tok0 + tl) * a.out.row + (long long)head * a.out.head + 128 * b +
+                                            (kt & ~1)) = w;
+          }
+          __syncwarp();
+        }
+      }
+      at_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
+    }
+  } else if (warp == kLtWTma) {
+    // ---------------------------------------------------------- items and tiles
+    const int np = kLtTile >> a.page_shift, pg = lane & (np - 1), part = lane >> (7 - a.page_shift);
+    uint32_t pos = 0, tiles = 0;                   // pairs and tiles so far
+    long long next = share.x0;
+    bool ok = true;
+    for (int i = 0; ok; i++) {
+      LtItem it;
+      it.b = -1;
+      while (next < share.x1) {
+        next = cur.part(p, next, share, it);
+        if (it.n > 0) break;
+        it.b = -1;
+      }
+      if (i >= 2 && !lt_wait(&s.sched_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u, p)) break;
+      if (lane < 12) s.bad[i & 1][lane >> 2][lane & 3] = 0u;
+      __syncwarp();
+      if (lane == 0) {
+        s.item[i & 1] = it;
+        mbar_arrive(&s.sched_full[i & 1]);
+      }
+      if (it.b < 0) break;
+      const int32_t *table = a.block_table + (size_t)it.b * a.max_pages;
+      auto page_row = [&](int j) {                 // the cache row of the lane's page; past the end: reads zeros
+        const int col = (((it.j0 + j) * kLtTile) >> a.page_shift) + pg;
+        const int id = col < a.max_pages ? __ldg(table + col) : -1;
+        return ((unsigned)id < (unsigned)a.num_pages ? id : a.num_pages) << a.page_shift;
+      };
+      int row = page_row(0);
+      for (int j = 0; j < it.n && ok; j++, tiles++) {
+        const int ahead = j + 1 < it.n ? page_row(j + 1) : 0;
+        for (int b = 0; b < kLtBlocks; b++, pos++) {
+          const uint32_t slot = pos % NP;
+          if (pos >= NP) ok = lt_wait(&s.kv_empty[slot], (pos / NP - 1) & 1u, p);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)kLtPair + a.stall);
+          __syncwarp();
+          if (part < 2)
+            lt_tma_2d(smem0 + slot * kLtPair + (uint32_t)(part * kLtChunk) + ((uint32_t)pg << (a.page_shift + 7)), &p.cmap,
+                      128 * b + 64 * part, row, &s.kv_full[slot]);
+        }
+        if (!ok) break;
+        if (tiles > 0) ok = lt_wait(&s.r_empty, (tiles - 1) & 1u, p);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&s.r_full, (uint32_t)kLtChunk + a.stall);
+        __syncwarp();
+        if (part == 0) lt_tma_2d(smem0 + G::kRope + ((uint32_t)pg << (a.page_shift + 7)), &p.cmap, kLatDim, row, &s.r_full);
+        row = ahead;
+      }
+    }
+    // copies in flight land before the CTA ends; nothing else may pass these barriers now
+    for (uint32_t q = pos > NP ? pos - NP : 0; q < pos; q++) mbar_wait_bounded(&s.kv_full[q % NP], (q / NP) & 1u, a.wait_ns);
+    if (tiles > 0) mbar_wait_bounded(&s.r_full, (tiles - 1) & 1u, a.wait_ns);
+    __syncwarp();
+  } else if (warp == kLtWMma) {
+    // ---------------------------------------------------------- MMA issue
+    // The whole warp goes through the loop, so that descriptors stay in uniform registers; one elected lane issues.
+    constexpr uint32_t id_s = lt_idesc(F16, N, false, false), id_o = lt_idesc(F16, N, true, true);
+    const uint32_t tu = __shfl_sync(kFull, tb, 0), ds = tu + 4u * N;
+    const uint64_t dq0 = at_desc(smem0 + G::kQ, 16), dr = at_desc(smem0 + G::kRope, 16), dk0 = at_desc(smem0, 16);
+    const uint64_t dv0 = at_desc(smem0, kLtChunk), dp0 = lt_desc_p<N>(smem0 + G::kP);
+    uint32_t pos = 0, tiles = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (ok && !mbar_wait_bounded(bar, parity, a.wait_ns)) {
+        atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+        ok = false;
+      }
+      ok = __all_sync(kFull, ok);
+    };
+    for (int i = 0; ok; i++) {
+      wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
+      if (!ok) break;
+      const LtItem &im = s.item[i & 1];
+      if (__shfl_sync(kFull, im.b, 0) < 0) break;
+      const int n = __shfl_sync(kFull, im.n, 0), end = __shfl_sync(kFull, im.end - im.j0 * kLtTile, 0);
+      wait(&s.q_full, (uint32_t)i & 1u);
+      for (int j = 0; j < n && ok; j++, tiles++) {
+        for (int b = 0; b < kLtBlocks; b++) {      // S: the latent's part, pair by pair as they come
+          const uint32_t slot = (pos + b) % NP;
+          wait(&s.kv_full[slot], ((pos + b) / NP) & 1u);
+          if (!ok) break;
+          at_fence_after();
+          if (at_elect()) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+              const uint32_t ka = (uint32_t)(slot * kLtPair + (k >> 2) * kLtChunk + (k & 3) * 32) >> 4;
+              const uint32_t kb = (uint32_t)((2 * b + (k >> 2)) * G::kQChunk + (k & 3) * 32) >> 4;
+              at_mma_ss(ds, dk0 + ka, dq0 + kb, id_s, b > 0 || k > 0);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        wait(&s.r_full, tiles & 1u);
+        if (!ok) break;
+        at_fence_after();
+        if (at_elect()) {
+#pragma unroll
+          for (int k = 0; k < 4; k++) at_mma_ss(ds, dr + (uint32_t)(k * 32 >> 4), dq0 + (uint32_t)((8 * G::kQChunk + k * 32) >> 4), id_s, 1u);
+          at_commit(&s.s_full);
+          if (!G::kAlias) at_commit(&s.r_empty);
+          if (j + 1 == n) at_commit(&s.q_empty);
+        }
+        __syncwarp();
+        wait(&s.p_full, tiles & 1u);
+        if (!ok) break;
+        at_fence_after();
+        const int left = end - j * kLtTile, steps = left >= kLtTile ? 8 : (left + 15) >> 4;   // groups of 16 tokens that some row sees
+        if (at_elect()) {
+#pragma unroll 1
+          for (int b = 0; b < kLtBlocks; b++) {
+            const uint32_t slot = (pos + b) % NP;
+            const uint64_t da = dv0 + (uint64_t)((slot * kLtPair) >> 4);
+#pragma unroll 1
+            for (int k = 0; k < steps; k++)
+              at_mma_ss(tu + (uint32_t)(b * N), da + (uint64_t)(128u * k), dp0 + (uint64_t)(2u * N * k), id_o, j > 0 || k > 0);
+            at_commit(&s.kv_empty[slot]);
+          }
+          if (G::kAlias) at_commit(&s.r_empty);
+          if (j + 1 == n) at_commit(&s.o_done);
+        }
+        __syncwarp();
+        pos += kLtBlocks;
+      }
+      if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
+    }
+    // every MMA issued has completed before tensor memory is released
+    if (at_elect()) at_commit(&s.drain);
+    mbar_wait_bounded(&s.drain, 0u, a.wait_ns);
+    __syncwarp();
+  } else if (warp == kLtWQ) {
+    // ---------------------------------------------------------- Q rows
+    int nq = 0;
+    for (int i = 0;; i++) {
+      if (!lt_wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u, p)) break;
+      const LtItem it = s.item[i & 1];
+      if (it.b < 0) break;
+      if (i > 0 && !lt_wait(&s.q_empty, (uint32_t)(i - 1) & 1u, p)) break;
+      // a box (64, hh, per): rows past the item's tokens are others' or zeros, and are not stored
+      if (lane == 0) mbar_arrive_expect_tx(&s.q_full, (uint32_t)(9 * 128 * p.hh * p.per));
+      __syncwarp();
+      if (lane < 9)
+        at_tma_3d(smem0 + G::kQ + (uint32_t)(lane * G::kQChunk), lane < 8 ? &p.qmap : &p.rmap, lane < 8 ? 64 * lane : 0, it.hpart * p.hh,
+                  it.first + it.tok0, &s.q_full);
+      nq++;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
+    }
+    if (nq > 0) mbar_wait_bounded(&s.q_full, (uint32_t)(nq - 1) & 1u, a.wait_ns);   // a copy in flight lands before the CTA ends
+    __syncwarp();
+  }
+  at_fence_before();
+  __syncthreads();
+  if (warp == kLtWMma) {
+    at_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512) : "memory");
+  }
+}
+
+// Joins the parts of the items that several CTAs took: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A CTA
+// has one row of an item at a time: 128 threads four elements each, four times over the sources (k, k + 4, ...),
+// which are summed up in that order at the end.
+template <int N, bool F16>
+__global__ void __launch_bounds__(512) lat_join_kernel(const __grid_constant__ LtArgs p, int ctas) {
+  __shared__ unsigned masks[kLtMaxSms / 32];
+  __shared__ float4 acc4[4][128];
+  __shared__ float2 stat4[4];
+  const LatArgs &a = p.a;
+  const int tid = threadIdx.x, words = (ctas + 31) / 32, d4 = tid & 127, sg = tid >> 7;
+  pdl_wait();
+  for (int k = tid; k < 32 * words; k += 512) {
+    const unsigned mask = __ballot_sync(kFull, k < ctas && __ldcg(&p.desc[2 * k + 1].y) >= 0);
+    if ((tid & 31) == 0) masks[k >> 5] = mask;
+  }
+  __syncthreads();
+  int count = 0;
+  for (int w = 0; w < words; w++) count += __popc(masks[w]);
+  const float c = a.scale * 1.44269504088896340736f;
+  for (int unit = blockIdx.x; unit < count * N; unit += gridDim.x) {
+    int left = unit / N, w = 0;                    // the (unit / N)-th set bit
+    while (left >= __popc(masks[w])) left -= __popc(masks[w++]);
+    unsigned bits = masks[w];
+    for (; left > 0; left--) bits &= bits - 1;
+    const int which = 32 * w + __ffs(bits) - 1;
+    const int4 d0 = __ldcg(p.desc + 2 * which), d1 = __ldcg(p.desc + 2 * which + 1);
+    const int r = unit % N, tl = (r * p.magic) >> 16, head = d0.y * p.hh + r - tl * p.hh;
+    if (tl >= p.per || tl >= d0.w || head >= a.heads) continue;
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = d1.x + sg; k0 <= d1.y; k0 += 16) {         // four sources at a time, so that their loads wait together
+      float2 st[4];
+      float4 u[4];
+      float t1 = top;
+#pragma unroll
+      for (int z = 0; z < 4; z++) {
+        const int k = k0 + 4 * z;
+        const size_t slot = k == d1.x ? d1.z : 2 * (k * p.gang + d1.w);
+        st[z] = make_float2(-INFINITY, 0.f);
+        if (k <= d1.y) {
+          st[z] = __ldcg(p.stat + slot * N + r);
+          u[z] = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot * N + r) * kLatDim) + d4);
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < 4; z++) t1 = fmaxf(t1, st[z].x);
+      const float f0 = top == t1 ? 1.f : at_exp2((top - t1) * c);
+      top = t1;
+      sum *= f0;
+      acc.x *= f0;
+      acc.y *= f0;
+      acc.z *= f0;
+      acc.w *= f0;
+#pragma unroll
+      for (int z = 0; z < 4; z++) {
+        if (st[z].x == -INFINITY && st[z].y == 0.f) continue;   // a part in which the row sees nothing, or none
+        const float f = at_exp2((st[z].x - t1) * c);
+        sum = fmaf(st[z].y, f, sum);
+        acc.x = fmaf(u[z].x, f, acc.x);
+        acc.y = fmaf(u[z].y, f, acc.y);
+        acc.z = fmaf(u[z].z, f, acc.z);
+        acc.w = fmaf(u[z].w, f, acc.w);
+      }
+    }
+    acc4[sg][d4] = acc;
+    if (d4 == 0) stat4[sg] = make_float2(top, sum);
+    __syncthreads();
+    if (sg == 0) {
+      const float t1 = fmaxf(fmaxf(stat4[0].x, stat4[1].x), fmaxf(stat4[2].x, stat4[3].x));
+      sum = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int z = 0; z < 4; z++) {
+        if (stat4[z].x == -INFINITY && stat4[z].y == 0.f) continue;
+        const float f = stat4[z].x == t1 ? 1.f : at_exp2((stat4[z].x - t1) * c);
+        const float4 u = acc4[z][d4];
+        sum = fmaf(stat4[z].y, f, sum);
+        acc.x = fmaf(u.x, f, acc.x);
+        acc.y = fmaf(u.y, f, acc.y);
+        acc.z = fmaf(u.z, f, acc.z);
+        acc.w = fmaf(u.w, f, acc.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const long long row = d0.x + d0.z + tl;
+      *reinterpret_cast<uint2 *>(a.out.p + row * a.out.row + (long long)head * a.out.head + 4 * d4) =
+          make_uint2(at_pack<F16>(acc.x * inv, acc.y * inv), at_pack<F16>(acc.z * inv, acc.w * inv));
+      if (a.lse && d4 == 0) a.lse[row * a.heads + head] = sum == 0.f ? -INFINITY : t1 * a.scale + logf(sum);
+    }
+    __syncthreads();
+  }
+}
+
+namespace {
+typedef void (*LtKernel)(const LtArgs);
+typedef void (*LtJoin)(const LtArgs, int);
+LtKernel lt_kernel(int n, int f16) {
+  if (n == 16) return f16 ? lat_tree_kernel<16, true> : lat_tree_kernel<16, false>;
+  if (n == 32) return f16 ? lat_tree_kernel<32, true> : lat_tree_kernel<32, false>;
+  return f16 ? lat_tree_kernel<64, true> : lat_tree_kernel<64, false>;
+}
+LtJoin lt_join(int n, int f16) {
+  if (n == 16) return f16 ? lat_join_kernel<16, true> : lat_join_kernel<16, false>;
+  if (n == 32) return f16 ? lat_join_kernel<32, true> : lat_join_kernel<32, false>;
+  return f16 ? lat_join_kernel<64, true> : lat_join_kernel<64, false>;
+}
+int lt_smem(int n) { return n == 16 ? LtGeom<16>::kSmem : (n == 32 ? LtGeom<32>::kSmem : LtGeom<64>::kSmem); }
+
+cudaError_t lt_encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                      int f16) {
+  const AttnMapEncodeFn enc = attn_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult e = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+cudaError_t lt_encode_rows(CUtensorMap *map, const RowView &r, int dim, const LtArgs &p) {
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)p.a.heads, (cuuint64_t)p.a.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)r.head * 2, (cuuint64_t)r.row * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.hh, (cuuint32_t)p.per};
+  return lt_encode(map, r.p, 3, dims, strides, box, p.a.f16);
+}
+}  // namespace
+
+cudaError_t lat_tree_setup(int f16) {
+  for (const int n : {16, 32, 64}) {
+    const cudaError_t err = cudaFuncSetAttribute(lt_kernel(n, f16), cudaFuncAttributeMaxDynamicSharedMemorySize, lt_smem(n));
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+LatWs lat_ws(int num_sms) {
+  LatWs w;
+  size_t off = kAttnCtrlBytes;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  w.desc = take(32 * (size_t)num_sms);
+  w.stat = take(8 * (size_t)(2 * num_sms) * kLtRows);
+  w.part = take(4 * (size_t)(2 * num_sms) * kLtRows * kLatDim);
+  w.total = off;
+  return w;
+}
+
+cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStream_t stream) {
+  LtArgs p;
+  memset(&p, 0, sizeof(p));
+  const LatWs w = lat_ws(num_sms);
+  p.a = a;
+  p.ctrl = reinterpret_cast<int *>(ws);
+  p.desc = reinterpret_cast<int4 *>(ws + w.desc);
+  p.stat = reinterpret_cast<float2 *>(ws + w.stat);
+  p.part = reinterpret_cast<float *>(ws + w.part);
+  p.hp = a.heads > kLtRows ? 2 : 1;
+  p.hh = (a.heads + p.hp - 1) / p.hp;
+  p.magic = (65536 + p.hh - 1) / p.hh;
+  // room for the mean request's tokens, if there is
+  const int mean = (int)(((long long)a.T + a.B - 1) / a.B), most = kLtRows / p.hh, rows = p.hh * (mean < most ? mean : most);
+  const int n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  p.per = n / p.hh;
+  p.gang = p.hp == 2 || mean > p.per ? 2 : 1;
+  const cuuint64_t cdims[2] = {(cuuint64_t)kLatRow, (cuuint64_t)a.num_pages << a.page_shift};
+  const cuuint64_t cstride[1] = {2 * kLatRow};
+  const cuuint32_t cbox[2] = {64, 1u << a.page_shift};
+  cudaError_t err = lt_encode(&p.cmap, a.cache, 2, cdims, cstride, cbox, a.f16);
+  if (err == cudaSuccess) err = lt_encode_rows(&p.qmap, a.q, kLatDim, p);
+  if (err == cudaSuccess) err = lt_encode_rows(&p.rmap, a.q_rope, kLatRope, p);
+  if (err != cudaSuccess) return err;
+  if (num_sms > kLtMaxSms) num_sms = kLtMaxSms;
+  const int grid = p.gang == 2 ? (num_sms < 2 ? 2 : num_sms & ~1) : num_sms;
+  lt_kernel(n, a.f16)<<<grid, kLtThreads, lt_smem(n), stream>>>(p);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * num_sms));
+  cfg.blockDim = dim3(512);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lt_join(n, a.f16), p, grid);
+}
+
+}  // namespace moe

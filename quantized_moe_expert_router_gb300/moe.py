@@ -52,7 +52,8 @@ EXPORTED = (
     "moe_attn_create", "moe_attn_destroy", "moe_attn_workspace_bytes", "moe_kv_plan", "moe_kv_append",
     "moe_attn_prompt", "moe_attn_tree", "moe_attn_get_device_status",
     "moe_rope_create", "moe_rope_destroy", "moe_rope_frequencies", "moe_rope_apply", "moe_rope_append",
-    "moe_latent_create", "moe_latent_destroy", "moe_latent_plan", "moe_latent_append",
+    "moe_latent_create", "moe_latent_destroy", "moe_latent_workspace_bytes", "moe_latent_get_device_status",
+    "moe_latent_plan", "moe_latent_append", "moe_latent_tree",
     "moe_status_string",
 )
 
@@ -156,6 +157,9 @@ def load_library(path: str = LIB_PATH):
             lib.moe_rope_append.argtypes = [P, P, I32, P, P, R, R, R, R, P, P, P]
             lib.moe_latent_create.argtypes = [ctypes.POINTER(moe_latent_config), I32, ctypes.POINTER(P)]
             lib.moe_latent_destroy.argtypes = [P]
+            lib.moe_latent_workspace_bytes.argtypes = [P, I32, I32, ctypes.POINTER(SZ)]
+            lib.moe_latent_get_device_status.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_int32)]
+            lib.moe_latent_tree.argtypes = [P, I32, I32, R, R, P, P, P, P, P, R, P, P, SZ, P]
             lib.moe_latent_plan.argtypes = lib.moe_kv_plan.argtypes
             lib.moe_latent_append.argtypes = [P, P, I32, P, P, R, R, R, R, P, P]
             lib.moe_status_string.argtypes = [I32]
@@ -712,6 +716,28 @@ class LatentAttention:
         self.close()
 
 
+def moe_latent_workspace_bytes(lat: LatentAttention, num_requests: int, num_rows: int) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_latent_workspace_bytes", load_library().moe_latent_workspace_bytes(
+        lat.handle, num_requests, num_rows, ctypes.byref(n)))
+    return n.value
+
+
+def alloc_latent_workspace(lat: LatentAttention, num_requests: int, num_rows: int, device=None) -> torch.Tensor:
+    """Zero-filled workspace (uint8) of moe_latent_workspace_bytes."""
+    n = moe_latent_workspace_bytes(lat, num_requests, num_rows)
+    return torch.zeros(n, dtype=torch.uint8, device=device or f"cuda:{lat.device}")
+
+
+def moe_latent_get_device_status(lat: LatentAttention, ws: torch.Tensor, stream=None) -> int:
+    fn, f = "moe_latent_get_device_status", ctypes.c_int32()
+    if ws.get_device() != lat.device or not ws.is_contiguous() or ws.nbytes < moe_latent_workspace_bytes(lat, 0, 0):
+        raise ValueError(f"{fn}: ws of {ws.nbytes} bytes on {ws.device} is not a workspace on cuda:{lat.device}")
+    _check(fn, load_library().moe_latent_get_device_status(
+        lat.handle, ws.data_ptr(), _stream(torch.cuda.current_stream(lat.device) if stream is None else stream), ctypes.byref(f)))
+    return f.value
+
+
 def moe_latent_plan(lat, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
                     stream=None) -> None:
     """moe_kv_plan for the latent cache."""
@@ -756,6 +782,36 @@ def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_o
     status = _lib.moe_latent_append(
         lat.handle, rope.handle, T, positions.data_ptr(), slots.data_ptr(), _latent_row(fn, "c", lat, c, (T, LATENT_DIM)),
         _latent_row(fn, "k_rope", lat, k_rope, (T, LATENT_ROPE)), qv, qo, cache.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(fn, status)
+
+
+def moe_latent_tree(lat, q, q_rope, cu, cached, block_table, cache, out, ws, tree_mask=None, lse=None, stream=None) -> None:
+    """Absorbed attention of the step's rows over the latent cache: q, out
+    [rows][heads][512], q_rope [rows][heads][64]; the rest as moe_attn_tree."""
+    fn, dev, i32, T, n = "moe_latent_tree", lat.device, torch.int32, q.shape[0], cu.numel()
+    hq = lat.heads
+    qs = (T, hq, LATENT_DIM)
+    if (cu.dtype is not i32 or not cu.is_contiguous() or cu.get_device() != dev
+            or ws.get_device() != dev or not ws.is_contiguous()
+            or cached.dtype is not i32 or cached.numel() != n - 1 or not cached.is_contiguous() or cached.get_device() != dev
+            or block_table.dtype is not i32 or block_table.shape != (n - 1, lat.max_pages) or not block_table.is_contiguous()
+            or block_table.get_device() != dev
+            or tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.numel() != T
+                                          or not tree_mask.is_contiguous() or tree_mask.get_device() != dev)
+            or lse is not None and (lse.dtype is not torch.float32 or lse.numel() != T * hq or not lse.is_contiguous()
+                                    or lse.get_device() != dev)):
+        _attn_refuse(fn, dev, ("cu", cu, i32, (n,)), ("cached", cached, i32, (n - 1,)),
+                     ("block_table", block_table, i32, (n - 1, lat.max_pages)), ("tree_mask", tree_mask, torch.int64, (T,)),
+                     ("lse", lse, torch.float32, (T, hq)))
+        _attn_ws(fn, dev, ws)
+        raise ValueError(f"{fn}: block_table has shape {tuple(block_table.shape)}, not {(n - 1, lat.max_pages)}")
+    _latent_cache(fn, lat, cache)
+    status = _lib.moe_latent_tree(
+        lat.handle, n - 1, T, _attn_rows(fn, "q", lat, q, qs), _attn_rows(fn, "q_rope", lat, q_rope, (T, hq, LATENT_ROPE)),
+        cu.data_ptr(), cached.data_ptr(), block_table.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(),
+        cache.data_ptr(), _attn_rows(fn, "out", lat, out, qs), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)
