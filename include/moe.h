@@ -610,6 +610,19 @@ moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, co
                              const moe_attn_rows *c, const moe_attn_rows *k_rope, const moe_attn_rows *q,
                              const moe_attn_rows *q_out, void *cache, cudaStream_t stream);
 
+/* Expanded form, causal over whole prompts: for row i of request b and head h
+ *   o[i] = sum_{j <= i} w_j v[j],  w = softmax_j(softmax_scale * (q[i] . [k[j] | k_rope[j]]))
+ * over the rows j of the same request, from the packed rows themselves.
+ *   q       [num_rows][heads][192]: the head's own 128 elements, then the turned 64
+ *   k, v    [num_rows][heads][128]: the latent's expansion, by the caller's product
+ *   k_rope  [num_rows][64], turned; for all heads (its head stride is not looked at)
+ *   out     [num_rows][heads][128] (may not overlap the inputs)
+ * cu, lse, rows outside the requests and what rows may hold that a row does not see: as
+ * moe_attn_prompt. */
+moe_status moe_latent_prompt(moe_latent_t lat, int num_requests, int num_rows, const moe_attn_rows *q, const moe_attn_rows *k,
+                             const moe_attn_rows *k_rope, const moe_attn_rows *v, const int32_t *cu, const moe_attn_rows *out,
+                             float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Absorbed form, over the cache: for row i of request b and head h
  *   o[i] = sum_j w_j c_j,  w = softmax_j(softmax_scale * (q[i] . c_j + q_rope[i] . r_j))
  * over the tokens that moe_attn_tree's row would see (all cached ones, and the fresh

@@ -67,7 +67,9 @@ struct AttnTreeWs {             // up to `stat`: zero between calls, but for the
 // Opt-in shared memory of the tcgen05 kernels (idempotent).
 cudaError_t attn_wide_setup(int head_dim, int f16);
 AttnWideWs attn_wide_ws(size_t off, int head_dim, int num_sms);
-cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaStream_t stream);
+cudaError_t attn_wide_latent_setup(int f16);
+// k_rope: expanded latent attention, queries of head_dim + 64 elements and this key part of 64 for all heads; else null.
+cudaError_t launch_attn_prompt(const AttnArgs &a, const RowView *k_rope, int *ctrl, int num_sms, cudaStream_t stream);
 cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWideWs &w, int num_sms, cudaStream_t stream);
 
 AttnTreeWs attn_tree_ws(int head_dim, int num_sms);

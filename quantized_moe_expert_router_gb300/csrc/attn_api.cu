@@ -150,7 +150,7 @@ moe_status moe_attn_prompt(moe_attn_t attn, int num_requests, int num_rows, cons
   a.lse = lse;
   DeviceGuard g(attn->device);
   if (!g.ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_attn_prompt(a, static_cast<int *>(ws), attn->num_sms, stream));
+  return cuda_status(launch_attn_prompt(a, nullptr, static_cast<int *>(ws), attn->num_sms, stream));
 }
 
 moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const moe_attn_rows *q, const int32_t *cu,

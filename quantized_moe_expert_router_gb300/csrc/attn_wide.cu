@@ -101,14 +101,32 @@ constexpr int kApMinTiles = 2;                   // key tiles of a CTA at least 
 template <int D>
 struct ApGeom {
   static constexpr int kTileBytes = kApTile * D * 2;
+  static constexpr int kQTile = kTileBytes;
   static constexpr int kStages = D == 128 ? 2 : 4; // of a key and a value tile
   static constexpr int kSmem = 2 * kTileBytes + kStages * 2 * kTileBytes + 1024;
 };
+// Latent attention, expanded: keys of 192 elements, of which the heads share the last 64, and values of 128.  Two
+// stages of 80 KB do not fit beside the 96 KB of Q, so the ring is of pieces, 128 tokens x 64 elements each: the value
+// tile's two, then the three of the key tile that S needs next.  A slot is free when its piece has been read for the last
+// time, so of the five pieces that a row tile's two products read, two of the next are there before and
+// three come while the other row tile's products run.
+constexpr int kApPiece = kApTile * 128;
+struct ApLatGeom {
+  static constexpr int kTileBytes = 2 * kApPiece;
+  static constexpr int kQTile = 3 * kApPiece;
+  static constexpr int kStages = 7;                // pieces
+  static constexpr int kSmem = 2 * kQTile + kStages * kApPiece + 1024;
+};
+template <int D, bool LAT>
+struct ApGeomOf { using type = ApGeom<D>; };
+template <int D>
+struct ApGeomOf<D, true> { using type = ApLatGeom; };
 
 struct ApArgs {
   CUtensorMap kmap, vmap;      // prompt: (64, 1, 128) boxes over [rows][kv_heads][D]; cache: (64, page, 1, 1) over
                                // [pages][kv_heads][page][D]; 128-byte swizzle
   CUtensorMap qmap;            // (64, group, per) boxes over [rows][q_heads][D]
+  CUtensorMap rmap;            // latent: (64, 1, 128) boxes over [rows][1][64], the key part that the heads share
   AttnArgs a;
   int *ctrl;                   // workspace control words
   int magic;                   // ceil(2^16 / group)
@@ -134,8 +152,24 @@ struct ApItem {
   int slot;                    // where the part goes; -1: the item is whole
 };
 
-struct ApSmem {
-  uint64_t kv_full[4], kv_empty[4];
+// What finds the items.  Prompts: requests by falling length.
+template <bool PAGED>
+struct ApSched {
+  uint16_t order[kApMaxB];
+  int tiles[kApMaxB];          // items per kv head of the k-th longest
+  int before[kApMaxB + 1];     // items (per kv head) of row tiles in which fewer than k + 1 requests take part
+};
+// Cache: the line of key tiles.
+template <>
+struct ApSched<true> {
+  long long work[kApMaxB + 1]; // tiles of the requests before
+  int first[kApMaxB], n[kApMaxB], cached[kApMaxB];   // first packed row, fresh rows, cached tokens
+  int cand[kApThreads / 32][32];
+};
+
+template <bool PAGED>
+struct ApSmem : ApSched<PAGED> {
+  uint64_t kv_full[7], kv_empty[7];
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], v_posted[2][3], v_clean[2][3], x_full[2], sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int wsum[kApThreads / 32];
@@ -143,18 +177,6 @@ struct ApSmem {
   int v_pos[2][3];             // by item parity: stages of the masked value tiles, counted from the CTA's start
   float2 stat[2][kApTile];     // (m, l) of the twins of a prompt
   uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
-  union {
-    struct {                   // prompts: requests by falling length
-      uint16_t order[kApMaxB];
-      int tiles[kApMaxB];      // items per kv head of the k-th longest
-      int before[kApMaxB + 1]; // items (per kv head) of row tiles in which fewer than k + 1 requests take part
-    };
-    struct {                   // cache: the line of key tiles
-      long long work[kApMaxB + 1];   // tiles of the requests before
-      int first[kApMaxB], n[kApMaxB], cached[kApMaxB];   // first packed row, fresh rows, cached tokens
-      int cand[kApThreads / 32][32];
-    };
-  };
   long long wsum2[kApThreads / 32];
 };
 
@@ -168,7 +190,7 @@ __device__ __forceinline__ int cache_nch(const AttnArgs &a, int n, int cached) {
 
 // The idx-th item by falling row tile: row tiles [tiles[k], tiles[k - 1]) have
 // the k longest requests.
-__device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, int idx, ApItem &it) {
+__device__ __forceinline__ void prompt_item(const ApSmem<false> &s, const ApArgs &p, int idx, ApItem &it) {
   const AttnArgs &a = p.a;
   const int e = at_idiv(idx, a.kv_heads);
   it.hk = idx - e * a.kv_heads;
@@ -197,7 +219,7 @@ __device__ __forceinline__ void prompt_item(const ApSmem &s, const ApArgs &p, in
 // The part of an item that starts at place x of the line of key tiles, up to
 // the end of the CTA's share; returns the place after it.  n = 0: the rows need
 // nothing of it (later tokens than theirs).
-__device__ __forceinline__ long long cache_part(const ApSmem &s, const ApArgs &p, long long x, const AtShare &share, ApItem &it) {
+__device__ __forceinline__ long long cache_part(const ApSmem<true> &s, const ApArgs &p, long long x, const AtShare &share, ApItem &it) {
   const AttnArgs &a = p.a;
   int lo = 0, hi = a.B - 1;                        // largest b with work[b] <= x
   while (lo < hi) {
@@ -283,17 +305,17 @@ __device__ __forceinline__ float ap_max(const float (&v)[128]) {
   return at_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
 }
 
-// TWINS: prompts whose items are one row tile each, over alternate key tiles.
-template <int D, bool F16, bool PAGED, bool TWINS>
+// TWINS: prompts whose items are one row tile each, over alternate key tiles.  LAT: keys of 192 elements (D = 128).
+template <int D, bool F16, bool PAGED, bool TWINS, bool LAT>
 __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_constant__ ApArgs p) {
   extern __shared__ uint8_t dsm[];
-  __shared__ ApSmem s;
-  using G = ApGeom<D>;
-  constexpr int kStages = G::kStages, kTB = G::kTileBytes, kHalves = D / 64;
+  __shared__ ApSmem<PAGED> s;
+  using G = typename ApGeomOf<D, LAT>::type;
+  constexpr int kStages = G::kStages, kTB = G::kTileBytes, kQT = G::kQTile, kHalves = D / 64, kQHalves = LAT ? 3 : kHalves;
   const AttnArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
-  const uint32_t q_smem = smem0, ring = smem0 + 2 * kTB;
+  const uint32_t q_smem = smem0, ring = smem0 + 2 * kQT;
   uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
 
   // the first lengths: on their way while the barriers are set up
@@ -332,6 +354,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.vmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
+    if (LAT) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.rmap)) : "memory");
   }
   if (warp == kApWMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
@@ -708,7 +731,38 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           else if (!PAGED) next = gridDim.x + atomicAdd(p.ctrl + kAttnCtrlNext, 1);
           // stage q: K[q] and V[q - ahead], as far as they are there
           const int n = it.n, ahead = (PAGED ? it.twin : TWINS) ? 2 : 1;
-          for (int q = 0; q < n + ahead; q++) {
+          if constexpr (LAT) {
+            // pieces in the order of their use: V[q - ahead], K[q]
+            auto take = [&](int z) {               // slot of piece pos + z, free
+              const int at = pos + z;
+              if (ok && at >= kStages) ok = wait(&s.kv_empty[at % kStages], (uint32_t)(at / kStages - 1) & 1u);
+              if (ok) mbar_arrive_expect_tx(&s.kv_full[at % kStages], (uint32_t)kApPiece + a.stall);
+              return at % kStages;
+            };
+            for (int q = 0; q < n + ahead && ok; q++) {
+              if (q >= ahead) {
+                const int s0 = take(0), s1 = take(1), j = q - ahead, row = it.first + j * kApTile;
+                if (!ok) break;
+                if (j >= it.m0) {                  // the scan may wait for these pieces now, as below
+                  s.v_pos[i & 1][j - it.m0] = pos;
+                  mbar_arrive(&s.v_posted[i & 1][j - it.m0]);
+                }
+                // elements 0 .. 63 lie in the lower slot
+                at_tma_3d(ring + min(s0, s1) * kApPiece, &p.vmap, 0, it.hk, row, &s.kv_full[min(s0, s1)]);
+                at_tma_3d(ring + max(s0, s1) * kApPiece, &p.vmap, 64, it.hk, row, &s.kv_full[max(s0, s1)]);
+                pos += 2;
+              }
+              if (q < n) {
+                const int row = it.first + q * kApTile;
+                for (int z = 0; z < 3; z++) {
+                  const int slot = take(0);
+                  if (!ok) break;
+                  at_tma_3d(ring + slot * kApPiece, z == 2 ? &p.rmap : &p.kmap, z == 2 ? 0 : 64 * z, z == 2 ? 0 : it.hk, row, &s.kv_full[slot]);
+                  pos++;
+                }
+              }
+            }
+          } else for (int q = 0; q < n + ahead; q++) {
             if (q >= n && q < ahead) continue;
             const int slot = pos % kStages;
             int page[2] = {0, 0};
@@ -771,7 +825,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       // one addition; one elected lane issues.
       constexpr uint32_t id_s = at_idesc(F16, kApTile, false), id_o = at_idesc(F16, D, true);
       const uint32_t tu = __shfl_sync(kFull, tb, 0);
-      const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring + kTB, kApTile * 128);
+      const uint64_t dq0 = at_desc(q_smem, 16), dk0 = at_desc(ring, 16), dv0 = at_desc(ring + (LAT ? 0 : kTB), kApTile * 128);
       int slot = 0;                                // next stage and its phase
       uint32_t phase = 0, clean = 0, np0 = 0, np1 = 0;   // clean: a phase bit per item parity and masked tile
       bool ok = true;
@@ -794,13 +848,34 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
       };
       auto issue_s = [&](int h, int q) {           // S of row tile h = Q of row tile q K: by the elected lane
-        const uint64_t da = dq0 + (uint64_t)(q * (kTB >> 4)), db = dk0 + (uint64_t)(slot * (2 * kTB >> 4));
+        const uint64_t da = dq0 + (uint64_t)(q * (kQT >> 4)), db = dk0 + (uint64_t)(slot * (2 * kTB >> 4));
 #pragma unroll
         for (int k = 0; k < D / 16; k++) {
           const uint32_t off = (uint32_t)((k >> 2) * (kApTile * 128) + (k & 3) * 32) >> 4;
           at_mma_ss(tu + 128u * h, da + off, db + off, id_s, k > 0);
         }
         at_commit(&s.s_full[h]);
+      };
+      uint32_t pos = 0;                            // latent: pieces so far
+      // Latent: S of row tile h from the pieces `at`, at + 1, at + 2, as they come; `last`: their last use
+      auto issue_s3 = [&](int h, int q, uint32_t at, bool last, bool q_last) {
+#pragma unroll 1
+        for (uint32_t z = 0; z < 3; z++) {
+          const uint32_t sl = (at + z) % kStages;
+          wait(&s.kv_full[sl], ((at + z) / kStages) & 1u);
+          at_fence_after();
+          if (at_elect() && ok) {
+            const uint64_t da = dq0 + (uint64_t)((q * kQT + (int)z * kApPiece) >> 4), db = dk0 + (uint64_t)((sl * kApPiece) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; k++) at_mma_ss(tu + 128u * h, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, z > 0 || k > 0);
+            if (last) at_commit(&s.kv_empty[sl]);
+            if (z == 2) {
+              at_commit(&s.s_full[h]);
+              if (q_last) at_commit(&s.q_empty);
+            }
+          }
+          if (!all_ok()) return;
+        }
       };
       for (int i = 0; ok; i++) {
         wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
@@ -813,63 +888,119 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const bool twin = PAGED ? __shfl_sync(kFull, im.twin, 0) : TWINS;
         const int ahead = twin ? 2 : 1;            // S of tile j + ahead follows PV of tile j
         wait(&s.q_full, (uint32_t)i & 1u);
-        for (int j = 0; j < ahead && j < n; j++) {
-          wait(&s.kv_full[slot], phase);
+        if constexpr (LAT) {
           if (!all_ok()) break;
-          at_fence_after();
-          if (at_elect()) {
+          for (int j = 0; j < ahead && j < n && ok; j++, pos += 3) {
+            const bool q_last = j + 1 == n;
             if (twin) {
-              issue_s(j, 0);
+              issue_s3(j, 0, pos, true, q_last);
             } else {
-              issue_s(0, 0);
-              if (n1 > 0) issue_s(1, 1);
+              issue_s3(0, 0, pos, n1 == 0, q_last && n1 == 0);
+              if (n1 > 0 && ok) issue_s3(1, 1, pos, true, q_last);
             }
-            at_commit(&s.kv_empty[slot]);
-            if (j + 1 == n) at_commit(&s.q_empty);
           }
-          __syncwarp();
-          next_stage();
-        }
-        for (int j = 0; j < n && ok; j++) {
-          wait(&s.kv_full[slot], phase);
-          if (j >= m0) {
-            const int z = j - m0, bit = 3 * (i & 1) + z;   // z: 0, 1 or 2
-            wait(&s.v_clean[i & 1][z], (clean >> bit) & 1u);
-            clean ^= 1u << bit;
-          }
-          const int left = end - j * kApTile;      // tokens of the tile that some row sees
-          const uint64_t db = dv0 + (uint64_t)(slot * (2 * kTB >> 4));
-          const uint32_t add = j >= ahead;
+          for (int j = 0; j < n && ok; j++) {
+            const uint32_t at = pos;               // V[j] at pieces `at`, at + 1, and K[j + ahead] behind it
+            const uint32_t s0 = at % kStages, s1 = (at + 1) % kStages, lo = min(s0, s1), hi = max(s0, s1);
+            wait(&s.kv_full[s0], (at / kStages) & 1u);
+            wait(&s.kv_full[s1], ((at + 1) / kStages) & 1u);
+            if (j >= m0) {
+              const int z = j - m0, bit = 3 * (i & 1) + z;   // z: 0, 1 or 2
+              wait(&s.v_clean[i & 1][z], (clean >> bit) & 1u);
+              clean ^= 1u << bit;
+            }
+            const int left = end - j * kApTile;    // tokens of the tile that some row sees
+            // the pair's second half of the elements is `hi - lo` slots on
+            const uint64_t db = at_desc(ring + lo * kApPiece, (hi - lo) * kApPiece);
+            const uint32_t add = j >= ahead;
+            pos += 2;
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const int nh = h ? n1 : n0;
-            if (twin ? (j & 1) == h : j < nh) {
-              uint32_t &np = h ? np1 : np0;
-              const bool more = twin ? j + 2 < n : j + 1 < nh;
-              wait(&s.p_full[h], np);
-              np ^= 1u;
-              at_fence_after();
-              if (at_elect() && ok) {
-                const uint32_t oc = tu + 256u + 128u * h, pc = tu + 128u * h;
-                if (left >= kApTile) {
-#pragma unroll
-                  for (int k = 0; k < kApTile / 16; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
-                } else {
+            for (int h = 0; h < 2; h++) {
+              const int nh = h ? n1 : n0;
+              if (twin ? (j & 1) == h : j < nh) {
+                uint32_t &np = h ? np1 : np0;
+                const bool more = twin ? j + 2 < n : j + 1 < nh, tail = twin || h || n1 == 0;   // the tile's last row tile
+                wait(&s.p_full[h], np);
+                np ^= 1u;
+                at_fence_after();
+                if (at_elect() && ok) {
+                  const uint32_t oc = tu + 256u + 128u * h, pc = tu + 128u * h;
 #pragma unroll 1
-                  for (int k = 0; 16 * k < left; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  for (int k = 0; k < kApTile / 16 && 16 * k < left; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  if (tail) {
+                    at_commit(&s.kv_empty[lo]);
+                    at_commit(&s.kv_empty[hi]);
+                  }
+                  if (!more) at_commit(&s.o_done[h]);
                 }
-                if (more) issue_s(h, twin ? 0 : h);
-                else at_commit(&s.o_done[h]);      // the row tile's last
-                if (twin || h || n1 == 0) {        // and the tile's last
-                  at_commit(&s.kv_empty[slot]);
-                  if (j + ahead + 1 == n) at_commit(&s.q_empty);
+                if (!all_ok()) break;
+                if (more) {
+                  issue_s3(h, twin ? 0 : h, pos, tail, tail && j + ahead + 1 == n);
+                  if (!ok) break;
                 }
               }
-              if (!all_ok()) break;
             }
+            if (j + ahead < n) pos += 3;
           }
-          if (!ok) break;
-          next_stage();
+        } else {
+          for (int j = 0; j < ahead && j < n; j++) {
+            wait(&s.kv_full[slot], phase);
+            if (!all_ok()) break;
+            at_fence_after();
+            if (at_elect()) {
+              if (twin) {
+                issue_s(j, 0);
+              } else {
+                issue_s(0, 0);
+                if (n1 > 0) issue_s(1, 1);
+              }
+              at_commit(&s.kv_empty[slot]);
+              if (j + 1 == n) at_commit(&s.q_empty);
+            }
+            __syncwarp();
+            next_stage();
+          }
+          for (int j = 0; j < n && ok; j++) {
+            wait(&s.kv_full[slot], phase);
+            if (j >= m0) {
+              const int z = j - m0, bit = 3 * (i & 1) + z;   // z: 0, 1 or 2
+              wait(&s.v_clean[i & 1][z], (clean >> bit) & 1u);
+              clean ^= 1u << bit;
+            }
+            const int left = end - j * kApTile;      // tokens of the tile that some row sees
+            const uint64_t db = dv0 + (uint64_t)(slot * (2 * kTB >> 4));
+            const uint32_t add = j >= ahead;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const int nh = h ? n1 : n0;
+              if (twin ? (j & 1) == h : j < nh) {
+                uint32_t &np = h ? np1 : np0;
+                const bool more = twin ? j + 2 < n : j + 1 < nh;
+                wait(&s.p_full[h], np);
+                np ^= 1u;
+                at_fence_after();
+                if (at_elect() && ok) {
+                  const uint32_t oc = tu + 256u + 128u * h, pc = tu + 128u * h;
+                  if (left >= kApTile) {
+#pragma unroll
+                    for (int k = 0; k < kApTile / 16; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  } else {
+#pragma unroll 1
+                    for (int k = 0; 16 * k < left; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  }
+                  if (more) issue_s(h, twin ? 0 : h);
+                  else at_commit(&s.o_done[h]);      // the row tile's last
+                  if (twin || h || n1 == 0) {        // and the tile's last
+                    at_commit(&s.kv_empty[slot]);
+                    if (j + ahead + 1 == n) at_commit(&s.q_empty);
+                  }
+                }
+                if (!all_ok()) break;
+              }
+            }
+            if (!ok) break;
+            next_stage();
+          }
         }
         if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
@@ -897,10 +1028,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         // others' or zeros, rows past the box what was there: none is stored
         if (ht == 0) {
           const int boxes = it.toks > p.per ? 2 : 1;
-          mbar_arrive_expect_tx(&s.q_full, (uint32_t)(boxes * p.per * a.group * D * 2));
+          mbar_arrive_expect_tx(&s.q_full, (uint32_t)(boxes * p.per * a.group * kQHalves * 128));
           for (int q = 0; q < boxes; q++)
-            for (int hf = 0; hf < kHalves; hf++)
-              at_tma_3d(q_smem + q * kTB + hf * (kApTile * 128), &p.qmap, 64 * hf, it.hk * a.group, it.first + it.tok0 + q * p.per,
+            for (int hf = 0; hf < kQHalves; hf++)
+              at_tma_3d(q_smem + q * kQT + hf * (kApTile * 128), &p.qmap, 64 * hf, it.hk * a.group, it.first + it.tok0 + q * p.per,
                         &s.q_full);
         }
         nq++;
@@ -912,17 +1043,26 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           const int pos = s.v_pos[i & 1][z], slot = pos % kStages;
           ok = at_wait(&s.kv_full[slot], (uint32_t)(pos / kStages) & 1u, a, p.ctrl);
           if (!ok) break;
+          int lo = 0, hi = 0;                      // latent: the slots of the tile's halves
+          if constexpr (LAT) {
+            const int next = (pos + 1) % kStages;
+            ok = at_wait(&s.kv_full[next], (uint32_t)((pos + 1) / kStages) & 1u, a, p.ctrl);
+            if (!ok) break;
+            lo = min(slot, next);
+            hi = max(slot, next);
+          }
           if (z == 0) posted[0] ^= 1u << (i & 1);
           else if (z == 1) posted[1] ^= 1u << (i & 1);
           else posted[2] ^= 1u << (i & 1);
-          uint8_t *tile = generic0 + 2 * kTB + (2 * slot + 1) * kTB;
+          uint8_t *tile = generic0 + 2 * kQT + (LAT ? lo * kApPiece : (2 * slot + 1) * kTB);
+          const int half = LAT ? (hi - lo) * kApPiece : kApTile * 128;
           // earlier tokens are seen by every row; PV leaves out the groups of 16 past the last one that is seen
           const int r0 = max(0, it.all - (it.j0 + j) * kApTile);
           const int r1 = min(kApTile, (it.end - (it.j0 + j) * kApTile + 15) & ~15);
           for (int hf = 0; hf < kHalves; hf++)
 #pragma unroll 4
             for (int e = r0 * 8 + ht; e < r1 * 8; e += 64) {
-              uint4 *at = reinterpret_cast<uint4 *>(tile + hf * (kApTile * 128)) + e;
+              uint4 *at = reinterpret_cast<uint4 *>(tile + hf * half) + e;
               const uint4 w = *at;
               const uint32_t f[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
               if (f[0] | f[1] | f[2] | f[3]) {
@@ -1038,8 +1178,12 @@ typedef void (*ApKernel)(const ApArgs);
 typedef void (*ApJoin)(const ApArgs, int);
 template <bool PAGED, bool TWINS>
 ApKernel ap_kernel(int head_dim, int f16) {
-  if (head_dim == 64) return f16 ? attn_wide_kernel<64, true, PAGED, TWINS> : attn_wide_kernel<64, false, PAGED, TWINS>;
-  return f16 ? attn_wide_kernel<128, true, PAGED, TWINS> : attn_wide_kernel<128, false, PAGED, TWINS>;
+  if (head_dim == 64) return f16 ? attn_wide_kernel<64, true, PAGED, TWINS, false> : attn_wide_kernel<64, false, PAGED, TWINS, false>;
+  return f16 ? attn_wide_kernel<128, true, PAGED, TWINS, false> : attn_wide_kernel<128, false, PAGED, TWINS, false>;
+}
+ApKernel ap_latent(bool twins, int f16) {
+  if (twins) return f16 ? attn_wide_kernel<128, true, false, true, true> : attn_wide_kernel<128, false, false, true, true>;
+  return f16 ? attn_wide_kernel<128, true, false, false, true> : attn_wide_kernel<128, false, false, false, true>;
 }
 ApJoin ap_join(int head_dim, int f16) {
   if (head_dim == 64) return f16 ? attn_join_kernel<64, true> : attn_join_kernel<64, false>;
@@ -1047,11 +1191,11 @@ ApJoin ap_join(int head_dim, int f16) {
 }
 int ap_smem(int head_dim) { return head_dim == 64 ? ApGeom<64>::kSmem : ApGeom<128>::kSmem; }
 
-// Packed rows [T][heads][D] in boxes of 64 elements x `heads_box` heads x `rows_box` rows.
-cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, int heads_box, int rows_box, const AttnArgs &a) {
+// Packed rows [T][heads][dim] in boxes of 64 elements x `heads_box` heads x `rows_box` rows.
+cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, int heads_box, int rows_box, int dim, const AttnArgs &a) {
   const AttnMapEncodeFn enc = attn_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)r.head * 2, (cuuint64_t)r.row * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows_box};
   const cuuint32_t estr[3] = {1, 1, 1};
@@ -1062,26 +1206,37 @@ cudaError_t encode_rows(CUtensorMap *map, const RowView &r, int T, int heads, in
 }
 
 // Row tiles of whole tokens, and their Q as boxes.
-cudaError_t encode_q(ApArgs *p) {
+cudaError_t encode_q(ApArgs *p, int dim) {
   const AttnArgs &a = p->a;
   p->magic = (65536 + a.group - 1) / a.group;
   p->per = kApTile / a.group;
-  return encode_rows(&p->qmap, a.q, a.T, a.q_heads, a.group, p->per, a);
+  return encode_rows(&p->qmap, a.q, a.T, a.q_heads, a.group, p->per, dim, a);
+}
+}  // namespace
+
+namespace {
+cudaError_t ap_setup(ApKernel k, int smem) {
+  cudaFuncAttributes at;
+  const cudaError_t err = cudaFuncGetAttributes(&at, k);
+  if (err != cudaSuccess) return err;
+  // the register shares of the warpgroups have to fit what the CTA is launched with
+  if (at.numRegs * kApThreads < kApRegsSoft * 256 + kApRegsRest * 128) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 }  // namespace
 
 cudaError_t attn_wide_setup(int head_dim, int f16) {
   const ApKernel kernels[3] = {ap_kernel<false, false>(head_dim, f16), ap_kernel<false, true>(head_dim, f16), ap_kernel<true, false>(head_dim, f16)};
   for (const ApKernel k : kernels) {
-    cudaFuncAttributes at;
-    cudaError_t err = cudaFuncGetAttributes(&at, k);
-    if (err != cudaSuccess) return err;
-    // the register shares of the warpgroups have to fit what the CTA is launched with
-    if (at.numRegs * kApThreads < kApRegsSoft * 256 + kApRegsRest * 128) return cudaErrorInvalidConfiguration;
-    err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ap_smem(head_dim));
+    const cudaError_t err = ap_setup(k, ap_smem(head_dim));
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
+}
+
+cudaError_t attn_wide_latent_setup(int f16) {
+  const cudaError_t err = ap_setup(ap_latent(false, f16), ApLatGeom::kSmem);
+  return err == cudaSuccess ? ap_setup(ap_latent(true, f16), ApLatGeom::kSmem) : err;
 }
 
 AttnWideWs attn_wide_ws(size_t off, int head_dim, int num_sms) {
@@ -1098,14 +1253,15 @@ AttnWideWs attn_wide_ws(size_t off, int head_dim, int num_sms) {
   return w;
 }
 
-cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaStream_t stream) {
+cudaError_t launch_attn_prompt(const AttnArgs &a, const RowView *k_rope, int *ctrl, int num_sms, cudaStream_t stream) {
   ApArgs p;
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.ctrl = ctrl;
-  cudaError_t err = encode_q(&p);
-  if (err == cudaSuccess) err = encode_rows(&p.kmap, a.k, a.T, a.kv_heads, 1, kApTile, a);
-  if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, 1, kApTile, a);
+  cudaError_t err = encode_q(&p, k_rope ? a.head_dim + 64 : a.head_dim);
+  if (err == cudaSuccess) err = encode_rows(&p.kmap, a.k, a.T, a.kv_heads, 1, kApTile, a.head_dim, a);
+  if (err == cudaSuccess) err = encode_rows(&p.vmap, a.v, a.T, a.kv_heads, 1, kApTile, a.head_dim, a);
+  if (err == cudaSuccess && k_rope) err = encode_rows(&p.rmap, *k_rope, a.T, 1, 1, kApTile, 64, a);
   if (err != cudaSuccess) return err;
   // Items at most: every request may end inside one.  Where row tiles are as few as
   // CTAs, an item is one row tile and the softmax warps of the other take every second
@@ -1115,7 +1271,9 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, int *ctrl, int num_sms, cudaSt
   p.span = items_of(p.per) <= num_sms ? p.per : 2 * p.per;
   const long long items = items_of(p.span);
   const int grid = (int)(items < num_sms ? items : num_sms);
-  (p.span == p.per ? ap_kernel<false, true> : ap_kernel<false, false>)(a.head_dim, a.f16)<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
+  const bool twins = p.span == p.per;
+  const ApKernel k = k_rope ? ap_latent(twins, a.f16) : (twins ? ap_kernel<false, true> : ap_kernel<false, false>)(a.head_dim, a.f16);
+  k<<<grid, kApThreads, k_rope ? ApLatGeom::kSmem : ap_smem(a.head_dim), stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1127,7 +1285,7 @@ cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWide
   p.desc = reinterpret_cast<int4 *>(ws + w.desc);
   p.stat = reinterpret_cast<float2 *>(ws + w.stat);
   p.part = reinterpret_cast<float4 *>(ws + w.part);
-  cudaError_t err = encode_q(&p);
+  cudaError_t err = encode_q(&p, a.head_dim);
   if (err == cudaSuccess) err = attn_encode_cache(&p.kmap, a.k_cache, a, 1 << a.page_shift);
   if (err == cudaSuccess) err = attn_encode_cache(&p.vmap, a.v_cache, a, 1 << a.page_shift);
   if (err != cudaSuccess) return err;

@@ -174,7 +174,8 @@ moe_status moe_latent_create(const moe_latent_config *cfg, int device, moe_laten
   DeviceGuard g(device);
   int sms = 0;
   if (!g.ok || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return MOE_ERR_CUDA;
-  if (lat_tree_setup(cfg->dtype == MOE_ATTN_F16) != cudaSuccess) return MOE_ERR_CUDA;
+  const int f16 = cfg->dtype == MOE_ATTN_F16;
+  if (lat_tree_setup(f16) != cudaSuccess || attn_wide_latent_setup(f16) != cudaSuccess) return MOE_ERR_CUDA;
   moe_latent *l = new (std::nothrow) moe_latent;
   if (!l) return MOE_ERR_OUT_OF_MEMORY;
   l->cfg = *cfg;
@@ -252,6 +253,37 @@ moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, co
   DeviceGuard g(lat->device);
   if (!g.ok) return MOE_ERR_CUDA;
   return cuda_status(launch_rope(&a, stream));
+}
+
+moe_status moe_latent_prompt(moe_latent_t lat, int num_requests, int num_rows, const moe_attn_rows *q, const moe_attn_rows *k,
+                             const moe_attn_rows *k_rope, const moe_attn_rows *v, const int32_t *cu, const moe_attn_rows *out,
+                             float *lse, void *ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!lat || !counts_ok(num_requests, num_rows)) return MOE_ERR_INVALID_ARG;
+  if (num_requests > MOE_ATTN_MAX_REQUESTS || num_rows > MOE_ATTN_MAX_ROWS) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (num_rows == 0 || num_requests == 0) return MOE_OK;
+  const LatArgs l = lat_args(*lat, num_requests, num_rows);
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  RowView r;
+  if (!row_view(q, num_rows, l.heads, kLatHead + kLatRope, &a.q) || !row_view(k, num_rows, l.heads, kLatHead, &a.k) ||
+      !row_view(k_rope, num_rows, 1, kLatRope, &r) || !row_view(v, num_rows, l.heads, kLatHead, &a.v) ||
+      !row_view(out, num_rows, l.heads, kLatHead, &a.out) || !words(cu) || !given(ws) || !lse_ok(lse))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < lat_ws(lat->num_sms).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  a.B = num_requests;
+  a.T = num_rows;
+  a.q_heads = a.kv_heads = l.heads;
+  a.group = 1;
+  a.head_dim = kLatHead;
+  a.f16 = l.f16;
+  a.scale = l.scale;
+  a.stall = l.stall;
+  a.wait_ns = l.wait_ns;
+  a.cu = cu;
+  a.lse = lse;
+  DeviceGuard g(lat->device);
+  if (!g.ok) return MOE_ERR_CUDA;
+  return cuda_status(launch_attn_prompt(a, &r, static_cast<int *>(ws), lat->num_sms, stream));
 }
 
 moe_status moe_latent_tree(moe_latent_t lat, int num_requests, int num_rows, const moe_attn_rows *q,

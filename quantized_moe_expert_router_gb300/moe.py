@@ -53,7 +53,7 @@ EXPORTED = (
     "moe_attn_prompt", "moe_attn_tree", "moe_attn_get_device_status",
     "moe_rope_create", "moe_rope_destroy", "moe_rope_frequencies", "moe_rope_apply", "moe_rope_append",
     "moe_latent_create", "moe_latent_destroy", "moe_latent_workspace_bytes", "moe_latent_get_device_status",
-    "moe_latent_plan", "moe_latent_append", "moe_latent_tree",
+    "moe_latent_plan", "moe_latent_append", "moe_latent_prompt", "moe_latent_tree",
     "moe_status_string",
 )
 
@@ -160,6 +160,7 @@ def load_library(path: str = LIB_PATH):
             lib.moe_latent_workspace_bytes.argtypes = [P, I32, I32, ctypes.POINTER(SZ)]
             lib.moe_latent_get_device_status.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_int32)]
             lib.moe_latent_tree.argtypes = [P, I32, I32, R, R, P, P, P, P, P, R, P, P, SZ, P]
+            lib.moe_latent_prompt.argtypes = [P, I32, I32, R, R, R, R, P, R, P, P, SZ, P]
             lib.moe_latent_plan.argtypes = lib.moe_kv_plan.argtypes
             lib.moe_latent_append.argtypes = [P, P, I32, P, P, R, R, R, R, P, P]
             lib.moe_status_string.argtypes = [I32]
@@ -782,6 +783,26 @@ def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_o
     status = _lib.moe_latent_append(
         lat.handle, rope.handle, T, positions.data_ptr(), slots.data_ptr(), _latent_row(fn, "c", lat, c, (T, LATENT_DIM)),
         _latent_row(fn, "k_rope", lat, k_rope, (T, LATENT_ROPE)), qv, qo, cache.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(fn, status)
+
+
+def moe_latent_prompt(lat, q, k, k_rope, v, cu, out, ws, lse=None, stream=None) -> None:
+    """Expanded causal attention over packed prompts: q [rows][heads][192], k, v,
+    out [rows][heads][128], k_rope [rows][64]; the rest as moe_attn_prompt."""
+    fn, dev, T, n, hq = "moe_latent_prompt", lat.device, q.shape[0], cu.numel(), lat.heads
+    ks = (T, hq, LATENT_HEAD)
+    if (cu.dtype is not torch.int32 or not cu.is_contiguous() or cu.get_device() != dev
+            or ws.get_device() != dev or not ws.is_contiguous()
+            or lse is not None and (lse.dtype is not torch.float32 or lse.numel() != T * hq or not lse.is_contiguous()
+                                    or lse.get_device() != dev)):
+        _attn_refuse(fn, dev, ("cu", cu, torch.int32, (n,)), ("lse", lse, torch.float32, (T, hq)))
+        _attn_ws(fn, dev, ws)
+    status = _lib.moe_latent_prompt(
+        lat.handle, n - 1, T, _attn_rows(fn, "q", lat, q, (T, hq, LATENT_HEAD + LATENT_ROPE)), _attn_rows(fn, "k", lat, k, ks),
+        _latent_row(fn, "k_rope", lat, k_rope, (T, LATENT_ROPE)), _attn_rows(fn, "v", lat, v, ks), cu.data_ptr(),
+        _attn_rows(fn, "out", lat, out, ks), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)
