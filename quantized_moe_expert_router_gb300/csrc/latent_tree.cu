@@ -2,32 +2,34 @@
 // tensor cores (moe_latent_tree): single tokens, drafted trees or the next part of a prompt.
 //
 // All heads of a token read the same cached vectors (c, r) of 512 + 64 elements, keys and
-// values at once, so a tile of 128 tokens comes once and serves up to 64 query rows (tokens x
+// values at once, so a tile of 64 tokens comes once and serves up to 64 query rows (tokens x
 // heads).  Query rows are the N of both products, tokens and latent elements the M:
-//   S^T = K Q^T                 M = 128 tokens, N rows, K = 576: A the tile as it lies, B = Q
+//   S^T = K Q^T                 M = 64 tokens, N rows, K = 576: A the tile as it lies, B = Q
 //   m' = max(m, max S);  P = 2^(c (S - m'));  l = l 2^(c (m - m')) + sum P,  c = softmax_scale * log2(e)
-//   O^T = O^T 2^(c (m - m')) + C^T P^T   M = 4 x 128 latent elements, N rows, K = 128 tokens: A the same tile
+//   O^T = O^T 2^(c (m - m')) + C^T P^T   M = 4 x 128 latent elements, N rows, K = 64 tokens: A the same tile
 //                               transposed (M-major), B = P^T
 // That way few rows cost little (N is 16, 32 or 64), the 512 x N fp32 of O^T fit tensor memory
-// with S^T beside them (5 N of 512 columns; rows as M would take 512 columns for O alone), and the tile is in
-// shared memory once.  The price: both products read A from shared memory at 4 KB a step of 16, so at
-// N = 64 they take 48 cycles a step and not 32.  The maximum of a row goes over tokens, which
-// are lanes; so the maximum that P is taken against moves only when some score passes it by 2^8
-// (in P's terms), one vote of the four warps a tile tells, and the sums stay per lane to the item's end.
-// P is rounded to the element type because the tensor cores multiply equal types; m, l and O are fp32, l
-// is summed from the unrounded values.
+// beside two S^T (6 N of 512 columns; rows as M would take 512 columns for O alone), and the tile is in
+// shared memory once.  The price: the products read A and B from shared memory at 128 bytes a cycle, which
+// bounds a step of 16 (measured: S 24, 25, 33 cycles at N = 16, 32, 64, O 39, 41, 49).
+// The maximum of a row goes over tokens, which are lanes; so the maximum that P is taken against moves only
+// when some score passes it by 2^8 (in P's terms), one vote of the four warps a tile tells, and the sums stay
+// per lane to the item's end.  P is rounded to the element type because the tensor cores multiply equal types; m, l
+// and O are fp32, l is summed from the unrounded values.
 //
 // An item is (request, whole tokens of it, a part of the heads): N rows at most.  More than 64
 // heads are two parts.  One CTA per SM, 12 warps:
-//   warp 0           tiles, 64 elements x a page a copy (128-byte swizzle): four pairs of 128 x 128 elements into a
-//                    ring of 4 or 5, then the key part; takes the items
-//   warp 1           MMA issue
+//   warp 0           tiles, 64 elements x a page a copy (128-byte swizzle): two halves of 64 x 256 elements into a
+//                    ring of 4 or 5, and with the second the key part into one of 2 or 3; takes the items
+//   warp 1           MMA issue: O of a tile when its P is there, else S of the next when that is
 //   warp 2           Q rows by boxes (64, heads, tokens)
-//   warps 4-7, 8-11  softmax of rows 0 .. N/2 - 1 and N/2 .. N - 1: a thread has a token, and the
-//                    N/2 rows in registers; the rescaling of O and the epilogue, a thread a latent element
-// A pair is free when the products of its 128 latent elements are done, so the next tile comes while
-// this one's values are multiplied.  With N = 64 shared memory is full: P lies where the key part was, which
-// is done when P is written.
+//   warps 4-7, 8-11  softmax of rows 0 .. N/2 - 1 and N/2 .. N - 1: a warp has 16 tokens, a thread two
+//                    of them and a quarter of the warp's rows (the fragment shape: an accumulator of 64 rows fills 16 of a
+//                    warp's 32 lanes); the rescaling of O and the epilogue, a thread a latent element
+// A half is free when the products of its latent elements are done, P lies where the tile's key part was.  With
+// N = 64 shared memory holds Q and two tiles, so that one comes while the other is worked on.  (One tile of 128 tokens
+// instead: S needs 17 % fewer cycles, but nothing comes between S and the values' products, and all SMs then
+// load and compute in step: 16 tokens at up to 100000 of 64 heads 204 us.)
 //
 // The tiles of all items stand in one line that the CTAs share (at_share); calls with two items
 // over the same tokens (two parts of the heads, or more tokens than a tile has room for) give each place of
@@ -40,11 +42,16 @@
 //
 // A wait knows its phase by parity alone, so no barrier may be two phases on when a waiter looks:
 //   sched_full    (item parity) item i + 2 is posted when sched_empty has all 10 arrivals of item i
-//   kv_full, r_full   filled again behind kv_empty, r_empty, which the MMA warp commits after its own wait and
-//                 behind p_full, which every softmax warp gives after its scan
-//   kv_empty, r_empty   waited for by the copy warp, whose lanes meet before they copy
+//   kv_full       filled again behind kv_empty, which the MMA warp commits behind the tile's p_full,
+//                 which every softmax warp gives after its scan.  The place of a second half is free only after that of
+//                 the key part that comes with it.
+//   kv_empty      waited for by the copy warp, whose lanes meet before they copy
 //   q_full        filled again behind q_empty; q_empty is waited for by warp 2 alone, and without that Q there is no next
-//   s_full, p_full, o_done   go to and fro between the MMA warp and the softmax warps
+//   s_full, p_full    (tile parity) S of tile t + 2 is issued after p_full of tile t has been waited for; P of tile t + 2
+//                 follows that S
+//   pv_done       (tile parity) S of tile t completes behind the products of tile t - 2, so a warp that has it
+//                 waits for the phase of tile t - 1, or having given P that of tile t, with the one before
+//                 on that barrier completed; the one after needs the P that it has not given
 // The softmax warps of a half also meet at a named barrier: a warp whose wait ran out goes on to
 // the next vote, which tells the others, and all four end together.
 #include <limits.h>
@@ -58,9 +65,9 @@
 namespace moe {
 
 constexpr int kLtThreads = 384;
-constexpr int kLtTile = 128;                      // tokens of a tile
+constexpr int kLtTile = 64;                       // tokens of a tile
 constexpr int kLtWTma = 0, kLtWMma = 1, kLtWQ = 2, kLtWSoft = 4;
-constexpr int kLtChunk = kLtTile * 128, kLtPair = 2 * kLtChunk;   // bytes of 64 and of 128 elements of a tile
+constexpr int kLtChunk = kLtTile * 128, kLtPair = 2 * kLtChunk, kLtHalf = 2 * kLtPair;   // bytes of 64, 128 and 256 elements of a tile
 constexpr int kLtBlocks = kLatDim / 128;          // of 128 latent elements
 constexpr int kLtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr int kLtMaxSms = 1024;
@@ -71,17 +78,16 @@ constexpr float kLtUnset = 1e30f;                 // in place of -c m before a r
 
 template <int N>
 struct LtGeom {
-  static constexpr bool kAlias = N == 64;         // P in the place of the key part
-  static constexpr int kPairs = N == 64 ? 4 : 5;
-  static constexpr int kRope = kPairs * kLtPair;
-  static constexpr int kP = kAlias ? kRope : kRope + kLtChunk;
-  static constexpr int kQ = kP + (kAlias ? kLtChunk : kLtTile * N * 2);
+  static constexpr int kHalves = N == 64 ? 4 : 5;
+  static constexpr int kParts = N == 64 ? 2 : 3;  // key parts
+  static constexpr int kRope = kHalves * kLtHalf; // a key part, then P in its place: 64 x 128 bytes, 64 x 2 N
+  static constexpr int kQ = kRope + kParts * kLtChunk;
   static constexpr int kQChunk = N * 128;         // 64 elements of the rows
   static constexpr int kSmem = kQ + 9 * kQChunk + 1024;
 };
 
 struct LtArgs {
-  CUtensorMap cmap;            // (64, page) boxes over [num_pages * page][576]
+  CUtensorMap cmap;            // (64, page or 64) boxes over [num_pages * page][576]
   CUtensorMap qmap, rmap;      // (64, hh, per) boxes over [T][heads][512] and [T][heads][64]
   LatArgs a;
   int *ctrl;
@@ -106,11 +112,11 @@ struct LtItem {
 
 struct LtSmem {
   uint64_t kv_full[5], kv_empty[5];
-  uint64_t r_full, r_empty, q_full, q_empty, s_full, p_full, o_done, sched_full[2], sched_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], sched_full[2], sched_empty[2], drain;
   uint32_t tmem;
   int fail[2];                 // the vote at which a wait was found to have run out
   LtItem item[2];
-  uint32_t bad[2][3][4];       // by item parity and masked tile: tokens with a non-finite latent
+  uint32_t bad[2][3][2];       // by item parity and masked tile: tokens with a non-finite latent
   float wmax[2][4][32], wsum[2][4][32];
   alignas(16) float mc[8][32]; // per softmax warp: -c m of its rows
   alignas(16) float f[8][32];  // and their factors
@@ -131,6 +137,15 @@ __device__ __forceinline__ bool lt_wait(uint64_t *bar, uint32_t parity, const Lt
   if (!ok && (threadIdx.x & 31) == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
   return ok;
 }
+// Whether the phase with `parity` is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
 // True in all of a half's 128 threads when it is in one of them.
 __device__ __forceinline__ bool lt_any(int half, bool x) {
   uint32_t r;
@@ -145,11 +160,6 @@ __device__ __forceinline__ bool lt_any(int half, bool x) {
 __device__ __forceinline__ void lt_sync(int half) {
   __syncwarp();
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + half) : "memory");
-}
-__device__ __forceinline__ float lt_redmax(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
 }
 // 8, 16 or 32 columns of this warp's 32 tensor-memory lanes.
 template <int C>
@@ -183,24 +193,23 @@ __device__ __forceinline__ void lt_st(uint32_t at, const float (&r)[C]) {
                  : "memory");
   }
 }
-// Sums over the warp's lanes of C values each: of value lane % C.
+// C / 2 columns of 16 of this warp's lanes as fragments: r[4 i + e] is column 8 i + 2 (lane & 3) + (e & 1) of row lane / 4 + 8 (e >> 1).
 template <int C>
-__device__ __forceinline__ float lt_lane_sums(float (&x)[C]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o >= C; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < C; i++) x[i] += __shfl_xor_sync(kFull, x[i], o);
-#pragma unroll
-  for (int o = C / 2; o >= 1; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; i++) {
-      const float got = __shfl_xor_sync(kFull, up ? x[i] : x[i + o], o);
-      x[i] = (up ? x[i + o] : x[i]) + got;
-    }
+__device__ __forceinline__ void lt_frag(uint32_t at, float (&r)[C / 2]) {
+  if constexpr (C == 32) {
+    at_ld_frag(at, r);
+  } else if constexpr (C == 16) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(at)
+                 : "memory");
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                 : "r"(at)
+                 : "memory");
   }
-  return x[0];
+  at_wait_ld(r);
 }
 
 // Descriptor of P^T: rows of tokens, 2 N bytes under the swizzle of that width (N-major); 8 rows apart.
@@ -214,8 +223,9 @@ template <int N>
 __device__ __forceinline__ int lt_p_at(int k, int c) {
   return k * 2 * N + ((N == 64 ? c ^ (k & 7) : (N == 32 ? c ^ ((k >> 1) & 3) : c ^ ((k >> 2) & 1))) << 4);
 }
-// Instruction descriptor: fp32 accumulator, M = 128, N rows; `at`: A is M-major, `bt`: B is N-major.
-__device__ __forceinline__ constexpr uint32_t lt_idesc(bool f16, int n, bool at, bool bt) { return at_idesc(f16, n, bt) | (at ? 1u << 15 : 0u); }
+// Instruction descriptors: S with M = 64 and both operands K-major, O with M = 128, A M-major and B N-major.
+__device__ __forceinline__ constexpr uint32_t lt_idesc_s(bool f16, int n) { return (at_idesc(f16, n, false) & ~(31u << 24)) | ((64u >> 4) << 24); }
+__device__ __forceinline__ constexpr uint32_t lt_idesc_o(bool f16, int n) { return at_idesc(f16, n, true) | (1u << 15); }
 
 // Of a request of n fresh rows: items of a place of the line, and tiles that its rows may see.
 __device__ __forceinline__ int lt_groups(const LtArgs &p, int n) { return p.hp * at_idiv(n + p.per - 1, p.per); }
@@ -295,32 +305,30 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
   extern __shared__ uint8_t dsm[];
   __shared__ LtSmem s;
   using G = LtGeom<N>;
-  constexpr int NP = G::kPairs, NC = N / 2;
+  constexpr uint32_t NH = G::kHalves, NR = G::kParts;
+  constexpr int NC = N / 2;
   const LatArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
   uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
 
   if (warp == 0) {
-    if (lane < NP) {
+    if (lane < (int)NH) {
       mbar_init(&s.kv_full[lane], 1);
       mbar_init(&s.kv_empty[lane], 1);
-    } else if (lane == 8) {
-      mbar_init(&s.r_full, 1);
-      mbar_init(&s.r_empty, 1);
-    } else if (lane == 9) {
+    } else if (lane >= 14 && lane < 16) {
+      mbar_init(&s.s_full[lane - 14], 1);
+      mbar_init(&s.p_full[lane - 14], 8);
+      mbar_init(&s.pv_done[lane - 14], 1);
+    } else if (lane >= 16 && lane < 18) {
+      mbar_init(&s.sched_full[lane - 16], 1);
+      mbar_init(&s.sched_empty[lane - 16], 10);    // 8 softmax warps, MMA warp, Q warp
+      s.fail[lane - 16] = INT_MAX;
+    } else if (lane == 18) {
       mbar_init(&s.q_full, 1);
       mbar_init(&s.q_empty, 1);
-    } else if (lane == 10) {
-      mbar_init(&s.s_full, 1);
-      mbar_init(&s.p_full, 8);
-    } else if (lane == 11) {
-      mbar_init(&s.o_done, 1);
+    } else if (lane == 19) {
       mbar_init(&s.drain, 1);
-    } else if (lane < 14 && lane >= 12) {
-      mbar_init(&s.sched_full[lane - 12], 1);
-      mbar_init(&s.sched_empty[lane - 12], 10);    // 8 softmax warps, MMA warp, Q warp
-      s.fail[lane - 12] = INT_MAX;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -382,12 +390,22 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       __syncthreads();
     }
     const int grid = p.gang == 2 ? (int)gridDim.x >> 1 : (int)gridDim.x, me = p.gang == 2 ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
-    // A part costs its CTA an epilogue and the join a source, some two tiles' time: equal parts may be longer than
-    // the mean by that, and by a sixteenth.
-    const long long mean = at_div(total + grid - 1, grid);
-    share = at_share<kLtThreads / 32>(
-        u.work, a.B, total, nitems, kLtMinTiles, u.cand, [&](int b) { return lt_items(p, u.n[b]); },
-        [&](int b) { return lt_nch(a, u.n[b], u.cached[b]); }, grid, me, 2 + (mean >> 4));
+    if (total <= grid) {                           // a tile a CTA: the line as it is
+      share.me = me;
+      share.len = share.c0 = share.c1 = 0;
+      share.ctas = (int)total;
+      share.per = 1;
+      share.rem = 0;
+      share.x0 = min((long long)me, total);
+      share.x1 = min((long long)me + 1, total);
+    } else {
+      // A part costs its CTA an epilogue and the join a source, some two tiles' time: equal parts may be longer than
+      // the mean by that, and by a sixteenth.
+      const long long mean = at_div(total + grid - 1, grid);
+      share = at_share<kLtThreads / 32>(
+          u.work, a.B, total, nitems, kLtMinTiles, u.cand, [&](int b) { return lt_items(p, u.n[b]); },
+          [&](int b) { return lt_nch(a, u.n[b], u.cached[b]); }, grid, me, 2 + (mean >> 4));
+    }
     int lo = 0, hi = a.B - 1;                      // largest b with work[b] <= x0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -412,12 +430,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
 
   if (warp >= kLtWSoft) {
     // ------------------------------------------------------------ softmax
-    const int h = (warp - kLtWSoft) >> 2, w4 = warp & 3, kt = 32 * w4 + lane;   // token of the tile; latent element of a block
+    const int h = (warp - kLtWSoft) >> 2, w4 = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * w4) << 16;
     const uint32_t ts = tb + lanes + 4u * N + (uint32_t)(h * NC), to = tb + lanes + (uint32_t)(h * NC);
     float *const mcw = s.mc[warp - kLtWSoft], *const fw = s.f[warp - kLtWSoft];
     const int cl = lane & (NC - 1), rl = h * NC + cl;                           // the row whose maximum the lane keeps
-    uint32_t ns = 0, ni = 0;                       // tiles and items so far
+    const int kt = 16 * w4 + (lane >> 2), qc = 2 * (lane & 3);                  // first of the thread's tokens of a tile; first of its rows of 8
+    uint32_t ns = 0;                               // tiles so far
     int nv = 0;                                    // votes so far
     bool ok = true;
     // 0: nobody says yes; 1: somebody does; 2: a wait has run out, all four warps end here
@@ -437,48 +456,55 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       const int tl_l = (rl * p.magic) >> 16, head_l = it.hpart * p.hh + rl - tl_l * p.hh;
       const bool valid_l = rl < rows && head_l < a.heads;
       float m_l = -INFINITY;                       // the maximum that P is taken against
-      float l[NC];
+      float l[NC / 4];
 #pragma unroll
-      for (int n = 0; n < NC; n++) l[n] = 0.f;
+      for (int n = 0; n < NC / 4; n++) l[n] = 0.f;
       if (lane < NC) mcw[lane] = valid_l ? kLtUnset : -kLtUnset;   // rows of no token have no say
       __syncwarp();
       bool dead = false;
       for (int j = 0; j < it.n; j++, ns++) {
-        const int tok = (it.j0 + j) * kLtTile + kt, col = tok >> a.page_shift;
+        const int tile0 = (it.j0 + j) * kLtTile, col = (tile0 + 16 * w4) >> a.page_shift;   // the warp's tokens are of one page
         const int id = col < a.max_pages ? __ldg(a.block_table + (size_t)it.b * a.max_pages + col) : -1;
         const bool held = (unsigned)id < (unsigned)a.num_pages;
-        const bool masked = j >= it.m0 || __any_sync(kFull, !held);
-        ok = lt_wait(&s.s_full, ns & 1u, p);
+        const uint32_t sb = ts + (ns & 1u) * N;
+        ok = lt_wait(&s.s_full[ns & 1u], (ns >> 1) & 1u, p);
         at_fence_after();
-        float v[NC];
-        lt_ld(ts, v);
-        if (masked) {
-          // rows that see this token: those of whole tokens
-          uint64_t sees = 0;
-          if (held && tok < it.end) {
-            const uint64_t ones = p.hh == 64 ? ~0ull : (1ull << p.hh) - 1ull;
-            const int f = tok - it.cached;
-            if (f < 0) {
-              sees = ~0ull;
-            } else if (a.tree_mask) {
-              for (int t = 0; t < it.toks; t++)
-                if (f < 64 && (__ldg(a.tree_mask + it.first + it.tok0 + t) >> f) & 1ull) sees |= ones << (t * p.hh);
-            } else {
-              const int t0 = max(0, f - it.tok0);  // rows from this token on
-              sees = t0 * p.hh >= 64 ? 0ull : ~0ull << (t0 * p.hh);
-            }
-          }
-          sees >>= h * NC;
+        float v[NC / 2];
+        lt_frag<NC>(sb, v);
+        uint32_t seen[2] = {~0u, ~0u};             // rows that see the thread's tokens
+        auto hide = [&]() {
 #pragma unroll
-          for (int n = 0; n < NC; n++) v[n] = (uint32_t)(sees >> n) & 1u ? v[n] : -INFINITY;
-          // the products take tokens in groups of 16, up to the last that some row sees
+          for (int n = 0; n < NC / 2; n++) v[n] = (seen[(n >> 1) & 1] >> (8 * (n >> 2) + qc + (n & 1))) & 1u ? v[n] : -INFINITY;
+        };
+        const bool masked = j >= it.m0 || !held;
+        if (masked) {
+          const uint64_t ones = p.hh == 64 ? ~0ull : (1ull << p.hh) - 1ull;
+#pragma unroll
+          for (int z = 0; z < 2; z++) {
+            const int tok = tile0 + kt + 8 * z, f = tok - it.cached;
+            uint64_t sees = 0;                     // whole tokens' rows
+            if (held && tok < it.end) {
+              if (f < 0) {
+                sees = ~0ull;
+              } else if (a.tree_mask) {
+                for (int t = 0; t < it.toks; t++)
+                  if (f < 64 && (__ldg(a.tree_mask + it.first + it.tok0 + t) >> f) & 1ull) sees |= ones << (t * p.hh);
+              } else {
+                const int t0 = max(0, f - it.tok0);                            // rows from this token on
+                sees = t0 * p.hh >= 64 ? 0ull : ~0ull << (t0 * p.hh);
+              }
+            }
+            seen[z] = (uint32_t)(sees >> (h * NC));
+          }
+          hide();
+          // the products take tokens in groups of 16, up to the last that some row sees; a thread a token and a pair
+          const int st = tid - 32 * kLtWSoft, t = st & 63, tok = tile0 + t;
           if (ok && j >= it.m0 && tok >= it.all && tok < ((it.end + 15) & ~15)) {
-            const uint32_t pos = 4u * ns + 2u * (uint32_t)h;
-            for (uint32_t q = pos; q < pos + 2; q++) {                         // half of the pairs each
-              const uint32_t slot = q % NP;
-              if (!mbar_try_wait(&s.kv_full[slot], (q / NP) & 1u)) continue;   // has completed: S needed it; orders the copies before the loads
+            const uint32_t pair = (uint32_t)(st >> 6), pos = 2u * ns + (pair >> 1), slot = pos % NH;
+            uint8_t *const from = generic0 + slot * kLtHalf + (pair & 1u) * kLtPair + t * 128;
+            if (mbar_try_wait(&s.kv_full[slot], (pos / NH) & 1u)) {            // has completed: S needed it; orders the copies before the loads
               for (int e = 0; e < 16; e++) {
-                uint4 *at = reinterpret_cast<uint4 *>(generic0 + slot * kLtPair + (e >> 3) * kLtChunk + kt * 128 + ((e & 7) ^ (kt & 7)) * 16);
+                uint4 *at = reinterpret_cast<uint4 *>(from + (e >> 3) * kLtChunk + ((e & 7) ^ (t & 7)) * 16);
                 const uint4 w = *at;
                 const uint32_t g[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
                 if (g[0] | g[1] | g[2] | g[3]) {
@@ -486,36 +512,47 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
 #pragma unroll
                   for (int z = 0; z < 4; z++) u[z] &= ~(((g[z] >> 15) & 0x00010001u) * 0xFFFFu);
                   *at = make_uint4(u[0], u[1], u[2], u[3]);
-                  atomicOr(&s.bad[i & 1][j - it.m0][kt >> 5], 1u << (kt & 31));
+                  atomicOr(&s.bad[i & 1][j - it.m0][t >> 5], 1u << (t & 31));
                 }
               }
             }
           }
           __syncwarp();
         }
-        const float2 c2 = make_float2(c, c);
-        float top = -INFINITY;
+        // v becomes c v - c m, the arguments of the exponentials
+        auto arguments = [&]() {
+          const float2 c2 = make_float2(c, c);
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 0; n < NC; n += 4) {
-          const float4 mc = *reinterpret_cast<const float4 *>(mcw + n);
-          const float2 t0 = ffma2(make_float2(v[n], v[n + 1]), c2, make_float2(mc.x, mc.y));
-          const float2 t1 = ffma2(make_float2(v[n + 2], v[n + 3]), c2, make_float2(mc.z, mc.w));
-          top = at_max3(top, t0.x, t0.y);
-          top = at_max3(top, t1.x, t1.y);
-        }
-        const int moved = vote(top > kLtSlack);
+          for (int n = 0; n < NC / 8; n++) {
+            const float2 mc = *reinterpret_cast<const float2 *>(mcw + 8 * n + qc);
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+              const float2 t = ffma2(make_float2(v[4 * n + 2 * z], v[4 * n + 2 * z + 1]), c2, mc);
+              v[4 * n + 2 * z] = t.x;
+              v[4 * n + 2 * z + 1] = t.y;
+              top[z] = at_max3(top[z], t.x, t.y);
+            }
+          }
+          return fmaxf(top[0], top[1]);
+        };
+        const int moved = vote(arguments() > kLtSlack);
         if (moved == 2) {
           dead = true;
           break;
         }
         if (moved) {
-          float mine = -INFINITY;
+          lt_frag<NC>(sb, v);                      // the scores again
+          hide();
 #pragma unroll
-          for (int n = 0; n < NC; n++) {
-            const float r = lt_redmax(v[n]);
-            if (cl == n) mine = r;
-          }
-          if (lane < NC) s.wmax[h][w4][lane] = mine;
+          for (int n = 0; n < NC / 8; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              float x = fmaxf(v[4 * n + e], v[4 * n + 2 + e]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+              if (lane < 4) s.wmax[h][w4][8 * n + qc + e] = x;
+            }
           lt_sync(h);
           const float m1 = fmaxf(fmaxf(m_l, fmaxf(s.wmax[h][0][cl], s.wmax[h][1][cl])), fmaxf(s.wmax[h][2][cl], s.wmax[h][3][cl]));
           const float f = m1 == m_l || m_l == -INFINITY || !valid_l ? 1.f : at_exp2((m_l - m1) * c);
@@ -526,9 +563,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
           }
           __syncwarp();
 #pragma unroll
-          for (int n = 0; n < NC; n++) l[n] *= fw[n];
+          for (int n = 0; n < NC / 4; n++) l[n] *= fw[8 * (n >> 1) + qc + (n & 1)];
           if (j > 0) {
-            // the products of the tile before are done: S of this one was issued behind them
+            ok = lt_wait(&s.pv_done[(ns - 1) & 1u], ((ns - 1) >> 1) & 1u, p) && ok;   // the products of the tile before
+            at_fence_after();
 #pragma unroll 1
             for (int b = 0; b < kLtBlocks; b++) {
               float o[NC];
@@ -539,42 +577,36 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
             }
             at_wait_st();
           }
+          arguments();
         }
-        uint8_t *const prow = generic0 + G::kP;
+        uint8_t *const pt = generic0 + G::kRope + (ns % NR) * kLtChunk + 2 * qc;
 #pragma unroll
-        for (int n = 0; n < NC; n += 8) {
-          uint32_t pk[4];
+        for (int n = 0; n < NC / 2; n++) v[n] = at_exp2(v[n]);
 #pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 mc = *reinterpret_cast<const float4 *>(mcw + n + e);
-            float2 t0 = ffma2(make_float2(v[n + e], v[n + e + 1]), c2, make_float2(mc.x, mc.y));
-            float2 t1 = ffma2(make_float2(v[n + e + 2], v[n + e + 3]), c2, make_float2(mc.z, mc.w));
-            t0.x = at_exp2(t0.x);
-            t0.y = at_exp2(t0.y);
-            t1.x = at_exp2(t1.x);
-            t1.y = at_exp2(t1.y);
-            l[n + e] += t0.x;
-            l[n + e + 1] += t0.y;
-            l[n + e + 2] += t1.x;
-            l[n + e + 3] += t1.y;
-            pk[e / 2] = at_pack<F16>(t0.x, t0.y);
-            pk[e / 2 + 1] = at_pack<F16>(t1.x, t1.y);
-          }
-          *reinterpret_cast<uint4 *>(prow + lt_p_at<N>(kt, h * (NC / 8) + n / 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
+        for (int n = 0; n < NC / 8; n++)
+#pragma unroll
+          for (int z = 0; z < 2; z++)
+            *reinterpret_cast<uint32_t *>(pt + lt_p_at<N>(kt + 8 * z, h * (NC / 8) + n)) = at_pack<F16>(v[4 * n + 2 * z], v[4 * n + 2 * z + 1]);
         at_fence_async();
         at_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full);
+        if (lane == 0) mbar_arrive(&s.p_full[ns & 1u]);
+        // beside the products
+#pragma unroll
+        for (int n = 0; n < NC / 4; n++) l[n] += v[4 * (n >> 1) + (n & 1)] + v[4 * (n >> 1) + 2 + (n & 1)];
       }
       if (dead) break;
       // -------------------------------------------------------------- epilogue
-      {
-        const float sum = lt_lane_sums(l);
-        if (lane < NC) s.wsum[h][w4][lane] = sum;
+#pragma unroll
+      for (int n = 0; n < NC / 4; n++) {
+        float x = l[n];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (lane < 4) s.wsum[h][w4][8 * (n >> 1) + qc + (n & 1)] = x;
       }
-      ok = lt_wait(&s.o_done, ni++ & 1u, p);
+      ok = lt_wait(&s.pv_done[(ns - 1) & 1u], ((ns - 1) >> 1) & 1u, p);
       if (vote(false) == 2) break;
+      const int el = 32 * w4 + lane;               // latent element of a block
       at_fence_after();
       const float l_l = (s.wsum[h][0][cl] + s.wsum[h][1][cl]) + (s.wsum[h][2][cl] + s.wsum[h][3][cl]);
       if (w4 == 0 && lane < NC && valid_l) {
@@ -584,21 +616,21 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       if (lane < NC) fw[lane] = l_l == 0.f ? 0.f : 1.f / l_l;
       __syncwarp();
       uint32_t anybad = 0;
-      const int wend = min(12, 4 * (it.n - it.m0));
+      const int wend = min(6, 2 * (it.n - it.m0));
 #pragma unroll
-      for (int w = 0; w < 12; w++)
-        if (w < wend) anybad |= s.bad[i & 1][w >> 2][w & 3];
+      for (int w = 0; w < 6; w++)
+        if (w < wend) anybad |= s.bad[i & 1][w >> 1][w & 1];
 #pragma unroll 1
       for (int b = 0; b < kLtBlocks; b++) {
         float o[NC];
         lt_ld(to + (uint32_t)(b * N), o);
         if (anybad) {
           for (int w = 0; w < wend; w++)
-            for (uint32_t bits = s.bad[i & 1][w >> 2][w & 3]; bits; bits &= bits - 1) {
+            for (uint32_t bits = s.bad[i & 1][w >> 1][w & 1]; bits; bits &= bits - 1) {
               const int tok = (it.j0 + it.m0) * kLtTile + 32 * w + __ffs(bits) - 1, f = tok - it.cached;
               if (tok >= it.end) continue;
               const long long page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (tok >> a.page_shift));
-              const long long at = ((page << a.page_shift) + (tok & ((1 << a.page_shift) - 1))) * kLatRow + 128 * b + kt;
+              const long long at = ((page << a.page_shift) + (tok & ((1 << a.page_shift) - 1))) * kLatRow + 128 * b + el;
               if (isfinite(at_value<F16>(__ldg(a.cache + at)))) continue;
 #pragma unroll
               for (int n = 0; n < NC; n++) {
@@ -612,7 +644,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
           __syncwarp();
         }
         if (it.slot >= 0) {
-          float *part = p.part + ((size_t)it.slot * N + h * NC) * kLatDim + 128 * b + kt;
+          float *part = p.part + ((size_t)it.slot * N + h * NC) * kLatDim + 128 * b + el;
 #pragma unroll
           for (int n = 0; n < NC; n++)
             if (h * NC + n < rows) part[(size_t)n * kLatDim] = o[n];
@@ -626,7 +658,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
             const int r = h * NC + n + (lane & 1), tl = (r * p.magic) >> 16, head = it.hpart * p.hh + r - tl * p.hh;
             if (r < rows && head < a.heads)
               *reinterpret_cast<uint32_t *>(a.out.p + (long long)(it.first + it.tok0 + tl) * a.out.row + (long long)head * a.out.head + 128 * b +
-                                            (kt & ~1)) = w;
+                                            (el & ~1)) = w;
           }
           __syncwarp();
         }
@@ -637,8 +669,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     }
   } else if (warp == kLtWTma) {
     // ---------------------------------------------------------- items and tiles
-    const int np = kLtTile >> a.page_shift, pg = lane & (np - 1), part = lane >> (7 - a.page_shift);
-    uint32_t pos = 0, tiles = 0;                   // pairs and tiles so far
+    const int box = min(a.page_shift, 6), np = kLtTile >> box, pg = lane & (np - 1), part = lane >> (6 - box);   // copies of 2^box tokens, 64 elements
+    const uint32_t place = (uint32_t)pg << (box + 7);
+    uint32_t pos = 0, tiles = 0;                   // halves and tiles so far
     long long next = share.x0;
     bool ok = true;
     for (int i = 0; ok; i++) {
@@ -650,7 +683,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
         it.b = -1;
       }
       if (i >= 2 && !lt_wait(&s.sched_empty[i & 1], (uint32_t)((i >> 1) - 1) & 1u, p)) break;
-      if (lane < 12) s.bad[i & 1][lane >> 2][lane & 3] = 0u;
+      if (lane < 6) s.bad[i & 1][lane >> 1][lane & 1] = 0u;
       __syncwarp();
       if (lane == 0) {
         s.item[i & 1] = it;
@@ -658,52 +691,115 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       }
       if (it.b < 0) break;
       const int32_t *table = a.block_table + (size_t)it.b * a.max_pages;
-      auto page_row = [&](int j) {                 // the cache row of the lane's page; past the end: reads zeros
-        const int col = (((it.j0 + j) * kLtTile) >> a.page_shift) + pg;
+      auto page_row = [&](int j) {                 // the cache row of the lane's copy; past the end: reads zeros
+        const int tok = (it.j0 + j) * kLtTile + (pg << box), col = tok >> a.page_shift;
         const int id = col < a.max_pages ? __ldg(table + col) : -1;
-        return ((unsigned)id < (unsigned)a.num_pages ? id : a.num_pages) << a.page_shift;
+        return (unsigned)id < (unsigned)a.num_pages ? (id << a.page_shift) + (tok & ((1 << a.page_shift) - 1)) : a.num_pages << a.page_shift;
       };
       int row = page_row(0);
       for (int j = 0; j < it.n && ok; j++, tiles++) {
         const int ahead = j + 1 < it.n ? page_row(j + 1) : 0;
-        for (int b = 0; b < kLtBlocks; b++, pos++) {
-          const uint32_t slot = pos % NP;
-          if (pos >= NP) ok = lt_wait(&s.kv_empty[slot], (pos / NP - 1) & 1u, p);
+        for (int z = 0; z < 2; z++, pos++) {
+          const uint32_t slot = pos % NH, to = smem0 + slot * kLtHalf + place;
+          if (pos >= NH) ok = lt_wait(&s.kv_empty[slot], (pos / NH - 1) & 1u, p);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)kLtPair + a.stall);
+          if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], (uint32_t)(kLtHalf + (z ? kLtChunk : 0)) + a.stall);
           __syncwarp();
-          if (part < 2)
-            lt_tma_2d(smem0 + slot * kLtPair + (uint32_t)(part * kLtChunk) + ((uint32_t)pg << (a.page_shift + 7)), &p.cmap,
-                      128 * b + 64 * part, row, &s.kv_full[slot]);
+          for (int e = part; e < 4 + z; e += 32 >> (6 - box))   // the second half's fifth is the key part
+            lt_tma_2d(e < 4 ? to + (uint32_t)(e * kLtChunk) : smem0 + G::kRope + (tiles % NR) * kLtChunk + place, &p.cmap, 256 * z + 64 * e, row,
+                      &s.kv_full[slot]);
         }
         if (!ok) break;
-        if (tiles > 0) ok = lt_wait(&s.r_empty, (tiles - 1) & 1u, p);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&s.r_full, (uint32_t)kLtChunk + a.stall);
-        __syncwarp();
-        if (part == 0) lt_tma_2d(smem0 + G::kRope + ((uint32_t)pg << (a.page_shift + 7)), &p.cmap, kLatDim, row, &s.r_full);
         row = ahead;
       }
     }
     // copies in flight land before the CTA ends; nothing else may pass these barriers now
-    for (uint32_t q = pos > NP ? pos - NP : 0; q < pos; q++) mbar_wait_bounded(&s.kv_full[q % NP], (q / NP) & 1u, a.wait_ns);
-    if (tiles > 0) mbar_wait_bounded(&s.r_full, (tiles - 1) & 1u, a.wait_ns);
+    for (uint32_t q = pos > NH ? pos - NH : 0; q < pos; q++) mbar_wait_bounded(&s.kv_full[q % NH], (q / NH) & 1u, a.wait_ns);
     __syncwarp();
   } else if (warp == kLtWMma) {
     // ---------------------------------------------------------- MMA issue
     // The whole warp goes through the loop, so that descriptors stay in uniform registers; one elected lane issues.
-    constexpr uint32_t id_s = lt_idesc(F16, N, false, false), id_o = lt_idesc(F16, N, true, true);
+    constexpr uint32_t id_s = lt_idesc_s(F16, N), id_o = lt_idesc_o(F16, N);
     const uint32_t tu = __shfl_sync(kFull, tb, 0), ds = tu + 4u * N;
-    const uint64_t dq0 = at_desc(smem0 + G::kQ, 16), dr = at_desc(smem0 + G::kRope, 16), dk0 = at_desc(smem0, 16);
-    const uint64_t dv0 = at_desc(smem0, kLtChunk), dp0 = lt_desc_p<N>(smem0 + G::kP);
-    uint32_t pos = 0, tiles = 0;
+    const uint64_t dq0 = at_desc(smem0 + G::kQ, 16), dr0 = at_desc(smem0 + G::kRope, 16), dk0 = at_desc(smem0, 16);
+    const uint64_t dv0 = at_desc(smem0, kLtChunk), dp0 = lt_desc_p<N>(smem0 + G::kRope);
+    // of the tile whose S comes next: its next half's slot and phase, its key part's slot, its own parity; whether its first
+    // half is issued
+    uint32_t ks = 0, kph = 0, rs = 0, sp = 0, half = 0;
+    // of the tile whose O comes next: its first half's slot, its key part's, its parity and phase
+    uint32_t os = 0, ors = 0, op = 0, oph = 0;
     bool ok = true;
+    // the lanes go on or end together
+    auto over = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, mbar_test(bar, parity)); };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      if (ok && !mbar_wait_bounded(bar, parity, a.wait_ns)) {
-        atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-        ok = false;
+      ok = __all_sync(kFull, ok && mbar_wait_bounded(bar, parity, a.wait_ns));
+      if (!ok && lane == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+    };
+    // A half of S, and the key part with the second.
+    auto issue_s = [&](bool last) {
+      // from lane 0, so that they are known to be the same in all lanes
+      const uint32_t slot = __shfl_sync(kFull, ks, 0), second = __shfl_sync(kFull, half, 0);
+      const uint32_t part = __shfl_sync(kFull, rs, 0), d = ds + __shfl_sync(kFull, sp, 0) * N;
+      at_fence_after();
+      if (at_elect()) {
+        uint64_t da = dk0 + (uint64_t)(slot * (kLtHalf >> 4)), db = dq0 + (uint64_t)(second * (4 * G::kQChunk >> 4));
+        uint32_t acc = second;
+#pragma unroll 1
+        for (int z = 0; z < 4; z++) {
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            at_mma_ss(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, acc);
+            acc = 1u;
+          }
+          da += (uint64_t)(kLtChunk >> 4);
+          db += (uint64_t)(G::kQChunk >> 4);
+        }
+        if (second) {
+          const uint64_t dr = dr0 + (uint64_t)(part * (kLtChunk >> 4));
+#pragma unroll
+          for (int k = 0; k < 4; k++) at_mma_ss(d, dr + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, 1u);
+          at_commit(&s.s_full[sp]);
+          if (last) at_commit(&s.q_empty);
+        }
       }
-      ok = __all_sync(kFull, ok);
+      __syncwarp();
+      if (++ks == NH) {
+        ks = 0;
+        kph ^= 1u;
+      }
+      if (half) {
+        rs = rs + 1 == NR ? 0 : rs + 1;
+        sp ^= 1u;
+      }
+      half ^= 1u;
+    };
+    // O of a tile with `left` tokens up to the last that some row sees: groups of 16 past it are left out
+    auto issue_o = [&](int left0, uint32_t add0) {
+      const int left = __shfl_sync(kFull, left0, 0);
+      const uint32_t add = __shfl_sync(kFull, add0, 0), part = __shfl_sync(kFull, ors, 0), slot0 = __shfl_sync(kFull, os, 0);
+      at_fence_after();
+      if (at_elect()) {
+        const uint64_t dp = dp0 + (uint64_t)(part * (kLtChunk >> 4));
+        const int steps = left >= kLtTile ? kLtTile / 16 : (left + 15) >> 4;
+        uint32_t sl = slot0;
+#pragma unroll 1
+        for (int b = 0; b < kLtBlocks; b++) {
+          const uint64_t da = dv0 + (uint64_t)(sl * (kLtHalf >> 4) + (b & 1) * (kLtPair >> 4));
+#pragma unroll
+          for (int k = 0; k < kLtTile / 16; k++)
+            if (k < steps) at_mma_ss(tu + (uint32_t)(b * N), da + (uint64_t)(128u * k), dp + (uint64_t)(2u * N * k), id_o, k > 0 ? 1u : add);
+          if (b & 1) {
+            at_commit(&s.kv_empty[sl]);
+            sl = sl + 1 == NH ? 0 : sl + 1;
+          }
+        }
+        at_commit(&s.pv_done[op]);
+      }
+      __syncwarp();
+      os = os + 2 >= NH ? os + 2 - NH : os + 2;
+      ors = ors + 1 == NR ? 0 : ors + 1;
+      oph ^= op;
+      op ^= 1u;
     };
     for (int i = 0; ok; i++) {
       wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
@@ -712,53 +808,29 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       if (__shfl_sync(kFull, im.b, 0) < 0) break;
       const int n = __shfl_sync(kFull, im.n, 0), end = __shfl_sync(kFull, im.end - im.j0 * kLtTile, 0);
       wait(&s.q_full, (uint32_t)i & 1u);
-      for (int j = 0; j < n && ok; j++, tiles++) {
-        for (int b = 0; b < kLtBlocks; b++) {      // S: the latent's part, pair by pair as they come
-          const uint32_t slot = (pos + b) % NP;
-          wait(&s.kv_full[slot], ((pos + b) / NP) & 1u);
-          if (!ok) break;
-          at_fence_after();
-          if (at_elect()) {
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-              const uint32_t ka = (uint32_t)(slot * kLtPair + (k >> 2) * kLtChunk + (k & 3) * 32) >> 4;
-              const uint32_t kb = (uint32_t)((2 * b + (k >> 2)) * G::kQChunk + (k & 3) * 32) >> 4;
-              at_mma_ss(ds, dk0 + ka, dq0 + kb, id_s, b > 0 || k > 0);
-            }
-          }
-          __syncwarp();
+      // What is ready goes first, O before S as it frees memory; S is two tiles ahead of O at most.
+      long long since = 0;                         // when there was nothing to do first; 0: there was something
+      for (int js = 0, jo = 0; ok && jo < n;) {
+        if (jo < js && over(&s.p_full[op], oph)) {
+          issue_o(end - jo * kLtTile, jo > 0);
+          jo++;
+          since = 0;
+          continue;
         }
-        if (!ok) break;
-        wait(&s.r_full, tiles & 1u);
-        if (!ok) break;
-        at_fence_after();
-        if (at_elect()) {
-#pragma unroll
-          for (int k = 0; k < 4; k++) at_mma_ss(ds, dr + (uint32_t)(k * 32 >> 4), dq0 + (uint32_t)((8 * G::kQChunk + k * 32) >> 4), id_s, 1u);
-          at_commit(&s.s_full);
-          if (!G::kAlias) at_commit(&s.r_empty);
-          if (j + 1 == n) at_commit(&s.q_empty);
+        if (js < n && js < jo + 2 && over(&s.kv_full[ks], kph)) {
+          const bool whole = half;
+          issue_s(js + 1 == n);
+          js += whole;
+          since = 0;
+          continue;
         }
-        __syncwarp();
-        wait(&s.p_full, tiles & 1u);
-        if (!ok) break;
-        at_fence_after();
-        const int left = end - j * kLtTile, steps = left >= kLtTile ? 8 : (left + 15) >> 4;   // groups of 16 tokens that some row sees
-        if (at_elect()) {
-#pragma unroll 1
-          for (int b = 0; b < kLtBlocks; b++) {
-            const uint32_t slot = (pos + b) % NP;
-            const uint64_t da = dv0 + (uint64_t)((slot * kLtPair) >> 4);
-#pragma unroll 1
-            for (int k = 0; k < steps; k++)
-              at_mma_ss(tu + (uint32_t)(b * N), da + (uint64_t)(128u * k), dp0 + (uint64_t)(2u * N * k), id_o, j > 0 || k > 0);
-            at_commit(&s.kv_empty[slot]);
-          }
-          if (G::kAlias) at_commit(&s.r_empty);
-          if (j + 1 == n) at_commit(&s.o_done);
+        // by cycles, two to a nanosecond: reading the global timer takes about a microsecond
+        const long long now = __shfl_sync(kFull, clock64(), 0);
+        if (since == 0) since = now;
+        if (now - since > 2 * (long long)a.wait_ns) {
+          if (lane == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
+          ok = false;
         }
-        __syncwarp();
-        pos += kLtBlocks;
       }
       if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
     }
@@ -962,7 +1034,7 @@ cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStre
   p.gang = p.hp == 2 || mean > p.per ? 2 : 1;
   const cuuint64_t cdims[2] = {(cuuint64_t)kLatRow, (cuuint64_t)a.num_pages << a.page_shift};
   const cuuint64_t cstride[1] = {2 * kLatRow};
-  const cuuint32_t cbox[2] = {64, 1u << a.page_shift};
+  const cuuint32_t cbox[2] = {64, (cuuint32_t)(a.page_shift < 6 ? 1 << a.page_shift : kLtTile)};
   cudaError_t err = lt_encode(&p.cmap, a.cache, 2, cdims, cstride, cbox, a.f16);
   if (err == cudaSuccess) err = lt_encode_rows(&p.qmap, a.q, kLatDim, p);
   if (err == cudaSuccess) err = lt_encode_rows(&p.rmap, a.q_rope, kLatRope, p);

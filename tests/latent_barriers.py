@@ -1,0 +1,314 @@
+"""The barrier protocols of the latent attention's kernels on the host, as
+``attn_barriers`` runs that of the attention: lat_tree_kernel, and attn_wide_kernel with
+its ring of pieces.
+
+``split_done`` False gives pv_done one barrier for all tiles, as a softmax warp that
+waits for the last two of an item would meet it: the model shows why there are two."""
+import random
+
+from attn_barriers import Bar
+
+
+class Overwritten(Exception):
+    pass
+
+
+class Tree:
+    """items: dicts n (tiles) and m0 (masked from there on); moves(half, tile) says whether the maximum moves there."""
+
+    def __init__(self, count, items, halves, parts, moves, split_done=True):
+        b = lambda name: Bar(name, count[name.split("[")[0]])  # noqa: E731
+        self.items, self.nh, self.nr, self.moves, self.split = items, halves, parts, moves, split_done
+        self.rng = random.Random(len(items))
+        self.kv_full, self.kv_empty = ([b(f"{n}[{i}]") for i in range(halves)] for n in ("kv_full", "kv_empty"))
+        self.part_of = [None] * parts                 # the tile whose key part, or P, a place holds
+        self.s_full, self.p_full, self.pv_done, self.sched_full, self.sched_empty = (
+            [b(f"{n}[{i}]") for i in range(2)] for n in ("s_full", "p_full", "pv_done", "sched_full", "sched_empty"))
+        self.q_full, self.q_empty = b("q_full"), b("q_empty")
+        self.votes = [Bar(f"vote{h}", 4) for h in range(2)]
+        self.pipe, self.copies, self.q_copies, self.posted = [], [], [], {}
+        self.roles = {"copy": self.tma(), "mma": self.mma(), "q": self.q()}
+        for h in range(2):
+            for w in range(4):
+                self.roles[f"soft{h}{w}"] = self.soft(h)
+        self.beside = {"pipe": self.pipe, "tiles": self.copies, "qcopies": self.q_copies}
+
+    def tma(self):
+        pos = tiles = 0
+        for i, it in enumerate(self.items + [None]):
+            if i >= 2:
+                yield self.sched_empty[i & 1], (i >> 1) - 1
+            self.posted[i] = it
+            self.sched_full[i & 1].arrive()
+            if it is None:
+                return
+            for _ in range(it["n"]):
+                for z in range(2):
+                    if pos >= self.nh:
+                        yield self.kv_empty[pos % self.nh], pos // self.nh - 1
+                    if z:                             # the key part comes with the second half: no barrier of its own
+                        if self.part_of[tiles % self.nr] is not None:
+                            raise Overwritten(f"tile {tiles} over tile {self.part_of[tiles % self.nr]}")
+                        self.part_of[tiles % self.nr] = tiles
+                    self.copies.append(self.kv_full[pos % self.nh].arrive)
+                    pos += 1
+                    yield None
+                tiles += 1
+
+    def free(self, tile):
+        self.part_of[tile % self.nr] = None
+
+    def mma(self):
+        issue = self.pipe.append
+        pos = tile = done = i = 0                     # halves and tiles of S, tiles of O
+
+        def scores(last):
+            nonlocal pos, tile
+            for _ in range(2):
+                yield self.kv_full[pos % self.nh], pos // self.nh
+                pos += 1
+            issue(self.s_full[tile & 1].arrive)
+            if last:
+                issue(self.q_empty.arrive)
+            tile += 1
+            yield None
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            it = self.posted[i]
+            if it is None:
+                return
+            n = it["n"]
+            yield self.q_full, i
+            js = jo = 0                               # what comes first goes by what is ready: any order is possible
+            while jo < n:
+                can_s, can_o = js < n and js < jo + 2, jo < js
+                if can_o and (not can_s or self.rng.random() < 0.5):
+                    yield self.p_full[done & 1], done >> 1
+                    issue(self.kv_empty[2 * done % self.nh].arrive)
+                    issue(lambda t=done: self.free(t))
+                    issue(self.kv_empty[(2 * done + 1) % self.nh].arrive)
+                    issue(self.pv_done[done & 1 if self.split else 0].arrive)
+                    done += 1
+                    jo += 1
+                    yield None
+                else:
+                    js += 1
+                    yield from scores(js == n)
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+    def q(self):
+        i = 0
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            if self.posted[i] is None:
+                return
+            if i > 0:
+                yield self.q_empty, i - 1
+            self.q_copies.append(self.q_full.arrive)
+            yield None
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+    def done(self, t):
+        return (self.pv_done[t & 1], t >> 1) if self.split else (self.pv_done[0], t)
+
+    def soft(self, h):
+        ns = nv = i = 0
+
+        def vote():
+            nonlocal nv
+            self.votes[h].arrive()
+            nv += 1
+            return self.votes[h], nv - 1
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            yield vote()
+            it = self.posted[i]
+            if it is None:
+                return
+            for j in range(it["n"]):
+                yield self.s_full[ns & 1], ns >> 1
+                if j >= it["m0"]:                     # the scan
+                    for pos in (2 * ns, 2 * ns + 1):
+                        yield self.kv_full[pos % self.nh], pos // self.nh
+                yield vote()
+                if self.moves(h, ns):
+                    yield vote()
+                    if j > 0:
+                        yield self.done(ns - 1)
+                self.p_full[ns & 1].arrive()
+                ns += 1
+                yield None
+            if not self.split and it["n"] > 1:
+                yield self.done(ns - 2)
+            yield self.done(ns - 1)
+            yield vote()
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+
+class Prompt:
+    """attn_wide_kernel's expanded form: items as in ``attn_barriers``, a ring of pieces (2 of a value tile, 3 of a key tile)."""
+
+    def __init__(self, count, items, stages=7):
+        b = lambda name: Bar(name, count[name.split("[")[0]])  # noqa: E731
+        self.items, self.stages = items, stages
+        self.kv_full, self.kv_empty = ([b(f"{n}[{i}]") for i in range(stages)] for n in ("kv_full", "kv_empty"))
+        self.s_full, self.p_full, self.o_done, self.sched_full, self.sched_empty = (
+            [b(f"{n}[{i}]") for i in range(2)] for n in ("s_full", "p_full", "o_done", "sched_full", "sched_empty"))
+        self.q_full, self.q_empty = b("q_full"), b("q_empty")
+        self.v_posted = [[b(f"v_posted[{p}][{z}]") for z in range(3)] for p in range(2)]
+        self.v_clean = [[b(f"v_clean[{p}][{z}]") for z in range(3)] for p in range(2)]
+        self.v_pos, self.pipe, self.copies, self.q_copies, self.posted = {}, [], [], [], {}
+        self.roles = {"copy": self.tma(), "mma": self.mma(), "help2": self.helper(2), "help3": self.helper(3)}
+        for h in range(2):
+            for w in range(4):
+                self.roles[f"soft{h}{w}"] = self.soft(h)
+        self.beside = {"pipe": self.pipe, "tiles": self.copies, "q": self.q_copies}
+
+    def tma(self):
+        pos = 0
+        for i, it in enumerate(self.items + [None]):
+            if i >= 2:
+                yield self.sched_empty[i & 1], (i >> 1) - 1
+            self.posted[i] = it
+            self.sched_full[i & 1].arrive()
+            if it is None:
+                return
+            n, ahead = it["n"], 2 if it["twin"] else 1
+            for q in range(n + ahead):
+                if q >= ahead:
+                    for z in range(2):
+                        if pos + z >= self.stages:
+                            yield self.kv_empty[(pos + z) % self.stages], (pos + z) // self.stages - 1
+                    z = q - ahead - it["m0"]
+                    if z >= 0:
+                        self.v_pos[i & 1, z] = pos
+                        self.v_posted[i & 1][z].arrive()
+                    for z in range(2):
+                        self.copies.append(self.kv_full[(pos + z) % self.stages].arrive)
+                    pos += 2
+                    yield None
+                if q < n:
+                    for _ in range(3):
+                        if pos >= self.stages:
+                            yield self.kv_empty[pos % self.stages], pos // self.stages - 1
+                        self.copies.append(self.kv_full[pos % self.stages].arrive)
+                        pos += 1
+                        yield None
+
+    def full(self, at):
+        return self.kv_full[at % self.stages], at // self.stages
+
+    def mma(self):
+        issue = self.pipe.append
+        pos, i, nps, clean = 0, 0, [0, 0], {}
+
+        def scores(h, at, last, q_last):
+            for z in range(3):
+                yield self.full(at + z)
+                if last:
+                    issue(self.kv_empty[(at + z) % self.stages].arrive)
+            issue(self.s_full[h].arrive)
+            if q_last:
+                issue(self.q_empty.arrive)
+            yield None
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            it = self.posted[i]
+            if it is None:
+                return
+            n, m0, n0, n1, twin = (it[k] for k in ("n", "m0", "n0", "n1", "twin"))
+            ahead = 2 if twin else 1
+            yield self.q_full, i
+            for j in range(min(ahead, n)):
+                if twin:
+                    yield from scores(j, pos, True, j + 1 == n)
+                else:
+                    yield from scores(0, pos, n1 == 0, j + 1 == n and n1 == 0)
+                    if n1 > 0:
+                        yield from scores(1, pos, True, j + 1 == n)
+                pos += 3
+            for j in range(n):
+                at = pos
+                yield self.full(at)
+                yield self.full(at + 1)
+                if j >= m0:
+                    key = (i & 1, j - m0)
+                    yield self.v_clean[key[0]][key[1]], clean.get(key, 0)
+                    clean[key] = clean.get(key, 0) + 1
+                pos += 2
+                for h, nh in enumerate((n0, n1)):
+                    if (j & 1) == h if twin else j < nh:
+                        more, tail = (j + 2 < n if twin else j + 1 < nh), twin or h or n1 == 0
+                        yield self.p_full[h], nps[h]
+                        nps[h] += 1
+                        if tail:
+                            issue(self.kv_empty[at % self.stages].arrive)
+                            issue(self.kv_empty[(at + 1) % self.stages].arrive)
+                        if not more:
+                            issue(self.o_done[h].arrive)
+                        yield None
+                        if more:
+                            yield from scores(h, pos, tail, tail and j + ahead + 1 == n)
+                if j + ahead < n:
+                    pos += 3
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+    def soft(self, h):
+        ns = ni = i = 0
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            it = self.posted[i]
+            if it is None:
+                return
+            nt = it["n1"] if h else it["n0"]
+            for _ in range(nt):
+                yield self.s_full[h], ns
+                ns += 1
+                self.p_full[h].arrive()
+                yield None
+            if nt:
+                yield self.o_done[h], ni
+                ni += 1
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+    def helper(self, warp):
+        uses, i = {}, 0
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            it = self.posted[i]
+            if it is None:
+                return
+            if warp == 2:
+                if i > 0:
+                    yield self.q_empty, i - 1
+                self.q_copies.append(self.q_full.arrive)
+                yield None
+            for j in range(it["m0"], it["n"]):
+                z = j - it["m0"]
+                key = (i & 1, z)
+                yield self.v_posted[i & 1][z], uses.get(key, 0)
+                uses[key] = uses.get(key, 0) + 1
+                yield self.full(self.v_pos[key])
+                yield self.full(self.v_pos[key] + 1)
+                self.v_clean[i & 1][z].arrive()
+                yield None
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+
+def random_tree_items(rng, n, longest):
+    out = []
+    for _ in range(n):
+        t = rng.randint(1, longest)
+        out.append(dict(n=t, m0=t - rng.randint(0, min(2, t))))
+    return out
+
+
+def moves_by(seed, often):
+    """The same answer for the four warps of a half."""
+    return lambda h, t: random.Random(f"{seed} {h} {t}").random() < often
