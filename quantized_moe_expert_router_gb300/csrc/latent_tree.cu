@@ -21,7 +21,9 @@
 // heads are two parts.  One CTA per SM, 12 warps:
 //   warp 0           tiles, 64 elements x a page a copy (128-byte swizzle): two halves of 64 x 256 elements into a
 //                    ring of 4 or 5, and with the second the key part into one of 2 or 3; takes the items
-//   warp 1           MMA issue: O of a tile when its P is there, else S of the next when that is
+//   warps 1, 3       MMA issue of S and of O: the products read shared memory all the time, which makes every wait's
+//                    look at a barrier slow, so one's products fill the other's waits (one issuer that takes what is ready: 163 us
+//                    where two have TBD, 16 tokens at up to 100000 of 64 heads)
 //   warp 2           Q rows by boxes (64, heads, tokens)
 //   warps 4-7, 8-11  softmax of rows 0 .. N/2 - 1 and N/2 .. N - 1: a warp has 16 tokens, a thread two
 //                    of them and a quarter of the warp's rows (the fragment shape: an accumulator of 64 rows fills 16 of a
@@ -41,17 +43,19 @@
 // the epilogue makes these elements NaN in the rows that do see it.
 //
 // A wait knows its phase by parity alone, so no barrier may be two phases on when a waiter looks:
-//   sched_full    (item parity) item i + 2 is posted when sched_empty has all 10 arrivals of item i
-//   kv_full       filled again behind kv_empty, which the MMA warp commits behind the tile's p_full,
+//   sched_full    (item parity) item i + 2 is posted when sched_empty has all 11 arrivals of item i
+//   kv_full       filled again behind kv_empty, which the O warp commits behind the tile's p_full,
 //                 which every softmax warp gives after its scan.  The place of a second half is free only after that of
 //                 the key part that comes with it.
 //   kv_empty      waited for by the copy warp, whose lanes meet before they copy
 //   q_full        filled again behind q_empty; q_empty is waited for by warp 2 alone, and without that Q there is no next
-//   s_full, p_full    (tile parity) S of tile t + 2 is issued after p_full of tile t has been waited for; P of tile t + 2
-//                 follows that S
-//   pv_done       (tile parity) S of tile t completes behind the products of tile t - 2, so a warp that has it
-//                 waits for the phase of tile t - 1, or having given P that of tile t, with the one before
-//                 on that barrier completed; the one after needs the P that it has not given
+//   s_full        (tile parity) S of tile t + 2 is issued behind p_full of tile t
+//   p_full        (tile parity) P of tile t + 2 follows its S, which the S warp issues after p_full of tile t has been waited
+//                 for, and its tile, whose second half lies where one of tile t - 1 or t lay: the O warp has waited for
+//                 p_full of that tile, hence of tile t - 1 at least; and S of tile t + 2 ... TBD
+//   pv_done       (tile parity) tile t lies, with its second half, where one of tile t - 3 or t - 2 lay, so with S of tile t the
+//                 products of tile t - 3 are done: a warp that has it may wait for those of tile t - 1, and then for those
+//                 of tile t; the next ones on these barriers need P that it has not given
 // The softmax warps of a half also meet at a named barrier: a warp whose wait ran out goes on to
 // the next vote, which tells the others, and all four end together.
 #include <limits.h>
@@ -66,7 +70,7 @@ namespace moe {
 
 constexpr int kLtThreads = 384;
 constexpr int kLtTile = 64;                       // tokens of a tile
-constexpr int kLtWTma = 0, kLtWMma = 1, kLtWQ = 2, kLtWSoft = 4;
+constexpr int kLtWTma = 0, kLtWS = 1, kLtWQ = 2, kLtWO = 3, kLtWSoft = 4;
 constexpr int kLtChunk = kLtTile * 128, kLtPair = 2 * kLtChunk, kLtHalf = 2 * kLtPair;   // bytes of 64, 128 and 256 elements of a tile
 constexpr int kLtBlocks = kLatDim / 128;          // of 128 latent elements
 constexpr int kLtMaxB = MOE_ATTN_MAX_REQUESTS;
@@ -136,15 +140,6 @@ __device__ __forceinline__ bool lt_wait(uint64_t *bar, uint32_t parity, const Lt
   const bool ok = __all_sync(kFull, mbar_wait_bounded(bar, parity, p.a.wait_ns));
   if (!ok && (threadIdx.x & 31) == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
   return ok;
-}
-// Whether the phase with `parity` is over, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
 }
 // True in all of a half's 128 threads when it is in one of them.
 __device__ __forceinline__ bool lt_any(int half, bool x) {
@@ -322,13 +317,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       mbar_init(&s.pv_done[lane - 14], 1);
     } else if (lane >= 16 && lane < 18) {
       mbar_init(&s.sched_full[lane - 16], 1);
-      mbar_init(&s.sched_empty[lane - 16], 10);    // 8 softmax warps, MMA warp, Q warp
+      mbar_init(&s.sched_empty[lane - 16], 11);    // 8 softmax warps, S, O and Q warps
       s.fail[lane - 16] = INT_MAX;
     } else if (lane == 18) {
       mbar_init(&s.q_full, 1);
       mbar_init(&s.q_empty, 1);
     } else if (lane == 19) {
-      mbar_init(&s.drain, 1);
+      mbar_init(&s.drain, 2);                      // S and O warps
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -337,7 +332,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.qmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.rmap)) : "memory");
   }
-  if (warp == kLtWMma) {
+  if (warp == kLtWS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -604,7 +599,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
         if (lane < 4) s.wsum[h][w4][8 * (n >> 1) + qc + (n & 1)] = x;
       }
-      ok = lt_wait(&s.pv_done[(ns - 1) & 1u], ((ns - 1) >> 1) & 1u, p);
+      if (ns > 1) ok = lt_wait(&s.pv_done[ns & 1u], ((ns - 2) >> 1) & 1u, p);
+      ok = lt_wait(&s.pv_done[(ns - 1) & 1u], ((ns - 1) >> 1) & 1u, p) && ok;
       if (vote(false) == 2) break;
       const int el = 32 * w4 + lane;               // latent element of a block
       at_fence_after();
@@ -716,123 +712,104 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     // copies in flight land before the CTA ends; nothing else may pass these barriers now
     for (uint32_t q = pos > NH ? pos - NH : 0; q < pos; q++) mbar_wait_bounded(&s.kv_full[q % NH], (q / NH) & 1u, a.wait_ns);
     __syncwarp();
-  } else if (warp == kLtWMma) {
+  } else if (warp == kLtWS || warp == kLtWO) {
     // ---------------------------------------------------------- MMA issue
     // The whole warp goes through the loop, so that descriptors stay in uniform registers; one elected lane issues.
-    constexpr uint32_t id_s = lt_idesc_s(F16, N), id_o = lt_idesc_o(F16, N);
-    const uint32_t tu = __shfl_sync(kFull, tb, 0), ds = tu + 4u * N;
-    const uint64_t dq0 = at_desc(smem0 + G::kQ, 16), dr0 = at_desc(smem0 + G::kRope, 16), dk0 = at_desc(smem0, 16);
-    const uint64_t dv0 = at_desc(smem0, kLtChunk), dp0 = lt_desc_p<N>(smem0 + G::kRope);
-    // of the tile whose S comes next: its next half's slot and phase, its key part's slot, its own parity; whether its first
-    // half is issued
-    uint32_t ks = 0, kph = 0, rs = 0, sp = 0, half = 0;
-    // of the tile whose O comes next: its first half's slot, its key part's, its parity and phase
-    uint32_t os = 0, ors = 0, op = 0, oph = 0;
+    const uint32_t tu = __shfl_sync(kFull, tb, 0);
     bool ok = true;
     // the lanes go on or end together
-    auto over = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, mbar_test(bar, parity)); };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       ok = __all_sync(kFull, ok && mbar_wait_bounded(bar, parity, a.wait_ns));
       if (!ok && lane == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-    };
-    // A half of S, and the key part with the second.
-    auto issue_s = [&](bool last) {
-      // from lane 0, so that they are known to be the same in all lanes
-      const uint32_t slot = __shfl_sync(kFull, ks, 0), second = __shfl_sync(kFull, half, 0);
-      const uint32_t part = __shfl_sync(kFull, rs, 0), d = ds + __shfl_sync(kFull, sp, 0) * N;
       at_fence_after();
-      if (at_elect()) {
-        uint64_t da = dk0 + (uint64_t)(slot * (kLtHalf >> 4)), db = dq0 + (uint64_t)(second * (4 * G::kQChunk >> 4));
-        uint32_t acc = second;
-#pragma unroll 1
-        for (int z = 0; z < 4; z++) {
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            at_mma_ss(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, acc);
-            acc = 1u;
-          }
-          da += (uint64_t)(kLtChunk >> 4);
-          db += (uint64_t)(G::kQChunk >> 4);
-        }
-        if (second) {
-          const uint64_t dr = dr0 + (uint64_t)(part * (kLtChunk >> 4));
-#pragma unroll
-          for (int k = 0; k < 4; k++) at_mma_ss(d, dr + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, 1u);
-          at_commit(&s.s_full[sp]);
-          if (last) at_commit(&s.q_empty);
-        }
-      }
-      __syncwarp();
-      if (++ks == NH) {
-        ks = 0;
-        kph ^= 1u;
-      }
-      if (half) {
-        rs = rs + 1 == NR ? 0 : rs + 1;
-        sp ^= 1u;
-      }
-      half ^= 1u;
     };
-    // O of a tile with `left` tokens up to the last that some row sees: groups of 16 past it are left out
-    auto issue_o = [&](int left0, uint32_t add0) {
-      const int left = __shfl_sync(kFull, left0, 0);
-      const uint32_t add = __shfl_sync(kFull, add0, 0), part = __shfl_sync(kFull, ors, 0), slot0 = __shfl_sync(kFull, os, 0);
-      at_fence_after();
-      if (at_elect()) {
-        const uint64_t dp = dp0 + (uint64_t)(part * (kLtChunk >> 4));
-        const int steps = left >= kLtTile ? kLtTile / 16 : (left + 15) >> 4;
-        uint32_t sl = slot0;
+    if (warp == kLtWS) {
+      constexpr uint32_t id_s = lt_idesc_s(F16, N);
+      const uint64_t dq0 = at_desc(smem0 + G::kQ, 16), dr0 = at_desc(smem0 + G::kRope, 16), dk0 = at_desc(smem0, 16);
+      uint32_t slot = 0, phase = 0, part = 0, t = 0;   // the next half's slot and phase, the tile's key part, tiles so far
+      for (int i = 0; ok; i++) {
+        wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
+        if (!ok) break;
+        const LtItem &im = s.item[i & 1];
+        if (__shfl_sync(kFull, im.b, 0) < 0) break;
+        const int n = __shfl_sync(kFull, im.n, 0);
+        wait(&s.q_full, (uint32_t)i & 1u);
+        for (int j = 0; j < n && ok; j++, t++) {
+          const uint32_t d = tu + 4u * N + (t & 1u) * N;
+          if (t >= 2) wait(&s.p_full[t & 1u], ((t >> 1) - 1) & 1u);      // the scores of tile t - 2 have been read
 #pragma unroll 1
-        for (int b = 0; b < kLtBlocks; b++) {
-          const uint64_t da = dv0 + (uint64_t)(sl * (kLtHalf >> 4) + (b & 1) * (kLtPair >> 4));
+          for (uint32_t z = 0; z < 2 && ok; z++) {
+            wait(&s.kv_full[slot], phase);
+            if (!ok) break;
+            if (at_elect()) {
+              uint64_t da = dk0 + (uint64_t)(slot * (kLtHalf >> 4)), db = dq0 + (uint64_t)(z * (4 * G::kQChunk >> 4));
+              uint32_t acc = z;
+#pragma unroll 1
+              for (int e = 0; e < 4; e++) {
 #pragma unroll
-          for (int k = 0; k < kLtTile / 16; k++)
-            if (k < steps) at_mma_ss(tu + (uint32_t)(b * N), da + (uint64_t)(128u * k), dp + (uint64_t)(2u * N * k), id_o, k > 0 ? 1u : add);
-          if (b & 1) {
-            at_commit(&s.kv_empty[sl]);
-            sl = sl + 1 == NH ? 0 : sl + 1;
+                for (int k = 0; k < 4; k++) {
+                  at_mma_ss(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, acc);
+                  acc = 1u;
+                }
+                da += (uint64_t)(kLtChunk >> 4);
+                db += (uint64_t)(G::kQChunk >> 4);
+              }
+              if (z) {
+                const uint64_t dr = dr0 + (uint64_t)(part * (kLtChunk >> 4));
+#pragma unroll
+                for (int k = 0; k < 4; k++) at_mma_ss(d, dr + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, 1u);
+                at_commit(&s.s_full[t & 1u]);
+                if (j + 1 == n) at_commit(&s.q_empty);
+              }
+            }
+            __syncwarp();
+            if (++slot == NH) {
+              slot = 0;
+              phase ^= 1u;
+            }
           }
+          part = part + 1 == NR ? 0 : part + 1;
         }
-        at_commit(&s.pv_done[op]);
+        if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
-      __syncwarp();
-      os = os + 2 >= NH ? os + 2 - NH : os + 2;
-      ors = ors + 1 == NR ? 0 : ors + 1;
-      oph ^= op;
-      op ^= 1u;
-    };
-    for (int i = 0; ok; i++) {
-      wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
-      if (!ok) break;
-      const LtItem &im = s.item[i & 1];
-      if (__shfl_sync(kFull, im.b, 0) < 0) break;
-      const int n = __shfl_sync(kFull, im.n, 0), end = __shfl_sync(kFull, im.end - im.j0 * kLtTile, 0);
-      wait(&s.q_full, (uint32_t)i & 1u);
-      // What is ready goes first, O before S as it frees memory; S is two tiles ahead of O at most.
-      long long since = 0;                         // when there was nothing to do first; 0: there was something
-      for (int js = 0, jo = 0; ok && jo < n;) {
-        if (jo < js && over(&s.p_full[op], oph)) {
-          issue_o(end - jo * kLtTile, jo > 0);
-          jo++;
-          since = 0;
-          continue;
+    } else {
+      constexpr uint32_t id_o = lt_idesc_o(F16, N);
+      const uint64_t dv0 = at_desc(smem0, kLtChunk), dp0 = lt_desc_p<N>(smem0 + G::kRope);
+      uint32_t slot = 0, part = 0, t = 0;              // of the tile: its first half's slot, its key part; tiles so far
+      for (int i = 0; ok; i++) {
+        wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
+        if (!ok) break;
+        const LtItem &im = s.item[i & 1];
+        if (__shfl_sync(kFull, im.b, 0) < 0) break;
+        const int n = __shfl_sync(kFull, im.n, 0), end = __shfl_sync(kFull, im.end - im.j0 * kLtTile, 0);
+        for (int j = 0; j < n && ok; j++, t++) {
+          // groups of 16 tokens up to the last that some row sees
+          const int left = end - j * kLtTile, steps = left >= kLtTile ? kLtTile / 16 : (left + 15) >> 4;
+          wait(&s.p_full[t & 1u], (t >> 1) & 1u);
+          if (!ok) break;
+          if (at_elect()) {
+            const uint64_t dp = dp0 + (uint64_t)(part * (kLtChunk >> 4));
+            const uint32_t add = j > 0;
+            uint32_t sl = slot;
+#pragma unroll 1
+            for (int b = 0; b < kLtBlocks; b++) {
+              const uint64_t da = dv0 + (uint64_t)(sl * (kLtHalf >> 4) + (b & 1) * (kLtPair >> 4));
+#pragma unroll
+              for (int k = 0; k < kLtTile / 16; k++)
+                if (k < steps) at_mma_ss(tu + (uint32_t)(b * N), da + (uint64_t)(128u * k), dp + (uint64_t)(2u * N * k), id_o, k > 0 ? 1u : add);
+              if (b & 1) {
+                at_commit(&s.kv_empty[sl]);
+                sl = sl + 1 == NH ? 0 : sl + 1;
+              }
+            }
+            at_commit(&s.pv_done[t & 1u]);
+          }
+          __syncwarp();
+          slot = slot + 2 >= NH ? slot + 2 - NH : slot + 2;
+          part = part + 1 == NR ? 0 : part + 1;
         }
-        if (js < n && js < jo + 2 && over(&s.kv_full[ks], kph)) {
-          const bool whole = half;
-          issue_s(js + 1 == n);
-          js += whole;
-          since = 0;
-          continue;
-        }
-        // by cycles, two to a nanosecond: reading the global timer takes about a microsecond
-        const long long now = __shfl_sync(kFull, clock64(), 0);
-        if (since == 0) since = now;
-        if (now - since > 2 * (long long)a.wait_ns) {
-          if (lane == 0) atomicOr(p.ctrl + kAttnCtrlFlags, MOE_FLAG_TIMEOUT);
-          ok = false;
-        }
+        if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
       }
-      if (lane == 0) mbar_arrive(&s.sched_empty[i & 1]);
     }
     // every MMA issued has completed before tensor memory is released
     if (at_elect()) at_commit(&s.drain);
@@ -861,7 +838,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
   }
   at_fence_before();
   __syncthreads();
-  if (warp == kLtWMma) {
+  if (warp == kLtWS) {
     at_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(512) : "memory");
   }

@@ -19,19 +19,19 @@ class Tree:
     def __init__(self, count, items, halves, parts, moves, split_done=True):
         b = lambda name: Bar(name, count[name.split("[")[0]])  # noqa: E731
         self.items, self.nh, self.nr, self.moves, self.split = items, halves, parts, moves, split_done
-        self.rng = random.Random(len(items))
         self.kv_full, self.kv_empty = ([b(f"{n}[{i}]") for i in range(halves)] for n in ("kv_full", "kv_empty"))
         self.part_of = [None] * parts                 # the tile whose key part, or P, a place holds
         self.s_full, self.p_full, self.pv_done, self.sched_full, self.sched_empty = (
             [b(f"{n}[{i}]") for i in range(2)] for n in ("s_full", "p_full", "pv_done", "sched_full", "sched_empty"))
         self.q_full, self.q_empty = b("q_full"), b("q_empty")
         self.votes = [Bar(f"vote{h}", 4) for h in range(2)]
-        self.pipe, self.copies, self.q_copies, self.posted = [], [], [], {}
-        self.roles = {"copy": self.tma(), "mma": self.mma(), "q": self.q()}
+        self.scores, self.values, self.copies, self.q_copies, self.posted = [], [], [], [], {}
+        self.roles = {"copy": self.tma(), "s": self.s(), "o": self.o(), "q": self.q()}
         for h in range(2):
             for w in range(4):
                 self.roles[f"soft{h}{w}"] = self.soft(h)
-        self.beside = {"pipe": self.pipe, "tiles": self.copies, "qcopies": self.q_copies}
+        # what runs beside the warps: the products of each issuer, in its order, the copies of tiles and of Q
+        self.beside = {"scores": self.scores, "values": self.values, "tiles": self.copies, "qcopies": self.q_copies}
 
     def tma(self):
         pos = tiles = 0
@@ -58,42 +58,43 @@ class Tree:
     def free(self, tile):
         self.part_of[tile % self.nr] = None
 
-    def mma(self):
-        issue = self.pipe.append
-        pos = tile = done = i = 0                     # halves and tiles of S, tiles of O
-
-        def scores(last):
-            nonlocal pos, tile
-            for _ in range(2):
-                yield self.kv_full[pos % self.nh], pos // self.nh
-                pos += 1
-            issue(self.s_full[tile & 1].arrive)
-            if last:
-                issue(self.q_empty.arrive)
-            tile += 1
-            yield None
+    def s(self):
+        pos = t = i = 0
         while True:
             yield self.sched_full[i & 1], i >> 1
             it = self.posted[i]
             if it is None:
                 return
-            n = it["n"]
             yield self.q_full, i
-            js = jo = 0                               # what comes first goes by what is ready: any order is possible
-            while jo < n:
-                can_s, can_o = js < n and js < jo + 2, jo < js
-                if can_o and (not can_s or self.rng.random() < 0.5):
-                    yield self.p_full[done & 1], done >> 1
-                    issue(self.kv_empty[2 * done % self.nh].arrive)
-                    issue(lambda t=done: self.free(t))
-                    issue(self.kv_empty[(2 * done + 1) % self.nh].arrive)
-                    issue(self.pv_done[done & 1 if self.split else 0].arrive)
-                    done += 1
-                    jo += 1
-                    yield None
-                else:
-                    js += 1
-                    yield from scores(js == n)
+            for j in range(it["n"]):
+                if t >= 2:
+                    yield self.p_full[t & 1], (t >> 1) - 1
+                for _ in range(2):
+                    yield self.kv_full[pos % self.nh], pos // self.nh
+                    pos += 1
+                self.scores.append(self.s_full[t & 1].arrive)
+                if j + 1 == it["n"]:
+                    self.scores.append(self.q_empty.arrive)
+                t += 1
+                yield None
+            self.sched_empty[i & 1].arrive()
+            i += 1
+
+    def o(self):
+        t = i = 0
+        while True:
+            yield self.sched_full[i & 1], i >> 1
+            it = self.posted[i]
+            if it is None:
+                return
+            for _ in range(it["n"]):
+                yield self.p_full[t & 1], t >> 1
+                self.values.append(self.kv_empty[2 * t % self.nh].arrive)
+                self.values.append(lambda t=t: self.free(t))
+                self.values.append(self.kv_empty[(2 * t + 1) % self.nh].arrive)
+                self.values.append(self.pv_done[t & 1 if self.split else 0].arrive)
+                t += 1
+                yield None
             self.sched_empty[i & 1].arrive()
             i += 1
 
@@ -140,7 +141,7 @@ class Tree:
                 self.p_full[ns & 1].arrive()
                 ns += 1
                 yield None
-            if not self.split and it["n"] > 1:
+            if ns > 1:
                 yield self.done(ns - 2)
             yield self.done(ns - 1)
             yield vote()

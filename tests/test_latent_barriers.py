@@ -11,7 +11,7 @@ import latent_barriers as lb
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_moe_expert_router_gb300", "csrc")
 TREE, WIDE = (open(os.path.join(CSRC, n)).read() for n in ("latent_tree.cu", "attn_wide.cu"))
 SOFT = [f"soft{h}{w}" for h in range(2) for w in range(4)]
-TREE_ROLES = ["copy", "mma", "q", "pipe", "tiles", "qcopies"] + SOFT
+TREE_ROLES = ["copy", "s", "o", "q", "scores", "values", "tiles", "qcopies"] + SOFT
 RINGS = [(4, 2), (5, 3)]                               # halves, key parts: 64 rows, and 32 or 16
 
 
@@ -22,7 +22,7 @@ def tree(items, ring, seed=0, often=0.5, **kw):
 
 def test_the_kernel_has_the_modelled_barriers():
     count = ab.counts(TREE)
-    assert count["p_full"] == 8 and count["sched_empty"] == 10
+    assert count["p_full"] == 8 and count["sched_empty"] == 11
     assert all(count[n] == 1 for n in ("kv_full", "kv_empty", "q_full", "q_empty", "s_full", "pv_done", "sched_full"))
     assert "kHalves = N == 64 ? 4 : 5" in TREE and "kParts = N == 64 ? 2 : 3" in TREE
     assert "s_full[2], p_full[2], pv_done[2]" in TREE
