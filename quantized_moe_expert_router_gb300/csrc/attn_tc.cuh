@@ -232,12 +232,11 @@ struct AtShare {
   // where CTA a, which holds the item's first unit, keeps its part: a CTA's first part is in its slot 0
   __device__ __forceinline__ int first_slot(int a, long long item0) const { return 2 * a + (!len && start(a) < item0); }
 };
-// All threads of the CTA (NW warps) call this; `scratch` is NW x 32 ints.  `grid` and `me`: the CTAs, or groups of
-// them, that share the line, and which of them this is; `above`: parts may be 31 units longer than the mean, or fewer.
+// All threads of the CTA (NW warps) call this; `scratch` is NW x 32 ints.
 template <int NW, typename Items, typename Nch>
 __device__ __forceinline__ AtShare at_share(const long long *work, int B, long long total, int nitems, int min_len,
-                                            int (*scratch)[32], Items items, Nch nch, int grid, int me, long long above = 31) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+                                            int (*scratch)[32], Items items, Nch nch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grid = gridDim.x, me = blockIdx.x;
   AtShare r;
   r.me = me;
   r.x0 = r.x1 = 0;
@@ -255,7 +254,7 @@ __device__ __forceinline__ AtShare at_share(const long long *work, int B, long l
     parts = 0;
 #pragma unroll
     for (int w = 0; w < NW; w++) parts += scratch[w][lane];
-    const unsigned fits = __ballot_sync(kFull, parts <= grid && lane <= above);
+    const unsigned fits = __ballot_sync(kFull, parts <= grid);
     if (fits) {
       r.len = len0 + __ffs(fits) - 1;
       int before = 0;

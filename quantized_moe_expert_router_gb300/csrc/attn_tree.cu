@@ -581,8 +581,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_few_kernel(const __grid_co
   };
   const AtShare share =
       at_share<kAtWarps>(s.t.work, a.B, total, nitems, kAtMinChunks, s.cand,
-                         [&](int b) { return request(b).tiles * a.kv_heads; }, [&](int b) { return request(b).nch; }, gridDim.x,
-                         blockIdx.x);
+                         [&](int b) { return request(b).tiles * a.kv_heads; }, [&](int b) { return request(b).nch; });
   const long long x0 = share.x0, x1 = share.x1;
   if (x0 >= x1) return;
 

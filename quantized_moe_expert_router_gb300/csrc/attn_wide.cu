@@ -403,8 +403,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
     }
     share = at_share<kApThreads / 32>(
         s.work, a.B, total, nitems, kApMinTiles, s.cand,
-        [&](int b) { return cache_tiles(p, s.n[b]) * a.kv_heads; }, [&](int b) { return cache_nch(a, s.n[b], s.cached[b]); },
-        gridDim.x, blockIdx.x);
+        [&](int b) { return cache_tiles(p, s.n[b]) * a.kv_heads; }, [&](int b) { return cache_nch(a, s.n[b], s.cached[b]); });
     if (tid == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless cache_part finds it
   } else {
     // requests by falling number of row tiles (equal ones by index), every CTA alike

@@ -76,7 +76,6 @@ constexpr int kLtBlocks = kLatDim / 128;          // of 128 latent elements
 constexpr int kLtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr int kLtMaxSms = 1024;
 constexpr int kLtRows = 64;                       // rows of an item at most
-constexpr int kLtMinTiles = 1;                    // tiles of a CTA at least
 constexpr float kLtSlack = 8.f;                   // log2 of the largest P
 constexpr float kLtUnset = 1e30f;                 // in place of -c m before a row has seen anything: any score passes it
 
@@ -127,13 +126,9 @@ struct LtSmem {
 };
 static_assert(offsetof(LtSmem, mc) % 16 == 0 && offsetof(LtSmem, f) % 16 == 0, "read four at a time");
 
-// While the CTA finds its share, in the place of the tiles.
+// While the CTA's copy warp finds its share, in the place of the tiles: of each request its items and their tiles.
 struct LtSetup {
-  long long work[kLtMaxB + 1];                    // tiles of the requests before
-  int n[kLtMaxB], cached[kLtMaxB];
-  int cand[kLtThreads / 32][32];
-  long long wsum2[kLtThreads / 32];
-  int wsum[kLtThreads / 32];
+  int items[kLtMaxB], nch[kLtMaxB];
 };
 
 __device__ __forceinline__ bool lt_wait(uint64_t *bar, uint32_t parity, const LtArgs &p) {
@@ -235,26 +230,129 @@ __device__ __forceinline__ void lt_request(const LatArgs &a, int b, int &first, 
   cached = min(max(__ldg(a.cached + b), 0), a.max_pages << a.page_shift);       // no sum with rows passes 2^31
 }
 
-// Walks the line of tiles from place x on.
+// Walks the line of tiles from the CTA's share on.
 struct LtCursor {
+  AtShare share;
   int b, first, n, cached, nch, items;
   long long work;              // tiles of the requests before b
+  // of the last part, when it is the first of several: what the join has to know
+  bool split;
+  int need;
+  long long item0;
   __device__ __forceinline__ void load(const LtArgs &p) {
     lt_request(p.a, b, first, n, cached);
     nch = lt_nch(p.a, n, cached);
     items = lt_items(p, n);
   }
+  __device__ __forceinline__ int member(const LtArgs &p) const { return p.gang == 2 ? (int)blockIdx.x & 1 : 0; }
+  // The share of this CTA, by one warp: a chain of a few hundred cycles a step, and of one look at each request, while the
+  // other warps have nothing to do yet.  (lo, hi, held): cu, cu + 1 and cached of request `lane`.
+  __device__ __forceinline__ void find(const LtArgs &p, LtSetup &u, int lo, int hi, int held) {
+    const LatArgs &a = p.a;
+    const int lane = threadIdx.x & 31, end = (a.B + 31) & ~31;
+    const int grid = p.gang == 2 ? (int)gridDim.x >> 1 : (int)gridDim.x, me = p.gang == 2 ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    long long total = 0;
+    int count = 0;
+    for (int r = lane; r < end; r += 32) {
+      if (r >= 32 && r < a.B) {
+        lo = __ldg(a.cu + r);
+        hi = __ldg(a.cu + r + 1);
+        held = __ldg(a.cached + r);
+      }
+      const int rows = r < a.B && lo >= 0 ? max(0, min(hi, a.T) - lo) : 0, c = min(max(held, 0), a.max_pages << a.page_shift);
+      const int i = rows ? lt_items(p, rows) : 0, t = rows ? lt_nch(a, rows, c) : 0;
+      u.items[r] = i;
+      u.nch[r] = t;
+      total += (long long)i * t;
+      count += i;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+    count = __reduce_add_sync(kFull, count);
+    __syncwarp();
+    AtShare r;
+    r.me = me;
+    r.len = r.c0 = r.c1 = 0;
+    r.x0 = r.x1 = r.rem = 0;
+    r.per = 1;
+    r.ctas = (int)min(total, (long long)grid);
+    if (total > grid) {
+      r.per = at_div(total, grid);
+      r.rem = total - r.per * grid;
+      // A part costs its CTA an epilogue and the join a source, some three tiles' time: equal parts may be longer than
+      // the mean by that, and by a sixteenth.
+      const long long mean = r.per + (r.rem > 0);
+      if (count <= grid && mean < (1 << 28)) {
+        auto fits = [&](int len) {
+          int parts = 0;
+          for (int q = lane; q < end; q += 32) parts += u.items[q] * at_idiv(u.nch[q] + len - 1, len);
+          return __reduce_add_sync(kFull, parts) <= grid;
+        };
+        int least = (int)mean, most = least + 3 + (least >> 4);
+        if (fits(most)) {
+          while (least < most) {
+            const int mid = (least + most) >> 1;
+            if (fits(mid)) most = mid; else least = mid + 1;
+          }
+          r.len = least;
+        }
+      }
+    }
+    if (!r.len && me < r.ctas) {
+      r.x0 = r.start(me);
+      r.x1 = r.start(me + 1);
+    }
+    b = first = n = cached = nch = items = 0;
+    work = 0;
+    long long before = 0, at = r.len ? (long long)me : r.x0;   // what counts: parts, or tiles
+    for (int q0 = 0; q0 < end; q0 += 32) {
+      const int i = u.items[q0 + lane], t = u.nch[q0 + lane], per_item = r.len ? at_idiv(t + r.len - 1, r.len) : t;
+      const long long v = (long long)i * t, w = (long long)i * per_item;
+      long long incl = v, incl_w = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(kFull, incl, o), y = __shfl_up_sync(kFull, incl_w, o);
+        if (lane >= o) {
+          incl += x;
+          incl_w += y;
+        }
+      }
+      const long long place = at - before - (incl_w - w);
+      const unsigned mine = __ballot_sync(kFull, place >= 0 && place < w);
+      if (mine && (r.len || r.x0 < r.x1)) {
+        const int src = __ffs(mine) - 1;
+        b = q0 + src;
+        work += __shfl_sync(kFull, incl - v, src);
+        items = __shfl_sync(kFull, i, src);
+        nch = __shfl_sync(kFull, t, src);
+        if (r.len) {
+          const int pi = __shfl_sync(kFull, per_item, src), k0 = (int)__shfl_sync(kFull, place, src), item = at_idiv(k0, pi), k = k0 - item * pi;
+          const long long i0 = work + (long long)item * nch;
+          r.x0 = i0 + (long long)k * r.len;
+          r.x1 = min(r.x0 + r.len, i0 + nch);
+          r.c0 = me - k;
+          r.c1 = r.c0 + pi - 1;
+        }
+        lt_request(a, b, first, n, cached);
+        break;
+      }
+      work += __shfl_sync(kFull, incl, 31);
+      before += __shfl_sync(kFull, incl_w, 31);
+    }
+    share = r;
+  }
   // The part of an item that starts at place x, up to the end of the CTA's share; returns the place after it.
   // it.n = 0: there is nothing to do here.
-  __device__ __forceinline__ long long part(const LtArgs &p, long long x, const AtShare &share, LtItem &it) {
+  __device__ __forceinline__ long long part(const LtArgs &p, long long x, LtItem &it) {
     const LatArgs &a = p.a;
     while (n == 0 || x >= work + (long long)items * nch) {
       work += (long long)items * nch;
       b++;
       load(p);
     }
-    const int item = (int)at_div(x - work, nch), member = p.gang == 2 ? (int)blockIdx.x & 1 : 0, group = p.gang * item + member;
-    const long long item0 = work + (long long)item * nch, xe = min(share.x1, item0 + nch);
+    const int item = (int)at_div(x - work, nch), group = p.gang * item + member(p);
+    item0 = work + (long long)item * nch;
+    const long long xe = min(share.x1, item0 + nch);
     const int tg = p.hp == 2 ? group >> 1 : group;
     it.b = b;
     it.first = first;
@@ -262,29 +360,32 @@ struct LtCursor {
     it.tok0 = tg * p.per;
     it.toks = min(n - it.tok0, p.per);
     it.n = 0;
+    split = false;
     if (it.toks <= 0) return xe;                   // the place's second item is not there
     it.cached = cached;
     const int lim = min(a.max_pages << a.page_shift, cached + n);
     it.all = a.tree_mask ? cached : cached + it.tok0 + 1;
     it.end = min(lim, cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : it.tok0 + it.toks));
-    const int need = (it.end + kLtTile - 1) / kLtTile;                           // tiles of these rows
+    need = (it.end + kLtTile - 1) / kLtTile;       // tiles of these rows
     it.j0 = (int)(x - item0);
     it.n = max(0, min((int)(xe - item0), need) - it.j0);
     const bool whole = it.j0 == 0 && it.n == need;
     it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > share.x0);
     it.m0 = max(0, it.all / kLtTile - it.j0);
-    if (!whole && it.j0 == 0) {
-      // for the join, at the CTA that holds the first part: the last part of a CTA's share, so that there is one at most
-      int c0, c1;
-      share.ctas_of(item0, item0 + need - 1, c0, c1);
-      if (share.len) c1 = c0 + (need - 1) / share.len;
-      if ((threadIdx.x & 31) == 0) {
-        int4 *d = p.desc + 2 * blockIdx.x;
-        d[0] = make_int4(it.first, it.hpart, it.tok0, it.toks);
-        d[1] = make_int4(c0, c1, it.slot, member);
-      }
-    }
+    split = !whole && it.j0 == 0;
     return xe;
+  }
+  // For the join, at the CTA that holds the first part: the last part of a CTA's share, so that there is one at most.
+  __device__ __forceinline__ void describe(const LtArgs &p, const LtItem &it) {
+    if (!split) return;
+    int c0, c1;
+    share.ctas_of(item0, item0 + need - 1, c0, c1);
+    if (share.len) c1 = c0 + (need - 1) / share.len;
+    if ((threadIdx.x & 31) == 0) {
+      int4 *d = p.desc + 2 * blockIdx.x;
+      d[0] = make_int4(it.first, it.hpart, it.tok0, it.toks);
+      d[1] = make_int4(c0, c1, it.slot, member(p));
+    }
   }
 };
 
@@ -307,7 +408,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
   const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
   uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
 
-  if (warp == 0) {
+  // the first lengths: on their way while the barriers are set up
+  int lo = 0, hi = 0, held0 = 0;
+  if (warp == kLtWTma && lane < a.B) {
+    lo = __ldg(a.cu + lane);
+    hi = __ldg(a.cu + lane + 1);
+    held0 = __ldg(a.cached + lane);
+  }
+  if (warp == kLtWO) {
     if (lane < (int)NH) {
       mbar_init(&s.kv_full[lane], 1);
       mbar_init(&s.kv_empty[lane], 1);
@@ -343,79 +451,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     *reinterpret_cast<uint4 *>(generic0 + G::kQ + chunk * G::kQChunk + row * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 
-  // the CTA's share of the line
-  AtShare share;
-  LtCursor cur;
-  {
-    LtSetup &u = *reinterpret_cast<LtSetup *>(generic0);
-    long long total = 0;
-    int nitems = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kLtThreads) {
-      const int b = b0 + tid;
-      int items = 0;
-      long long v = 0;
-      if (b < a.B) {
-        int first, n, cached;
-        lt_request(a, b, first, n, cached);
-        u.n[b] = n;
-        u.cached[b] = cached;
-        items = lt_items(p, n);
-        v = (long long)items * lt_nch(a, n, cached);
-      }
-      long long incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += t;
-      }
-      items = __reduce_add_sync(kFull, items);
-      if (lane == 31) {
-        u.wsum2[warp] = incl;
-        u.wsum[warp] = items;
-      }
-      __syncthreads();
-      long long at = total;
-#pragma unroll
-      for (int w = 0; w < kLtThreads / 32; w++) {
-        at += w < warp ? u.wsum2[w] : 0;
-        total += u.wsum2[w];
-        nitems += u.wsum[w];
-      }
-      if (b < a.B) u.work[b] = at + incl - v;
-      __syncthreads();
-    }
-    const int grid = p.gang == 2 ? (int)gridDim.x >> 1 : (int)gridDim.x, me = p.gang == 2 ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
-    if (total <= grid) {                           // a tile a CTA: the line as it is
-      share.me = me;
-      share.len = share.c0 = share.c1 = 0;
-      share.ctas = (int)total;
-      share.per = 1;
-      share.rem = 0;
-      share.x0 = min((long long)me, total);
-      share.x1 = min((long long)me + 1, total);
-    } else {
-      // A part costs its CTA an epilogue and the join a source, some two tiles' time: equal parts may be longer than
-      // the mean by that, and by a sixteenth.
-      const long long mean = at_div(total + grid - 1, grid);
-      share = at_share<kLtThreads / 32>(
-          u.work, a.B, total, nitems, kLtMinTiles, u.cand, [&](int b) { return lt_items(p, u.n[b]); },
-          [&](int b) { return lt_nch(a, u.n[b], u.cached[b]); }, grid, me, 2 + (mean >> 4));
-    }
-    int lo = 0, hi = a.B - 1;                      // largest b with work[b] <= x0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (u.work[mid] <= share.x0) lo = mid; else hi = mid - 1;
-    }
-    cur.b = lo;
-    cur.work = u.work[lo];
-    cur.n = u.n[lo];
-    cur.cached = u.cached[lo];
-    cur.nch = lt_nch(a, cur.n, cur.cached);
-    cur.items = lt_items(p, cur.n);
-    cur.first = __ldg(a.cu + lo);
-    if (tid == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless LtCursor finds it
-  }
-  at_fence_async();                                // what was written here is written again by copies, or read by the MMAs
+  at_fence_async();                                // the MMAs read what was written here
   at_fence_before();
   __syncthreads();
   at_fence_after();
@@ -668,13 +704,18 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     const int box = min(a.page_shift, 6), np = kLtTile >> box, pg = lane & (np - 1), part = lane >> (6 - box);   // copies of 2^box tokens, 64 elements
     const uint32_t place = (uint32_t)pg << (box + 7);
     uint32_t pos = 0, tiles = 0;                   // halves and tiles so far
-    long long next = share.x0;
+    LtCursor cur;
+    if (lane == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);          // nothing to join, unless the cursor finds it
+    cur.find(p, *reinterpret_cast<LtSetup *>(generic0), lo, hi, held0);
+    at_fence_async();                              // copies come where the requests' tiles were counted
+    __syncwarp();
+    long long next = cur.share.x0;
     bool ok = true;
     for (int i = 0; ok; i++) {
       LtItem it;
       it.b = -1;
-      while (next < share.x1) {
-        next = cur.part(p, next, share, it);
+      while (next < cur.share.x1) {
+        next = cur.part(p, next, it);
         if (it.n > 0) break;
         it.b = -1;
       }
@@ -706,6 +747,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
                       &s.kv_full[slot]);
         }
         if (!ok) break;
+        if (j == 0) cur.describe(p, it);
         row = ahead;
       }
     }
@@ -844,9 +886,57 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
   }
 }
 
-// Joins the parts of the items that several CTAs took: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  A CTA
-// has one row of an item at a time: 128 threads four elements each, four times over the sources (k, k + 4, ...),
-// which are summed up in that order at the end.
+// Joins the parts of the items that several CTAs took: o = sum_k 2^(c (m_k - m)) O_k / sum_k 2^(c (m_k - m)) l_k.  128
+// threads have a row, four elements each.  Of items of up to 8 parts a CTA takes four rows at once, a fourth of its threads one each;
+// of items of more parts one row at a time, the fourths of the threads every fourth part, summed up in
+// that order at the end.  Latency bounds it: the parts lie in L2, and four loads of a thread wait together.
+constexpr int kLtJoinFew = 8;
+struct LtSum {
+  float top, sum;
+  float4 acc;
+  // parts k0, k0 + step, ... c1 of row r
+  template <int N>
+  __device__ __forceinline__ void add(const LtArgs &p, int4 d1, int k0, int step, int r, int d4, float c) {
+    for (; k0 <= d1.y; k0 += 4 * step) {
+      float2 st[4];
+      float4 u[4];
+      float t1 = top;
+#pragma unroll
+      for (int z = 0; z < 4; z++) {
+        const int k = k0 + step * z;
+        const size_t slot = k == d1.x ? d1.z : 2 * (k * p.gang + d1.w);
+        st[z] = make_float2(-INFINITY, 0.f);
+        u[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= d1.y) {
+          st[z] = __ldcg(p.stat + slot * N + r);
+          u[z] = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot * N + r) * kLatDim) + d4);
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < 4; z++) t1 = fmaxf(t1, st[z].x);
+      const float f0 = top == t1 ? 1.f : at_exp2((top - t1) * c);
+      top = t1;
+      sum *= f0;
+      acc.x *= f0;
+      acc.y *= f0;
+      acc.z *= f0;
+      acc.w *= f0;
+#pragma unroll
+      for (int z = 0; z < 4; z++) one(st[z], u[z], c);
+    }
+  }
+  // a part whose maximum is not above `top`
+  __device__ __forceinline__ void one(float2 st, float4 u, float c) {
+    if (st.x == -INFINITY && st.y == 0.f) return;  // the row sees nothing there
+    const float f = st.x == top ? 1.f : at_exp2((st.x - top) * c);
+    sum = fmaf(st.y, f, sum);
+    acc.x = fmaf(u.x, f, acc.x);
+    acc.y = fmaf(u.y, f, acc.y);
+    acc.z = fmaf(u.z, f, acc.z);
+    acc.w = fmaf(u.w, f, acc.w);
+  }
+};
+
 template <int N, bool F16>
 __global__ void __launch_bounds__(512) lat_join_kernel(const __grid_constant__ LtArgs p, int ctas) {
   __shared__ unsigned masks[kLtMaxSms / 32];
@@ -863,76 +953,37 @@ __global__ void __launch_bounds__(512) lat_join_kernel(const __grid_constant__ L
   int count = 0;
   for (int w = 0; w < words; w++) count += __popc(masks[w]);
   const float c = a.scale * 1.44269504088896340736f;
-  for (int unit = blockIdx.x; unit < count * N; unit += gridDim.x) {
-    int left = unit / N, w = 0;                    // the (unit / N)-th set bit
+  const int quads = count * (N / 4);
+  for (int unit = blockIdx.x; unit < 4 * quads; unit += gridDim.x) {
+    const int rr = unit / quads, quad = unit - rr * quads;
+    int left = quad / (N / 4), w = 0;              // the item: the left-th set bit
     while (left >= __popc(masks[w])) left -= __popc(masks[w++]);
     unsigned bits = masks[w];
     for (; left > 0; left--) bits &= bits - 1;
     const int which = 32 * w + __ffs(bits) - 1;
     const int4 d0 = __ldcg(p.desc + 2 * which), d1 = __ldcg(p.desc + 2 * which + 1);
-    const int r = unit % N, tl = (r * p.magic) >> 16, head = d0.y * p.hh + r - tl * p.hh;
-    if (tl >= p.per || tl >= d0.w || head >= a.heads) continue;
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = d1.x + sg; k0 <= d1.y; k0 += 16) {         // four sources at a time, so that their loads wait together
-      float2 st[4];
-      float4 u[4];
-      float t1 = top;
+    const bool few = d1.y - d1.x < kLtJoinFew;
+    if (few && rr > 0) continue;
+    const int r = 4 * (quad % (N / 4)) + (few ? sg : rr), tl = (r * p.magic) >> 16, head = d0.y * p.hh + r - tl * p.hh;
+    const bool valid = tl < p.per && tl < d0.w && head < a.heads;
+    LtSum t = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (valid) t.add<N>(p, d1, few ? d1.x : d1.x + sg, few ? 1 : 4, r, d4, c);
+    if (!few) {
+      acc4[sg][d4] = t.acc;
+      if (d4 == 0) stat4[sg] = make_float2(t.top, t.sum);
+      __syncthreads();
+      t = {fmaxf(fmaxf(stat4[0].x, stat4[1].x), fmaxf(stat4[2].x, stat4[3].x)), 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-      for (int z = 0; z < 4; z++) {
-        const int k = k0 + 4 * z;
-        const size_t slot = k == d1.x ? d1.z : 2 * (k * p.gang + d1.w);
-        st[z] = make_float2(-INFINITY, 0.f);
-        if (k <= d1.y) {
-          st[z] = __ldcg(p.stat + slot * N + r);
-          u[z] = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot * N + r) * kLatDim) + d4);
-        }
-      }
-#pragma unroll
-      for (int z = 0; z < 4; z++) t1 = fmaxf(t1, st[z].x);
-      const float f0 = top == t1 ? 1.f : at_exp2((top - t1) * c);
-      top = t1;
-      sum *= f0;
-      acc.x *= f0;
-      acc.y *= f0;
-      acc.z *= f0;
-      acc.w *= f0;
-#pragma unroll
-      for (int z = 0; z < 4; z++) {
-        if (st[z].x == -INFINITY && st[z].y == 0.f) continue;   // a part in which the row sees nothing, or none
-        const float f = at_exp2((st[z].x - t1) * c);
-        sum = fmaf(st[z].y, f, sum);
-        acc.x = fmaf(u[z].x, f, acc.x);
-        acc.y = fmaf(u[z].y, f, acc.y);
-        acc.z = fmaf(u[z].z, f, acc.z);
-        acc.w = fmaf(u[z].w, f, acc.w);
-      }
+      for (int z = 0; z < 4; z++) t.one(stat4[z], acc4[z][d4], c);
+      __syncthreads();
     }
-    acc4[sg][d4] = acc;
-    if (d4 == 0) stat4[sg] = make_float2(top, sum);
-    __syncthreads();
-    if (sg == 0) {
-      const float t1 = fmaxf(fmaxf(stat4[0].x, stat4[1].x), fmaxf(stat4[2].x, stat4[3].x));
-      sum = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int z = 0; z < 4; z++) {
-        if (stat4[z].x == -INFINITY && stat4[z].y == 0.f) continue;
-        const float f = stat4[z].x == t1 ? 1.f : at_exp2((stat4[z].x - t1) * c);
-        const float4 u = acc4[z][d4];
-        sum = fmaf(stat4[z].y, f, sum);
-        acc.x = fmaf(u.x, f, acc.x);
-        acc.y = fmaf(u.y, f, acc.y);
-        acc.z = fmaf(u.z, f, acc.z);
-        acc.w = fmaf(u.w, f, acc.w);
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (valid && (few || sg == 0)) {
+      const float inv = t.sum == 0.f ? 0.f : 1.f / t.sum;
       const long long row = d0.x + d0.z + tl;
       *reinterpret_cast<uint2 *>(a.out.p + row * a.out.row + (long long)head * a.out.head + 4 * d4) =
-          make_uint2(at_pack<F16>(acc.x * inv, acc.y * inv), at_pack<F16>(acc.z * inv, acc.w * inv));
-      if (a.lse && d4 == 0) a.lse[row * a.heads + head] = sum == 0.f ? -INFINITY : t1 * a.scale + logf(sum);
+          make_uint2(at_pack<F16>(t.acc.x * inv, t.acc.y * inv), at_pack<F16>(t.acc.z * inv, t.acc.w * inv));
+      if (a.lse && d4 == 0) a.lse[row * a.heads + head] = t.sum == 0.f ? -INFINITY : t.top * a.scale + logf(t.sum);
     }
-    __syncthreads();
   }
 }
 
@@ -1021,7 +1072,7 @@ cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStre
   lt_kernel(n, a.f16)<<<grid, kLtThreads, lt_smem(n), stream>>>(p);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * num_sms));
+  cfg.gridDim = dim3((unsigned)(4 * num_sms));
   cfg.blockDim = dim3(512);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
