@@ -109,7 +109,9 @@ struct ApGeom {
 // stages of 80 KB do not fit beside the 96 KB of Q, so the ring is of pieces, 128 tokens x 64 elements each: the value
 // tile's two, then the three of the key tile that S needs next.  A slot is free when its piece has been read for the last
 // time, so of the five pieces that a row tile's two products read, two of the next are there before and
-// three come while the other row tile's products run.
+// three come while the other row tile's products run.  A tile's pieces share a barrier (kv_full, four in turn):
+// beside the products, which read shared memory all the time, each look at one costs 100 to 200 cycles (8192 tokens of
+// 32 heads: 568 us with a barrier a piece).
 constexpr int kApPiece = kApTile * 128;
 struct ApLatGeom {
   static constexpr int kTileBytes = 2 * kApPiece;
@@ -174,7 +176,8 @@ struct ApSmem : ApSched<PAGED> {
   uint32_t tmem;
   int wsum[kApThreads / 32];
   ApItem item[2];
-  int v_pos[2][3];             // by item parity: stages of the masked value tiles, counted from the CTA's start
+  int v_pos[2][3], v_tile[2][3];   // by item parity: stages of the masked value tiles, counted from the CTA's start; latent:
+                               // their first pieces, and their places among the tiles
   float2 stat[2][kApTile];     // (m, l) of the twins of a prompt
   uint32_t bad[2][2][3][4];    // by item parity, scanning warp and masked tile: tokens with a non-finite v
   long long wsum2[kApThreads / 32];
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       // ---------------------------------------------------------- items and key/value tiles
       // over the cache every lane copies a page of the tile; else lane 0 the whole tile
       if (PAGED || lane == 0) {
-        int pos = 0;
+        int pos = 0, tiles = 0;                    // stages so far; latent: pieces, and tiles of keys and of values
         long long next = PAGED ? share.x0 : blockIdx.x;
         bool ok = true;
         // over the cache the warp waits as one; else lane 0 is alone
@@ -735,28 +738,36 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             auto take = [&](int z) {               // slot of piece pos + z, free
               const int at = pos + z;
               if (ok && at >= kStages) ok = wait(&s.kv_empty[at % kStages], (uint32_t)(at / kStages - 1) & 1u);
-              if (ok) mbar_arrive_expect_tx(&s.kv_full[at % kStages], (uint32_t)kApPiece + a.stall);
               return at % kStages;
             };
             for (int q = 0; q < n + ahead && ok; q++) {
               if (q >= ahead) {
                 const int s0 = take(0), s1 = take(1), j = q - ahead, row = it.first + j * kApTile;
                 if (!ok) break;
+                uint64_t *bar = &s.kv_full[tiles & 3];
+                mbar_arrive_expect_tx(bar, (uint32_t)(2 * kApPiece) + a.stall);
                 if (j >= it.m0) {                  // the scan may wait for these pieces now, as below
                   s.v_pos[i & 1][j - it.m0] = pos;
+                  s.v_tile[i & 1][j - it.m0] = tiles;
                   mbar_arrive(&s.v_posted[i & 1][j - it.m0]);
                 }
                 // elements 0 .. 63 lie in the lower slot
-                at_tma_3d(ring + min(s0, s1) * kApPiece, &p.vmap, 0, it.hk, row, &s.kv_full[min(s0, s1)]);
-                at_tma_3d(ring + max(s0, s1) * kApPiece, &p.vmap, 64, it.hk, row, &s.kv_full[max(s0, s1)]);
+                at_tma_3d(ring + min(s0, s1) * kApPiece, &p.vmap, 0, it.hk, row, bar);
+                at_tma_3d(ring + max(s0, s1) * kApPiece, &p.vmap, 64, it.hk, row, bar);
                 pos += 2;
+                tiles++;
               }
               if (q < n) {
                 const int row = it.first + q * kApTile;
+                uint64_t *bar = &s.kv_full[tiles & 3];
+                int slot = take(0);                // behind it nothing waits for the barrier's last phase any more
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar, (uint32_t)(3 * kApPiece) + a.stall);
+                tiles++;
                 for (int z = 0; z < 3; z++) {
-                  const int slot = take(0);
+                  if (z) slot = take(0);
                   if (!ok) break;
-                  at_tma_3d(ring + slot * kApPiece, z == 2 ? &p.rmap : &p.kmap, z == 2 ? 0 : 64 * z, z == 2 ? 0 : it.hk, row, &s.kv_full[slot]);
+                  at_tma_3d(ring + slot * kApPiece, z == 2 ? &p.rmap : &p.kmap, z == 2 ? 0 : 64 * z, z == 2 ? 0 : it.hk, row, bar);
                   pos++;
                 }
               }
@@ -805,8 +816,9 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
         }
         // copies in flight land before the CTA ends
-        for (int q = (pos > kStages ? pos - kStages : 0); q < pos; q++)
-          mbar_wait_bounded(&s.kv_full[q % kStages], (uint32_t)(q / kStages) & 1u, a.wait_ns);
+        const int rounds = LAT ? tiles : pos, bars = LAT ? 4 : kStages;
+        for (int q = (rounds > bars ? rounds - bars : 0); q < rounds; q++)
+          mbar_wait_bounded(&s.kv_full[q % bars], (uint32_t)(q / bars) & 1u, a.wait_ns);
         if (!PAGED && !TWINS) {
           // the last CTA to have taken its last item leaves the counters at zero
           __threadfence();
@@ -855,26 +867,23 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
         at_commit(&s.s_full[h]);
       };
-      uint32_t pos = 0;                            // latent: pieces so far
-      // Latent: S of row tile h from the pieces `at`, at + 1, at + 2, as they come; `last`: their last use
+      uint32_t pos = 0, tiles = 0;                 // latent: pieces and tiles so far
+      auto wait_tile = [&](uint32_t t) { wait(&s.kv_full[t & 3u], (t >> 2) & 1u); };
+      // Latent: S of row tile h from the pieces `at`, at + 1, at + 2, which are there; `last`: their last use.  By the elected lane.
       auto issue_s3 = [&](int h, int q, uint32_t at, bool last, bool q_last) {
+        uint64_t da = dq0 + (uint64_t)(q * (kQT >> 4));
+        uint32_t sl = at % kStages;
 #pragma unroll 1
-        for (uint32_t z = 0; z < 3; z++) {
-          const uint32_t sl = (at + z) % kStages;
-          wait(&s.kv_full[sl], ((at + z) / kStages) & 1u);
-          at_fence_after();
-          if (at_elect() && ok) {
-            const uint64_t da = dq0 + (uint64_t)((q * kQT + (int)z * kApPiece) >> 4), db = dk0 + (uint64_t)((sl * kApPiece) >> 4);
+        for (int z = 0; z < 3; z++) {
+          const uint64_t db = dk0 + (uint64_t)(sl * (kApPiece >> 4));
 #pragma unroll
-            for (int k = 0; k < 4; k++) at_mma_ss(tu + 128u * h, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, z > 0 || k > 0);
-            if (last) at_commit(&s.kv_empty[sl]);
-            if (z == 2) {
-              at_commit(&s.s_full[h]);
-              if (q_last) at_commit(&s.q_empty);
-            }
-          }
-          if (!all_ok()) return;
+          for (int k = 0; k < 4; k++) at_mma_ss(tu + 128u * h, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), id_s, k > 0 ? 1u : (uint32_t)(z > 0));
+          if (last) at_commit(&s.kv_empty[sl]);
+          da += (uint64_t)(kApPiece >> 4);
+          sl = sl + 1 == kStages ? 0 : sl + 1;
         }
+        at_commit(&s.s_full[h]);
+        if (q_last) at_commit(&s.q_empty);
       };
       for (int i = 0; ok; i++) {
         wait(&s.sched_full[i & 1], (uint32_t)(i >> 1) & 1u);
@@ -888,21 +897,25 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const int ahead = twin ? 2 : 1;            // S of tile j + ahead follows PV of tile j
         wait(&s.q_full, (uint32_t)i & 1u);
         if constexpr (LAT) {
-          if (!all_ok()) break;
-          for (int j = 0; j < ahead && j < n && ok; j++, pos += 3) {
+          for (int j = 0; j < ahead && j < n && ok; j++) {
             const bool q_last = j + 1 == n;
-            if (twin) {
-              issue_s3(j, 0, pos, true, q_last);
-            } else {
-              issue_s3(0, 0, pos, n1 == 0, q_last && n1 == 0);
-              if (n1 > 0 && ok) issue_s3(1, 1, pos, true, q_last);
+            wait_tile(tiles++);
+            at_fence_after();
+            if (at_elect() && ok) {
+              if (twin) {
+                issue_s3(j, 0, pos, true, q_last);
+              } else {
+                issue_s3(0, 0, pos, n1 == 0, q_last && n1 == 0);
+                if (n1 > 0) issue_s3(1, 1, pos, true, q_last);
+              }
             }
+            if (!all_ok()) break;
+            pos += 3;
           }
           for (int j = 0; j < n && ok; j++) {
-            const uint32_t at = pos;               // V[j] at pieces `at`, at + 1, and K[j + ahead] behind it
-            const uint32_t s0 = at % kStages, s1 = (at + 1) % kStages, lo = min(s0, s1), hi = max(s0, s1);
-            wait(&s.kv_full[s0], (at / kStages) & 1u);
-            wait(&s.kv_full[s1], ((at + 1) / kStages) & 1u);
+            // V[j] at pieces pos, pos + 1, and K[j + ahead] behind it
+            const uint32_t s0 = pos % kStages, s1 = s0 + 1 == kStages ? 0 : s0 + 1, lo = min(s0, s1), hi = max(s0, s1);
+            wait_tile(tiles++);
             if (j >= m0) {
               const int z = j - m0, bit = 3 * (i & 1) + z;   // z: 0, 1 or 2
               wait(&s.v_clean[i & 1][z], (clean >> bit) & 1u);
@@ -912,6 +925,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
             // the pair's second half of the elements is `hi - lo` slots on
             const uint64_t db = at_desc(ring + lo * kApPiece, (hi - lo) * kApPiece);
             const uint32_t add = j >= ahead;
+            bool keys = false;                     // K[j + ahead] is known to be there: waited for behind the first PV
             pos += 2;
 #pragma unroll
             for (int h = 0; h < 2; h++) {
@@ -919,27 +933,39 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
               if (twin ? (j & 1) == h : j < nh) {
                 uint32_t &np = h ? np1 : np0;
                 const bool more = twin ? j + 2 < n : j + 1 < nh, tail = twin || h || n1 == 0;   // the tile's last row tile
+                const bool q_last = tail && j + ahead + 1 == n, at_once = more && keys;
                 wait(&s.p_full[h], np);
                 np ^= 1u;
                 at_fence_after();
                 if (at_elect() && ok) {
                   const uint32_t oc = tu + 256u + 128u * h, pc = tu + 128u * h;
+                  if (left >= kApTile) {
+#pragma unroll
+                    for (int k = 0; k < kApTile / 16; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  } else {
 #pragma unroll 1
-                  for (int k = 0; k < kApTile / 16 && 16 * k < left; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                    for (int k = 0; 16 * k < left; k++) at_mma_ts(oc, pc + 8u * k, db + (uint64_t)(128u * k), id_o, k > 0 ? 1u : add);
+                  }
                   if (tail) {
                     at_commit(&s.kv_empty[lo]);
                     at_commit(&s.kv_empty[hi]);
                   }
                   if (!more) at_commit(&s.o_done[h]);
+                  if (at_once) issue_s3(h, twin ? 0 : h, pos, tail, q_last);
+                }
+                if (more && !at_once) {
+                  wait_tile(tiles);
+                  keys = true;
+                  at_fence_after();
+                  if (at_elect() && ok) issue_s3(h, twin ? 0 : h, pos, tail, q_last);
                 }
                 if (!all_ok()) break;
-                if (more) {
-                  issue_s3(h, twin ? 0 : h, pos, tail, tail && j + ahead + 1 == n);
-                  if (!ok) break;
-                }
               }
             }
-            if (j + ahead < n) pos += 3;
+            if (j + ahead < n) {
+              pos += 3;
+              tiles++;
+            }
           }
         } else {
           for (int j = 0; j < ahead && j < n; j++) {
@@ -1040,16 +1066,10 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           ok = at_wait(&s.v_posted[i & 1][z], (ph >> (i & 1)) & 1u, a, p.ctrl);
           if (!ok) break;
           const int pos = s.v_pos[i & 1][z], slot = pos % kStages;
-          ok = at_wait(&s.kv_full[slot], (uint32_t)(pos / kStages) & 1u, a, p.ctrl);
+          const int bar = LAT ? s.v_tile[i & 1][z] & 3 : slot;
+          ok = at_wait(&s.kv_full[bar], (uint32_t)(LAT ? s.v_tile[i & 1][z] >> 2 : pos / kStages) & 1u, a, p.ctrl);
           if (!ok) break;
-          int lo = 0, hi = 0;                      // latent: the slots of the tile's halves
-          if constexpr (LAT) {
-            const int next = (pos + 1) % kStages;
-            ok = at_wait(&s.kv_full[next], (uint32_t)((pos + 1) / kStages) & 1u, a, p.ctrl);
-            if (!ok) break;
-            lo = min(slot, next);
-            hi = max(slot, next);
-          }
+          const int next = (pos + 1) % kStages, lo = min(slot, next), hi = max(slot, next);   // latent: the slots of the tile's halves
           if (z == 0) posted[0] ^= 1u << (i & 1);
           else if (z == 1) posted[1] ^= 1u << (i & 1);
           else posted[2] ^= 1u << (i & 1);

@@ -6,7 +6,7 @@ its ring of pieces.
 waits for the last two of an item would meet it: the model shows why there are two."""
 import random
 
-from attn_barriers import Bar
+from attn_barriers import Aliased, Bar
 
 
 class Overwritten(Exception):
@@ -155,13 +155,13 @@ class Prompt:
     def __init__(self, count, items, stages=7):
         b = lambda name: Bar(name, count[name.split("[")[0]])  # noqa: E731
         self.items, self.stages = items, stages
-        self.kv_full, self.kv_empty = ([b(f"{n}[{i}]") for i in range(stages)] for n in ("kv_full", "kv_empty"))
+        self.kv_full, self.kv_empty = [b(f"kv_full[{i}]") for i in range(4)], [b(f"kv_empty[{i}]") for i in range(stages)]
         self.s_full, self.p_full, self.o_done, self.sched_full, self.sched_empty = (
             [b(f"{n}[{i}]") for i in range(2)] for n in ("s_full", "p_full", "o_done", "sched_full", "sched_empty"))
         self.q_full, self.q_empty = b("q_full"), b("q_empty")
         self.v_posted = [[b(f"v_posted[{p}][{z}]") for z in range(3)] for p in range(2)]
         self.v_clean = [[b(f"v_clean[{p}][{z}]") for z in range(3)] for p in range(2)]
-        self.v_pos, self.pipe, self.copies, self.q_copies, self.posted = {}, [], [], [], {}
+        self.v_tile, self.seen, self.pipe, self.copies, self.q_copies, self.posted = {}, {}, [], [], [], {}
         self.roles = {"copy": self.tma(), "mma": self.mma(), "help2": self.helper(2), "help3": self.helper(3)}
         for h in range(2):
             for w in range(4):
@@ -169,7 +169,7 @@ class Prompt:
         self.beside = {"pipe": self.pipe, "tiles": self.copies, "q": self.q_copies}
 
     def tma(self):
-        pos = 0
+        pos = tiles = 0
         for i, it in enumerate(self.items + [None]):
             if i >= 2:
                 yield self.sched_empty[i & 1], (i >> 1) - 1
@@ -179,42 +179,40 @@ class Prompt:
                 return
             n, ahead = it["n"], 2 if it["twin"] else 1
             for q in range(n + ahead):
-                if q >= ahead:
-                    for z in range(2):
+                for pieces in ([2] if q >= ahead else []) + ([3] if q < n else []):
+                    for z in range(pieces):
                         if pos + z >= self.stages:
                             yield self.kv_empty[(pos + z) % self.stages], (pos + z) // self.stages - 1
+                        if z == (1 if pieces == 2 else 0):       # armed: the copies' bytes are what completes it
+                            self.armed(tiles)
                     z = q - ahead - it["m0"]
-                    if z >= 0:
-                        self.v_pos[i & 1, z] = pos
+                    if pieces == 2 and z >= 0:
+                        self.v_tile[i & 1, z] = tiles
                         self.v_posted[i & 1][z].arrive()
-                    for z in range(2):
-                        self.copies.append(self.kv_full[(pos + z) % self.stages].arrive)
-                    pos += 2
+                    self.copies.append(self.kv_full[tiles & 3].arrive)
+                    pos += pieces
+                    tiles += 1
                     yield None
-                if q < n:
-                    for _ in range(3):
-                        if pos >= self.stages:
-                            yield self.kv_empty[pos % self.stages], pos // self.stages - 1
-                        self.copies.append(self.kv_full[pos % self.stages].arrive)
-                        pos += 1
-                        yield None
 
-    def full(self, at):
-        return self.kv_full[at % self.stages], at // self.stages
+    def armed(self, t):
+        """A barrier is armed for a tile when nobody waits for its last phase any more."""
+        if self.kv_full[t & 3].done != t >> 2 or self.seen.get(t - 4, 0) != (t - 4 >= 0):
+            raise Aliased(f"kv_full[{t & 3}] armed for tile {t}")
+
+    def full(self, t):
+        return self.kv_full[t & 3], t >> 2
 
     def mma(self):
         issue = self.pipe.append
-        pos, i, nps, clean = 0, 0, [0, 0], {}
+        pos, tiles, i, nps, clean = 0, 0, 0, [0, 0], {}
 
         def scores(h, at, last, q_last):
-            for z in range(3):
-                yield self.full(at + z)
-                if last:
+            if last:
+                for z in range(3):
                     issue(self.kv_empty[(at + z) % self.stages].arrive)
             issue(self.s_full[h].arrive)
             if q_last:
                 issue(self.q_empty.arrive)
-            yield None
         while True:
             yield self.sched_full[i & 1], i >> 1
             it = self.posted[i]
@@ -224,22 +222,28 @@ class Prompt:
             ahead = 2 if twin else 1
             yield self.q_full, i
             for j in range(min(ahead, n)):
+                yield self.full(tiles)
+                self.seen[tiles] = 1
+                tiles += 1
                 if twin:
-                    yield from scores(j, pos, True, j + 1 == n)
+                    scores(j, pos, True, j + 1 == n)
                 else:
-                    yield from scores(0, pos, n1 == 0, j + 1 == n and n1 == 0)
+                    scores(0, pos, n1 == 0, j + 1 == n and n1 == 0)
                     if n1 > 0:
-                        yield from scores(1, pos, True, j + 1 == n)
+                        scores(1, pos, True, j + 1 == n)
                 pos += 3
+                yield None
             for j in range(n):
                 at = pos
-                yield self.full(at)
-                yield self.full(at + 1)
+                yield self.full(tiles)
+                self.seen[tiles] = 1
+                tiles += 1
                 if j >= m0:
                     key = (i & 1, j - m0)
                     yield self.v_clean[key[0]][key[1]], clean.get(key, 0)
                     clean[key] = clean.get(key, 0) + 1
                 pos += 2
+                keys = False
                 for h, nh in enumerate((n0, n1)):
                     if (j & 1) == h if twin else j < nh:
                         more, tail = (j + 2 < n if twin else j + 1 < nh), twin or h or n1 == 0
@@ -250,11 +254,16 @@ class Prompt:
                             issue(self.kv_empty[(at + 1) % self.stages].arrive)
                         if not more:
                             issue(self.o_done[h].arrive)
-                        yield None
+                        if more and not keys:
+                            yield self.full(tiles)
+                            self.seen[tiles] = 1
+                            keys = True
                         if more:
-                            yield from scores(h, pos, tail, tail and j + ahead + 1 == n)
+                            scores(h, pos, tail, tail and j + ahead + 1 == n)
+                        yield None
                 if j + ahead < n:
                     pos += 3
+                    tiles += 1
             self.sched_empty[i & 1].arrive()
             i += 1
 
@@ -294,8 +303,7 @@ class Prompt:
                 key = (i & 1, z)
                 yield self.v_posted[i & 1][z], uses.get(key, 0)
                 uses[key] = uses.get(key, 0) + 1
-                yield self.full(self.v_pos[key])
-                yield self.full(self.v_pos[key] + 1)
+                yield self.full(self.v_tile[key])
                 self.v_clean[i & 1][z].arrive()
                 yield None
             self.sched_empty[i & 1].arrive()
