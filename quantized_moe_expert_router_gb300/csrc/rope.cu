@@ -16,7 +16,7 @@
 
 namespace moe {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 __device__ __forceinline__ float2 rope_unpack(uint32_t w, int f16) {
   if (f16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
@@ -29,12 +29,18 @@ __device__ __forceinline__ uint32_t rope_pack(float lo, float hi, int f16) {
   return r;
 }
 
-// A thread has one unit of 16 elements, which holds 8 pairs in either layout (half: 8
-// elements of the first half of the turned part and 8 of the second; interleaved: 16
-// in a row), of HP heads, so that the 8 sines and cosines serve HP heads and 2 HP loads of
-// 16 bytes wait together.  Threads of a row: array by array, units of a head side by side.
+// A thread has one unit of 16 elements, 8 of the first half of the turned part (or of the copied one) and the 8
+// in their place in the second half, which hold 8 pairs in either layout; of HP heads, so
+// that the 8 sines and cosines serve HP heads and 2 HP loads of 16 bytes wait together.
+// Threads of a row: array by array, units of a head side by side, then heads, a thread's own ones as far apart as the
+// threads reach: neighbouring threads touch neighbouring 16 bytes in every instruction.
+//
+// Bound: HBM.  16384 rows, q of 16 heads and k, v of 8 of 128: 40.6 us, 6.4 TB/s (a plain copy has 6.6 to 6.7); 16384
+// latent rows with q of 64 heads, 128 bytes of every 384: 49.4 us, 6.0 TB/s; 8192 rows, q of 24 heads and k of 4, half of
+// 128 elements turned: 18.1 us, 6.5 TB/s; one row 2.4 us, a launch.  Eight CTAs of 128 threads an SM (64 registers) keep
+// most loads in flight: with 6 and 10 CTAs the latent rows took 54.3 and 64.9 us, with 256 threads 57.3.
 template <bool F16, bool INTERLEAVED, int HP>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeArgs a) {
   const int i = blockIdx.y * kRopeThreads + threadIdx.x;
   const int r = i / a.per_row, t = blockIdx.x * a.rows_per_block + r;
   if (r >= a.rows_per_block || t >= a.T) return;
@@ -43,21 +49,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (int e = 1; e < kRopeSegs; e++) z += e < a.segs && k >= a.seg[e].first;
   const RopeSeg &s = a.seg[z];
   k -= s.first;
-  const int h0 = k / s.units * HP, u = k - k / s.units * s.units;
+  const int h0 = k / s.units, u = k - h0 * s.units, apart = (s.heads + HP - 1) / HP;   // first head, and from one to the next
   const bool turned = u < s.turned;
   const int pos = __ldg(a.positions + t);
   const int slot = s.cached ? __ldg(a.slots + t) : 0;
   // elements of the unit's two vectors
-  const int e0 = turned && !INTERLEAVED ? 8 * u : 16 * u;
-  const int e1 = turned && !INTERLEAVED ? e0 + a.pairs : e0 + 8;
+  const int e0 = turned ? 8 * u : 8 * (s.turned + u), e1 = e0 + 8 * (turned ? s.turned : s.units - s.turned);
   const uint16_t *src = s.src + t * s.src_row + h0 * s.src_head;
   uint4 x[HP], y[HP];
 #pragma unroll
   for (int h = 0; h < HP; h++) {
     x[h] = y[h] = make_uint4(0u, 0u, 0u, 0u);
-    if (h0 + h >= s.heads) continue;
-    x[h] = *reinterpret_cast<const uint4 *>(src + h * s.src_head + e0);
-    y[h] = *reinterpret_cast<const uint4 *>(src + h * s.src_head + e1);
+    if (h0 + h * apart >= s.heads) continue;
+    x[h] = *reinterpret_cast<const uint4 *>(src + h * apart * s.src_head + e0);
+    y[h] = *reinterpret_cast<const uint4 *>(src + h * apart * s.src_head + e1);
   }
   if (pos < 0 || (s.cached && (unsigned)slot >= (unsigned)a.num_slots)) return;
   uint16_t *dst = s.dst + h0 * s.dst_head;
@@ -67,7 +72,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     float cs[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) {
-      const int part = (int)(((uint64_t)(uint32_t)pos * a.turns[8 * u + e]) >> 32);   // turns times 2^32, signed
+      const int pair = !INTERLEAVED ? 8 * u + e : 4 * u + (e & 3) + (e & 4 ? 4 * s.turned : 0);
+      const int part = (int)(((uint64_t)(uint32_t)pos * a.turns[pair]) >> 32);        // turns times 2^32, signed
       const float angle = (float)part * (6.283185307179586f / 4294967296.f);
       sn[e] = __sinf(angle) * a.factor;
       cs[e] = __cosf(angle) * a.factor;
@@ -95,9 +101,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 #pragma unroll
   for (int h = 0; h < HP; h++) {
-    if (h0 + h >= s.heads) continue;
-    *reinterpret_cast<uint4 *>(dst + h * s.dst_head + e0) = x[h];
-    *reinterpret_cast<uint4 *>(dst + h * s.dst_head + e1) = y[h];
+    if (h0 + h * apart >= s.heads) continue;
+    *reinterpret_cast<uint4 *>(dst + h * apart * s.dst_head + e0) = x[h];
+    *reinterpret_cast<uint4 *>(dst + h * apart * s.dst_head + e1) = y[h];
   }
 }
 
@@ -107,7 +113,6 @@ void rope_args(const moe_rope &rope, int num_rows, const int32_t *positions, Rop
   a->T = num_rows;
   a->positions = positions;
   a->factor = rope.cfg.attn_factor;
-  a->pairs = rope.cfg.dims / 2;
   a->interleaved = rope.cfg.layout == MOE_ROPE_INTERLEAVED;
   a->f16 = rope.cfg.dtype == MOE_ATTN_F16;
 }
@@ -132,8 +137,9 @@ cudaError_t launch_rope(RopeArgs *a, cudaStream_t stream) {
   if (!a->segs || !a->T) return cudaSuccess;
   long long units = 0;
   for (int z = 0; z < a->segs; z++) units += (long long)a->seg[z].heads * a->seg[z].units;
-  // a thread a head until the GPU is full of threads, then one for 4
-  const int hp = units * a->T <= (1 << 18) ? 1 : 4;
+  // A thread a head until the GPU has some 400 of them an SM, then one for 4 heads, which need a fourth of the sines.  us with one
+  // and with 4 heads, 40 heads of 128 and 8 of v: 64 rows 2.6, 2.9; 256 rows 4.1, 3.2; 1024 rows 8.5, 5.2.
+  const int hp = units * a->T <= (1 << 16) ? 1 : 4;
   int per_row = 0;
   for (int z = 0; z < a->segs; z++) {
     a->seg[z].first = per_row;

@@ -34,7 +34,7 @@ struct RopeArgs {
   RopeSeg seg[kRopeSegs];
   const int32_t *positions, *slots;
   float factor;
-  int T, segs, per_row, rows_per_block, pairs, interleaved, f16, page_shift, num_slots;
+  int T, segs, per_row, rows_per_block, interleaved, f16, page_shift, num_slots;
 };
 
 void rope_args(const moe_rope &rope, int num_rows, const int32_t *positions, RopeArgs *a);
