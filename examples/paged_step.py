@@ -7,6 +7,7 @@ with prompts of different lengths; then every step verifies a small tree of
 drafted rows per stream:
 
     moe_kv_plan     pages, slots, positions and tree masks from the lengths
+    moe_rope_apply  queries and keys turned by the positions
     moe_kv_append   the rows' keys and values to their slots
     moe_attn_prompt (admission) or moe_attn_tree (verification)
     moe_route_forward
@@ -49,6 +50,7 @@ class Block:
         self.wqkv = (torch.randn((HIDDEN, width), generator=g, device=DEV) * HIDDEN ** -0.5).bfloat16()
         self.wo = (torch.randn((Q_HEADS * HEAD_DIM, HIDDEN), generator=g, device=DEV) * HIDDEN ** -0.5).bfloat16()
         self.attn = moe.Attention(Q_HEADS, KV_HEADS, HEAD_DIM, PAGE, POOL, TABLE)
+        self.rope = moe.Rope(HEAD_DIM)
         self.ws = moe.alloc_attn_workspace(self.attn, len(PROMPTS), rows)
         self.k_cache, self.v_cache = (torch.zeros((POOL, KV_HEADS, PAGE, HEAD_DIM), dtype=torch.bfloat16, device=DEV) for _ in range(2))
         self.layer = moe.Layer(EXPERTS, TOP_K, HIDDEN, INTERMEDIATE, rows)
@@ -98,7 +100,8 @@ def main(steps=3, accepted=None):
         slots, positions = (torch.empty(rows, dtype=torch.int32, device=DEV) for _ in range(2))
         mask = torch.empty(rows, dtype=torch.int64, device=DEV) if step else None
         moe.moe_kv_plan(attn, ints(cached), ints(fresh), free, table, cu, slots, positions, info, parents=parents, tree_mask=mask)
-        q, k, v = block.qkv(x)                        # a model would rotate q and k by `positions` here
+        q, k, v = block.qkv(x)
+        moe.moe_rope_apply(block.rope, positions, q, q, k, k)
         moe.moe_kv_append(attn, k, v, slots, block.k_cache, block.v_cache)
         out = torch.empty((rows, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=DEV)
         if step == 0:

@@ -602,13 +602,15 @@ moe_status moe_latent_plan(moe_latent_t lat, int num_requests, int num_rows, con
 
 /* Write latent rows into the cache and turn the rotary part of q beside it (one launch):
  * for every row t with a position >= 0 and a slot in range, c[t] (512) and the turned
- * k_rope[t] (64; the first `dims` turn) go to slot slots[t].  q, q_out: [num_rows][heads][64] or both
- * NULL, turned for every row with a position >= 0; q_out is q itself or does not
- * overlap the inputs.  The head stride of c and k_rope is not looked at.  Slots must
- * be distinct.  rope has the cache's dtype and dims <= 64. */
+ * k_rope[t] (64; the first `dims` turn) go to slot slots[t].  For every row with a position
+ * >= 0: q is turned into q_out ([num_rows][heads][64], both or neither NULL; q_out is q
+ * itself or does not overlap the inputs), and k_rope into k_out (as k_rope, or NULL; may
+ * not overlap the inputs), which moe_latent_prompt reads.  The head strides of c, k_rope
+ * and k_out are not looked at.  Slots must be distinct.  rope has the cache's dtype and
+ * dims <= 64. */
 moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, const int32_t *positions, const int32_t *slots,
                              const moe_attn_rows *c, const moe_attn_rows *k_rope, const moe_attn_rows *q,
-                             const moe_attn_rows *q_out, void *cache, cudaStream_t stream);
+                             const moe_attn_rows *q_out, const moe_attn_rows *k_out, void *cache, cudaStream_t stream);
 
 /* Expanded form, causal over whole prompts: for row i of request b and head h
  *   o[i] = sum_{j <= i} w_j v[j],  w = softmax_j(softmax_scale * (q[i] . [k[j] | k_rope[j]]))

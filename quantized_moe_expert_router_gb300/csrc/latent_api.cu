@@ -229,17 +229,19 @@ moe_status moe_latent_plan(moe_latent_t lat, int num_requests, int num_rows, con
 
 moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, const int32_t *positions, const int32_t *slots,
                              const moe_attn_rows *c, const moe_attn_rows *k_rope, const moe_attn_rows *q,
-                             const moe_attn_rows *q_out, void *cache, cudaStream_t stream) {
+                             const moe_attn_rows *q_out, const moe_attn_rows *k_out, void *cache, cudaStream_t stream) {
   if (!lat || !rope || num_rows < 0 || !q != !q_out) return MOE_ERR_INVALID_ARG;
   if (lat->device != rope->device || lat->cfg.dtype != rope->cfg.dtype) return MOE_ERR_INVALID_ARG;
   if (num_rows > MOE_ATTN_MAX_ROWS || rope->cfg.dims > kLatRope) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (num_rows == 0) return MOE_OK;
-  RowView vc, vk, vq, vo;
+  RowView vc, vk, vq, vo, vr;
   if (!row_view(c, num_rows, 1, kLatDim, &vc) || !row_view(k_rope, num_rows, 1, kLatRope, &vk) || !words(positions) ||
       !words(slots) || !given(cache))
     return MOE_ERR_INVALID_ARG;
   if (q && (!row_view(q, num_rows, lat->cfg.heads, kLatRope, &vq) || !row_view(q_out, num_rows, lat->cfg.heads, kLatRope, &vo)))
     return MOE_ERR_INVALID_ARG;
+  // k_rope is read for the cache by other threads than those that write k_out
+  if (k_out && (!row_view(k_out, num_rows, 1, kLatRope, &vr) || vr.p == vk.p)) return MOE_ERR_INVALID_ARG;
   RopeArgs a;
   rope_args(*rope, num_rows, positions, &a);
   a.slots = slots;
@@ -250,6 +252,7 @@ moe_status moe_latent_append(moe_latent_t lat, moe_rope_t rope, int num_rows, co
   rope_add(&a, seg_cache(vc, at, kLatRow, 0, page, 1, kLatDim / 16, 0));
   rope_add(&a, seg_cache(vk, at + kLatDim, kLatRow, 0, page, 1, kLatRope / 16, rope->cfg.dims / 16));
   if (q) rope_add(&a, seg_rows(vq, vo, lat->cfg.heads, kLatRope / 16, rope->cfg.dims / 16));
+  if (k_out) rope_add(&a, seg_rows(vk, vr, 1, kLatRope / 16, rope->cfg.dims / 16));
   DeviceGuard g(lat->device);
   if (!g.ok) return MOE_ERR_CUDA;
   return cuda_status(launch_rope(&a, stream));

@@ -27,7 +27,7 @@ struct RopeSeg {
   int first;                         // threads of a row before this array's
 };
 
-constexpr int kRopeSegs = 3;
+constexpr int kRopeSegs = 4;
 
 struct RopeArgs {
   uint64_t turns[kRopeMaxPairs];

@@ -162,7 +162,7 @@ def load_library(path: str = LIB_PATH):
             lib.moe_latent_tree.argtypes = [P, I32, I32, R, R, P, P, P, P, P, R, P, P, SZ, P]
             lib.moe_latent_prompt.argtypes = [P, I32, I32, R, R, R, R, P, R, P, P, SZ, P]
             lib.moe_latent_plan.argtypes = lib.moe_kv_plan.argtypes
-            lib.moe_latent_append.argtypes = [P, P, I32, P, P, R, R, R, R, P, P]
+            lib.moe_latent_append.argtypes = [P, P, I32, P, P, R, R, R, R, R, P, P]
             lib.moe_status_string.argtypes = [I32]
             lib.moe_status_string.restype = ctypes.c_char_p
             for name in EXPORTED[:-1]:
@@ -765,9 +765,10 @@ def _latent_cache(fn, lat, cache):
                          f"cuda:{lat.device}")
 
 
-def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_out=None, stream=None) -> None:
+def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_out=None, k_out=None, stream=None) -> None:
     """Latents c [rows][512] and turned key parts k_rope [rows][64] into their slots
-    of the cache; q [rows][heads][64] (the queries' rotary part) turned into q_out."""
+    of the cache; q [rows][heads][64] (the queries' rotary part) turned into q_out,
+    and k_rope into k_out as well (another array)."""
     fn, dev, T = "moe_latent_append", lat.device, positions.numel()
     _same(fn, lat, rope)
     if (positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev
@@ -782,7 +783,8 @@ def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_o
     _latent_cache(fn, lat, cache)
     status = _lib.moe_latent_append(
         lat.handle, rope.handle, T, positions.data_ptr(), slots.data_ptr(), _latent_row(fn, "c", lat, c, (T, LATENT_DIM)),
-        _latent_row(fn, "k_rope", lat, k_rope, (T, LATENT_ROPE)), qv, qo, cache.data_ptr(),
+        _latent_row(fn, "k_rope", lat, k_rope, (T, LATENT_ROPE)), qv, qo,
+        None if k_out is None else _latent_row(fn, "k_out", lat, k_out, (T, LATENT_ROPE)), cache.data_ptr(),
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(fn, status)

@@ -164,8 +164,12 @@ def test_latent_append_parity(rows, heads, dims, page, with_q):
     before = q.clone()
     cache = torch.full(lat.cache_shape, 7.0, dtype=dt, device=DEV)
     part = q[:, :, 128:] if with_q else None
-    moe.moe_latent_append(lat, rope, x[:, :512], x[:, 512:], pos, slots, cache, q=part, q_out=part)
+    ko = torch.full((rows, 72), 7.0, dtype=dt, device=DEV) if with_q else None
+    moe.moe_latent_append(lat, rope, x[:, :512], x[:, 512:], pos, slots, cache, q=part, q_out=part, k_out=ko[:, :64] if with_q else None)
     live = pos >= 0
+    if with_q:                                       # every row with a position, slot or none
+        ref.check(ko[live][:, None, :64], [w[live] for w in ref.turn(x[:, None, 512:], pos, f, True, 1.25)], "k_out")
+        assert (ko[~live] == 7.0).all() and (ko[:, 64:] == 7.0).all()
     if with_q:
         ref.check(q[:, :, 128:], ref.turn(before[:, :, 128:], pos, f, True, 1.25), "q")
     assert torch.equal(q[:, :, :128], before[:, :, :128]) and torch.equal(q[~live], before[~live])
@@ -247,3 +251,8 @@ def test_refusals():
         moe.moe_latent_append(lat, rope, c[:, :512], c[:, 512:], pos, pos[:2], cache)
     with pytest.raises(ValueError, match="c of shape"):
         moe.moe_latent_append(lat, rope, c, c[:, 512:], pos, pos, cache)
+    with pytest.raises(ValueError, match="k_out of shape"):
+        moe.moe_latent_append(lat, rope, c[:, :512], c[:, 512:], pos, pos, cache, k_out=c)
+    with pytest.raises(moe.MoEError) as e:                         # in place: the cache's threads read it
+        moe.moe_latent_append(lat, rope, c[:, :512], c[:, 512:], pos, pos, cache, k_out=c[:, 512:])
+    assert e.value.status == 1

@@ -92,7 +92,7 @@ def test_null_and_negative_arguments_are_refused():
     assert lib.moe_rope_apply(r.handle, 1, 64, 16, 1, moe._pack_rows(24, 64, 64), rows, 0, None, None, None) == 1
     assert lib.moe_rope_apply(r.handle, 0, 64, None, 1, None, None, 0, None, None, None) == 0
     assert lib.moe_rope_append(None, r.handle, 1, 16, 16, rows, rows, rows, rows, 16, 16, None) == 1
-    assert lib.moe_latent_append(None, r.handle, 1, 16, 16, rows, rows, None, None, 16, None) == 1
+    assert lib.moe_latent_append(None, r.handle, 1, 16, 16, rows, rows, None, None, None, 16, None) == 1
 
 
 @pytest.mark.parametrize("kw,status", [
