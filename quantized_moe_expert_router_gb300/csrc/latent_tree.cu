@@ -22,8 +22,8 @@
 //   warp 0           tiles, 64 elements x a page a copy (128-byte swizzle): two halves of 64 x 256 elements into a
 //                    ring of 4 or 5, and with the second the key part into one of 2 or 3; takes the items
 //   warps 1, 3       MMA issue of S and of O: the products read shared memory all the time, which makes every wait's
-//                    look at a barrier slow, so one's products fill the other's waits (one issuer that takes what is ready: 163 us
-//                    where two have TBD, 16 tokens at up to 100000 of 64 heads)
+//                    look at a barrier slow (100 to 200 cycles), so one's products fill the other's waits (one issuer that
+//                    takes what is ready: 163 us where two have 154, 16 tokens at up to 100000 of 64 heads)
 //   warp 2           Q rows by boxes (64, heads, tokens)
 //   warps 4-7, 8-11  softmax of rows 0 .. N/2 - 1 and N/2 .. N - 1: a warp has 16 tokens, a thread two
 //                    of them and a quarter of the warp's rows (the fragment shape: an accumulator of 64 rows fills 16 of a
@@ -38,6 +38,8 @@
 // the line to two CTAs, which read the same tiles at the same time: the second one from L2.  A
 // part of an item goes to the workspace (fp32 O, m, l); lat_join_kernel joins them in the order of the context.
 //
+// Where contexts are short or items many, an item is not cut: there is nothing to join then.
+//
 // A token that a row does not see has P = 0, but 0 times an infinite or NaN latent is NaN: in
 // tiles with tokens that not every row sees the softmax warps zero such elements after S, note the token, and
 // the epilogue makes these elements NaN in the rows that do see it.
@@ -50,14 +52,17 @@
 //   kv_empty      waited for by the copy warp, whose lanes meet before they copy
 //   q_full        filled again behind q_empty; q_empty is waited for by warp 2 alone, and without that Q there is no next
 //   s_full        (tile parity) S of tile t + 2 is issued behind p_full of tile t
-//   p_full        (tile parity) P of tile t + 2 follows its S, which the S warp issues after p_full of tile t has been waited
-//                 for, and its tile, whose second half lies where one of tile t - 1 or t lay: the O warp has waited for
-//                 p_full of that tile, hence of tile t - 1 at least; and S of tile t + 2 ... TBD
+//   p_full        (tile parity) P of tile t + 2 follows its S.  That S comes after the S warp has waited for p_full of tile t,
+//                 and needs the whole tile t + 2, whose second half lies where one of tile t lay: behind the O warp's wait
+//                 for p_full of tile t.
 //   pv_done       (tile parity) tile t lies, with its second half, where one of tile t - 3 or t - 2 lay, so with S of tile t the
 //                 products of tile t - 3 are done: a warp that has it may wait for those of tile t - 1, and then for those
 //                 of tile t; the next ones on these barriers need P that it has not given
 // The softmax warps of a half also meet at a named barrier: a warp whose wait ran out goes on to
 // the next vote, which tells the others, and all four end together.
+//
+// Bound: for up to 64 rows HBM, or the copies' latency behind a ring of two tiles; for more the tensor pipe's reads of shared
+// memory (a tile's products alone take 1970 cycles at N = 64, 1490 at N = 16; FINAL).
 #include <limits.h>
 #include <math.h>
 #include <stddef.h>
@@ -98,6 +103,8 @@ struct LtArgs {
   int per;                     // tokens of an item
   int gang;                    // CTAs (1 or 2) to a place of the line
   int magic;                   // ceil(2^16 / hh)
+  int whole;                   // items are not cut: no parts, no join
+  int slack;                   // tiles by which equal parts may be longer than the mean
   int4 *desc;                  // per CTA, of the item whose first part it holds and others the rest:
                                // (first, head part, tok0, toks), (first group, last group, its slot, place in the group)
   float *part;                 // [2 * grid][N][512]  O of a part
@@ -233,17 +240,22 @@ __device__ __forceinline__ void lt_request(const LatArgs &a, int b, int &first, 
 // Walks the line of tiles from the CTA's share on.
 struct LtCursor {
   AtShare share;
-  int b, first, n, cached, nch, items;
-  long long work;              // tiles of the requests before b
+  int b, first, n, cached, items;
+  int places;                  // of an item of b in the line
+  bool few;                    // items that are not cut, at most one for a CTA
+  long long work;              // places of the requests before b
   // of the last part, when it is the first of several: what the join has to know
   bool split;
   int need;
   long long item0;
   __device__ __forceinline__ void load(const LtArgs &p) {
     lt_request(p.a, b, first, n, cached);
-    nch = lt_nch(p.a, n, cached);
+    places = per_item(p, lt_nch(p.a, n, cached));
     items = lt_items(p, n);
   }
+  // An item's places are its tiles.  One that is not cut is that CTA's in whose share it starts; it has three places more, its
+  // epilogue's and its first copies' time, or a single place where there is a CTA for each.
+  __device__ __forceinline__ int per_item(const LtArgs &p, int tiles) const { return !p.whole ? tiles : (few ? 1 : tiles + 3); }
   __device__ __forceinline__ int member(const LtArgs &p) const { return p.gang == 2 ? (int)blockIdx.x & 1 : 0; }
   // The share of this CTA, by one warp: a chain of a few hundred cycles a step, and of one look at each request, while the
   // other warps have nothing to do yet.  (lo, hi, held): cu, cu + 1 and cached of request `lane`.
@@ -263,12 +275,14 @@ struct LtCursor {
       const int i = rows ? lt_items(p, rows) : 0, t = rows ? lt_nch(a, rows, c) : 0;
       u.items[r] = i;
       u.nch[r] = t;
-      total += (long long)i * t;
+      total += (long long)i * (p.whole ? t + 3 : t);
       count += i;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
     count = __reduce_add_sync(kFull, count);
+    few = p.whole && count <= grid;
+    if (few) total = count;
     __syncwarp();
     AtShare r;
     r.me = me;
@@ -279,16 +293,16 @@ struct LtCursor {
     if (total > grid) {
       r.per = at_div(total, grid);
       r.rem = total - r.per * grid;
-      // A part costs its CTA an epilogue and the join a source, some three tiles' time: equal parts may be longer than
-      // the mean by that, and by a sixteenth.
+      // A share of the line that ends within items is two parts and more, with an epilogue each (with 64 rows some two tiles' time)
+      // and a source of the join: equal parts may be longer than the mean by that.
       const long long mean = r.per + (r.rem > 0);
-      if (count <= grid && mean < (1 << 28)) {
+      if (!p.whole && count <= grid && mean < (1 << 28)) {
         auto fits = [&](int len) {
           int parts = 0;
           for (int q = lane; q < end; q += 32) parts += u.items[q] * at_idiv(u.nch[q] + len - 1, len);
           return __reduce_add_sync(kFull, parts) <= grid;
         };
-        int least = (int)mean, most = least + 3 + (least >> 4);
+        int least = (int)mean, most = least + p.slack;
         if (fits(most)) {
           while (least < most) {
             const int mid = (least + most) >> 1;
@@ -302,12 +316,12 @@ struct LtCursor {
       r.x0 = r.start(me);
       r.x1 = r.start(me + 1);
     }
-    b = first = n = cached = nch = items = 0;
+    b = first = n = cached = places = items = 0;
     work = 0;
     long long before = 0, at = r.len ? (long long)me : r.x0;   // what counts: parts, or tiles
     for (int q0 = 0; q0 < end; q0 += 32) {
-      const int i = u.items[q0 + lane], t = u.nch[q0 + lane], per_item = r.len ? at_idiv(t + r.len - 1, r.len) : t;
-      const long long v = (long long)i * t, w = (long long)i * per_item;
+      const int i = u.items[q0 + lane], t = i ? per_item(p, u.nch[q0 + lane]) : 0, unit = r.len ? at_idiv(t + r.len - 1, r.len) : t;
+      const long long v = (long long)i * t, w = (long long)i * unit;
       long long incl = v, incl_w = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -324,12 +338,12 @@ struct LtCursor {
         b = q0 + src;
         work += __shfl_sync(kFull, incl - v, src);
         items = __shfl_sync(kFull, i, src);
-        nch = __shfl_sync(kFull, t, src);
+        places = __shfl_sync(kFull, t, src);
         if (r.len) {
-          const int pi = __shfl_sync(kFull, per_item, src), k0 = (int)__shfl_sync(kFull, place, src), item = at_idiv(k0, pi), k = k0 - item * pi;
-          const long long i0 = work + (long long)item * nch;
+          const int pi = __shfl_sync(kFull, unit, src), k0 = (int)__shfl_sync(kFull, place, src), item = at_idiv(k0, pi), k = k0 - item * pi;
+          const long long i0 = work + (long long)item * places;
           r.x0 = i0 + (long long)k * r.len;
-          r.x1 = min(r.x0 + r.len, i0 + nch);
+          r.x1 = min(r.x0 + r.len, i0 + places);
           r.c0 = me - k;
           r.c1 = r.c0 + pi - 1;
         }
@@ -345,14 +359,14 @@ struct LtCursor {
   // it.n = 0: there is nothing to do here.
   __device__ __forceinline__ long long part(const LtArgs &p, long long x, LtItem &it) {
     const LatArgs &a = p.a;
-    while (n == 0 || x >= work + (long long)items * nch) {
-      work += (long long)items * nch;
+    while (n == 0 || x >= work + (long long)items * places) {
+      work += (long long)items * places;
       b++;
       load(p);
     }
-    const int item = (int)at_div(x - work, nch), group = p.gang * item + member(p);
-    item0 = work + (long long)item * nch;
-    const long long xe = min(share.x1, item0 + nch);
+    const int item = (int)at_div(x - work, places), group = p.gang * item + member(p);
+    item0 = work + (long long)item * places;
+    const long long xe = p.whole ? item0 + places : min(share.x1, item0 + places);
     const int tg = p.hp == 2 ? group >> 1 : group;
     it.b = b;
     it.first = first;
@@ -361,14 +375,14 @@ struct LtCursor {
     it.toks = min(n - it.tok0, p.per);
     it.n = 0;
     split = false;
-    if (it.toks <= 0) return xe;                   // the place's second item is not there
+    if (it.toks <= 0 || (p.whole && x > item0)) return xe;   // the place's second item is not there; the item is another CTA's
     it.cached = cached;
     const int lim = min(a.max_pages << a.page_shift, cached + n);
     it.all = a.tree_mask ? cached : cached + it.tok0 + 1;
     it.end = min(lim, cached + (a.tree_mask ? min(n, MOE_ATTN_MAX_TREE) : it.tok0 + it.toks));
     need = (it.end + kLtTile - 1) / kLtTile;       // tiles of these rows
     it.j0 = (int)(x - item0);
-    it.n = max(0, min((int)(xe - item0), need) - it.j0);
+    it.n = p.whole ? need : max(0, min((int)(xe - item0), need) - it.j0);
     const bool whole = it.j0 == 0 && it.n == need;
     it.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > share.x0);
     it.m0 = max(0, it.all / kLtTile - it.j0);
@@ -408,13 +422,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
   const uint32_t smem0 = (smem_u32(dsm) + 1023u) & ~1023u;
   uint8_t *const generic0 = dsm + (smem0 - smem_u32(dsm));
 
-  // the first lengths: on their way while the barriers are set up
-  int lo = 0, hi = 0, held0 = 0;
-  if (warp == kLtWTma && lane < a.B) {
-    lo = __ldg(a.cu + lane);
-    hi = __ldg(a.cu + lane + 1);
-    held0 = __ldg(a.cached + lane);
-  }
   if (warp == kLtWO) {
     if (lane < (int)NH) {
       mbar_init(&s.kv_full[lane], 1);
@@ -451,6 +458,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     *reinterpret_cast<uint4 *>(generic0 + G::kQ + chunk * G::kQChunk + row * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 
+  pdl_wait();                                      // the kernel before is done: what follows reads its results
+  int lo = 0, hi = 0, held0 = 0;
+  if (warp == kLtWTma && lane < a.B) {
+    lo = __ldg(a.cu + lane);
+    hi = __ldg(a.cu + lane + 1);
+    held0 = __ldg(a.cached + lane);
+  }
   at_fence_async();                                // the MMAs read what was written here
   at_fence_before();
   __syncthreads();
@@ -528,20 +542,24 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
             seen[z] = (uint32_t)(sees >> (h * NC));
           }
           hide();
-          // the products take tokens in groups of 16, up to the last that some row sees; a thread a token and a pair
-          const int st = tid - 32 * kLtWSoft, t = st & 63, tok = tile0 + t;
-          if (ok && j >= it.m0 && tok >= it.all && tok < ((it.end + 15) & ~15)) {
-            const uint32_t pair = (uint32_t)(st >> 6), pos = 2u * ns + (pair >> 1), slot = pos % NH;
-            uint8_t *const from = generic0 + slot * kLtHalf + (pair & 1u) * kLtPair + t * 128;
-            if (mbar_try_wait(&s.kv_full[slot], (pos / NH) & 1u)) {            // has completed: S needed it; orders the copies before the loads
-              for (int e = 0; e < 16; e++) {
-                uint4 *at = reinterpret_cast<uint4 *>(from + (e >> 3) * kLtChunk + ((e & 7) ^ (t & 7)) * 16);
+          // The products take tokens in groups of 16, up to the last that some row sees: of those that not every row sees, all 256
+          // threads look at 16 bytes each, so that a few tokens at a context's end cost one look.
+          const int t0 = max(0, it.all - tile0), t1 = min(kLtTile, ((it.end + 15) & ~15) - tile0);
+          if (ok && j >= it.m0 && t0 < t1) {
+            const uint32_t pos = 2u * ns, slot[2] = {pos % NH, (pos + 1) % NH};
+            // have completed: S needed them; orders the copies before the loads
+            if (mbar_try_wait(&s.kv_full[slot[0]], (pos / NH) & 1u) && mbar_try_wait(&s.kv_full[slot[1]], ((pos + 1) / NH) & 1u)) {
+#pragma unroll 4
+              for (int e = 64 * t0 + tid - 32 * kLtWSoft; e < 64 * t1; e += 256) {
+                const int t = e >> 6, z = e & 63;  // token, 16 bytes of its latent
+                uint4 *at = reinterpret_cast<uint4 *>(generic0 + (z & 32 ? slot[1] : slot[0]) * kLtHalf + ((z >> 3) & 3) * kLtChunk + t * 128 +
+                                                      ((z & 7) ^ (t & 7)) * 16);
                 const uint4 w = *at;
                 const uint32_t g[4] = {at_nonfinite<F16>(w.x), at_nonfinite<F16>(w.y), at_nonfinite<F16>(w.z), at_nonfinite<F16>(w.w)};
                 if (g[0] | g[1] | g[2] | g[3]) {
                   uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                  for (int z = 0; z < 4; z++) u[z] &= ~(((g[z] >> 15) & 0x00010001u) * 0xFFFFu);
+                  for (int y = 0; y < 4; y++) u[y] &= ~(((g[y] >> 15) & 0x00010001u) * 0xFFFFu);
                   *at = make_uint4(u[0], u[1], u[2], u[3]);
                   atomicOr(&s.bad[i & 1][j - it.m0][t >> 5], 1u << (t & 31));
                 }
@@ -705,7 +723,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     const uint32_t place = (uint32_t)pg << (box + 7);
     uint32_t pos = 0, tiles = 0;                   // halves and tiles so far
     LtCursor cur;
-    if (lane == 0) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);          // nothing to join, unless the cursor finds it
+    if (lane == 0 && !p.whole) p.desc[2 * blockIdx.x + 1] = make_int4(0, -1, 0, 0);   // nothing to join, unless the cursor finds it
     cur.find(p, *reinterpret_cast<LtSetup *>(generic0), lo, hi, held0);
     at_fence_async();                              // copies come where the requests' tiles were counted
     __syncwarp();
@@ -1060,6 +1078,20 @@ cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStre
   const int n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
   p.per = n / p.hh;
   p.gang = p.hp == 2 || mean > p.per ? 2 : 1;
+  if (num_sms > kLtMaxSms) num_sms = kLtMaxSms;
+  const int grid = p.gang == 2 ? (num_sms < 2 ? 2 : num_sms & ~1) : num_sms;
+  p.slack = 3 + n / 32;
+  // Items stay whole where that costs less than parts and their join: in tiles' time (1.25 us) 2.4, and the parts' way
+  // through L2, up to 4 for one of 64 rows on every SM and twice that where a CTA has several items.  It costs, where every item
+  // has a CTA, the tiles of the longest above a CTA's share (the longest is what the block table has room for, the mean
+  // taken to be 0.6 of it); else half of an item at the end, a fifth where a CTA has many.  us whole and cut:
+  //   1 row of 16 heads at 120 tokens 10.1, 11.6, at 250 13.1, 11.4; 64 requests of up to 250 13.9, 16.3, of up to 500 20.0, 18.5
+  //   64 heads, 64 requests of up to 500 24.5, 30.8, of up to 1000 36.9, 33.8; 512 of up to 2000 156, 181, of up to 4000 283, 268
+  //   8 trees of 8 and 64 heads at up to 250 18.0, 20.6, at up to 500 24.4, 22.2; 64 of them at up to 2000 93, 110, 4000 186, 149
+  const double places = grid / p.gang, tiles = (double)(((long long)a.max_pages << a.page_shift) + kLtTile - 1) / kLtTile;
+  const double items = (double)a.B * ((p.hp * ((mean + p.per - 1) / p.per) + p.gang - 1) / p.gang);
+  const double share = 0.6 * items * tiles / places, parts = items > places ? 2 : (items * tiles < places ? items * tiles / places : 1);
+  p.whole = (items > places ? (items > 2 * places ? 0.2 : 0.5) * tiles : tiles - (share > 1 ? share : 1)) <= 2.4 + 4 * (n / 64.) * parts;
   const cuuint64_t cdims[2] = {(cuuint64_t)kLatRow, (cuuint64_t)a.num_pages << a.page_shift};
   const cuuint64_t cstride[1] = {2 * kLatRow};
   const cuuint32_t cbox[2] = {64, (cuuint32_t)(a.page_shift < 6 ? 1 << a.page_shift : kLtTile)};
@@ -1067,19 +1099,20 @@ cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStre
   if (err == cudaSuccess) err = lt_encode_rows(&p.qmap, a.q, kLatDim, p);
   if (err == cudaSuccess) err = lt_encode_rows(&p.rmap, a.q_rope, kLatRope, p);
   if (err != cudaSuccess) return err;
-  if (num_sms > kLtMaxSms) num_sms = kLtMaxSms;
-  const int grid = p.gang == 2 ? (num_sms < 2 ? 2 : num_sms & ~1) : num_sms;
-  lt_kernel(n, a.f16)<<<grid, kLtThreads, lt_smem(n), stream>>>(p);
-  if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(4 * num_sms));
-  cfg.blockDim = dim3(512);
-  cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kLtThreads);
+  cfg.dynamicSmemBytes = (size_t)lt_smem(n);
+  if ((err = cudaLaunchKernelEx(&cfg, lt_kernel(n, a.f16), p)) != cudaSuccess || p.whole) return err;
+  cfg.gridDim = dim3((unsigned)(4 * num_sms));
+  cfg.blockDim = dim3(512);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, lt_join(n, a.f16), p, grid);
 }
 
