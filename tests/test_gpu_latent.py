@@ -288,6 +288,69 @@ def test_lengths_past_the_block_table_are_cut():
     attn_ref.check(*c.run(), ref.attend(c.q, x, x[:, :, :512], vis, SCALE))
 
 
+@pytest.mark.parametrize("heads,cached,fresh", [
+    (16, [(31 * i) % 250 for i in range(17)], [1] * 17), (64, [(53 * i) % 500 for i in range(70)], [1] * 70),
+    (64, [200, 90, 30, 7], [8, 3, 8, 1]), (128, [(17 * i) % 130 for i in range(90)], [1 + i % 3 for i in range(90)]), (5, [70], [20]),
+])
+def test_items_whole_and_cut(heads, cached, fresh):
+    """The table's width decides whether items are cut: the same requests in a table as wide as they need and in a wide one."""
+    c = Latent(heads, 16, torch.bfloat16, cached, fresh, seed=30)
+    mask = random_words(fresh, 7)
+    want = c.want(mask)
+    attn_ref.check(*c.run(mask), want, "narrow")
+    more = torch.full((len(fresh), 3000), -1, dtype=torch.int32, device=DEV)
+    c.table = torch.cat([c.table, more], 1)
+    c.lat = moe.LatentAttention(heads, 16, c.cache.shape[0], c.table.shape[1], c.dt)
+    attn_ref.check(*c.run(mask), want, "wide")
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each: the same bits as one after the other."""
+    cs = [Latent(64, 32, torch.bfloat16, [9000, 700], [2, 1], seed=31), Latent(16, 16, torch.bfloat16, [3000] * 20, [1] * 20, seed=32)]
+    alone = [c.run() for c in cs]
+    streams, outs = [torch.cuda.Stream() for _ in cs], [torch.empty_like(a[0]) for a in alone]
+    spaces = [moe.alloc_latent_workspace(c.lat, 20, 20) for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, o, w in zip(cs, streams, outs, spaces):
+            moe.moe_latent_tree(c.lat, c.q[:, :, :512], c.q[:, :, 512:], c.cu, c.cached, c.table, c.cache, o, w, stream=s)
+    torch.cuda.synchronize()
+    for c, o, a, w in zip(cs, outs, alone, spaces):
+        assert torch.equal(o, a[0]) and moe.moe_latent_get_device_status(c.lat, w) == 0
+
+
+def test_results_follow_the_kernel_before():
+    """The call's kernels may start before the kernel ahead of them in the stream ends: they read its results all the same."""
+    c = Latent(16, 16, torch.bfloat16, [400, 30], [1, 2], seed=33)
+    want, q = c.run()[0], c.q.clone()
+    ws, out = moe.alloc_latent_workspace(c.lat, 2, 3), torch.empty((3, 16, 512), dtype=c.dt, device=DEV)
+    big = torch.randn((1 << 24,), device=DEV)
+    for _ in range(10):
+        c.q.zero_()
+        big.mul_(1.0)
+        c.q.copy_(q)
+        moe.moe_latent_tree(c.lat, c.q[:, :, :512], c.q[:, :, 512:], c.cu, c.cached, c.table, c.cache, out, ws)
+        got = out.clone()
+        assert torch.equal(got, want)
+
+
+def test_latent_plan_is_the_plan_of_its_pages():
+    cached, fresh, parents = [40, 0, 17], [5, 3, 64], [-1, 0, 0, 1, 3, -1, -1, 1] + [i - 1 for i in range(64)]
+    lat, attn = moe.LatentAttention(8, 16, 40, 8), moe.Attention(8, 2, 64, 16, 40, 8)
+    table = np.full((3, 8), -1, np.int32)
+    table[0, :3], table[2, :2] = [3, 1, 2], [9, 4]
+    got = []
+    for call, handle in ((moe.moe_latent_plan, lat), (moe.moe_kv_plan, attn)):
+        t, cu, slots, positions = ints(table.tolist()), ints([0] * 4), ints([-7] * 80), ints([-7] * 80)
+        words, info = torch.full((80,), -7, dtype=torch.int64, device=DEV), ints([0] * 4)
+        call(handle, ints(cached), ints(fresh), ints(list(range(10, 40))), t, cu, slots, positions, info, parents=ints(parents + [-1] * 8), tree_mask=words)
+        got.append([x.cpu().numpy() for x in (t, cu, slots, positions, words, info)])
+    want = attn_ref.plan(cached, fresh, list(range(10, 40)), table, 16, 40, 80, parents + [-1] * 8)
+    for a, b, w in zip(*got, want):
+        np.testing.assert_array_equal(a, w)
+        np.testing.assert_array_equal(b, w)
+
+
 def test_a_wait_that_runs_out_is_reported():
     """Copies that never complete (the handle's test hook): the call ends, the flag is raised once, and the
     workspace works again."""
