@@ -18,13 +18,14 @@ inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK 
 // Restores the caller's current device on scope exit.
 struct DeviceGuard {
   int prev = -1;
-  bool ok = false;
+  bool ok = false, changed = false;
   explicit DeviceGuard(int dev) {
     if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
+    changed = prev != dev;
+    ok = !changed || cudaSetDevice(dev) == cudaSuccess;
   }
   ~DeviceGuard() {
-    if (ok && prev >= 0) cudaSetDevice(prev);
+    if (ok && changed) cudaSetDevice(prev);
   }
 };
 

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
 
   // the first lengths: on their way while the barriers are set up
   int lo0 = 0, hi0 = 0;
-  if (!PAGED && tid < a.B) {
+  if (!PAGED && !LAT && tid < a.B) {
     lo0 = __ldg(a.cu + tid);
     hi0 = __ldg(a.cu + tid + 1);
   }
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if constexpr (LAT) pdl_wait();                   // the kernel before is done: what follows reads its results
   long long total = 0;                             // prompt: items; cache: key tiles
   AtShare share = {};
   if constexpr (PAGED) {
@@ -411,7 +412,8 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
   } else {
     // requests by falling number of row tiles (equal ones by index), every CTA alike
     for (int b = tid; b < a.B; b += kApThreads) {
-      const int lo = b == tid ? lo0 : __ldg(a.cu + b), n = max(0, min(b == tid ? hi0 : __ldg(a.cu + b + 1), a.T) - lo);
+      const bool there = !LAT && b == tid;
+      const int lo = there ? lo0 : __ldg(a.cu + b), n = max(0, min(there ? hi0 : __ldg(a.cu + b + 1), a.T) - lo);
       s.before[b] = lo < 0 ? 0 : at_idiv(n + p.span - 1, p.span);
     }
     __syncthreads();
@@ -1292,8 +1294,22 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, const RowView *k_rope, int *ct
   const int grid = (int)(items < num_sms ? items : num_sms);
   const bool twins = p.span == p.per;
   const ApKernel k = k_rope ? ap_latent(twins, a.f16) : (twins ? ap_kernel<false, true> : ap_kernel<false, false>)(a.head_dim, a.f16);
-  k<<<grid, kApThreads, k_rope ? ApLatGeom::kSmem : ap_smem(a.head_dim), stream>>>(p);
-  return cudaGetLastError();
+  if (!k_rope) {
+    k<<<grid, kApThreads, ap_smem(a.head_dim), stream>>>(p);
+    return cudaGetLastError();
+  }
+  // its launch, and the setting up of its barriers, beside the end of the kernel before
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kApThreads);
+  cfg.dynamicSmemBytes = ApLatGeom::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
 }
 
 cudaError_t launch_attn_wide_tree(const AttnArgs &a, uint8_t *ws, const AttnWideWs &w, int num_sms, cudaStream_t stream) {

@@ -41,6 +41,7 @@ __device__ __forceinline__ uint32_t rope_pack(float lo, float hi, int f16) {
 // most loads in flight: with 6 and 10 CTAs the latent rows took 54.3 and 64.9 us, with 256 threads 57.3.
 template <bool F16, bool INTERLEAVED, int HP>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeArgs a) {
+  pdl_wait();                                      // the kernel before is done: what follows reads its results
   const int i = blockIdx.y * kRopeThreads + threadIdx.x;
   const int r = i / a.per_row, t = blockIdx.x * a.rows_per_block + r;
   if (r >= a.rows_per_block || t >= a.T) return;
@@ -149,8 +150,16 @@ cudaError_t launch_rope(RopeArgs *a, cudaStream_t stream) {
   a->rows_per_block = per_row >= kRopeThreads ? 1 : kRopeThreads / per_row;
   const dim3 grid((unsigned)((a->T + a->rows_per_block - 1) / a->rows_per_block),
                   (unsigned)((a->rows_per_block * per_row + kRopeThreads - 1) / kRopeThreads));
-  (hp == 1 ? rope_pick<1>(*a) : rope_pick<4>(*a))<<<grid, kRopeThreads, 0, stream>>>(*a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};                     // its launch beside the end of the kernel before
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, hp == 1 ? rope_pick<1>(*a) : rope_pick<4>(*a), *a);
 }
 
 }  // namespace moe
