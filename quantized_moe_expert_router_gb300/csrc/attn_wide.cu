@@ -110,8 +110,9 @@ struct ApGeom {
 // tile's two, then the three of the key tile that S needs next.  A slot is free when its piece has been read for the last
 // time, so of the five pieces that a row tile's two products read, two of the next are there before and
 // three come while the other row tile's products run.  A tile's pieces share a barrier (kv_full, four in turn):
-// beside the products, which read shared memory all the time, each look at one costs 100 to 200 cycles (8192 tokens of
-// 32 heads: 568 us with a barrier a piece).
+// beside the products, which read shared memory all the time, each look at one costs 100 to 200 cycles.  8192 tokens of
+// 32 heads 456 us, 1510 TFLOP/s (568 with a barrier a piece); bound by shared memory: S reads 8 KB of it a step of 64 cycles,
+// with the copies 2660 cycles for the tensor pipe's 2560.
 constexpr int kApPiece = kApTile * 128;
 struct ApLatGeom {
   static constexpr int kTileBytes = 2 * kApPiece;

@@ -33,10 +33,10 @@
 // instead: S needs 17 % fewer cycles, but nothing comes between S and the values' products, and all SMs then
 // load and compute in step: 16 tokens at up to 100000 of 64 heads 204 us.)
 //
-// The tiles of all items stand in one line that the CTAs share (at_share); calls with two items
+// The tiles of all items stand in one line that the CTAs share (LtCursor); calls with two items
 // over the same tokens (two parts of the heads, or more tokens than a tile has room for) give each place of
 // the line to two CTAs, which read the same tiles at the same time: the second one from L2.  A
-// part of an item goes to the workspace (fp32 O, m, l); lat_join_kernel joins them in the order of the context.
+// part of an item goes to the workspace (fp32 O, m, l); lat_join_kernel joins them, always in the same order.
 //
 // Where contexts are short or items many, an item is not cut: there is nothing to join then.
 //
@@ -61,8 +61,10 @@
 // The softmax warps of a half also meet at a named barrier: a warp whose wait ran out goes on to
 // the next vote, which tells the others, and all four end together.
 //
-// Bound: for up to 64 rows HBM, or the copies' latency behind a ring of two tiles; for more the tensor pipe's reads of shared
-// memory (a tile's products alone take 1970 cycles at N = 64, 1490 at N = 16; FINAL).
+// Bound: for up to 64 rows over long contexts HBM (16 tokens at up to 100000 of 64 heads 154 us, 5.2 TB/s; 16 heads,
+// 16 at up to 60000, 86 us, 5.6), with 5 us of start, uneven ends and the join; for more rows shared memory (a tile's products
+// alone 1970 cycles at N = 64, 1490 at N = 16; some 2600 to 3000 beside one another and behind a ring of two tiles: 128 heads, 16 at
+// up to 60000, 157 us, 730 TFLOP/s); for short contexts a chain of latencies: one token at 50 9 us, at 1000 12, join 3 of it.
 #include <limits.h>
 #include <math.h>
 #include <stddef.h>
