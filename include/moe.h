@@ -579,7 +579,7 @@ typedef struct {
   int32_t num_pages;      /* pages of the cache: num_pages * page_size < 2^31 */
   int32_t max_pages;      /* entries of a block-table row (its stride) */
   int32_t dtype;          /* MOE_ATTN_BF16 or MOE_ATTN_F16 */
-  float softmax_scale;    /* multiplies q . k (finite, > 0); 1 / sqrt(192) as a rule */
+  float softmax_scale;    /* multiplies q . k (1e-30 to 1e30); 1 / sqrt(192) as a rule */
   uint32_t flags;         /* MOE_ATTN_TEST_STALL, or 0 */
 } moe_latent_config;
 

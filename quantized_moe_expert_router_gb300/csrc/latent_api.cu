@@ -163,7 +163,7 @@ moe_status moe_rope_append(moe_attn_t attn, moe_rope_t rope, int num_rows, const
 
 moe_status moe_latent_create(const moe_latent_config *cfg, int device, moe_latent_t *out) {
   if (!cfg || !out || device < 0) return MOE_ERR_INVALID_ARG;
-  if ((cfg->flags & ~MOE_ATTN_TEST_STALL) || !(cfg->softmax_scale > 0.f) || !isfinite(cfg->softmax_scale)) return MOE_ERR_INVALID_ARG;
+  if ((cfg->flags & ~MOE_ATTN_TEST_STALL) || !(cfg->softmax_scale >= 1e-30f && cfg->softmax_scale <= 1e30f)) return MOE_ERR_INVALID_ARG;
   if (cfg->dtype != MOE_ATTN_BF16 && cfg->dtype != MOE_ATTN_F16) return MOE_ERR_INVALID_ARG;
   if (cfg->heads < 1 || cfg->heads > MOE_LATENT_MAX_HEADS) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (cfg->latent_dim != kLatDim || cfg->rope_dim != kLatRope || cfg->head_dim != kLatHead) return MOE_ERR_UNSUPPORTED_SHAPE;

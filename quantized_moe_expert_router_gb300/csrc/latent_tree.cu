@@ -65,6 +65,7 @@
 // 16 at up to 60000, 86 us, 5.6), with 5 us of start, uneven ends and the join; for more rows shared memory (a tile's products
 // alone 1970 cycles at N = 64, 1490 at N = 16; some 2600 to 3000 beside one another and behind a ring of two tiles: 128 heads, 16 at
 // up to 60000, 157 us, 730 TFLOP/s); for short contexts a chain of latencies: one token at 50 9 us, at 1000 12, join 3 of it.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stddef.h>
@@ -84,7 +85,7 @@ constexpr int kLtMaxB = MOE_ATTN_MAX_REQUESTS;
 constexpr int kLtMaxSms = 1024;
 constexpr int kLtRows = 64;                       // rows of an item at most
 constexpr float kLtSlack = 8.f;                   // log2 of the largest P
-constexpr float kLtUnset = 1e30f;                 // in place of -c m before a row has seen anything: any score passes it
+constexpr float kLtUnset = FLT_MAX;               // in place of -m before a row has seen anything: any finite score passes it
 
 template <int N>
 struct LtGeom {
@@ -130,10 +131,10 @@ struct LtSmem {
   LtItem item[2];
   uint32_t bad[2][3][2];       // by item parity and masked tile: tokens with a non-finite latent
   float wmax[2][4][32], wsum[2][4][32];
-  alignas(16) float mc[8][32]; // per softmax warp: -c m of its rows
+  alignas(16) float m[8][32];  // per softmax warp: -m of its rows
   alignas(16) float f[8][32];  // and their factors
 };
-static_assert(offsetof(LtSmem, mc) % 16 == 0 && offsetof(LtSmem, f) % 16 == 0, "read four at a time");
+static_assert(offsetof(LtSmem, m) % 16 == 0 && offsetof(LtSmem, f) % 16 == 0, "read four at a time");
 
 // While the CTA's copy warp finds its share, in the place of the tiles: of each request its items and their tiles.
 struct LtSetup {
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
     const int h = (warp - kLtWSoft) >> 2, w4 = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * w4) << 16;
     const uint32_t ts = tb + lanes + 4u * N + (uint32_t)(h * NC), to = tb + lanes + (uint32_t)(h * NC);
-    float *const mcw = s.mc[warp - kLtWSoft], *const fw = s.f[warp - kLtWSoft];
+    float *const mw = s.m[warp - kLtWSoft], *const fw = s.f[warp - kLtWSoft];
     const int cl = lane & (NC - 1), rl = h * NC + cl;                           // the row whose maximum the lane keeps
     const int kt = 16 * w4 + (lane >> 2), qc = 2 * (lane & 3);                  // first of the thread's tokens of a tile; first of its rows of 8
     uint32_t ns = 0;                               // tiles so far
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
       float l[NC / 4];
 #pragma unroll
       for (int n = 0; n < NC / 4; n++) l[n] = 0.f;
-      if (lane < NC) mcw[lane] = valid_l ? kLtUnset : -kLtUnset;   // rows of no token have no say
+      if (lane < NC) mw[lane] = valid_l ? kLtUnset : -kLtUnset;   // rows of no token have no say
       __syncwarp();
       bool dead = false;
       for (int j = 0; j < it.n; j++, ns++) {
@@ -570,16 +571,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
           }
           __syncwarp();
         }
-        // v becomes c v - c m, the arguments of the exponentials
+        // v becomes c (v - m), the arguments of the exponentials: 0 at the maximum however large the scores are
         auto arguments = [&]() {
           const float2 c2 = make_float2(c, c);
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int n = 0; n < NC / 8; n++) {
-            const float2 mc = *reinterpret_cast<const float2 *>(mcw + 8 * n + qc);
+            const float2 m = *reinterpret_cast<const float2 *>(mw + 8 * n + qc);
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-              const float2 t = ffma2(make_float2(v[4 * n + 2 * z], v[4 * n + 2 * z + 1]), c2, mc);
+              const float2 t = ffma2(at_add2(make_float2(v[4 * n + 2 * z], v[4 * n + 2 * z + 1]), m), c2, make_float2(0.f, 0.f));
               v[4 * n + 2 * z] = t.x;
               v[4 * n + 2 * z + 1] = t.y;
               top[z] = at_max3(top[z], t.x, t.y);
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lat_tree_kernel(const __grid_co
           const float f = m1 == m_l || m_l == -INFINITY || !valid_l ? 1.f : at_exp2((m_l - m1) * c);
           m_l = m1;
           if (lane < NC) {
-            mcw[lane] = valid_l ? (m1 == -INFINITY ? kLtUnset : -m1 * c) : -kLtUnset;
+            mw[lane] = valid_l ? (m1 == -INFINITY ? kLtUnset : -m1) : -kLtUnset;
             fw[lane] = f;
           }
           __syncwarp();

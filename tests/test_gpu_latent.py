@@ -228,6 +228,19 @@ def test_tree_large_scores():
     attn_ref.check(*c.run(), c.want())
 
 
+def test_tree_scores_far_below_zero():
+    """Scores of -10^33, thousands of roundings apart: the largest has all the weight."""
+    c = Latent(16, 16, torch.bfloat16, [300], [1], seed=34)
+    x = (1.0 + torch.rand((301, 576), device=DEV)).mul(1e15).bfloat16()
+    x[:, 512:] = 0.0
+    p = torch.arange(301, device=DEV)
+    c.cache[c.table[0].long()[p // 16], p % 16] = x
+    c.q[:] = -1e17
+    out, lse = c.run()
+    best = x[:, :512].double().sum(1).argmin()
+    assert torch.equal(out[0], x[best, :512].expand(16, 512)) and (lse < -1e32).all()
+
+
 def test_tree_rising_scores():
     """Every tile's maximum passes the last one's: the rescaling runs at each of them, in every row."""
     c = Latent(33, 128, torch.float16, [1500], [1], seed=25)

@@ -99,7 +99,8 @@ def test_null_and_negative_arguments_are_refused():
     (dict(heads=0), 2), (dict(heads=129), 2), (dict(latent_dim=256), 2), (dict(rope_dim=32), 2), (dict(head_dim=64), 2),
     (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=256), 2), (dict(num_pages=0), 2), (dict(max_pages=0), 2),
     (dict(num_pages=2 ** 27), 2), (dict(max_pages=2 ** 27), 2), (dict(dtype=2), 1), (dict(softmax_scale=0.0), 1),
-    (dict(softmax_scale=math.nan), 1), (dict(softmax_scale=-1.0), 1), (dict(flags=1), 1), (dict(flags=0x80000001), 1),
+    (dict(softmax_scale=math.nan), 1), (dict(softmax_scale=-1.0), 1), (dict(softmax_scale=1e-31), 1), (dict(softmax_scale=1e31), 1),
+    (dict(flags=1), 1), (dict(flags=0x80000001), 1),
 ])
 def test_latent_create_refuses(kw, status):
     cfg = moe.moe_latent_config(**{**dict(heads=16, latent_dim=512, rope_dim=64, head_dim=128, page_size=16, num_pages=64, max_pages=8,
