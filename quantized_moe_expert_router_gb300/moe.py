@@ -426,8 +426,15 @@ class Attention:
         self.close()
 
 
+def _kind(fn, handle, kind):
+    """Another kind of handle would be read as what it is not."""
+    if not isinstance(handle, kind):
+        raise TypeError(f"{fn}: {type(handle).__name__} is not a {kind.__name__}")
+
+
 def moe_attn_workspace_bytes(attn: Attention, num_requests: int, num_rows: int) -> int:
     n = ctypes.c_size_t()
+    _kind("moe_attn_workspace_bytes", attn, Attention)
     _check("moe_attn_workspace_bytes", load_library().moe_attn_workspace_bytes(
         attn.handle, num_requests, num_rows, ctypes.byref(n)))
     return n.value
@@ -441,6 +448,7 @@ def alloc_attn_workspace(attn: Attention, num_requests: int, num_rows: int, devi
 
 def moe_attn_get_device_status(attn: Attention, ws: torch.Tensor, stream=None) -> int:
     fn, f = "moe_attn_get_device_status", ctypes.c_int32()
+    _kind(fn, attn, Attention)
     if ws.get_device() != attn.device or not ws.is_contiguous() or ws.nbytes < moe_attn_workspace_bytes(attn, 0, 0):
         raise ValueError(f"{fn}: ws of {ws.nbytes} bytes on {ws.device} is not a workspace on cuda:{attn.device}")
     _check(fn, load_library().moe_attn_get_device_status(
@@ -526,6 +534,7 @@ def moe_kv_plan(attn, cached, fresh, free_pages, block_table, cu, slots, positio
                 stream=None) -> None:
     """Block table entries, row offsets, slots, positions and (from parents)
     tree masks of one step; int32 tensors, tree_mask int64."""
+    _kind("moe_kv_plan", attn, Attention)
     _plan("moe_kv_plan", _lib.moe_kv_plan, attn, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents, tree_mask, stream)
 
 
@@ -642,7 +651,9 @@ def moe_rope_apply(rope, positions, q, q_out, k=None, k_out=None, stream=None) -
     """Turn q and k [rows][heads][head_dim] by positions (int32 [rows]) into q_out
     and k_out, each its input itself or an array apart.  Rows at negative
     positions are left out."""
-    fn, dev, T, d = "moe_rope_apply", rope.device, positions.numel(), q.shape[-1]
+    fn = "moe_rope_apply"
+    _kind(fn, rope, Rope)
+    dev, T, d = rope.device, positions.numel(), q.shape[-1]
     if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev:
         _attn_refuse(fn, dev, ("positions", positions, torch.int32, (T,)))
     if (k is None) != (k_out is None):
@@ -659,8 +670,10 @@ def moe_rope_apply(rope, positions, q, q_out, k=None, k_out=None, stream=None) -
         _check(fn, status)
 
 
-def _same(fn, a, b):
-    """The handles of one call: one device, one element type."""
+def _same(fn, a, kind, b):
+    """The handles of one call: a `kind` and a Rope, of one device and one element type."""
+    _kind(fn, a, kind)
+    _kind(fn, b, Rope)
     if a.device != b.device:
         raise ValueError(f"{fn}: handles on cuda:{a.device} and cuda:{b.device}")
     if a.dtype is not b.dtype:
@@ -670,8 +683,9 @@ def _same(fn, a, b):
 def moe_rope_append(attn, rope, q, k, v, positions, slots, q_out, k_cache, v_cache, stream=None) -> None:
     """moe_rope_apply of q into q_out and of k, with v, into their slots of the
     caches, in one launch."""
-    fn, dev, dt, T = "moe_rope_append", attn.device, attn.dtype, positions.numel()
-    _same(fn, attn, rope)
+    fn = "moe_rope_append"
+    _same(fn, attn, Attention, rope)
+    dev, dt, T = attn.device, attn.dtype, positions.numel()
     qs, ks, cs = (T, attn.q_heads, attn.head_dim), (T, attn.kv_heads, attn.head_dim), attn.cache_shape
     if (positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev
             or slots.dtype is not torch.int32 or slots.numel() != T or not slots.is_contiguous() or slots.get_device() != dev):
@@ -719,6 +733,7 @@ class LatentAttention:
 
 def moe_latent_workspace_bytes(lat: LatentAttention, num_requests: int, num_rows: int) -> int:
     n = ctypes.c_size_t()
+    _kind("moe_latent_workspace_bytes", lat, LatentAttention)
     _check("moe_latent_workspace_bytes", load_library().moe_latent_workspace_bytes(
         lat.handle, num_requests, num_rows, ctypes.byref(n)))
     return n.value
@@ -732,6 +747,7 @@ def alloc_latent_workspace(lat: LatentAttention, num_requests: int, num_rows: in
 
 def moe_latent_get_device_status(lat: LatentAttention, ws: torch.Tensor, stream=None) -> int:
     fn, f = "moe_latent_get_device_status", ctypes.c_int32()
+    _kind(fn, lat, LatentAttention)
     if ws.get_device() != lat.device or not ws.is_contiguous() or ws.nbytes < moe_latent_workspace_bytes(lat, 0, 0):
         raise ValueError(f"{fn}: ws of {ws.nbytes} bytes on {ws.device} is not a workspace on cuda:{lat.device}")
     _check(fn, load_library().moe_latent_get_device_status(
@@ -742,6 +758,7 @@ def moe_latent_get_device_status(lat: LatentAttention, ws: torch.Tensor, stream=
 def moe_latent_plan(lat, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents=None, tree_mask=None,
                     stream=None) -> None:
     """moe_kv_plan for the latent cache."""
+    _kind("moe_latent_plan", lat, LatentAttention)
     _plan("moe_latent_plan", _lib.moe_latent_plan, lat, cached, fresh, free_pages, block_table, cu, slots, positions, info, parents,
           tree_mask, stream)
 
@@ -769,8 +786,9 @@ def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_o
     """Latents c [rows][512] and turned key parts k_rope [rows][64] into their slots
     of the cache; q [rows][heads][64] (the queries' rotary part) turned into q_out,
     and k_rope into k_out as well (another array)."""
-    fn, dev, T = "moe_latent_append", lat.device, positions.numel()
-    _same(fn, lat, rope)
+    fn = "moe_latent_append"
+    _same(fn, lat, LatentAttention, rope)
+    dev, T = lat.device, positions.numel()
     if (positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev
             or slots.dtype is not torch.int32 or slots.numel() != T or not slots.is_contiguous() or slots.get_device() != dev):
         _attn_refuse(fn, dev, ("positions", positions, torch.int32, (T,)), ("slots", slots, torch.int32, (T,)))
@@ -793,7 +811,9 @@ def moe_latent_append(lat, rope, c, k_rope, positions, slots, cache, q=None, q_o
 def moe_latent_prompt(lat, q, k, k_rope, v, cu, out, ws, lse=None, stream=None) -> None:
     """Expanded causal attention over packed prompts: q [rows][heads][192], k, v,
     out [rows][heads][128], k_rope [rows][64]; the rest as moe_attn_prompt."""
-    fn, dev, T, n, hq = "moe_latent_prompt", lat.device, q.shape[0], cu.numel(), lat.heads
+    fn = "moe_latent_prompt"
+    _kind(fn, lat, LatentAttention)
+    dev, T, n, hq = lat.device, q.shape[0], cu.numel(), lat.heads
     ks = (T, hq, LATENT_HEAD)
     if (cu.dtype is not torch.int32 or not cu.is_contiguous() or cu.get_device() != dev
             or ws.get_device() != dev or not ws.is_contiguous()
@@ -813,8 +833,9 @@ def moe_latent_prompt(lat, q, k, k_rope, v, cu, out, ws, lse=None, stream=None) 
 def moe_latent_tree(lat, q, q_rope, cu, cached, block_table, cache, out, ws, tree_mask=None, lse=None, stream=None) -> None:
     """Absorbed attention of the step's rows over the latent cache: q, out
     [rows][heads][512], q_rope [rows][heads][64]; the rest as moe_attn_tree."""
-    fn, dev, i32, T, n = "moe_latent_tree", lat.device, torch.int32, q.shape[0], cu.numel()
-    hq = lat.heads
+    fn = "moe_latent_tree"
+    _kind(fn, lat, LatentAttention)
+    dev, i32, T, n, hq = lat.device, torch.int32, q.shape[0], cu.numel(), lat.heads
     qs = (T, hq, LATENT_DIM)
     if (cu.dtype is not i32 or not cu.is_contiguous() or cu.get_device() != dev
             or ws.get_device() != dev or not ws.is_contiguous()

@@ -398,6 +398,15 @@ def test_refusals():
     assert e.value.status == 4
     with pytest.raises(ValueError, match="not a workspace"):
         moe.moe_latent_get_device_status(c.lat, ws[:1024])
+    attn, rope, i32 = moe.Attention(4, 4, 64, 16, 2, 2), moe.Rope(64), torch.zeros(4, dtype=torch.int32, device=DEV)
+    for call in (lambda: moe.moe_kv_plan(c.lat, *[i32] * 8), lambda: moe.moe_latent_plan(attn, *[i32] * 8),
+                 lambda: moe.moe_attn_get_device_status(c.lat, ws), lambda: moe.moe_latent_get_device_status(attn, ws),
+                 lambda: moe.moe_attn_workspace_bytes(c.lat, 1, 1), lambda: moe.moe_latent_workspace_bytes(attn, 1, 1),
+                 lambda: moe.moe_rope_apply(attn, i32[:2], out, out), lambda: moe.moe_latent_tree(attn, **good),
+                 lambda: moe.moe_latent_append(c.lat, attn, c.q[:, 0, :512], c.q[:, 0, 512:], i32[:2], i32[:2], c.cache),
+                 lambda: moe.moe_rope_append(c.lat, rope, out, out, out, i32, i32, out, out, out)):
+        with pytest.raises(TypeError, match="not a"):              # another kind of handle
+            call()
     none = c.q[:0]
     moe.moe_latent_tree(c.lat, none[:, :, :512], none[:, :, 512:], ints([0, 0]), c.cached, c.table, c.cache, out[:0], ws)
     moe.moe_latent_tree(c.lat, good["q"], good["q_rope"], ints([0]), ints([]), c.table[:0], c.cache, out, ws)
