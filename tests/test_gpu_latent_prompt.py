@@ -108,6 +108,22 @@ def test_one_infinite_value_reaches_the_rows_that_see_it():
     attn_ref.check(torch.where(hit, 0, out), None, [torch.where(hit, 0.0, w[0]), None, w[2], None])
 
 
+@pytest.mark.parametrize("n", [300, 1200])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_scores_thousands_of_roundings_apart(n, sign):
+    """Scores of 10^33 on either side of zero: the largest that a row sees has all its weight.
+    Token of rank 128 a + b: 64 keys of 2^50 (1 + a / 128) and 64 of 2^50 (1 + b / 128) by queries of
+    2^56 and 2^49, integers below 2^22 times 2^92, so all sums are exact and no two alike."""
+    q, k, v, r = rows(n, 2, torch.bfloat16, 60)
+    rank = torch.randperm(n, generator=torch.Generator().manual_seed(61)).to(DEV)
+    k = torch.cat([rank.div(128, rounding_mode="floor")[:, None].expand(n, 64), (rank % 128)[:, None].expand(n, 64)], 1)
+    k = (2.0 ** 50 * (1 + k / 128.0))[:, None].expand(n, 2, 128).bfloat16().contiguous()
+    q[:, :, :64], q[:, :, 64:], r = sign * 2.0 ** 56, sign * 2.0 ** 49, torch.zeros_like(r)
+    out, lse = run(q, k, v, r, [n])
+    at = (sign * rank).cummax(0).indices[:, None, None].expand(n, 2, 128)
+    assert torch.equal(out, v.gather(0, at)) and (lse * sign > 1e32).all()
+
+
 @pytest.mark.parametrize("order", ["heads_first", "gaps"])
 def test_strides(order):
     heads, lengths, dt = 6, [150, 45], torch.bfloat16
