@@ -111,7 +111,7 @@ struct ApGeom {
 // time, so of the five pieces that a row tile's two products read, two of the next are there before and
 // three come while the other row tile's products run.  A tile's pieces share a barrier (kv_full, four in turn):
 // beside the products, which read shared memory all the time, each look at one costs 100 to 200 cycles.  8192 tokens of
-// 32 heads 456 us, 1510 TFLOP/s (568 with a barrier a piece); bound by shared memory: S reads 8 KB of it a step of 64 cycles,
+// 32 heads 458 us, 1500 TFLOP/s (568 with a barrier a piece); bound by shared memory: S reads 8 KB of it a step of 64 cycles,
 // with the copies 2660 cycles for the tensor pipe's 2560.
 constexpr int kApPiece = kApTile * 128;
 struct ApLatGeom {
