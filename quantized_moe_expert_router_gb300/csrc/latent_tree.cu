@@ -948,7 +948,10 @@ struct LtSum {
   }
   // a part whose maximum is not above `top`
   __device__ __forceinline__ void one(float2 st, float4 u, float c) {
-    if (st.x == -INFINITY && st.y == 0.f) return;  // the row sees nothing there
+    if (st.x == -INFINITY && st.y == 0.f) {        // no weight there: u is 0, or NaN by an infinite element of a latent
+      acc = make_float4(acc.x + u.x, acc.y + u.y, acc.z + u.z, acc.w + u.w);
+      return;
+    }
     const float f = st.x == top ? 1.f : at_exp2((st.x - top) * c);
     sum = fmaf(st.y, f, sum);
     acc.x = fmaf(u.x, f, acc.x);

@@ -221,6 +221,24 @@ def test_tree_offsets_past_32_bits():
     attn_ref.check(out, None, ref.attend(q, x[:, None], x[:, None, :512], vis, SCALE))
 
 
+@pytest.mark.parametrize("n", [40, 20000])
+def test_tree_scores_of_minus_infinity(n):
+    """Tokens whose infinite element gives a score of -infinity, whole parts of a context among them: no weight, and a NaN there."""
+    c = Latent(16, 16, torch.bfloat16, [n], [1], seed=35)
+    c.q[:, :, 7] = 1.0
+    unseen = torch.arange(n + 1, device=DEV) < n // 2
+    p = torch.arange(n // 2, device=DEV)
+    c.cache[c.table[0].long()[p // 16], p % 16, 7] = -math.inf
+    want = c.want(unseen=[unseen])
+    out, lse = c.run()
+    assert out[:, :, 7].isnan().all()
+    out[:, :, 7] = want[0][:, :, 7].to(out.dtype)
+    attn_ref.check(out, lse, want)
+    c.cache[..., 7] = -math.inf                                     # no token is left
+    out, lse = c.run()
+    assert out[:, :, 7].isnan().all() and (out.nan_to_num() == 0).all() and (lse == -math.inf).all()
+
+
 def test_tree_large_scores():
     """Scores of hundreds: the maximum moves many times, and weights underflow."""
     c = Latent(16, 16, torch.bfloat16, [2000], [2], seed=24)
