@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include "attn.h"
 #include "gemv_core.cuh"
@@ -143,6 +144,12 @@ __device__ __forceinline__ float at_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Whether a row whose maximum is m has to take m off its scores before it scales them.  c v - c m in one fma is exact
+// but for the rounding of c m, which gives every weight of the row a factor of up to 2^(ulp(c m) / 2): one for all, as long as
+// m stays, but another for tiles, twins or parts with another m, and past 2^31 it overflows P.  Up to 2^10 the factor is within
+// 2^-15 ln 2 of one, a twentieth of f16's rounding; ordinary scores stay below that, and their way is a subtraction shorter.
+constexpr float kAtFar = 1024.f;
+__device__ __forceinline__ bool at_far(float m, float c) { return fabsf(m) <= FLT_MAX && fabsf(m) * c > kAtFar; }
 __device__ __forceinline__ float at_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

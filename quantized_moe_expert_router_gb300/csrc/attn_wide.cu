@@ -479,9 +479,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       if constexpr (PAGED)
         if (a.tree_mask) word = __ldg(a.tree_mask + it.first + lim);
       float m = -INFINITY;                         // the maximum that P is taken against
-      // Past 2^24 the rounding of c m alone moves P by more than 2 and in the end overflows it: a warp with such a row takes m
-      // off its scores first.  Done in every tile this took 1.5% of a prompt of 8192.
-      bool far = false;
+      bool far = false;                            // a row of the warp takes m off its scores before it scales them
       float2 l2 = make_float2(0.f, 0.f);
       for (int j = 0; j < nt; j++, ns++) {
         const int jl = twin ? 2 * j + h : j, tok0 = (it.j0 + jl) * kApTile;
@@ -515,11 +513,11 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         const float top = ap_max(v);
         if (j == 0) {
           m = real ? top : INFINITY;               // rows of no token hold anything: P = 0, and no say in the vote below
-          if (LAT) far = __any_sync(kFull, real && fabsf(m) * c > 0x1p24f);
+          if (LAT) far = __any_sync(kFull, at_far(m, c));
         } else if (__any_sync(kFull, (top - m) * c > kApSlack)) {
           const float m1 = fmaxf(m, top), f = m1 == -INFINITY ? 1.f : at_exp2((m - m1) * c);
           m = m1;
-          if (LAT) far = __any_sync(kFull, real && fabsf(m) * c > 0x1p24f);
+          if (LAT) far = __any_sync(kFull, at_far(m, c));
           l2.x *= f;
           l2.y *= f;
           // PV of the tile before is done: S of this one was issued behind it
@@ -536,14 +534,15 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
         }
         float mc = m == -INFINITY ? 0.f : -m * c;
         if (LAT && far) {
-          const float2 off = make_float2(mc == 0.f ? 0.f : -m, mc == 0.f ? 0.f : -m);
+          const bool mine = at_far(m, c);
+          const float2 off = make_float2(mine ? -m : 0.f, mine ? -m : 0.f);
 #pragma unroll
           for (int e = 0; e < 64; e++) {
             const float2 t = at_add2(make_float2(v[2 * e], v[2 * e + 1]), off);
             v[2 * e] = t.x;
             v[2 * e + 1] = t.y;
           }
-          mc = 0.f;
+          mc = mine ? 0.f : mc;
         }
         const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
