@@ -259,6 +259,7 @@ struct AtSums {
   int lim[2];                  // the rows' fresh rows
   int b, cached, ctx;          // request, its cached tokens, and the end of its context
   float o[D / 8][4], m[2], l[2];
+  bool far;                    // a row of the warp takes m off its scores before it scales them
   __device__ __forceinline__ void begin(const AtTable &s, const AtArgs &p, const AtItem &it, int request) {
     const AttnArgs &a = p.a;
     const int g = (threadIdx.x & 31) >> 2, q4 = threadIdx.x & 3;
@@ -282,6 +283,7 @@ struct AtSums {
       m[z] = -INFINITY;
       l[z] = 0.f;
     }
+    far = false;
 #pragma unroll
     for (int d = 0; d < D / 8; d++)
 #pragma unroll
@@ -351,7 +353,8 @@ struct AtSums {
       for (int t = 1; t < kTok / 8; t++) top[z] = at_max3(top[z], sc[t][2 * z], sc[t][2 * z + 1]);
       up |= (top[z] - m[z]) * c > kAtSlack;    // -inf - -inf: NaN, not above
     }
-    if (__any_sync(kFull, up)) {
+    float ref[2] = {m[0], m[1]};                   // what c takes off the scores with them
+    if (far || __any_sync(kFull, up)) {
 #pragma unroll
       for (int z = 0; z < 2; z++) {
         float m1 = fmaxf(m[z], top[z]);
@@ -365,12 +368,26 @@ struct AtSums {
           o[d][2 * z] *= f;
           o[d][2 * z + 1] *= f;
         }
+        ref[z] = m1;
+      }
+      far = __any_sync(kFull, at_far(m[0], c) || at_far(m[1], c));
+      if (far) {
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+          const float off = at_far(m[z], c) ? -m[z] : 0.f;
+          if (off != 0.f) ref[z] = 0.f;
+#pragma unroll
+          for (int t = 0; t < kTok / 8; t++) {
+            sc[t][2 * z] += off;
+            sc[t][2 * z + 1] += off;
+          }
+        }
       }
     }
     uint32_t pf[kBlocks][4];
 #pragma unroll
     for (int z = 0; z < 2; z++) {
-      const float mc = m[z] == -INFINITY ? 0.f : -m[z] * c;
+      const float mc = ref[z] == -INFINITY ? 0.f : -ref[z] * c;
 #pragma unroll
       for (int t = 0; t < kTok / 8; t++) {
         const float e0 = at_exp2(fmaf(sc[t][2 * z], c, mc)), e1 = at_exp2(fmaf(sc[t][2 * z + 1], c, mc));

@@ -511,39 +511,42 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
           }
         }
         const float top = ap_max(v);
-        if (j == 0) {
-          m = real ? top : INFINITY;               // rows of no token hold anything: P = 0, and no say in the vote below
-          if (LAT) far = __any_sync(kFull, at_far(m, c));
-        } else if (__any_sync(kFull, (top - m) * c > kApSlack)) {
-          const float m1 = fmaxf(m, top), f = m1 == -INFINITY ? 1.f : at_exp2((m - m1) * c);
-          m = m1;
-          if (LAT) far = __any_sync(kFull, at_far(m, c));
-          l2.x *= f;
-          l2.y *= f;
-          // PV of the tile before is done: S of this one was issued behind it
+        float ref = m;                             // what c takes off the scores with them
+        if (j == 0 || far || __any_sync(kFull, (top - m) * c > kApSlack)) {
+          if (j == 0) {
+            m = real ? top : INFINITY;             // rows of no token hold anything: P = 0, and no say in the vote
+          } else {
+            const float m1 = fmaxf(m, top), f = m1 == -INFINITY ? 1.f : at_exp2((m - m1) * c);
+            m = m1;
+            l2.x *= f;
+            l2.y *= f;
+            // PV of the tile before is done: S of this one was issued behind it
 #pragma unroll 1
-          for (int q = 0; q < D / 32; q++) {
-            float o[32];
-            at_ld32(to + 32u * q, o);
-            at_wait_ld(o);
+            for (int q = 0; q < D / 32; q++) {
+              float o[32];
+              at_ld32(to + 32u * q, o);
+              at_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 32; e++) o[e] *= f;
-            at_st32(to + 32u * q, o);
+              for (int e = 0; e < 32; e++) o[e] *= f;
+              at_st32(to + 32u * q, o);
+            }
+            at_wait_st();
           }
-          at_wait_st();
-        }
-        float mc = m == -INFINITY ? 0.f : -m * c;
-        if (LAT && far) {
-          const bool mine = at_far(m, c);
-          const float2 off = make_float2(mine ? -m : 0.f, mine ? -m : 0.f);
+          ref = m;
+          far = __any_sync(kFull, at_far(m, c));
+          if (far) {
+            const float own = at_far(m, c) ? -m : 0.f;
+            const float2 off = make_float2(own, own);
 #pragma unroll
-          for (int e = 0; e < 64; e++) {
-            const float2 t = at_add2(make_float2(v[2 * e], v[2 * e + 1]), off);
-            v[2 * e] = t.x;
-            v[2 * e + 1] = t.y;
+            for (int e = 0; e < 64; e++) {
+              const float2 t = at_add2(make_float2(v[2 * e], v[2 * e + 1]), off);
+              v[2 * e] = t.x;
+              v[2 * e + 1] = t.y;
+            }
+            if (own != 0.f) ref = 0.f;
           }
-          mc = mine ? 0.f : mc;
         }
+        const float mc = ref == -INFINITY ? 0.f : -ref * c;
         const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

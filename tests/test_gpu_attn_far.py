@@ -1,5 +1,6 @@
 """Attention on scores that are large against their differences, where c m (the scaled maximum) rounded by itself
-would move a weight by more than the result's rounding: the expanded latent prompt, against the definition in 64 bits.
+would move a weight by more than the result's rounding: prompts and trees in each of their kernels, and the
+expanded latent prompt, against the definition in 64 bits.
 
 Scores are integers of at most 24 bits times a power of two, sums of three products of powers of two and small
 integers, so every one of them is exact in fp32 and the bound has no part that grows with them:
@@ -15,7 +16,7 @@ import torch
 
 from attn_ref import LOST, U
 from quantized_moe_expert_router_gb300 import moe
-from test_gpu_attn import built, offsets  # noqa: F401  (built: the module's build fixture)
+from test_gpu_attn import Cache, built, offsets  # noqa: F401  (built: the module's build fixture)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -112,3 +113,46 @@ def test_latent_prompt(heads, n, dt, power, sign, kind, scale):
     moe.moe_latent_prompt(lat, q, k, r, v, offsets([n]), out, ws, lse=lse)
     assert moe.moe_latent_get_device_status(lat, ws) == 0
     check(out, lse, definition(q[..., :128], k, v, causal(n), f.scale))
+
+
+@pytest.mark.parametrize("power,sign,kind,scale", SCORES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("hk,g,d,n", [(1, 4, 64, 700), (2, 2, 128, 700), (45, 2, 64, 500), (24, 4, 128, 500)])
+def test_prompt(hk, g, d, n, dt, power, sign, kind, scale):
+    scores(dt, power)
+    f, t = Far(power, sign, kind, d ** -0.5 if scale is None else scale, 128, 2), TYPES[dt]
+    q, k, v = f.queries((n, hk * g, d), t), f.keys((n, hk, d), t), f.values((n, hk, d), t)
+    attn = moe.Attention(hk * g, hk, d, 16, 1, 1, t, softmax_scale=f.scale)
+    ws, out = moe.alloc_attn_workspace(attn, 1, n), torch.empty((n, hk * g, d), dtype=t, device=DEV)
+    lse = torch.empty((n, hk * g), dtype=torch.float32, device=DEV)
+    moe.moe_attn_prompt(attn, q, k, v, offsets([n]), out, ws, lse=lse)
+    assert moe.moe_attn_get_device_status(attn, ws) == 0
+    check(out, lse, definition(q, k, v, causal(n), f.scale))
+
+
+@pytest.mark.parametrize("power,sign,kind,scale", SCORES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("hk,g,d,page,cached,fresh,cols,group", [
+    (2, 4, 128, 16, [1500, 90], [1, 3], 2, 16), (1, 8, 64, 32, [2000], [2], 2, 32),                   # few items
+    (8, 4, 128, 16, [300 + 7 * i for i in range(24)], [1] * 24, 2, 16), (8, 4, 64, 64, [500] * 24, [1] * 24, 2, 32),   # many
+    (2, 2, 128, 128, [3000, 40], [33, 60], 300, 128), (2, 1, 64, 64, [3000, 0, 700], [64, 64, 50], 1100, 128),      # many rows
+    (4, 16, 128, 16, [150 + 9 * i for i in range(40)], [9] * 40, 300, 128),
+])
+def test_tree(hk, g, d, page, cached, fresh, cols, group, dt, power, sign, kind, scale):
+    scores(dt, power)
+    f, t = Far(power, sign, kind, d ** -0.5 if scale is None else scale, group, 3), TYPES[dt]
+    c = Cache(hk * g, hk, d, page, t, cached, fresh, seed=7, extra_cols=cols)
+    q, lo, parts = f.queries((c.T, hk * g, d), t), 0, []
+    for b, (a, n) in enumerate(zip(cached, fresh)):
+        k, v = f.keys((a + n, hk, d), t), f.values((a + n, hk, d), t)
+        p = torch.arange(a + n, device=DEV)
+        pg = c.table[b, p // page].long()
+        c.k[pg, :, p % page], c.v[pg, :, p % page] = k, v
+        parts.append(definition(q[lo:lo + n], k, v, causal(a + n)[a:], f.scale))
+        lo += n
+    attn = moe.Attention(hk * g, hk, d, page, c.k.shape[0], c.table.shape[1], t, softmax_scale=f.scale)
+    ws, out = moe.alloc_attn_workspace(attn, len(fresh), c.T), torch.empty_like(q)
+    lse = torch.empty((c.T, hk * g), dtype=torch.float32, device=DEV)
+    moe.moe_attn_tree(attn, q, c.cu, c.cached, c.table, c.k, c.v, out, ws, lse=lse)
+    assert moe.moe_attn_get_device_status(attn, ws) == 0
+    check(out, lse, [torch.cat([p[i] for p in parts]) for i in range(3)])
