@@ -150,6 +150,12 @@ __device__ __forceinline__ float at_exp2(float x) {
 // 2^-15 ln 2 of one, a twentieth of f16's rounding; ordinary scores stay below that, and their way is a subtraction shorter.
 constexpr float kAtFar = 1024.f;
 __device__ __forceinline__ bool at_far(float m, float c) { return fabsf(m) <= FLT_MAX && fabsf(m) * c > kAtFar; }
+// In place of the sum of a part that there is not: its O may be anything.
+constexpr float kAtNoPart = -1.f;
+// A joined row's maximum before its first part.  A part in which the row has no weight (it sees nothing, or scores of -infinity alone) has
+// m = -infinity: its factor is 0, and its O, which is 0 or the NaN that no weight makes of an infinite value, is counted as in
+// a row that is not cut.  Against -infinity the factor itself would be NaN.
+constexpr float kAtLeast = -FLT_MAX;
 __device__ __forceinline__ float at_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

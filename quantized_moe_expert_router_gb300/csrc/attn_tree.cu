@@ -476,7 +476,7 @@ struct AtSums {
 // A row being joined: N of its elements.
 template <int N>
 struct AtRow {
-  float top = -INFINITY, sum = 0.f, acc[N];
+  float top = kAtLeast, sum = 0.f, acc[N];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int e = 0; e < N; e++) acc[e] = 0.f;
@@ -494,7 +494,7 @@ struct AtRow {
     for (int e = 0; e < N; e++) acc[e] *= f0;
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      const bool some = st[k].y != 0.f;          // else a part in which the row sees nothing, or none (v may hold anything)
+      const bool some = !(st[k].y < 0.f);        // else no part (v may hold anything)
       const float f = some ? at_exp2((st[k].x - t1) * c) : 0.f;
       sum = fmaf(st[k].y, f, sum);
 #pragma unroll
@@ -552,7 +552,7 @@ __device__ __forceinline__ void at_gather(const AtArgs &p, int c0, int c1, int s
     for (int q = 0; q < 8; q++) {
       const int k = min(k0 + q, c1);
       const size_t ps = (size_t)(k == c0 ? slot0 : 2 * k) * kAtRows + r;
-      st[q] = k0 + q <= c1 ? __ldcg(p.stat + ps) : make_float2(-INFINITY, 0.f);
+      st[q] = k0 + q <= c1 ? __ldcg(p.stat + ps) : make_float2(-INFINITY, kAtNoPart);
 #pragma unroll
       for (int w = 0; w < N / 4; w++) v[q][w] = __ldcg(reinterpret_cast<const float4 *>(p.part + ps * D + N * hl) + w);
     }
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_many_kernel(const __grid_c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < 2 * kAtWarps) s.seg[tid >> 1][tid & 1].item0 = -1;
-  (&s.stat[0][0][0])[tid] = make_float2(-INFINITY, 0.f);             // no part: a source of no weight
+  (&s.stat[0][0][0])[tid] = make_float2(-INFINITY, kAtNoPart);       // until there is a part
   long long total;
   int nitems;
   at_table<kTok>(s.t, a, total, nitems);
@@ -864,13 +864,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_many_kernel(const __grid_c
     const int w = __shfl_sync(kFull, which, q0), o = __shfl_sync(kFull, (int)out, q0);
     Row row;
     row.clear();
-    for (int q = q0; q < q1; q += 4) {             // four at a time; past the run: of no weight
+    for (int q = q0; q < q1; q += 4) {             // four at a time; past the run: no part
       float2 st[4];
       float4 v[4][N / 4];
 #pragma unroll
       for (int e = 0; e < 4; e++) {
         const int z = min(q + e, 2 * kAtWarps - 1);
-        st[e] = q + e < q1 ? s.stat[z >> 1][z & 1][r] : make_float2(-INFINITY, 0.f);
+        st[e] = q + e < q1 ? s.stat[z >> 1][z & 1][r] : make_float2(-INFINITY, kAtNoPart);
         const float4 *src = reinterpret_cast<const float4 *>(part_of(z >> 1, z & 1) + r * kLd + N * hl);
 #pragma unroll
         for (int k = 0; k < N / 4; k++) v[e][k] = src[k];

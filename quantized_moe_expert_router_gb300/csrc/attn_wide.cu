@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kApThreads, 1) attn_wide_kernel(const __grid_c
       }
       if (!ok) break;
       float l = l2.x + l2.y;
-      if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (kApTile * h + (tid & 127))] = make_float2(m, l);
+      if (PAGED && it.slot >= 0) p.stat[(size_t)it.slot * kApRows + (kApTile * h + (tid & 127))] = make_float2(m, nt > 0 ? l : kAtNoPart);
       if (nt > 0) {
         // ---------------------------------------------------------- epilogue
         if (!at_wait(&s.o_done[h], ni++ & 1u, a, p.ctrl)) break;
@@ -1168,7 +1168,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const int rt = r & (kApTile - 1), dt = (rt * p.magic) >> 16, tl = (r / kApTile) * p.per + dt;   // as in the kernel above
     if (dt >= p.per || tl >= toks) continue;
     const int nsrc = (c1 - c0 + 1) << twin;        // twins: two sources a part, 128 rows apart
-    float top = -INFINITY, sum = 0.f;
+    float top = kAtLeast, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int q0 = 0; q0 < nsrc; q0 += 8) {         // eight sources at a time, so that their loads wait together
       float2 st[8];
@@ -1178,7 +1178,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       for (int z = 0; z < 8; z++) {
         const int q = q0 + z, k = c0 + (q >> twin), slot = k == c0 ? slot0 : 2 * k;
         const int row = r + (twin && (q & 1) ? kApTile : 0);
-        st[z] = make_float2(-INFINITY, 0.f);
+        st[z] = make_float2(-INFINITY, kAtNoPart);
         if (q < nsrc) {
           st[z] = __ldcg(p.stat + (size_t)slot * kApRows + row);
           u[z] = __ldcg(p.part + ((size_t)slot * (D / 4) + d4) * kApRows + row);
@@ -1195,7 +1195,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       acc.w *= f0;
 #pragma unroll
       for (int z = 0; z < 8; z++) {
-        if (st[z].y == 0.f) continue;              // a part in which the row sees nothing (it may hold no O), or none
+        if (st[z].y < 0.f) continue;               // no part, or a twin without a tile
         const float f = at_exp2((st[z].x - t1) * c);
         sum = fmaf(st[z].y, f, sum);
         acc.x = fmaf(u[z].x, f, acc.x);
