@@ -502,8 +502,9 @@ moe_status moe_attn_tree(moe_attn_t attn, int num_requests, int num_rows, const 
  *                    d(t) = dims / 2 * ln(original / (2 pi t)) / ln(theta) is the pair that makes t turns
  *                    over the original context.  attn_factor is given apart.
  *   MOE_ROPE_BANDS   f = s w + (1 - s) w / factor, s = clamp((original w / (2 pi) - low) / (high - low), 0, 1)
- * Angles are exact at any int32 position (frequencies have 53 bits); sines and
- * cosines are off by 2^-20 at most, products are fp32, results are rounded once.
+ * f_i is a double (moe_rope_frequencies).  The angle p f_i is good to 2^-29 at any int32
+ * position, its sine and cosine are off by 2^-20 at most, products are fp32 and results are
+ * rounded once.
  * Rows whose position is negative (moe_kv_plan gives -1 to rows of no request) are
  * left out: nothing is written for them. */
 typedef struct moe_rope *moe_rope_t;

@@ -39,6 +39,17 @@ void frequencies(const moe_rope_config &c, double *f) {
   }
 }
 
+// f radians in turns, times 2^64: f's 53 bits times 64 of 2^66 / (2 pi), rounded once.  A quotient in 64 bits would be off by
+// 2^-53 of itself, which a position of 2^31 makes some 90 of the 2^-32 turns that the kernel takes.
+uint64_t turns_of(double f) {
+  int e;
+  const uint64_t bits = (uint64_t)ldexp(frexp(f, &e), 53);   // f = bits 2^(e - 53), e <= 1
+  const int shift = 55 - e;
+  if (shift > 120) return 0;
+  const unsigned __int128 product = (unsigned __int128)bits * 0xA2F9836E4E44152Aull;
+  return (uint64_t)((product + ((unsigned __int128)1 << (shift - 1))) >> shift);
+}
+
 // A row array: source, destination rows.
 RopeSeg seg_rows(const RowView &src, const RowView &dst, int heads, int units, int turned) {
   RopeSeg s;
@@ -94,7 +105,7 @@ moe_status moe_rope_create(const moe_rope_config *cfg, int device, moe_rope_t *o
   r->device = device;
   frequencies(*cfg, r->freq);
   // frequencies are at most one radian, so the turns stay below 2^64
-  for (int i = 0; i < cfg->dims / 2; i++) r->turns[i] = (uint64_t)(r->freq[i] / kTwoPi * 18446744073709551616.0);
+  for (int i = 0; i < cfg->dims / 2; i++) r->turns[i] = turns_of(r->freq[i]);
   *out = r;
   return MOE_OK;
 }

@@ -5,10 +5,10 @@
 // Pair i of a head, (x, y), becomes s (x cos a - y sin a, x sin a + y cos a) with a = p f_i.
 // A product in fp32 would lose the angle of far positions (p = 10^6: an error of 0.06),
 // so f_i comes as turns a position in 64-bit fixed point and p f_i is an integer product
-// whose whole turns fall off: what is left is exact to p 2^-56 turns (the frequency's own
-// 53 bits), and its upper 32 bits, taken as signed, are the angle within [-pi, pi].  There the
-// SFU's sine and cosine are off by at most 2^-20.9 absolutely, against the 2^-9 or 2^-12 of the
-// result's own rounding; the products are fp32.
+// whose whole turns fall off: what is left is exact to p 2^-64 turns, and its upper 32 bits, taken
+// as signed, are the angle within [-pi, pi], off by 2^-29 at most.  As an fp32 number of radians it is off by
+// 2^-21 (two roundings and that of 2 pi), and there the SFU's sine and cosine are off by at most 2^-21.1
+// absolutely: 2^-20 in all, against the 2^-9 or 2^-12 of the result's own rounding; the products are fp32.
 #include <string.h>
 
 #include "gemv_core.cuh"
