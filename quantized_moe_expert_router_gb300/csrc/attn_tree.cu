@@ -259,7 +259,7 @@ struct AtSums {
   int lim[2];                  // the rows' fresh rows
   int b, cached, ctx;          // request, its cached tokens, and the end of its context
   float o[D / 8][4], m[2], l[2];
-  bool far;                    // a row of the warp takes m off its scores before it scales them
+  bool far;                    // a row of the lane takes m off its scores before it scales them
   __device__ __forceinline__ void begin(const AtTable &s, const AtArgs &p, const AtItem &it, int request) {
     const AttnArgs &a = p.a;
     const int g = (threadIdx.x & 31) >> 2, q4 = threadIdx.x & 3;
@@ -354,7 +354,8 @@ struct AtSums {
       up |= (top[z] - m[z]) * c > kAtSlack;    // -inf - -inf: NaN, not above
     }
     float ref[2] = {m[0], m[1]};                   // what c takes off the scores with them
-    if (far || __any_sync(kFull, up)) {
+    if (__any_sync(kFull, up || far)) {
+      far = false;
 #pragma unroll
       for (int z = 0; z < 2; z++) {
         float m1 = fmaxf(m[z], top[z]);
@@ -368,19 +369,14 @@ struct AtSums {
           o[d][2 * z] *= f;
           o[d][2 * z + 1] *= f;
         }
-        ref[z] = m1;
-      }
-      far = __any_sync(kFull, at_far(m[0], c) || at_far(m[1], c));
-      if (far) {
+        const bool own = at_far(m1, c);
+        const float off = own ? -m1 : 0.f;
+        ref[z] = own ? 0.f : m1;
+        far |= own;
 #pragma unroll
-        for (int z = 0; z < 2; z++) {
-          const float off = at_far(m[z], c) ? -m[z] : 0.f;
-          if (off != 0.f) ref[z] = 0.f;
-#pragma unroll
-          for (int t = 0; t < kTok / 8; t++) {
-            sc[t][2 * z] += off;
-            sc[t][2 * z + 1] += off;
-          }
+        for (int t = 0; t < kTok / 8; t++) {
+          sc[t][2 * z] += off;
+          sc[t][2 * z + 1] += off;
         }
       }
     }
