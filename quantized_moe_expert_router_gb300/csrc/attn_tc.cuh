@@ -147,7 +147,8 @@ __device__ __forceinline__ float at_exp2(float x) {
 // Whether a row whose maximum is m has to take m off its scores before it scales them.  c v - c m in one fma is exact
 // but for the rounding of c m, which gives every weight of the row a factor of up to 2^(ulp(c m) / 2): one for all, as long as
 // m stays, but another for tiles, twins or parts with another m, and past 2^31 it overflows P.  Up to 2^10 the factor is within
-// 2^-15 ln 2 of one, a twentieth of f16's rounding; ordinary scores stay below that, and their way is a subtraction shorter.
+// 2^-15 ln 2 of one, a twentieth of f16's rounding; ordinary scores stay below that, and
+// their way is a subtraction shorter (a latent prompt of 8192 tokens with it everywhere: 461 us for 458).
 constexpr float kAtFar = 1024.f;
 __device__ __forceinline__ bool at_far(float m, float c) { return fabsf(m) <= FLT_MAX && fabsf(m) * c > kAtFar; }
 // In place of the sum of a part that there is not: its O may be anything.

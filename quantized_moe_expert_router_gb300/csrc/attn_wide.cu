@@ -111,8 +111,10 @@ struct ApGeom {
 // time, so of the five pieces that a row tile's two products read, two of the next are there before and
 // three come while the other row tile's products run.  A tile's pieces share a barrier (kv_full, four in turn):
 // beside the products, which read shared memory all the time, each look at one costs 100 to 200 cycles.  8192 tokens of
-// 32 heads 458 us, 1500 TFLOP/s (568 with a barrier a piece); bound by shared memory: S reads 8 KB of it a step of 64 cycles,
-// with the copies 2660 cycles for the tensor pipe's 2560.
+// 32 heads 458 us, 1500 TFLOP/s (568 with a barrier a piece; for seconds on end 496, at the 1.9 GHz of the power cap).  A step, two
+// row tiles and a key tile, is 2560 cycles of the tensor pipe and 2660 of shared memory (S reads 8 KB in 64 cycles, and the
+// copies), and takes 3900 by clock reads: the issuing warp spends 2670 in the issue of its products, with that behind it, waits
+// 440 for values, P and keys, and is 800 between those, where the pipe can run dry.
 constexpr int kApPiece = kApTile * 128;
 struct ApLatGeom {
   static constexpr int kTileBytes = 2 * kApPiece;

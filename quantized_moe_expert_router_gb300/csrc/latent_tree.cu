@@ -62,9 +62,10 @@
 // the next vote, which tells the others, and all four end together.
 //
 // Bound: for up to 64 rows over long contexts HBM (16 tokens at up to 100000 of 64 heads 154 us, 5.2 TB/s; 16 heads,
-// 16 at up to 60000, 86 us, 5.6), with 5 us of start, uneven ends and the join; for more rows shared memory (a tile's products
-// alone 1970 cycles at N = 64, 1490 at N = 16; some 2600 to 3000 beside one another and behind a ring of two tiles: 128 heads, 16 at
-// up to 60000, 157 us, 730 TFLOP/s); for short contexts a chain of latencies: one token at 50 9 us, at 1000 12, join 3 of it.
+// 16 at up to 60000, 84 us, 5.7); for more rows shared memory (a tile's products alone 1970 cycles at N = 64, 1490 at N = 16; by clock
+// reads 2600 to 3300 beside one another and behind a ring of two tiles: 128 heads, 16 at up to 60000, 157 us, 730 TFLOP/s); for short
+// contexts a chain of latencies: one token at 50 9 us, at 1000 12, join 3 of it.  Around the tiles the first scores come 5
+// (one request) to 9 us after the start, an item's epilogue takes 1 (N = 16) to 2.3, the join 4 (N = 16) to 7.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -1094,6 +1095,8 @@ cudaError_t launch_lat_tree(const LatArgs &a, uint8_t *ws, int num_sms, cudaStre
   //   1 row of 16 heads at 120 tokens 10.1, 11.6, at 250 13.1, 11.4; 64 requests of up to 250 13.9, 16.3, of up to 500 20.0, 18.5
   //   64 heads, 64 requests of up to 500 24.5, 30.8, of up to 1000 36.9, 33.8; 512 of up to 2000 156, 181, of up to 4000 283, 268
   //   8 trees of 8 and 64 heads at up to 250 18.0, 20.6, at up to 500 24.4, 22.2; 64 of them at up to 2000 93, 110, 4000 186, 149
+  // These tables were as wide as the longest context.  The rule knows the call's sizes only, the lengths are on the device: a table
+  // of capacity counts as long contexts, whose items are cut, at the second figure of each pair.
   const double places = grid / p.gang, tiles = (double)(((long long)a.max_pages << a.page_shift) + kLtTile - 1) / kLtTile;
   const double items = (double)a.B * ((p.hp * ((mean + p.per - 1) / p.per) + p.gang - 1) / p.gang);
   const double share = 0.6 * items * tiles / places, parts = items > places ? 2 : (items * tiles < places ? items * tiles / places : 1);

@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t rope_pack(float lo, float hi, int f16) {
 //
 // Bound: HBM.  16384 rows, q of 16 heads and k, v of 8 of 128: 40.6 us, 6.4 TB/s (a plain copy has 6.6 to 6.7); 16384
 // latent rows with q of 64 heads, 128 bytes of every 384: 49.4 us, 6.0 TB/s; 8192 rows, q of 24 heads and k of 4, half of
-// 128 elements turned: 18.1 us, 6.5 TB/s; one row 2.4 us, a launch.  Eight CTAs of 128 threads an SM (64 registers) keep
+// 128 elements turned: 18.1 us, 6.5 TB/s; one row 2.0 us, a launch.  Eight CTAs of 128 threads an SM (64 registers) keep
 // most loads in flight: with 6 and 10 CTAs the latent rows took 54.3 and 64.9 us, with 256 threads 57.3.
 template <bool F16, bool INTERLEAVED, int HP>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeArgs a) {

@@ -90,20 +90,16 @@ SCORES = [(20, 1, "spread", 1.0), (24, 1, "spread", None), (24, -1, "spread", No
           (25, 1, "rise", None), (40, 1, "spread", 2.0 ** -18), (36, 1, "ties", None), (60, -1, "ties", None)]
 
 
-def scores(dt, power):
-    if dt == "f16" and power > 26:
-        pytest.skip("past f16's elements")
+FORMS = pytest.mark.parametrize("dt,power,sign,kind,scale", [(dt, *s) for dt in TYPES for s in SCORES if dt == "bf16" or s[0] <= 26])   # f16 ends at 2^16
 
 
 def causal(n):
     return torch.ones((n, n), dtype=torch.bool, device=DEV).tril()
 
 
-@pytest.mark.parametrize("power,sign,kind,scale", SCORES)
-@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@FORMS
 @pytest.mark.parametrize("heads,n", [(4, 700), (90, 500)])             # single row tiles over alternate key tiles, pairs
 def test_latent_prompt(heads, n, dt, power, sign, kind, scale):
-    scores(dt, power)
     f, t = Far(power, sign, kind, 192 ** -0.5 if scale is None else scale, 128, 1), TYPES[dt]
     q, k, v = f.queries((n, heads, 192), t), f.keys((n, heads, 128), t), f.values((n, heads, 128), t)
     lat = moe.LatentAttention(heads, 16, 1, 1, t, softmax_scale=f.scale)
@@ -115,11 +111,9 @@ def test_latent_prompt(heads, n, dt, power, sign, kind, scale):
     check(out, lse, definition(q[..., :128], k, v, causal(n), f.scale))
 
 
-@pytest.mark.parametrize("power,sign,kind,scale", SCORES)
-@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@FORMS
 @pytest.mark.parametrize("hk,g,d,n", [(1, 4, 64, 700), (2, 2, 128, 700), (45, 2, 64, 500), (24, 4, 128, 500)])
 def test_prompt(hk, g, d, n, dt, power, sign, kind, scale):
-    scores(dt, power)
     f, t = Far(power, sign, kind, d ** -0.5 if scale is None else scale, 128, 2), TYPES[dt]
     q, k, v = f.queries((n, hk * g, d), t), f.keys((n, hk, d), t), f.values((n, hk, d), t)
     attn = moe.Attention(hk * g, hk, d, 16, 1, 1, t, softmax_scale=f.scale)
@@ -130,8 +124,7 @@ def test_prompt(hk, g, d, n, dt, power, sign, kind, scale):
     check(out, lse, definition(q, k, v, causal(n), f.scale))
 
 
-@pytest.mark.parametrize("power,sign,kind,scale", SCORES)
-@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@FORMS
 @pytest.mark.parametrize("hk,g,d,page,cached,fresh,cols,group", [
     (2, 4, 128, 16, [1500, 90], [1, 3], 2, 16), (1, 8, 64, 32, [2000], [2], 2, 32),                   # few items
     (8, 4, 128, 16, [300 + 7 * i for i in range(24)], [1] * 24, 2, 16), (8, 4, 64, 64, [500] * 24, [1] * 24, 2, 32),   # many
@@ -139,7 +132,6 @@ def test_prompt(hk, g, d, n, dt, power, sign, kind, scale):
     (4, 16, 128, 16, [150 + 9 * i for i in range(40)], [9] * 40, 300, 128),
 ])
 def test_tree(hk, g, d, page, cached, fresh, cols, group, dt, power, sign, kind, scale):
-    scores(dt, power)
     f, t = Far(power, sign, kind, d ** -0.5 if scale is None else scale, group, 3), TYPES[dt]
     c = Cache(hk * g, hk, d, page, t, cached, fresh, seed=7, extra_cols=cols)
     q, lo, parts = f.queries((c.T, hk * g, d), t), 0, []
