@@ -1,6 +1,6 @@
 """Attention on scores that are large against their differences, where c m (the scaled maximum) rounded by itself
-would move a weight by more than the result's rounding: prompts and trees in each of their kernels, and the
-expanded latent prompt, against the definition in 64 bits.
+would move a weight by more than the result's rounding: prompts and trees in each of their kernels, and both
+latent forms, against the definition in 64 bits.
 
 Scores are integers of at most 24 bits times a power of two, sums of three products of powers of two and small
 integers, so every one of them is exact in fp32 and the bound has no part that grows with them:
@@ -16,7 +16,7 @@ import torch
 
 from attn_ref import LOST, U
 from quantized_moe_expert_router_gb300 import moe
-from test_gpu_attn import Cache, built, offsets  # noqa: F401  (built: the module's build fixture)
+from test_gpu_attn import Cache, built, ints, offsets  # noqa: F401  (built: the module's build fixture)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -147,4 +147,33 @@ def test_tree(hk, g, d, page, cached, fresh, cols, group, dt, power, sign, kind,
     lse = torch.empty((c.T, hk * g), dtype=torch.float32, device=DEV)
     moe.moe_attn_tree(attn, q, c.cu, c.cached, c.table, c.k, c.v, out, ws, lse=lse)
     assert moe.moe_attn_get_device_status(attn, ws) == 0
+    check(out, lse, [torch.cat([p[i] for p in parts]) for i in range(3)])
+
+
+@FORMS
+@pytest.mark.parametrize("heads,page,cached,fresh,wide", [
+    (16, 16, [1500], [1], False), (64, 64, [1700, 90], [3, 1], False), (128, 32, [700, 1200, 3], [2, 5, 1], False),    # cut
+    (16, 64, [150 + 3 * i for i in range(60)], [1] * 60, False), (16, 64, [150 + 3 * i for i in range(60)], [1] * 60, True),   # whole, and cut
+])
+def test_latent_tree(heads, page, cached, fresh, wide, dt, power, sign, kind, scale):
+    """The scores come from the key part alone, so that the values are the latents of the other forms' values."""
+    f, t = Far(power, sign, kind, 192 ** -0.5 if scale is None else scale, 64, 4), TYPES[dt]
+    need = [-(-(a + n) // page) for a, n in zip(cached, fresh)]
+    table = torch.full((len(need), max(need) + (2000 if wide else 0)), -1, dtype=torch.int32, device=DEV)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(5)).int().to(DEV)
+    cache = torch.full((sum(need), page, 576), math.nan, dtype=t, device=DEV)
+    T, lo, at, parts = sum(fresh), 0, 0, []
+    q = f.queries((T, heads, 64), t)
+    for b, (a, n) in enumerate(zip(cached, fresh)):
+        table[b, :need[b]] = order[at:at + need[b]]
+        k, v = f.keys((a + n, 1, 64), t), f.values((a + n, 1, 512), t)
+        p = torch.arange(a + n, device=DEV)
+        cache[table[b, p // page].long(), p % page] = torch.cat([v, k], 2)[:, 0]
+        parts.append(definition(q[lo:lo + n], k, v, causal(a + n)[a:], f.scale))
+        lo, at = lo + n, at + need[b]
+    lat = moe.LatentAttention(heads, page, sum(need), table.shape[1], t, softmax_scale=f.scale)
+    ws, out = moe.alloc_latent_workspace(lat, len(fresh), T), torch.empty((T, heads, 512), dtype=t, device=DEV)
+    lse = torch.empty((T, heads), dtype=torch.float32, device=DEV)
+    moe.moe_latent_tree(lat, torch.zeros_like(out), q, offsets(fresh), ints(cached), table, cache, out, ws, lse=lse)
+    assert moe.moe_latent_get_device_status(lat, ws) == 0
     check(out, lse, [torch.cat([p[i] for p in parts]) for i in range(3)])
