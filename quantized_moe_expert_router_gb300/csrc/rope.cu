@@ -8,7 +8,7 @@
 // whose whole turns fall off: what is left is exact to p 2^-64 turns, and its upper 32 bits, taken
 // as signed, are the angle within [-pi, pi], off by 2^-29 at most.  As an fp32 number of radians it is off by
 // 2^-21 (two roundings and that of 2 pi), and there the SFU's sine and cosine are off by at most 2^-21.1
-// absolutely: 2^-20 in all, against the 2^-9 or 2^-12 of the result's own rounding; the products are fp32.
+// absolutely: 2^-20 in all, against the 2^-8 or 2^-11 of the result's own rounding; the products are fp32.
 #include <string.h>
 
 #include "gemv_core.cuh"
